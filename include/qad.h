@@ -234,6 +234,105 @@ int qad_moe_bwd_scalegrad(const qad_moe_shape* s, const void* w13, const float* 
 int qad_moe_combine(const void* rows, const int32_t* row_of, const float* p, void* out, int64_t T, int32_t topk,
                     int64_t d, qad_stream_t stream);
 
+/*
+ * Residual addition + RMSNorm, with the activation quantizers of the per-row grids on its output:
+ * what stands before every quantized layer of the model (the residual stream and its norms are kept
+ * in high precision; AngelSlim mcore_qad walkthrough, section 二.3: each quantized matmul's input is
+ * fake-quantized first).
+ *   r     = bf16(x + res)                       (r = x without res); the norm reads r as stored
+ *   rstd  = 1 / sqrt(mean(r^2) + eps)           fp32
+ *   y     = bf16(r * rstd * gamma)              for the router, or as the layer's x
+ *   scale = fp32(max |y| / 448) (E4M3) or / 127 (INT8), per row
+ *   codes = E4M3 or INT8 code of fp32(y / scale); y_hat = bf16(code value * scale)
+ * -- the same bits as the layer's own activation quantizer gives for y.
+ *   x     bf16 [T, d], ldx elements between rows     res    bf16 [T, d], ldres between rows, or NULL
+ *   gamma bf16 [d]                                   res_out bf16 [T, d] or NULL: r (may be res itself
+ *                                                           when ldres == d, or x when ldx == d)
+ *   y, y_hat bf16 [T, d], codes uint8 [T, d], scale fp32 [T], rstd fp32 [T]: each may be NULL, but one of
+ *   y, y_hat and codes must be given, and codes need scale; y_hat, codes and scale must be NULL with
+ *   QAD_ACT_NONE.  Outputs other than res_out may not overlap inputs.
+ * Requires d % 16 == 0, d <= QAD_RMSNORM_MAX_D (else QAD_ERR_UNSUPPORTED), ldx, ldres >= d and multiples
+ * of 8, eps >= 0.  A row of zeros gives y = 0, scale 0 and codes of +-0.
+ */
+typedef enum { QAD_ACT_NONE = 0, QAD_ACT_E4M3 = 1, QAD_ACT_INT8 = 2 } qad_act;
+enum { QAD_RMSNORM_MAX_D = 16384 };
+int qad_rmsnorm_fwd(const void* x, const void* res, const void* gamma, float eps, int act, void* res_out, void* y,
+                    void* y_hat, void* codes, float* scale, float* rstd, int64_t T, int64_t d, int64_t ldx,
+                    int64_t ldres, qad_stream_t stream);
+
+/*
+ * Gradient of qad_rmsnorm_fwd (straight through the quantizers).  With n = r * rstd, dn = dy * gamma:
+ *   dx     = bf16(rstd * (dn - n * mean(dn * n)) + dres)   the gradient of x and of res alike
+ *   dgamma = sum over rows of dy * n                        fp32, summed in a fixed order
+ *   dy     bf16 [T, d]         dres bf16 [T, d] or NULL: the gradient arriving at res_out
+ *   r      bf16 [T, d], ldr between rows: the forward's res_out (x without res)    rstd fp32 [T]
+ *   dx     bf16 [T, d] (may be dy or dres)          dgamma fp32 [d] or NULL (overwritten)
+ *   ws     needed with dgamma: 256-byte aligned, ws_bytes >= qad_rmsnorm_workspace_bytes(T, d)
+ */
+size_t qad_rmsnorm_workspace_bytes(int64_t T, int64_t d);
+int qad_rmsnorm_bwd(const void* dy, const void* dres, const void* r, const void* gamma, const float* rstd, void* dx,
+                    float* dgamma, int64_t T, int64_t d, int64_t ldr, void* ws, size_t ws_bytes, qad_stream_t stream);
+
+/*
+ * Softmax cross entropy of hidden states against the output head, without keeping the logits: the
+ * language-model part of the total loss ("MCoreQAD Backend", YAML lm_weight; walkthrough section
+ * 二.5: total = lm_weight * lm_loss + distill_weight * distill_loss; section 二.3: the output layer is
+ * not quantized).  z = h . w^T:
+ *   loss[i] = lse[i] - z[i, target[i]] (0 for target < 0),  lse[i] = log(sum_v exp(z[i, v]))
+ *   dh[i]   = g[i] * (sum_v q[i, v] * w[v] - w[target[i]])          q = softmax(z)
+ *   dw[v]   = sum_i g[i] * (q[i, v] - 1[v = target[i]]) * h[i]
+ *   h bf16 [N, d], ldh between rows          w bf16 [V, d], ldw between rows
+ *   target int32 [N]: the row's token; negative: the row carries no loss and no gradient (lse is still
+ *          written); >= V: the same, and QAD_DEV_BAD_INDEX is set in the workspace's error word
+ *   g      fp32 [N] or NULL (1): the derivative of the total loss with respect to each row's loss,
+ *          e.g. lm_weight / tokens; loss itself is not scaled by it
+ *   loss, lse fp32 [N] (written)
+ *   dh     bf16 [N, d] or NULL; added to when accumulate != 0, else overwritten
+ *   dw     bf16 [V, d] or NULL (overwritten); one of dh and dw must be given.  Every row of h, also
+ *          one without a target, must be finite when dw is asked for.
+ *   ws     256-byte aligned, ws_bytes >= qad_linear_ce_workspace_bytes(N, d, V, dh != NULL, dw != NULL).
+ *          Its first word is the device error word (qad_check_device_error), cleared by each call.
+ * The logits exist one piece of the vocabulary at a time (at most 1 GB of exp(logits) in bf16, and
+ * only when a gradient is asked for); sums and gradients are accumulated in fp32.
+ * Requires d % 16 == 0, ldh, ldw >= d and multiples of 8, N, V < 2^30, d <= 65536.
+ */
+size_t qad_linear_ce_workspace_bytes(int64_t N, int64_t d, int64_t V, int dh, int dw);
+int qad_linear_ce_fwd(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* target, float* loss,
+                      float* lse, int64_t N, int64_t d, int64_t V, void* ws, size_t ws_bytes, qad_stream_t stream);
+int qad_linear_ce_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* target, const float* g,
+                          float* loss, float* lse, void* dh, void* dw, int accumulate, int64_t N, int64_t d, int64_t V,
+                          void* ws, size_t ws_bytes, qad_stream_t stream);
+
+/*
+ * Distillation from the teacher's top K logits ("MCoreQAD Backend", distill_topk: the divergence is
+ * computed only on the teacher's top-k tokens, so [tokens, vocab] is never materialised; walkthrough
+ * section 二.5: types kl, rkl and a mix of both by the teacher's confidence).  Both distributions are
+ * softmaxes over the row's kept tokens; b = inv_temp, z[i, k] = <h[i], w[idx[i, k]]>:
+ *   p = softmax_k(b * t_logit[i, k]),  q = softmax_k(b * z[i, k])
+ *   loss[i] = (1 - m) * sum_k p (log p - log q) + m * sum_k q (log q - log p),  m = mix[i]
+ *   dh[i]   = g[i] * b * sum_k ((1 - m) (q - p) + m q (log q - log p - RKL)) * w[idx[i, k]]
+ *   h bf16 [N, d], ldh between rows     w bf16 [V, d], ldw between rows (no gradient: the head is frozen)
+ *   idx int32 [N, K], t_logit fp32 [N, K] (logits or log-probabilities: a row's common offset does not
+ *       matter).  A slot with idx < 0 or t_logit = -inf does not count; idx >= V neither, and
+ *       QAD_DEV_BAD_INDEX is set in *err.  A row that keeps no slot has loss 0 and dh 0.
+ *   mix fp32 [N] or NULL (0: forward KL; 1: reverse KL)
+ *   g   fp32 [N] or NULL (1): the derivative of the total loss with respect to each row's loss
+ *   loss fp32 [N] (written)
+ *   dh  bf16 [N, d]; added to when accumulate != 0 (after qad_linear_ce_fwd_bwd: the total loss's
+ *       gradient), else overwritten
+ *   err int32 [1] or NULL: a device error word of the caller's, OR-ed into (qad_check_device_error)
+ * Requires d % 16 == 0, d <= QAD_DISTILL_MAX_D, 1 <= K <= QAD_DISTILL_MAX_K, ldh, ldw >= d and multiples
+ * of 8, inv_temp > 0 and finite.
+ */
+enum { QAD_DISTILL_MAX_D = 16384, QAD_DISTILL_MAX_K = 1024 };
+int qad_distill_topk_fwd(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* idx,
+                         const float* t_logit, const float* mix, float inv_temp, float* loss, int64_t N, int64_t d,
+                         int64_t V, int64_t K, int32_t* err, qad_stream_t stream);
+int qad_distill_topk_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* idx,
+                             const float* t_logit, const float* mix, float inv_temp, const float* g, float* loss,
+                             void* dh, int accumulate, int64_t N, int64_t d, int64_t V, int64_t K, int32_t* err,
+                             qad_stream_t stream);
+
 /* Synchronises `stream`, copies the device error word of `ws` into *code (host
  * pointer, may be NULL) and returns QAD_OK if it is zero, QAD_ERR_DEVICE otherwise. */
 int qad_check_device_error(void* ws, qad_stream_t stream, int32_t* code);
@@ -288,7 +387,9 @@ enum {
   QAD_K_GEMM_WGRAD_FC2 = 11, QAD_K_GEMM_WGRAD_FC1 = 12, QAD_K_SCALE_REDUCE = 13,
   QAD_K_GEMM_FC1_RECOMPUTE = 14, /* QAD_FLAG_RECOMPUTE: fc1 again in the dgrad call (Z1 only) */
   QAD_K_DEPLOY_SCALES = 15,      /* QAD_FMT_NVFP4_E4M3: the deployed weight scales */
-  QAD_K_COUNT = 16
+  QAD_K_RMSNORM = 16, QAD_K_RMSNORM_BWD = 17,
+  QAD_K_CE_LOGITS = 18, QAD_K_CE_DH = 19, QAD_K_CE_DW = 20, QAD_K_DISTILL = 21,
+  QAD_K_COUNT = 22
 };
 int qad_profile_enable(int on);
 int qad_profile_reset(void);

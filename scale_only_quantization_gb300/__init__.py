@@ -25,13 +25,17 @@ VIEWS = ["HEADER", "OFFSETS", "COUNTS", "ROW_TOKEN", "ROW_SLOT", "ROW_OF", "W13_
          "H_HAT", "Y", "DY", "DZ1", "DA1", "XQ", "W13_CODES", "W2_CODES", "A1_CODES", "H_CODES", "A_SCALE",
          "H_SCALE", "S13_DEPLOYED", "S2_DEPLOYED"]
 VIEW = {n: i for i, n in enumerate(VIEWS)}
-KERNELS = 16
+KERNELS = 22
+QAD_ACT_NONE, QAD_ACT_E4M3, QAD_ACT_INT8 = range(3)
+QAD_RMSNORM_MAX_D, QAD_DISTILL_MAX_D, QAD_DISTILL_MAX_K = 16384, 16384, 1024
 
 EXPORTS = ["qad_fakequant_fwd", "qad_moe_workspace_bytes", "qad_moe_fwd", "qad_moe_bwd_dgrad",
            "qad_moe_bwd_scalegrad", "qad_check_device_error", "qad_status_string", "qad_moe_debug_view",
            "qad_profile_enable", "qad_profile_reset", "qad_profile_read", "qad_kernel_name", "qad_launch_count",
            "qad_debug_quotient", "qad_route_permute_noalloc", "qad_debug_wait_timeout", "qad_moe_combine",
-           "qad_nvfp4_deploy_scales"]
+           "qad_nvfp4_deploy_scales", "qad_rmsnorm_workspace_bytes", "qad_rmsnorm_fwd", "qad_rmsnorm_bwd",
+           "qad_linear_ce_workspace_bytes", "qad_linear_ce_fwd", "qad_linear_ce_fwd_bwd", "qad_distill_topk_fwd",
+           "qad_distill_topk_fwd_bwd"]
 
 
 class QADError(RuntimeError):
@@ -50,6 +54,7 @@ class MoEShape(ctypes.Structure):
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 _SHAPE = ctypes.POINTER(MoEShape)
 
 
@@ -83,6 +88,18 @@ def lib():
                                                          _P, _P, _P]),
             "qad_moe_combine": (ctypes.c_int, [_P, _P, _P, _P, _I64, ctypes.c_int32, _I64, _P]),
             "qad_nvfp4_deploy_scales": (ctypes.c_int, [_P, _P, _I64, _I64, _P]),
+            "qad_rmsnorm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+            "qad_rmsnorm_fwd": (ctypes.c_int, [_P, _P, _P, _F32, ctypes.c_int] + [_P] * 6 + [_I64] * 4 + [_P]),
+            "qad_rmsnorm_bwd": (ctypes.c_int, [_P] * 7 + [_I64] * 3 + [_P, ctypes.c_size_t, _P]),
+            "qad_linear_ce_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, ctypes.c_int, ctypes.c_int]),
+            "qad_linear_ce_fwd": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _P,
+                                                 ctypes.c_size_t, _P]),
+            "qad_linear_ce_fwd_bwd": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, ctypes.c_int, _I64,
+                                                     _I64, _I64, _P, ctypes.c_size_t, _P]),
+            "qad_distill_topk_fwd": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _F32, _P, _I64, _I64, _I64, _I64,
+                                                    _P, _P]),
+            "qad_distill_topk_fwd_bwd": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _F32, _P, _P, _P, ctypes.c_int,
+                                                        _I64, _I64, _I64, _I64, _P, _P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -97,6 +114,10 @@ def status_string(status):
 
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _stream(stream):
@@ -207,6 +228,55 @@ def qad_route_permute_noalloc(topk_idx, T, topk, E, row_token, row_slot, row_of,
 def qad_moe_combine(rows, row_of, p, out, T, topk, d, stream=None):
     return _check(lib().qad_moe_combine(_ptr(rows), _ptr(row_of), _ptr(p), _ptr(out), int(T), int(topk), int(d),
                                         _stream(stream)), "qad_moe_combine")
+
+
+def qad_rmsnorm_workspace_bytes(T, d):
+    return int(lib().qad_rmsnorm_workspace_bytes(int(T), int(d)))
+
+
+def qad_rmsnorm_fwd(x, res, gamma, eps, act, res_out, y, y_hat, codes, scale, rstd, T, d, ldx, ldres, stream=None):
+    """Residual addition + RMSNorm with an optional 8-bit output (see include/qad.h)."""
+    return _check(lib().qad_rmsnorm_fwd(_ptr(x), _ptr(res), _ptr(gamma), float(eps), int(act), _ptr(res_out), _ptr(y),
+                                        _ptr(y_hat), _ptr(codes), _ptr(scale), _ptr(rstd), int(T), int(d), int(ldx),
+                                        int(ldres), _stream(stream)), "qad_rmsnorm_fwd")
+
+
+def qad_rmsnorm_bwd(dy, dres, r, gamma, rstd, dx, dgamma, T, d, ldr, ws=None, stream=None):
+    return _check(lib().qad_rmsnorm_bwd(_ptr(dy), _ptr(dres), _ptr(r), _ptr(gamma), _ptr(rstd), _ptr(dx),
+                                        _ptr(dgamma), int(T), int(d), int(ldr), _ptr(ws), _nbytes(ws),
+                                        _stream(stream)), "qad_rmsnorm_bwd")
+
+
+def qad_linear_ce_workspace_bytes(N, d, V, dh, dw):
+    return int(lib().qad_linear_ce_workspace_bytes(int(N), int(d), int(V), int(bool(dh)), int(bool(dw))))
+
+
+def qad_linear_ce_fwd(h, ldh, w, ldw, target, loss, lse, N, d, V, ws, stream=None):
+    """Cross entropy of hidden states against the head w, without keeping the logits (see include/qad.h)."""
+    return _check(lib().qad_linear_ce_fwd(_ptr(h), int(ldh), _ptr(w), int(ldw), _ptr(target), _ptr(loss), _ptr(lse),
+                                          int(N), int(d), int(V), _ptr(ws), _nbytes(ws), _stream(stream)),
+                  "qad_linear_ce_fwd")
+
+
+def qad_linear_ce_fwd_bwd(h, ldh, w, ldw, target, g, loss, lse, dh, dw, accumulate, N, d, V, ws, stream=None):
+    return _check(lib().qad_linear_ce_fwd_bwd(_ptr(h), int(ldh), _ptr(w), int(ldw), _ptr(target), _ptr(g), _ptr(loss),
+                                              _ptr(lse), _ptr(dh), _ptr(dw), int(accumulate), int(N), int(d), int(V),
+                                              _ptr(ws), _nbytes(ws), _stream(stream)), "qad_linear_ce_fwd_bwd")
+
+
+def qad_distill_topk_fwd(h, ldh, w, ldw, idx, t_logit, mix, inv_temp, loss, N, d, V, K, err=None, stream=None):
+    """Divergence from the teacher's top K logits over the teacher's own tokens (see include/qad.h)."""
+    return _check(lib().qad_distill_topk_fwd(_ptr(h), int(ldh), _ptr(w), int(ldw), _ptr(idx), _ptr(t_logit), _ptr(mix),
+                                             float(inv_temp), _ptr(loss), int(N), int(d), int(V), int(K), _ptr(err),
+                                             _stream(stream)), "qad_distill_topk_fwd")
+
+
+def qad_distill_topk_fwd_bwd(h, ldh, w, ldw, idx, t_logit, mix, inv_temp, g, loss, dh, accumulate, N, d, V, K,
+                             err=None, stream=None):
+    return _check(lib().qad_distill_topk_fwd_bwd(_ptr(h), int(ldh), _ptr(w), int(ldw), _ptr(idx), _ptr(t_logit),
+                                                 _ptr(mix), float(inv_temp), _ptr(g), _ptr(loss), _ptr(dh),
+                                                 int(accumulate), int(N), int(d), int(V), int(K), _ptr(err),
+                                                 _stream(stream)), "qad_distill_topk_fwd_bwd")
 
 
 def qad_debug_wait_timeout(err_word, budget_cycles, stream=None):

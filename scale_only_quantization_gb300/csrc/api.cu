@@ -224,7 +224,7 @@ const char* qad_status_string(int status) {
     case QAD_OK: return "ok";
     case QAD_ERR_INVALID_ARG: return "invalid argument (null or misaligned pointer, bad size or flag)";
     case QAD_ERR_UNSUPPORTED:
-      return "unsupported shape (needs d, F multiples of 16 -- of 128 for INT4 weights, d % 256 == 0 and F % 128 == 0 "
+      return "unsupported shape (see the entry point; the layer needs d, F multiples of 16 -- of 128 for INT4 weights, d % 256 == 0 and F % 128 == 0 "
              "with the E4M3 tensor path or the in-GEMM dequant --, topk <= min(E, 32), E <= 1024)";
     case QAD_ERR_WORKSPACE: return "workspace smaller than qad_moe_workspace_bytes()";
     case QAD_ERR_CUDA: return "CUDA runtime call or kernel launch failed";
@@ -415,6 +415,117 @@ int qad_moe_combine(const void* rows, const int32_t* row_of, const float* p, voi
   return to_status(launch_combine(rows, row_of, p, out, T, topk, d, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// A [rows, d] bf16 tensor with ld elements between rows: 16-byte aligned rows, none overlapping
+static bool ok_rows(const void* p, int64_t ld, int64_t d) { return ok_ptr(p) && ld >= d && ld % 8 == 0; }
+
+size_t qad_rmsnorm_workspace_bytes(int64_t T, int64_t d) {
+  if (T < 0 || d <= 0 || d % 16 || d > QAD_RMSNORM_MAX_D) return 0;
+  return up(4 * (size_t)norm_groups(T > 0 ? T : 1) * (size_t)d);
+}
+
+int qad_rmsnorm_fwd(const void* x, const void* res, const void* gamma, float eps, int act, void* res_out, void* y,
+                    void* y_hat, void* codes, float* scale, float* rstd, int64_t T, int64_t d, int64_t ldx,
+                    int64_t ldres, qad_stream_t stream) {
+  if (T < 0 || d <= 0 || !(eps >= 0.0f) || act < QAD_ACT_NONE || act > QAD_ACT_INT8) return QAD_ERR_INVALID_ARG;
+  if (d % 16 || d > QAD_RMSNORM_MAX_D || T > 0x7fffffff) return QAD_ERR_UNSUPPORTED;
+  if (act == QAD_ACT_NONE && (y_hat || codes || scale)) return QAD_ERR_INVALID_ARG;
+  if (codes && !scale) return QAD_ERR_INVALID_ARG;  // codes mean nothing without their scales
+  if (T == 0) return QAD_OK;
+  if (!ok_rows(x, ldx, d) || !ok_ptr(gamma) || (res && !ok_rows(res, ldres, d))) return QAD_ERR_INVALID_ARG;
+  for (const void* o : {(const void*)res_out, (const void*)y, (const void*)y_hat, (const void*)codes,
+                        (const void*)scale, (const void*)rstd})
+    if (o && !aligned16(o)) return QAD_ERR_INVALID_ARG;
+  if (!y && !y_hat && !codes) return QAD_ERR_INVALID_ARG;
+  const int kind = act == QAD_ACT_E4M3 ? kQE4M3 : act == QAD_ACT_INT8 ? kQInt8 : kQNone;
+  return to_status(launch_rmsnorm_fwd(x, ldx, res, ldres, gamma, eps, kind, res_out, y, y_hat, codes, scale, rstd, T, d,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qad_rmsnorm_bwd(const void* dy, const void* dres, const void* r, const void* gamma, const float* rstd, void* dx,
+                    float* dgamma, int64_t T, int64_t d, int64_t ldr, void* ws, size_t ws_bytes, qad_stream_t stream) {
+  if (T < 0 || d <= 0) return QAD_ERR_INVALID_ARG;
+  if (d % 16 || d > QAD_RMSNORM_MAX_D || T > 0x7fffffff) return QAD_ERR_UNSUPPORTED;
+  if (dgamma && !aligned16(dgamma)) return QAD_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return dgamma ? to_status(cudaMemsetAsync(dgamma, 0, 4 * (size_t)d, st)) : QAD_OK;
+  if (!ok_ptr(dy) || (dres && !aligned16(dres)) || !ok_rows(r, ldr, d) || !ok_ptr(gamma) || !ok_ptr(rstd) ||
+      !ok_ptr(dx))
+    return QAD_ERR_INVALID_ARG;
+  if (dgamma) {
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return QAD_ERR_INVALID_ARG;
+    if (ws_bytes < qad_rmsnorm_workspace_bytes(T, d)) return QAD_ERR_WORKSPACE;
+  }
+  return to_status(launch_rmsnorm_bwd(dy, dres, r, ldr, gamma, rstd, dx, dgamma, static_cast<float*>(ws), T, d, st));
+}
+
+size_t qad_linear_ce_workspace_bytes(int64_t N, int64_t d, int64_t V, int dh, int dw) {
+  CeLayout L;
+  return ce_layout_of(N, d, V, dh, dw, &L) == QAD_OK ? L.total : 0;
+}
+
+static int linear_ce_call(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* target, const float* g,
+                          float* loss, float* lse, void* dh, void* dw, int accumulate, int64_t N, int64_t d, int64_t V,
+                          void* ws, size_t ws_bytes, qad_stream_t stream) {
+  CeLayout L;
+  const int rc = ce_layout_of(N, d, V, dh != nullptr, dw != nullptr, &L);
+  if (rc != QAD_OK) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return QAD_ERR_INVALID_ARG;
+  if (ws_bytes < L.total) return QAD_ERR_WORKSPACE;
+  if ((dh && !aligned16(dh)) || (dw && !aligned16(dw)) || (g && !aligned16(g))) return QAD_ERR_INVALID_ARG;
+  if (N == 0) {
+    QAD_TRY(cudaMemsetAsync(ws, 0, 256, st));
+    return dw ? to_status(cudaMemsetAsync(dw, 0, 2 * (size_t)(V * d), st)) : QAD_OK;
+  }
+  if (!ok_rows(h, ldh, d) || !ok_rows(w, ldw, d) || !ok_ptr(target) || !ok_ptr(loss) || !ok_ptr(lse))
+    return QAD_ERR_INVALID_ARG;
+  return to_status(linear_ce(L, h, ldh, w, ldw, target, g, loss, lse, dh, dw, accumulate ? 1 : 0, N, d, V,
+                             static_cast<uint8_t*>(ws), st));
+}
+
+int qad_linear_ce_fwd(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* target, float* loss,
+                      float* lse, int64_t N, int64_t d, int64_t V, void* ws, size_t ws_bytes, qad_stream_t stream) {
+  return linear_ce_call(h, ldh, w, ldw, target, nullptr, loss, lse, nullptr, nullptr, 0, N, d, V, ws, ws_bytes, stream);
+}
+
+int qad_linear_ce_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* target, const float* g,
+                          float* loss, float* lse, void* dh, void* dw, int accumulate, int64_t N, int64_t d, int64_t V,
+                          void* ws, size_t ws_bytes, qad_stream_t stream) {
+  if (!dh && !dw) return QAD_ERR_INVALID_ARG;
+  return linear_ce_call(h, ldh, w, ldw, target, g, loss, lse, dh, dw, accumulate, N, d, V, ws, ws_bytes, stream);
+}
+
+static int distill_call(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* idx,
+                        const float* t_logit, const float* mix, float inv_temp, const float* g, float* loss, void* dh,
+                        int accumulate, int64_t N, int64_t d, int64_t V, int64_t K, int32_t* err,
+                        qad_stream_t stream) {
+  if (N < 0 || d <= 0 || V <= 0 || K <= 0 || !(inv_temp > 0.0f && inv_temp < 3.0e38f)) return QAD_ERR_INVALID_ARG;
+  if (d % 16 || d > QAD_DISTILL_MAX_D || K > QAD_DISTILL_MAX_K || N > 0x7fffffff || V > 0x7fffffff)
+    return QAD_ERR_UNSUPPORTED;
+  if (N == 0) return QAD_OK;
+  if (!ok_rows(h, ldh, d) || !ok_rows(w, ldw, d) || !ok_ptr(idx) || !ok_ptr(t_logit) || !ok_ptr(loss))
+    return QAD_ERR_INVALID_ARG;
+  if ((mix && !aligned16(mix)) || (g && !aligned16(g)) || (dh && !aligned16(dh)) ||
+      (reinterpret_cast<uintptr_t>(err) & 3u))
+    return QAD_ERR_INVALID_ARG;
+  return to_status(launch_distill_topk(h, ldh, w, ldw, idx, t_logit, mix, inv_temp, g, loss, dh, accumulate ? 1 : 0, N,
+                                       d, V, K, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qad_distill_topk_fwd(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* idx,
+                         const float* t_logit, const float* mix, float inv_temp, float* loss, int64_t N, int64_t d,
+                         int64_t V, int64_t K, int32_t* err, qad_stream_t stream) {
+  return distill_call(h, ldh, w, ldw, idx, t_logit, mix, inv_temp, nullptr, loss, nullptr, 0, N, d, V, K, err, stream);
+}
+
+int qad_distill_topk_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* idx,
+                             const float* t_logit, const float* mix, float inv_temp, const float* g, float* loss,
+                             void* dh, int accumulate, int64_t N, int64_t d, int64_t V, int64_t K, int32_t* err,
+                             qad_stream_t stream) {
+  if (!dh && N > 0) return QAD_ERR_INVALID_ARG;
+  return distill_call(h, ldh, w, ldw, idx, t_logit, mix, inv_temp, g, loss, dh, accumulate, N, d, V, K, err, stream);
+}
+
 int qad_check_device_error(void* ws, qad_stream_t stream, int32_t* code) {
   if (!ws) return QAD_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -510,7 +621,8 @@ const char* qad_kernel_name(int id) {
                                            "gemm_fc1_swiglu_aq", "gemm_fc2", "combine", "dy_gather",
                                            "gemm_dgrad_fc2_swiglu_bwd", "gemm_dgrad_fc1", "dx_combine",
                                            "gemm_wgrad_fc2_scalegrad", "gemm_wgrad_fc1_scalegrad", "scale_reduce",
-                                           "gemm_fc1_recompute", "deploy_scales"};
+                                           "gemm_fc1_recompute", "deploy_scales", "rmsnorm", "rmsnorm_bwd",
+                                           "ce_logits", "ce_dh", "ce_dw", "distill_topk"};
   return (id >= 0 && id < QAD_K_COUNT) ? names[id] : "unknown";
 }
 

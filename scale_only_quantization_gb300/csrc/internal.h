@@ -125,4 +125,32 @@ cudaError_t gemm_dgrad_fc1(const GemmCtx& c);   // dA1 <- dZ1 . W13_hat
 cudaError_t gemm_wgrad_fc2(const GemmCtx& c, const void* w2, const float* s2, float* ds2, int accumulate);
 cudaError_t gemm_wgrad_fc1(const GemmCtx& c, const void* w13, const float* s13, float* ds13, int accumulate);
 
+// ---- residual RMSNorm (norm.cu); kind: kQNone, kQE4M3 or kQInt8 ----
+int norm_groups(int64_t T);  // partial dgamma rows of the backward's workspace
+cudaError_t launch_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* gamma, float eps,
+                               int kind, void* r, void* y, void* y_hat, void* codes, float* scale, float* rstd,
+                               int64_t T, int64_t d, cudaStream_t st);
+cudaError_t launch_rmsnorm_bwd(const void* dy, const void* dres, const void* r, int64_t ldr, const void* gamma,
+                               const float* rstd, void* dx, float* dgamma, float* part, int64_t T, int64_t d,
+                               cudaStream_t st);
+
+// ---- linear cross entropy (head.cu) ----
+// Byte offsets of its workspace; `piece`: columns of the vocabulary per piece, `parts`: partial
+// sums per row of a sweep
+struct CeLayout {
+  int piece, parts;
+  size_t header, ref, zt, tcol, mul, tval, psum, pmax, u, p, total;
+};
+int ce_layout_of(int64_t N, int64_t d, int64_t V, int grad, int dw, CeLayout* L);
+// loss and lse; dh / dw may be null; header words: [0] device errors, [1] a second sweep is needed
+cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* target,
+                      const float* g, float* loss, float* lse, void* dh, void* dw, int accumulate, int64_t N, int64_t d,
+                      int64_t V, uint8_t* ws, cudaStream_t st);
+
+// ---- distillation from the teacher's top logits (distill.cu); dh may be null ----
+cudaError_t launch_distill_topk(const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* idx,
+                                const float* t, const float* mix, float inv_temp, const float* g, float* loss, void* dh,
+                                int accumulate, int64_t N, int64_t d, int64_t V, int64_t K, int32_t* err,
+                                cudaStream_t st);
+
 }  // namespace qad

@@ -1,0 +1,371 @@
+// Residual addition + root-mean-square norm of token rows, with the activation quantizers of the
+// per-row grids (E4M3, INT8) on its output, and the norm's gradient.
+//
+//   r = bf16(x + res)            the residual stream is stored in bf16, and the norm reads it as stored
+//   rstd = 1 / sqrt(mean(r^2) + eps)
+//   y = bf16(r * rstd * gamma)   the value the router, the layer and its quantizer read
+//   s = fp32(max |y| / Qmax), code = q(y / s), y_hat = bf16(q(y / s) * s)   as the layer's own AQ
+// Backward (straight through the quantizer), n = r * rstd, dn = dy * gamma:
+//   dx = rstd * (dn - n * mean(dn * n)) + dres,   dgamma = sum over rows of dy * n
+// All sums are fp32.  One pass over the data: a row stays in registers between its reductions.
+#include "common.cuh"
+#include "internal.h"
+
+namespace qad {
+namespace {
+
+struct NormFwd {
+  const __nv_bfloat16 *x, *res, *gamma;
+  __nv_bfloat16 *r, *y, *y_hat;
+  uint8_t* codes;
+  float *scale, *rstd;
+  int64_t T, ldx, ldres;
+  int nv, d;  // 16-byte vectors of a row, and its elements
+  float eps;
+};
+
+// Sum (or maximum) over the W warps that share a row; every thread of the group returns it.
+template <int W, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* smem, int warp_in_row, int lane, int bar) {
+  v = MAX ? warp_max(v) : warp_sum(v);
+  if constexpr (W > 1) {
+    if (lane == 0) smem[warp_in_row] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * W) : "memory");
+    v = smem[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v = MAX ? fmaxf(v, smem[i]) : v + smem[i];
+  }
+  return v;
+}
+
+// W warps per row, each lane keeping VPL vectors of it; the block's other warps take other rows.
+template <int VPL, int W, int KIND>
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) rmsnorm_fwd_kernel(const NormFwd p) {
+  constexpr int RB = W > 4 ? 1 : 4 / W;
+  __shared__ float red[RB][2][W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp / W, wr = warp % W, t = wr * 32 + lane;
+  const int64_t row = (int64_t)blockIdx.x * RB + grp;
+  if (row >= p.T) return;  // a whole group leaves: its named barrier is its own
+  const uint4* xr = reinterpret_cast<const uint4*>(p.x + row * p.ldx);
+  uint4 v[VPL];
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = i * 32 * W + t;
+    v[i] = c < p.nv ? __ldcs(xr + c) : make_uint4(0, 0, 0, 0);
+  }
+  if (p.res) {
+    const uint4* rr = reinterpret_cast<const uint4*>(p.res + row * p.ldres);
+    uint4 u[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = i * 32 * W + t;
+      u[i] = c < p.nv ? __ldcs(rr + c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      float a[8], b[8];
+      unpack8(v[i], a);
+      unpack8(u[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] += b[j];
+      v[i] = pack8(a);
+    }
+  }
+  if (p.r) {
+    uint4* ro = reinterpret_cast<uint4*>(p.r + row * p.d);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = i * 32 * W + t;
+      if (c < p.nv) ro[c] = v[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    float a[8];
+    unpack8(v[i], a);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(a[j], a[j], sum);
+  }
+  sum = row_reduce<W, false>(sum, red[grp][0], wr, lane, 1 + grp);
+  float rstd = rsqrtf(sum / (float)p.d + p.eps);
+  if (sum == INFINITY) {  // the squares leave fp32's range (|r| > 1e19 / sqrt(d)): scaled by 2^-64 they do not
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      float a[8];
+      unpack8(v[i], a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(a[j] * 0x1p-64f, a[j] * 0x1p-64f, sum);
+    }
+    if constexpr (W > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(32 * W) : "memory");
+    sum = row_reduce<W, false>(sum, red[grp][0], wr, lane, 1 + grp);
+    rstd = rsqrtf(sum / (float)p.d) * 0x1p-64f;  // eps is below the last place
+  }
+  if (t == 0 && p.rstd) p.rstd[row] = rstd;
+  const uint4* gr = reinterpret_cast<const uint4*>(p.gamma);
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = i * 32 * W + t;
+    float a[8], g[8];
+    unpack8(v[i], a);
+    unpack8(c < p.nv ? __ldg(gr + c) : make_uint4(0, 0, 0, 0), g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = a[j] * rstd * g[j];
+    v[i] = pack8(a);
+    if constexpr (KIND != kQNone) {
+      unpack8(v[i], a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(a[j]));
+    }
+  }
+  if (p.y) {
+    uint4* yo = reinterpret_cast<uint4*>(p.y + row * p.d);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = i * 32 * W + t;
+      if (c < p.nv) yo[c] = v[i];
+    }
+  }
+  if constexpr (KIND != kQNone) {
+    amax = row_reduce<W, true>(amax, red[grp][1], wr, lane, 1 + grp);
+    const float s = __fdiv_rn(amax, KIND == kQE4M3 ? 448.0f : 127.0f);
+    if (t == 0 && p.scale) p.scale[row] = s;
+    if (!p.codes && !p.y_hat) return;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = i * 32 * W + t;
+      if (c >= p.nv) continue;
+      float a[8];
+      uint32_t code[2];
+      unpack8(v[i], a);
+      if constexpr (KIND == kQE4M3) {
+        fakequant_e4m3_codes<8, true>(a, s, code);
+      } else {
+        float x[8];
+        act_quotients<8>(a, s, x);
+        code[0] = code[1] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float q = q_int8(x[j]);
+          code[j / 4] |= ((uint32_t)(int)q & 0xffu) << (8 * (j % 4));
+          a[j] = __fmul_rn(copysignf(q, x[j]), s);
+        }
+      }
+      if (p.codes) reinterpret_cast<uint2*>(p.codes + row * p.d)[c] = make_uint2(code[0], code[1]);
+      if (p.y_hat) reinterpret_cast<uint4*>(p.y_hat + row * p.d)[c] = pack8(a);
+    }
+  }
+}
+
+struct NormBwd {
+  const __nv_bfloat16 *dy, *dres, *r, *gamma;
+  const float* rstd;
+  __nv_bfloat16* dx;
+  float* part;  // [gridDim.x * rows per block, d] partial dgamma, or null
+  int64_t T, ldr;
+  int nv, d;
+};
+
+// Rows are taken in turn by groups of W warps on a fixed grid; each lane keeps the norm-weight
+// gradient of its own columns in registers over all rows of its group, so the sum over rows
+// costs one fp32 row per group, added in a fixed order by rmsnorm_dgamma_kernel.
+template <int VPL, int W>
+__global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(const NormBwd p) {
+  constexpr int RB = 8 / W;
+  __shared__ float red[RB][2][W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp / W, wr = warp % W, t = wr * 32 + lane;
+  const int64_t step = (int64_t)gridDim.x * RB;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 gm[VPL];
+  float dg[VPL][8];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = i * 32 * W + t;
+    gm[i] = c < p.nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma) + c) : zero;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
+  }
+  int flip = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RB + grp; row < p.T; row += step) {
+    const uint4* rr = reinterpret_cast<const uint4*>(p.r + row * p.ldr);
+    const uint4* dyr = reinterpret_cast<const uint4*>(p.dy + row * p.d);
+    uint4 n[VPL], g[VPL], e[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = i * 32 * W + t;
+      n[i] = c < p.nv ? __ldcs(rr + c) : zero;
+      g[i] = c < p.nv ? __ldcs(dyr + c) : zero;
+    }
+    if (p.dres) {
+      const uint4* er = reinterpret_cast<const uint4*>(p.dres + row * p.d);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int c = i * 32 * W + t;
+        e[i] = c < p.nv ? __ldcs(er + c) : zero;
+      }
+    }
+    const float rstd = __ldg(p.rstd + row);
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      float a[8], b[8], w[8];
+      unpack8(n[i], a);
+      unpack8(g[i], b);
+      unpack8(gm[i], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float nn = a[j] * rstd;
+        dg[i][j] = fmaf(b[j], nn, dg[i][j]);
+        dot = fmaf(b[j] * w[j], nn, dot);
+      }
+    }
+    dot = row_reduce<W, false>(dot, red[grp][flip], wr, lane, 1 + grp);
+    flip ^= 1;  // the next row's partial sums must not overwrite what a slower warp still reads
+    const float m = dot / (float)p.d;
+    uint4* out = reinterpret_cast<uint4*>(p.dx + row * p.d);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = i * 32 * W + t;
+      float a[8], b[8], w[8], o[8];
+      unpack8(n[i], a);
+      unpack8(g[i], b);
+      unpack8(gm[i], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = rstd * (b[j] * w[j] - a[j] * rstd * m);
+      if (p.dres) {
+        unpack8(e[i], a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] += a[j];
+      }
+      if (c < p.nv) out[c] = pack8(o);
+    }
+  }
+  if (p.part) {
+    float* pr = p.part + ((int64_t)blockIdx.x * RB + grp) * p.d;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = i * 32 * W + t;
+      if (c < p.nv) {
+        reinterpret_cast<float4*>(pr)[2 * c] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+        reinterpret_cast<float4*>(pr)[2 * c + 1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+      }
+    }
+  }
+}
+
+// dgamma[c] = sum over the partial rows, in a fixed order: 32 columns per block, each of 32 warps
+// adding every 32nd row.
+__global__ void __launch_bounds__(1024) rmsnorm_dgamma_kernel(const float* __restrict__ part, int parts, int d,
+                                                              float* __restrict__ dgamma) {
+  __shared__ float s[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.0f;
+  if (c < d)
+    for (int i = warp; i < parts; i += 32) v += part[(int64_t)i * d + c];
+  s[warp][lane] = v;
+  __syncthreads();
+  v = warp_sum(s[lane][warp]);
+  const int cw = blockIdx.x * 32 + warp;
+  if (lane == 0 && cw < d) dgamma[cw] = v;
+}
+
+template <int VPL, int W>
+cudaError_t fwd_kind(const NormFwd& p, int kind, cudaStream_t st) {
+  constexpr int RB = W > 4 ? 1 : 4 / W;
+  const int64_t blocks = (p.T + RB - 1) / RB;
+  const int threads = W > 4 ? 32 * W : 128;
+  if (kind == kQE4M3) rmsnorm_fwd_kernel<VPL, W, kQE4M3><<<(unsigned)blocks, threads, 0, st>>>(p);
+  else if (kind == kQInt8) rmsnorm_fwd_kernel<VPL, W, kQInt8><<<(unsigned)blocks, threads, 0, st>>>(p);
+  else rmsnorm_fwd_kernel<VPL, W, kQNone><<<(unsigned)blocks, threads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int VPL, int W>
+cudaError_t bwd_launch(const NormBwd& p, int groups, cudaStream_t st) {
+  constexpr int RB = 8 / W;
+  rmsnorm_bwd_kernel<VPL, W><<<(unsigned)((groups + RB - 1) / RB), 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Partial dgamma rows: a constant so that the workspace size needs no device query; 8 row groups
+// for each of 152 SMs.
+constexpr int kNormGroups = 1216;
+
+int norm_groups(int64_t T) { return (int)(T < kNormGroups ? (T + 7) / 8 * 8 : kNormGroups); }
+
+cudaError_t launch_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* gamma, float eps,
+                               int kind, void* r, void* y, void* y_hat, void* codes, float* scale, float* rstd,
+                               int64_t T, int64_t d, cudaStream_t st) {
+  NormFwd p = {};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.res = static_cast<const __nv_bfloat16*>(res);
+  p.gamma = static_cast<const __nv_bfloat16*>(gamma);
+  p.r = static_cast<__nv_bfloat16*>(r);
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.y_hat = static_cast<__nv_bfloat16*>(y_hat);
+  p.codes = static_cast<uint8_t*>(codes);
+  p.scale = scale;
+  p.rstd = rstd;
+  p.T = T;
+  p.ldx = ldx;
+  p.ldres = ldres;
+  p.nv = (int)(d / 8);
+  p.d = (int)d;
+  p.eps = eps;
+  prof_begin(QAD_K_RMSNORM, st);
+  const int lanes1 = (p.nv + 31) / 32;  // vectors per lane with one warp per row
+  cudaError_t e;
+  if (lanes1 <= 1) e = fwd_kind<1, 1>(p, kind, st);
+  else if (lanes1 <= 2) e = fwd_kind<2, 1>(p, kind, st);
+  else if (lanes1 <= 4) e = fwd_kind<4, 1>(p, kind, st);
+  else if (lanes1 <= 8) e = fwd_kind<2, 4>(p, kind, st);
+  else if (lanes1 <= 12) e = fwd_kind<3, 4>(p, kind, st);
+  else if (lanes1 <= 16) e = fwd_kind<4, 4>(p, kind, st);
+  else if (lanes1 <= 32) e = fwd_kind<8, 4>(p, kind, st);
+  else e = fwd_kind<8, 8>(p, kind, st);
+  prof_end(QAD_K_RMSNORM, st);
+  return e;
+}
+
+cudaError_t launch_rmsnorm_bwd(const void* dy, const void* dres, const void* r, int64_t ldr, const void* gamma,
+                               const float* rstd, void* dx, float* dgamma, float* part, int64_t T, int64_t d,
+                               cudaStream_t st) {
+  NormBwd p = {};
+  p.dy = static_cast<const __nv_bfloat16*>(dy);
+  p.dres = static_cast<const __nv_bfloat16*>(dres);
+  p.r = static_cast<const __nv_bfloat16*>(r);
+  p.gamma = static_cast<const __nv_bfloat16*>(gamma);
+  p.rstd = rstd;
+  p.dx = static_cast<__nv_bfloat16*>(dx);
+  p.part = dgamma ? part : nullptr;
+  p.T = T;
+  p.ldr = ldr;
+  p.nv = (int)(d / 8);
+  p.d = (int)d;
+  const int groups = norm_groups(T);
+  const int lanes1 = (p.nv + 31) / 32;
+  prof_begin(QAD_K_RMSNORM_BWD, st);
+  cudaError_t e;
+  if (lanes1 <= 1) e = bwd_launch<1, 1>(p, groups, st);
+  else if (lanes1 <= 2) e = bwd_launch<2, 1>(p, groups, st);
+  else if (lanes1 <= 4) e = bwd_launch<2, 2>(p, groups, st);
+  else if (lanes1 <= 8) e = bwd_launch<2, 4>(p, groups, st);
+  else if (lanes1 <= 12) e = bwd_launch<3, 4>(p, groups, st);
+  else if (lanes1 <= 16) e = bwd_launch<2, 8>(p, groups, st);
+  else if (lanes1 <= 32) e = bwd_launch<4, 8>(p, groups, st);
+  else e = bwd_launch<8, 8>(p, groups, st);
+  prof_end(QAD_K_RMSNORM_BWD, st);
+  if (e != cudaSuccess || !dgamma) return e;
+  note_launches(1);
+  rmsnorm_dgamma_kernel<<<(unsigned)((d + 31) / 32), 1024, 0, st>>>(part, groups, (int)d, dgamma);
+  return cudaGetLastError();
+}
+
+}  // namespace qad
