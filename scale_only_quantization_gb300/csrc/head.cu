@@ -217,6 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
   const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* late = reinterpret_cast<int32_t*>(tmem_slot + 2);  // error word of the waits that drain
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -232,6 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
+    *late = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -292,11 +294,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
       }
     }
     if (*abort_flag) {  // let every load land before the CTA releases its shared memory
-      int32_t dummy = 0;
       for (int s = 0; s < STAGES; ++s)
         if (armed & (1u << s)) {
           volatile int zero = 0;
-          if (leader) mbar_wait(full_bar(s), (armed_parity >> s) & 1u, &zero, &dummy);
+          if (leader) mbar_wait(full_bar(s), (armed_parity >> s) & 1u, &zero, late);
         }
     }
   } else if (warp == 1 && lane == 0 && leader) {
@@ -336,8 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     }
     mma_commit(drain_bar, 1);
     volatile int zero = 0;
-    int32_t dummy = 0;
-    mbar_wait(drain_bar, 0, &zero, &dummy);
+    mbar_wait(drain_bar, 0, &zero, late);
   } else if (warp >= 2) {
     // ------------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, half = (warp - 2) >> 2;
