@@ -479,7 +479,7 @@ cudaError_t launch_one(const Distill& p, int64_t N, cudaStream_t st) {
 // so that the loss has the same bits: warp i's vectors are i * 32 + lane + 32 CW j.
 template <int CW, int V>
 __global__ void __launch_bounds__(kFwdThreads, 8) distill_fwd_kernel(const Distill p) {
-  extern __shared__ __align__(16) uint8_t sm[];
+  extern __shared__ __align__(128) uint8_t sm[];
   const int nv = p.d / 8, K = p.K;
   uint4* hs = reinterpret_cast<uint4*>(sm);
   float* z = reinterpret_cast<float*>(hs + nv);

@@ -18,6 +18,8 @@
 // The products run on SM pairs (tcgen05 cta_group::2, 256 x 256 tiles) with the roles and
 // barriers of the grouped GEMMs: warp 0 of each CTA loads, warp 1 of the leader issues the MMAs,
 // warps 2-9 run the epilogue of one accumulator while the other is filled.
+#include <utility>
+
 #include "internal.h"
 #include "tcgen05.cuh"
 
@@ -27,15 +29,22 @@ namespace {
 constexpr int kTile = 256;            // rows and columns of a pair tile
 constexpr int kThreadsH = 320;
 constexpr int kEpiWarps = 8;
-constexpr float kMaxAbove = 60.0f;    // exp(60) summed over 2^31 columns stays below fp32's range
+constexpr float kMaxAbove = 60.0f;    // exp(60) summed over 2^30 columns stays below fp32's range
 
-enum { M_LOGITS = 0, M_U = 1, M_DW = 2 };
+// M_LOGITS: e [rows, piece];  M_U: U += e W;  M_DW: dW = e^T h.  With kFewRows token rows or fewer the
+// products are taken transposed (M_*_T: the vocabulary, or the columns of U, as the 256 rows of a
+// tile and the tokens as its 128 columns), so that the tensor cores do not multiply empty rows and
+// the head streams at the memory's rate.
+enum { M_LOGITS = 0, M_U = 1, M_DW = 2, M_LOGITS_T = 3, M_U_T = 4, M_DW_T = 5 };
+constexpr int kFewRows = 128;
+constexpr int kMaxPairs = 76;  // SM pairs of the grid at most: bounds the partial sums of a split contraction
 
 struct HeadParams {
   const int32_t* gate;  // null, or a word: 0 = nothing to do
   int32_t* err;
   int mt, nt, num_kb;   // tiles along the output's rows and columns, K blocks
   int n_fast;           // tile order: columns fastest
+  int split;            // the pairs share out all K blocks evenly, tiles cut where a share ends (U)
   int a_row0, b_row0;   // first row of the A / B tensors of this piece
   int64_t N;            // token rows
   // logits: columns c0 .. c0 + cols of the vocabulary
@@ -43,22 +52,32 @@ struct HeadParams {
   const float *ref, *mul;       // per row: reference, factor (null: 1)
   const float* tval;            // per row: what the target's column holds (null: 0)
   const int32_t* target;        // per row: the target's column
-  float *psum, *pmax;           // [column halves of tiles, N] sums without the target / maxima, or null
+  float *psum, *pmax;           // partial sums without the target / maxima, or null
+  int part0;                    // first part of this piece
   int store_p;
-  // U
-  float* u;
+  __nv_bfloat16* p;             // transposed logits: e [piece, kFewRows]
+  // U [N, d]: a tile's first segment; its others in `rest`, a tile of 256 x TN per pair (only the first tile of a
+  // pair's share can have begun in another's)
+  float *u, *rest;
   int d, add;
 };
 
+// The kernels of a call are launched as dependents of one another: each is set up while the one before it
+// ends, and touches memory only after this wait, which the whole grid before it has completed by.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 template <int MODE> struct HCfg {
-  static constexpr bool A_MN = MODE == M_DW, B_MN = MODE != M_LOGITS;
+  static constexpr bool A_MN = MODE == M_DW || MODE == M_U_T, B_MN = MODE != M_LOGITS && MODE != M_LOGITS_T;
+  static constexpr int TN = MODE == M_LOGITS_T || MODE == M_U_T ? kFewRows : kTile;  // columns of a tile
   static constexpr int ATOMS = MODE == M_U ? 1 : 2;
   static constexpr int BKE = ATOMS * BK;
-  static constexpr int A_ATOM = BM * 128, B_ATOM = BM * 128;
+  static constexpr int A_ATOM = BM * 128, B_ATOM = TN / 2 * 128;
   static constexpr int A_BYTES = ATOMS * A_ATOM, B_BYTES = ATOMS * B_ATOM;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = (192 * 1024) / STAGE;
-  static constexpr int STAGING = MODE == M_U ? 0 : kEpiWarps * 4096;
+  static constexpr bool BOXES = MODE == M_LOGITS || MODE == M_DW || MODE == M_DW_T;  // stores through TMA
+  static constexpr int STAGING = BOXES ? kEpiWarps * 4096 : MODE == M_LOGITS_T ? 4 * kFewRows * 4 : 0;
   static constexpr int SMEM = STAGES * STAGE + 512 + 1024 + STAGING;
 };
 
@@ -76,6 +95,58 @@ __device__ __forceinline__ HTile htile(const HeadParams& p, int t) {
   }
   return x;
 }
+
+// A split contraction.  As many whole rounds of tiles as there are, one tile per pair at a time and all
+// at the same K block (they share their operands in L2); the K blocks of the `rest` tiles that do not
+// fill a round are shared out evenly over the pairs (over as many as there are blocks): pair i takes
+// [i * all / pairs, (i + 1) * all / pairs) of all = rest * num_kb.  The segments of such a tile are numbered from the first pair that touches
+// it.  (Shared out evenly from the start, the pairs run at different K blocks and re-read the operands
+// from HBM: 6.75 against 6.43 ms for the 8192 x 2048 x 151936 step unsplit.)
+__host__ __device__ inline int64_t split_pairs(int64_t num_kb, int64_t rest, int64_t pairs) {
+  return rest * num_kb < pairs ? rest * num_kb : pairs;
+}
+__host__ __device__ inline int64_t split_first(int64_t rest_tile, int64_t num_kb, int64_t rest, int64_t pairs) {
+  return ((rest_tile * num_kb + 1) * pairs - 1) / (rest * num_kb);  // the largest pair whose share starts at or before it
+}
+__host__ __device__ inline int64_t split_last(int64_t rest_tile, int64_t num_kb, int64_t rest, int64_t pairs) {
+  return ((rest_tile + 1) * num_kb * pairs - 1) / (rest * num_kb);
+}
+
+// The tiles, or parts of tiles, of one pair: every role of the CTA walks the same sequence.
+struct Walk {
+  int tile, kb0, kb1, seg;
+  int next_tile, whole, pairs, pair, sharers;  // whole: tiles that are not split; sharers: pairs that share the others
+  int64_t at, end;                    // this pair's share of the rest, in K blocks
+  __device__ __forceinline__ Walk(const HeadParams& p, int pair_, int pairs_) : pairs(pairs_), pair(pair_) {
+    const int tiles = p.mt * p.nt, rest = p.split ? tiles % pairs : 0;
+    whole = tiles - rest;
+    next_tile = pair;
+    sharers = (int)split_pairs(p.num_kb, rest, pairs);
+    at = end = 0;
+    if (pair < sharers) {
+      at = (int64_t)pair * rest * p.num_kb / sharers;
+      end = (int64_t)(pair + 1) * rest * p.num_kb / sharers;
+    }
+  }
+  __device__ __forceinline__ bool next(const HeadParams& p) {
+    if (next_tile < whole) {
+      tile = next_tile;
+      kb0 = 0;
+      kb1 = p.num_kb;
+      seg = 0;
+      next_tile += pairs;
+      return true;
+    }
+    if (at >= end) return false;
+    const int rt = (int)(at / p.num_kb);
+    tile = whole + rt;
+    kb0 = (int)(at - (int64_t)rt * p.num_kb);
+    kb1 = end - at < p.num_kb - kb0 ? kb0 + (int)(end - at) : p.num_kb;
+    seg = pair - (int)split_first(rt, p.num_kb, p.mt * p.nt - whole, sharers);
+    at += kb1 - kb0;
+    return true;
+  }
+};
 
 // A 32 x 32 bf16 box of this warp through its staging memory (64-byte swizzle: 16-byte chunk c of
 // row r at c ^ ((r >> 1) & 3)) and out by TMA; two boxes in turn.
@@ -111,52 +182,168 @@ __device__ __forceinline__ void epi_logits(const HeadParams& p, const CUtensorMa
   const int target = live ? __ldg(p.target + row) - p.c0 - col0 : -1;  // within these 128 columns
   const bool edge = col0 + 128 > p.cols;
   float sum = 0.0f, top = -INFINITY;
+  uint32_t r[32], next[32];
+  tmem_ld32_issue(tbase + half * 128, r);
+  tmem_wait32(r);
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
-    uint32_t r[32];
-    tmem_ld32_issue(tbase + half * 128 + 32 * c, r);
-    tmem_wait32(r);
-    const int tc = target - 32 * c;
-    const int valid = p.cols - (col0 + 32 * c);
+    if (c < 3) tmem_ld32_issue(tbase + half * 128 + 32 * (c + 1), next);
+    const int tc = target - 32 * c, valid = p.cols - (col0 + 32 * c);
+    // the chunks that hold no row's target, and lie inside the vocabulary, need no comparison per element
+    const bool special = edge || __any_sync(0xffffffffu, (unsigned)tc < 32u);
     uint4 out[4];
     uint32_t* o = reinterpret_cast<uint32_t*>(out);
+    if (special) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      float e[2];
+      for (int i = 0; i < 32; i += 2) {
+        float e[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float z = __uint_as_float(r[i + j]);
-        float x = __expf(z - ref);
-        const bool out_of = edge && i + j >= valid;
-        if (!out_of) top = fmaxf(top, z);
-        if (out_of || i + j == tc) x = 0.0f;
-        sum += x;
-        x *= mul;
-        if (i + j == tc) x = tv;
-        e[j] = x;
+        for (int j = 0; j < 2; ++j) {
+          const float z = __uint_as_float(r[i + j]);
+          float x = __expf(z - ref);
+          const bool out_of = edge && i + j >= valid;
+          if (!out_of) top = fmaxf(top, z);
+          if (out_of || i + j == tc) x = 0.0f;
+          sum += x;
+          x *= mul;
+          if (i + j == tc) x = tv;
+          e[j] = x;
+        }
+        o[i / 2] = pack_bf16(e[0], e[1]);
       }
-      o[i / 2] = pack_bf16(e[0], e[1]);
+    } else if (p.psum) {  // the sweep: no factor
+      const uint64_t nr2 = f2pack(-ref, -ref);
+      uint64_t sum2 = f2pack(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float a = __uint_as_float(r[i]), b = __uint_as_float(r[i + 1]);
+        const float2 x = f2unpack(f2add(f2pack(a, b), nr2));
+        const float e0 = __expf(x.x), e1 = __expf(x.y);
+        top = fmaxf(top, fmaxf(a, b));
+        sum2 = f2add(sum2, f2pack(e0, e1));
+        o[i / 2] = pack_bf16(e0, e1);
+      }
+      const float2 s2 = f2unpack(sum2);
+      sum += s2.x + s2.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+        o[i / 2] = pack_bf16(__expf(__uint_as_float(r[i]) - ref) * mul, __expf(__uint_as_float(r[i + 1]) - ref) * mul);
     }
     if (p.store_p && y < p.N) store_box32(tm, stage_base, buf, lane, out, col0 + 32 * c, y);
+    if (c < 3) {
+      tmem_wait32(next);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = next[i];
+    }
   }
   if (p.psum && live) {
-    const int64_t at = (int64_t)((p.c0 / kTile + ti.nb) * 2 + half) * p.N + row;
+    const int64_t at = (int64_t)(p.part0 + 2 * ti.nb + half) * p.N + row;
     p.psum[at] = sum;
     p.pmax[at] = top;
   }
 }
 
-// Row r's 128 columns of U += e W, fp32 in global memory
-__device__ __forceinline__ void epi_u(const HeadParams& p, const HTile& ti, int rank, uint32_t tbase, int q, int lane,
-                                      int half) {
-  const int64_t row = ti.mb * kTile + rank * BM + 32 * q + lane;
+// Vocabulary row v's e for 64 of the tokens (32 at a time); sums[c], tops[c]: this lane's token of chunk c, over
+// all rows that this warp has seen
+__device__ __forceinline__ void epi_logits_t(const HeadParams& p, const float* tok, const HTile& ti, int rank,
+                                             uint32_t tbase, int q, int lane, int half, float (&sums)[2],
+                                             float (&tops)[2]) {
+  const int vr = ti.mb * kTile + rank * BM + 32 * q + lane;  // within the piece
+  const bool live = vr < p.cols;
+  const int v = p.c0 + vr;
+  const float4* ref = reinterpret_cast<const float4*>(tok);
+  const float4* mul = ref + kFewRows / 4;
+  const float4* tv = mul + kFewRows / 4;
+  const int4* tgt = reinterpret_cast<const int4*>(tv + kFewRows / 4);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int n0 = 64 * half + 32 * c;
+    if (n0 >= p.N && !p.store_p) continue;  // tokens that are not there; their e (K of the next product) must be 0
+    uint32_t r[32];
+    tmem_ld32_issue(tbase + n0, r);
+    tmem_wait32(r);
+    float x[32];
+    uint4 out[4];
+    uint32_t* o = reinterpret_cast<uint32_t*>(out);
+#pragma unroll
+    for (int i4 = 0; i4 < 8; ++i4) {
+      const float4 rf = ref[n0 / 4 + i4], mf = mul[n0 / 4 + i4], tf = tv[n0 / 4 + i4];
+      const int4 tg = tgt[n0 / 4 + i4];
+      const float rr[4] = {rf.x, rf.y, rf.z, rf.w}, mm[4] = {mf.x, mf.y, mf.z, mf.w}, tt[4] = {tf.x, tf.y, tf.z, tf.w};
+      const int gg[4] = {tg.x, tg.y, tg.z, tg.w};
+      float y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = __expf(__uint_as_float(r[4 * i4 + i]) - rr[i]);
+        const bool none = !live || n0 + 4 * i4 + i >= p.N;
+        x[4 * i4 + i] = none || gg[i] == v ? 0.0f : e;
+        y[i] = none ? 0.0f : gg[i] == v ? tt[i] : e * mm[i];
+      }
+      o[2 * i4] = pack_bf16(y[0], y[1]);
+      o[2 * i4 + 1] = pack_bf16(y[2], y[3]);
+    }
+    if (p.store_p) {
+      uint4* to = reinterpret_cast<uint4*>(p.p + (int64_t)vr * kFewRows + n0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to[i] = out[i];
+    }
+    if (p.psum) {
+      float z[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = live ? __uint_as_float(r[i]) : -INFINITY;
+      // over the warp's 32 rows: each step halves the tokens a lane carries, until it has its own
+#pragma unroll
+      for (int off = 16; off; off /= 2) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+          x[i] = (up ? x[i + off] : x[i]) + __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + off], off);
+          z[i] = fmaxf(up ? z[i + off] : z[i], __shfl_xor_sync(0xffffffffu, up ? z[i] : z[i + off], off));
+        }
+      }
+      sums[c] += x[0];
+      tops[c] = fmaxf(tops[c], z[0]);
+    }
+  }
+}
+
+// Row dd (a column of U) of 64 tokens: U^T += W^T e, this segment's partial sums, fp32
+__device__ __forceinline__ void epi_u_t(const HeadParams& p, const HTile& ti, int seg, int pair, int rank,
+                                        uint32_t tbase, int q, int lane, int half) {
+  const int dt = rank * BM + 32 * q + lane, dd = ti.mb * kTile + dt;
+  float* u = seg == 0 ? p.u + dd : p.rest + (int64_t)pair * kTile * kFewRows + dt;
+  const int64_t pitch = seg == 0 ? p.d : kTile;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int n0 = 64 * half + 32 * c;
+    if (n0 >= p.N) continue;
+    uint32_t r[32];
+    tmem_ld32_issue(tbase + n0, r);
+    tmem_wait32(r);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (n0 + i >= p.N || dd >= p.d) continue;
+      float* at = u + (n0 + i) * pitch;
+      *at = __uint_as_float(r[i]) + (p.add ? *at : 0.0f);
+    }
+    __syncwarp();  // the next tensor-memory load is the whole warp's
+  }
+}
+
+// Row r's 128 columns of U += e W, this segment's partial sums, fp32 in global memory
+__device__ __forceinline__ void epi_u(const HeadParams& p, const HTile& ti, int seg, int pair, int rank, uint32_t tbase,
+                                      int q, int lane, int half) {
+  const int rt = rank * BM + 32 * q + lane;
+  const int64_t row = (int64_t)ti.mb * kTile + rt;
   const int col0 = ti.nb * kTile + half * 128;
+  float* to = seg == 0 ? p.u + row * p.d + col0 : p.rest + ((int64_t)pair * kTile + rt) * kTile + half * 128;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32];
     tmem_ld32_issue(tbase + half * 128 + 32 * c, r);
     tmem_wait32(r);
-    float4* u = reinterpret_cast<float4*>(p.u + row * p.d + col0 + 32 * c);
+    float4* u = reinterpret_cast<float4*>(to + 32 * c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (row >= p.N || col0 + 32 * c + 4 * i >= p.d) continue;
@@ -201,8 +388,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const HeadParams p) {
   using C = HCfg<MODE>;
-  constexpr int STAGES = C::STAGES, BKE = C::BKE, ATOMS = C::ATOMS;
-  constexpr uint32_t IDESC = instr_desc<kTile, C::A_MN, C::B_MN>();
+  constexpr int STAGES = C::STAGES, BKE = C::BKE, ATOMS = C::ATOMS, TN = C::TN;
+  constexpr uint32_t IDESC = instr_desc<TN, C::A_MN, C::B_MN>();
+  let_next_start();
+  wait_for_previous();
   if (p.gate && *p.gate == 0) return;  // the whole grid alike
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -237,9 +426,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  float* tok = reinterpret_cast<float*>(smem_raw + (stage_out - smem_u32(smem_raw)));  // M_LOGITS_T: per token values
+  if constexpr (MODE == M_LOGITS_T) {
+    for (int i = threadIdx.x; i < kFewRows; i += kThreadsH) {
+      const bool live = i < p.N;
+      tok[i] = live ? p.ref[i] : 0.0f;
+      tok[kFewRows + i] = live && p.mul ? p.mul[i] : 1.0f;
+      tok[2 * kFewRows + i] = live && p.tval ? p.tval[i] : 0.0f;
+      reinterpret_cast<int32_t*>(tok)[3 * kFewRows + i] = live ? p.target[i] : -1;
+    }
+  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(2u * kTile)
+                 "r"(2u * TN)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
@@ -248,8 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = p.mt * p.nt;
-  const int first = (int)cluster_id(), step = (int)cluster_count();
+  const int pair = (int)cluster_id(), pairs = (int)cluster_count();
+  Walk wk(p, pair, pairs);
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------------ TMA producer (both CTAs)
@@ -258,10 +457,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     bool ok = true;
-    const int half = (int)rank * BM;
-    for (int t = first; ok && t < total; t += step) {
-      const HTile ti = htile(p, t);
-      for (int kb = 0; kb < p.num_kb; ++kb) {
+    const int half = (int)rank * BM, half_n = (int)rank * (TN / 2);
+    while (ok && wk.next(p)) {
+      const HTile ti = htile(p, wk.tile);
+      for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
         if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
           ok = false;
           break;
@@ -279,11 +478,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
             tma_load_2d(sa + i * C::A_ATOM, &tmA, kb * BKE + i * BK, p.a_row0 + ti.mb * kTile + half, fb);
         }
 #pragma unroll
-        for (int i = 0; i < (C::B_MN ? 2 : ATOMS); ++i) {
+        for (int i = 0; i < (C::B_MN ? TN / 128 : ATOMS); ++i) {
           if constexpr (C::B_MN)
-            tma_load_2d(sb + i * BKE * 128, &tmB, ti.nb * kTile + half + i * 64, p.b_row0 + kb * BKE, fb);
+            tma_load_2d(sb + i * BKE * 128, &tmB, ti.nb * TN + half_n + i * 64, p.b_row0 + kb * BKE, fb);
           else
-            tma_load_2d(sb + i * C::B_ATOM, &tmB, kb * BKE + i * BK, p.b_row0 + ti.nb * kTile + half, fb);
+            tma_load_2d(sb + i * C::B_ATOM, &tmB, kb * BKE + i * BK, p.b_row0 + ti.nb * TN + half_n, fb);
         }
         armed |= 1u << stage;
         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -305,11 +504,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
-    for (int t = first; ok && t < total; t += step) {
+    while (ok && wk.next(p)) {
       if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.err)) break;
       tc_fence_after();
-      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTile);
-      for (int kb = 0; kb < p.num_kb; ++kb) {
+      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * TN);
+      for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
         if (!mbar_wait(full_bar(stage), phase, abort_flag, p.err)) {
           ok = false;
           break;
@@ -322,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
                                       : smem_desc(sa + (k / 4) * C::A_ATOM + (k % 4) * 32, 16, 1024);
           const uint64_t bd = C::B_MN ? smem_desc(sb + k * 2048, BKE * 128, 1024)
                                       : smem_desc(sb + (k / 4) * C::B_ATOM + (k % 4) * 32, 16, 1024);
-          mma_issue<false>(d_tmem, ad, bd, IDESC, (kb | k) != 0 ? 1u : 0u);
+          mma_issue<false>(d_tmem, ad, bd, IDESC, kb != wk.kb0 || k != 0 ? 1u : 0u);
         }
         mma_commit(empty_bar(stage), 3);
         if (++stage == STAGES) {
@@ -344,15 +543,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     const uint32_t my_stage = stage_out + (uint32_t)(warp - 2) * 4096u;
     int acc = 0;
     uint32_t acc_phase = 0, buf = 0;
-    if constexpr (MODE != M_U) tma_prefetch_desc(&tmC);
-    for (int t = first; t < total; t += step) {
-      const HTile ti = htile(p, t);
+    float sums[2] = {0.0f, 0.0f}, tops[2] = {-INFINITY, -INFINITY};
+    if constexpr (C::BOXES) tma_prefetch_desc(&tmC);
+    while (wk.next(p)) {
+      const HTile ti = htile(p, wk.tile);
       const bool got = mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.err);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
-      const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile);
+      const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * TN);
       if constexpr (MODE == M_LOGITS) epi_logits(p, &tmC, ti, (int)rank, tbase, q, lane, half, my_stage, buf);
-      else if constexpr (MODE == M_U) epi_u(p, ti, (int)rank, tbase, q, lane, half);
+      else if constexpr (MODE == M_U) epi_u(p, ti, wk.seg, pair, (int)rank, tbase, q, lane, half);
+      else if constexpr (MODE == M_LOGITS_T) epi_logits_t(p, tok, ti, (int)rank, tbase, q, lane, half, sums, tops);
+      else if constexpr (MODE == M_U_T) epi_u_t(p, ti, wk.seg, pair, (int)rank, tbase, q, lane, half);
       else epi_dw(p, &tmC, ti, (int)rank, tbase, q, lane, half, my_stage, buf);
       tc_fence_before();
       __syncwarp();
@@ -360,8 +562,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
-    if constexpr (MODE != M_U) {
+    if constexpr (C::BOXES) {
       if (lane == 0) bulk_wait_all();
+    }
+    if constexpr (MODE == M_LOGITS_T) {  // one part per CTA and lane quadrant
+      if (p.psum)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int n = 64 * half + 32 * c + lane;
+          const int64_t at = (int64_t)(p.part0 + (pair * 2 + (int)rank) * 4 + q) * kFewRows + n;
+          p.psum[at] = sums[c];
+          p.pmax[at] = tops[c];
+        }
     }
   }
 
@@ -370,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2u * kTile) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2u * TN) : "memory");
   }
 }
 
@@ -381,8 +593,10 @@ __global__ void __launch_bounds__(128) ce_ref_kernel(const __nv_bfloat16* __rest
                                                      const int32_t* __restrict__ target, int64_t N, int d, int64_t V,
                                                      float* __restrict__ ref, float* __restrict__ zt,
                                                      int32_t* __restrict__ tcol, int32_t* hdr) {
+  let_next_start();
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x < 64) hdr[threadIdx.x] = 0;  // nothing of this call has written it yet
   if (row >= N) return;
   const int32_t t = __ldg(target + row);
   const bool bad = t >= V;
@@ -401,49 +615,51 @@ __global__ void __launch_bounds__(128) ce_ref_kernel(const __nv_bfloat16* __rest
   if (lane == 0) {
     ref[row] = zt[row] = acc;
     tcol[row] = (int32_t)v;
-    if (bad) atomicOr(hdr, QAD_DEV_BAD_INDEX);
   }
 }
 
-// Per row, from the sweep's partial sums: the loss, lse and the factors of the gradients.  A row
-// whose largest logit lies over kMaxAbove above its reference asks for the second sweep (again = 0).
-// One block per 32 rows, its 8 warps taking the parts in turn.
-__global__ void __launch_bounds__(256) ce_stats_kernel(const int32_t* gate, const float* __restrict__ psum,
-                                                       const float* __restrict__ pmax, int parts, int64_t N,
-                                                       const int32_t* __restrict__ target, int64_t V,
-                                                       const float* __restrict__ g, const float* __restrict__ zt,
-                                                       float* __restrict__ ref, float* __restrict__ mul,
-                                                       float* __restrict__ tval, float* __restrict__ loss,
-                                                       float* __restrict__ lse, int again, int32_t* request) {
+// Per row, from the sweep's partial sums [parts, np]: the loss, lse and the factors of the gradients.
+// A row whose largest logit lies over kMaxAbove above its reference asks for the second sweep (again =
+// 0).  One block per 32 rows, its 32 warps taking the parts in turn.
+__global__ void __launch_bounds__(1024) ce_stats_kernel(const int32_t* gate, const float* __restrict__ psum,
+                                                        const float* __restrict__ pmax, int parts, int np, int64_t N,
+                                                        const int32_t* __restrict__ target, int64_t V,
+                                                        const float* __restrict__ g, const float* __restrict__ zt,
+                                                        float* __restrict__ ref, float* __restrict__ mul,
+                                                        float* __restrict__ tval, float* __restrict__ loss,
+                                                        float* __restrict__ lse, int again, int32_t* hdr) {
+  let_next_start();
+  wait_for_previous();
   if (gate && *gate == 0) return;
-  __shared__ float ss[8][32], sm[8][32];
+  __shared__ float ss[32][33], sm[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t first = (int64_t)blockIdx.x * 32;
   float s = 0.0f, m = -INFINITY;
-  if (row < N)
-    for (int i = warp; i < parts; i += 8) {
-      s += psum[(int64_t)i * N + row];
-      m = fmaxf(m, pmax[(int64_t)i * N + row]);
+  if (first + lane < N)
+#pragma unroll 4
+    for (int i = warp; i < parts; i += 32) {
+      s += psum[(int64_t)i * np + first + lane];
+      m = fmaxf(m, pmax[(int64_t)i * np + first + lane]);
     }
   ss[warp][lane] = s;
   sm[warp][lane] = m;
   __syncthreads();
-  if (warp || row >= N) return;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    s += ss[i][lane];
-    m = fmaxf(m, sm[i][lane]);
-  }
+  const int64_t row = first + warp;  // from here a warp per row
+  if (row >= N) return;
+  s = warp_sum(ss[lane][warp]);
+  m = warp_max(sm[lane][warp]);
+  if (lane) return;
+  const int32_t t = target[row];
+  if (!again && t >= V) atomicOr(hdr, QAD_DEV_BAD_INDEX);
   const float r = ref[row], z = zt[row];
   if (!again && m - r > kMaxAbove && m < INFINITY) {  // an infinite logit gains nothing from it
     ref[row] = m;
-    atomicOr(request, 1);
+    atomicOr(hdr + 1, 1);
     return;
   }
   const float et = expf(z - r);  // 1 unless the row's reference was replaced
   const float total = s + et;
   const float l = (r - z) + (r == z ? log1pf(s) : logf(total));
-  const int32_t t = target[row];
   const bool live = t >= 0 && t < V;
   const float gi = live ? (g ? g[row] : 1.0f) : 0.0f;
   loss[row] = live ? l : 0.0f;
@@ -453,21 +669,45 @@ __global__ void __launch_bounds__(256) ce_stats_kernel(const int32_t* gate, cons
   tval[row] = live ? -gi * (s / total) : 0.0f;
 }
 
-// dh_i = mul_i U_i + tval_i w_t (+ dh_i): one warp per row
-__global__ void __launch_bounds__(128) ce_dh_kernel(const float* __restrict__ u, const __nv_bfloat16* __restrict__ w,
-                                                    int64_t ldw, const int32_t* __restrict__ tcol,
-                                                    const float* __restrict__ mul, const float* __restrict__ tval,
-                                                    int64_t N, int d, int accumulate, __nv_bfloat16* dh) {
+// How the product with the head was split: its K blocks, tiles (row-major over token rows and columns, or
+// over columns alone when it was taken transposed), those that are whole, and the pairs that share the rest
+struct Segments {
+  int64_t num_kb, tiles, whole, pairs;
+  int nt, transposed;
+};
+
+// dh_i = mul_i U_i + tval_i w_t (+ dh_i), U_i the sum of its segments: one warp per row, a tile's 256
+// columns at a time
+__global__ void __launch_bounds__(128) ce_dh_kernel(const float* __restrict__ u, const float* __restrict__ rest,
+                                                    const Segments sg,
+                                                    const __nv_bfloat16* __restrict__ w, int64_t ldw,
+                                                    const int32_t* __restrict__ tcol, const float* __restrict__ mul,
+                                                    const float* __restrict__ tval, int64_t N, int d, int accumulate,
+                                                    __nv_bfloat16* dh) {
+  wait_for_previous();
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= N) return;
   const float a = __ldg(mul + row), b = __ldg(tval + row);
   const uint4* wr = reinterpret_cast<const uint4*>(w + (int64_t)__ldg(tcol + row) * ldw);
-  const float4* ur = reinterpret_cast<const float4*>(u + row * d);
   uint4* out = reinterpret_cast<uint4*>(dh + row * d);
-  for (int c = lane; c < d / 8; c += 32) {
-    const float4 u0 = ur[2 * c], u1 = ur[2 * c + 1];
-    float v[8], x[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+  for (int i = blockIdx.y; i * 256 < d; i += gridDim.y) {
+    const int c = 32 * i + lane;
+    const int64_t tile = sg.transposed ? i : (row / kTile) * sg.nt + i;
+    const int64_t rt = tile - sg.whole, rest_tiles = sg.tiles - sg.whole;
+    const int p0 = rt < 0 ? 0 : (int)split_first(rt, sg.num_kb, rest_tiles, sg.pairs);
+    const int p1 = rt < 0 ? 0 : (int)split_last(rt, sg.num_kb, rest_tiles, sg.pairs);
+    if (c >= d / 8) continue;
+    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8];
+#pragma unroll 4
+    for (int pr = p0; pr <= p1; ++pr) {
+      const float* at = pr == p0         ? u + row * d + 8 * c
+                        : sg.transposed ? rest + ((int64_t)pr * kFewRows + row) * kTile + 8 * lane
+                                        : rest + ((int64_t)pr * kTile + row % kTile) * kTile + 8 * lane;
+      const float4 u0 = reinterpret_cast<const float4*>(at)[0], u1 = reinterpret_cast<const float4*>(at)[1];
+      x[0] += u0.x; x[1] += u0.y; x[2] += u0.z; x[3] += u0.w;
+      x[4] += u1.x; x[5] += u1.y; x[6] += u1.z; x[7] += u1.w;
+    }
     unpack8(__ldg(wr + c), v);
     // a row that carries no loss keeps its zero gradient whatever its logits were
 #pragma unroll
@@ -484,9 +724,9 @@ __global__ void __launch_bounds__(128) ce_dh_kernel(const float* __restrict__ u,
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// SM pairs that can run the kernel at the same time (its persistent grid)
 template <int MODE>
-cudaError_t launch_head(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const HeadParams& p,
-                        int kid, cudaStream_t st) {
+int head_pairs(cudaError_t* err) {
   auto kern = head_gemm_kernel<MODE>;
   constexpr int SMEM = HCfg<MODE>::SMEM;
   static int max_pairs[64] = {0};  // per device
@@ -495,7 +735,10 @@ cudaError_t launch_head(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
   if (dev < 0 || dev >= 64) dev = 0;
   if (!max_pairs[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess) {
+      *err = e;
+      return 0;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
     cfg.blockDim = dim3(kThreadsH, 1, 1);
@@ -505,18 +748,45 @@ cudaError_t launch_head(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
       cudaGetLastError();
       n = num_sms() / 2;
     }
-    max_pairs[dev] = n;
+    max_pairs[dev] = n < kMaxPairs ? n : kMaxPairs;
   }
-  const int64_t tiles = (int64_t)p.mt * p.nt;
-  const int64_t pairs = tiles < max_pairs[dev] ? tiles : max_pairs[dev];
-  if (pairs < 1) return cudaSuccess;
-  prof_begin(kid, st);
-  kern<<<(unsigned)(2 * pairs), kThreadsH, SMEM, st>>>(ta, tb, tc, p);
-  prof_end(kid, st);
-  return cudaGetLastError();
+  return max_pairs[dev];
 }
 
-constexpr size_t kPieceBytes = size_t(1) << 30;  // bound on the stored piece of exp(logits)
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+}
+
+// *used (may be null): the pairs launched
+template <int MODE>
+cudaError_t launch_head(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const HeadParams& p,
+                        int kid, cudaStream_t st, int* used = nullptr) {
+  cudaError_t e = cudaSuccess;
+  const int most = head_pairs<MODE>(&e);
+  if (e != cudaSuccess) return e;
+  const int64_t units = (int64_t)p.mt * p.nt * (p.split ? p.num_kb : 1);
+  const int pairs = (int)(units < most ? units : most);
+  if (used) *used = pairs;
+  if (pairs < 1) return cudaSuccess;
+  prof_begin(kid, st);
+  e = launch_dependent(head_gemm_kernel<MODE>, dim3((unsigned)(2 * pairs), 1, 1), kThreadsH, HCfg<MODE>::SMEM, st, ta, tb,
+                       tc, p);
+  prof_end(kid, st);
+  return e;
+}
+
+constexpr size_t kPieceBytes = size_t(1000) << 20;  // bound on the stored piece of exp(logits)
 
 size_t align_up(size_t v) { return (v + 1023) / 1024 * 1024; }
 
@@ -525,13 +795,16 @@ size_t align_up(size_t v) { return (v + 1023) / 1024 * 1024; }
 int ce_layout_of(int64_t N, int64_t d, int64_t V, int grad, int dw, CeLayout* L) {
   if (N < 0 || d <= 0 || V <= 0) return QAD_ERR_INVALID_ARG;
   if (d % 16 || d > 65536 || V >= (int64_t(1) << 30) || N >= (int64_t(1) << 30)) return QAD_ERR_UNSUPPORTED;
-  L->parts = (int)(2 * cdiv(V, kTile));
+  const bool few = N <= kFewRows;
+  const int64_t width = few ? kFewRows : N;  // tokens in a row of the stored piece and of the partial sums
   // pieces of equal width (whole tiles) whose exp(logits) stay within kPieceBytes; one at least
   const int64_t vt = cdiv(V, kTile);
-  int64_t most = (int64_t)(kPieceBytes / 2) / (kTile * (N > 0 ? N : 1));
+  int64_t most = (int64_t)(kPieceBytes / 2) / (kTile * width);
   if (most < 1) most = 1;
-  const int64_t pieces = cdiv(vt, most);
-  L->piece = (int)(cdiv(vt, pieces) * kTile);
+  L->pieces = (int)cdiv(vt, most);
+  L->piece = (int)(cdiv(vt, L->pieces) * kTile);
+  L->pieces = (int)cdiv(V, L->piece);
+  L->parts = few ? L->pieces * kMaxPairs * 8 : (int)(2 * vt);
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes); return at; };
   L->header = take(256);
@@ -540,10 +813,11 @@ int ce_layout_of(int64_t N, int64_t d, int64_t V, int grad, int dw, CeLayout* L)
   L->tcol = take(4 * (size_t)N);
   L->mul = take(4 * (size_t)N);
   L->tval = take(4 * (size_t)N);
-  L->psum = take(4 * (size_t)N * L->parts);
-  L->pmax = take(4 * (size_t)N * L->parts);
+  L->psum = take(4 * (size_t)width * L->parts);
+  L->pmax = take(4 * (size_t)width * L->parts);
   L->u = take(grad ? 4 * (size_t)(N * d) : 0);
-  L->p = take(grad || dw ? 2 * (size_t)N * L->piece : 0);
+  L->rest = take(grad ? 4 * (size_t)kMaxPairs * kTile * (few ? kFewRows : kTile) : 0);
+  L->p = take(grad || dw ? 2 * (size_t)width * L->piece : 0);
   L->total = o;
   return QAD_OK;
 }
@@ -560,25 +834,32 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   float* psum = reinterpret_cast<float*>(ws + L.psum);
   float* pmax = reinterpret_cast<float*>(ws + L.pmax);
   float* u = reinterpret_cast<float*>(ws + L.u);
+  float* rest = reinterpret_cast<float*>(ws + L.rest);
+  void* ep = ws + L.p;
   const auto* hb = static_cast<const __nv_bfloat16*>(h);
   const auto* wb = static_cast<const __nv_bfloat16*>(w);
-  cudaError_t e = cudaMemsetAsync(hdr, 0, 256, st);
-  if (e != cudaSuccess) return e;
-  CUtensorMap th, tw, tps, tp, tw_mn, th_mn, tp_mn, tdw;
-  if (!make_tmap(&th, h, d, N, ldh, BM) || !make_tmap(&tw, w, d, V, ldw, BM)) return cudaErrorInvalidValue;
-  tps = th;
-  if (dh || dw) {
-    if (!make_store_tmap(&tps, ws + L.p, L.piece, N, L.piece) || !make_tmap(&tp, ws + L.p, L.piece, N, L.piece, BM) ||
-        !make_tmap(&tw_mn, w, d, V, ldw, HCfg<M_U>::BKE))
-      return cudaErrorInvalidValue;
+  const bool few = N <= kFewRows;
+  const int64_t width = few ? kFewRows : N;
+  cudaError_t e = cudaSuccess;
+  // operands K-major for the logits; the head MN-major for U; e [token, piece] or, transposed, [piece, token]
+  CUtensorMap tm_h, tm_w, tm_es, tm_e, tm_wu, tm_hd, tm_ed, tm_dw;
+  bool ok = make_tmap(&tm_h, h, d, N, ldh, few ? kFewRows / 2 : BM) && make_tmap(&tm_w, w, d, V, ldw, BM);
+  tm_es = tm_h;
+  if (ok && (dh || dw) && !few) ok = make_store_tmap(&tm_es, ep, L.piece, N, L.piece);
+  if (ok && dh) {
+    ok = make_tmap(&tm_wu, w, d, V, ldw, few ? HCfg<M_U_T>::BKE : HCfg<M_U>::BKE) &&
+         (few ? make_tmap(&tm_e, ep, kFewRows, L.piece, kFewRows, HCfg<M_U_T>::BKE)
+              : make_tmap(&tm_e, ep, L.piece, N, L.piece, BM));
   }
-  if (dw) {
-    if (!make_tmap(&th_mn, h, d, N, ldh, HCfg<M_DW>::BKE) ||
-        !make_tmap(&tp_mn, ws + L.p, L.piece, N, L.piece, HCfg<M_DW>::BKE) || !make_store_tmap(&tdw, dw, d, V, d))
-      return cudaErrorInvalidValue;
+  if (ok && dw) {
+    ok = make_tmap(&tm_hd, h, d, N, ldh, HCfg<M_DW>::BKE) && make_store_tmap(&tm_dw, dw, d, V, d) &&
+         (few ? make_tmap(&tm_ed, ep, kFewRows, L.piece, kFewRows, BM)
+              : make_tmap(&tm_ed, ep, L.piece, N, L.piece, HCfg<M_DW>::BKE));
   }
-  note_launches(2);
+  if (!ok) return cudaErrorInvalidValue;
+  note_launches(1);
   ce_ref_kernel<<<(unsigned)cdiv(N, 4), 128, 0, st>>>(hb, ldh, wb, ldw, target, N, (int)d, V, ref, zt, tcol, hdr);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
   HeadParams base = {};
   base.err = hdr;
@@ -586,46 +867,84 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   base.d = (int)d;
   base.ref = ref;
   base.target = tcol;
-  auto logits = [&](int64_t c0, int64_t cols) {
+  int parts = 0;  // partial sums of the sweep so far
+  auto logits = [&](int piece, const int32_t* gate, bool sums, bool store, bool final) -> cudaError_t {
+    const int64_t c0 = (int64_t)piece * L.piece, cols = V - c0 < L.piece ? V - c0 : L.piece;
     HeadParams p = base;
-    p.c0 = p.b_row0 = (int)c0;
+    p.gate = gate;
+    p.c0 = (int)c0;
     p.cols = (int)cols;
+    p.num_kb = (int)cdiv(d, HCfg<M_LOGITS>::BKE);
+    p.store_p = store;
+    if (sums) {
+      p.psum = psum;
+      p.pmax = pmax;
+      p.part0 = parts;
+    }
+    if (final) {  // normalised, with the target's column
+      p.mul = mul;
+      p.tval = tval;
+    }
+    if (few) {
+      p.a_row0 = (int)c0;
+      p.mt = (int)cdiv(cols, kTile);
+      p.nt = 1;
+      p.p = static_cast<__nv_bfloat16*>(ep);
+      int pairs = 0;
+      const cudaError_t e = launch_head<M_LOGITS_T>(tm_w, tm_h, tm_es, p, QAD_K_CE_LOGITS, st, &pairs);
+      parts += pairs * 8;
+      return e;
+    }
+    p.b_row0 = (int)c0;
     p.mt = (int)cdiv(N, kTile);
     p.nt = (int)cdiv(cols, kTile);
-    p.num_kb = (int)cdiv(d, HCfg<M_LOGITS>::BKE);
-    return p;
+    parts += 2 * p.nt;
+    return launch_head<M_LOGITS>(tm_h, tm_w, tm_es, p, QAD_K_CE_LOGITS, st);
+  };
+  Segments sg = {};
+  auto product = [&](int piece, const int32_t* gate) -> cudaError_t {
+    const int64_t c0 = (int64_t)piece * L.piece;
+    // every piece is contracted over the same number of K blocks, so that their segments are the same: the
+    // last one's rows of the head past V read as zeros
+    const int64_t cols = L.pieces > 1 ? L.piece : V;
+    HeadParams q = base;
+    q.gate = gate;
+    q.nt = few ? 1 : (int)cdiv(d, kTile);
+    q.mt = few ? (int)cdiv(d, kTile) : (int)cdiv(N, kTile);
+    q.n_fast = 1;
+    q.split = 1;
+    q.u = u;
+    q.rest = rest;
+    q.add = c0 > 0;
+    q.num_kb = (int)cdiv(cols, few ? HCfg<M_U_T>::BKE : HCfg<M_U>::BKE);
+    int pairs = 0;
+    cudaError_t e;
+    if (few) {
+      q.a_row0 = (int)c0;
+      e = launch_head<M_U_T>(tm_wu, tm_e, tm_e, q, QAD_K_CE_DH, st, &pairs);
+    } else {
+      q.b_row0 = (int)c0;
+      e = launch_head<M_U>(tm_e, tm_wu, tm_e, q, QAD_K_CE_DH, st, &pairs);
+    }
+    const int64_t tiles = (int64_t)q.mt * q.nt;
+    const int64_t rest = tiles % pairs;
+    sg = {q.num_kb, tiles, tiles - rest, split_pairs(q.num_kb, rest, pairs), q.nt, few ? 1 : 0};
+    return e;
   };
   // the sweep: exp(logits) of a piece, then its product with the piece of the head
   auto sweep = [&](const int32_t* gate) -> cudaError_t {
-    for (int64_t c0 = 0; c0 < V; c0 += L.piece) {
-      const int64_t cols = V - c0 < L.piece ? V - c0 : L.piece;
-      HeadParams p = logits(c0, cols);
-      p.gate = gate;
-      p.psum = psum;
-      p.pmax = pmax;
-      p.store_p = dh != nullptr;
-      cudaError_t e = launch_head<M_LOGITS>(th, tw, tps, p, QAD_K_CE_LOGITS, st);
-      if (e != cudaSuccess) return e;
-      if (!dh) continue;
-      HeadParams q = base;
-      q.gate = gate;
-      q.b_row0 = (int)c0;
-      q.mt = (int)cdiv(N, kTile);
-      q.nt = (int)cdiv(d, kTile);
-      q.n_fast = 1;
-      q.num_kb = (int)cdiv(cols, HCfg<M_U>::BKE);
-      q.u = u;
-      q.add = c0 > 0;
-      e = launch_head<M_U>(tp, tw_mn, tp, q, QAD_K_CE_DH, st);
+    parts = 0;
+    for (int i = 0; i < L.pieces; ++i) {
+      cudaError_t e = logits(i, gate, true, dh != nullptr, false);
+      if (e == cudaSuccess && dh) e = product(i, gate);
       if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
   };
   auto stats = [&](const int32_t* gate, int again) {
-    ce_stats_kernel<<<(unsigned)cdiv(N, 32), 256, 0, st>>>(gate, psum, pmax, L.parts, N, target, V, g, zt, ref, mul,
-                                                            tval, loss, lse, again, hdr + 1);
     note_launches(1);
-    return cudaGetLastError();
+    return launch_dependent(ce_stats_kernel, dim3((unsigned)cdiv(N, 32), 1, 1), 1024, 0, st, gate, psum, pmax, parts,
+                            (int)width, N, target, V, g, zt, ref, mul, tval, loss, lse, again, hdr);
   };
   if ((e = sweep(nullptr)) != cudaSuccess) return e;
   if ((e = stats(nullptr, 0)) != cudaSuccess) return e;
@@ -633,27 +952,25 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   if ((e = stats(hdr + 1, 1)) != cudaSuccess) return e;
   if (dh) {
     note_launches(1);
-    ce_dh_kernel<<<(unsigned)cdiv(N, 4), 128, 0, st>>>(u, wb, ldw, tcol, mul, tval, N, (int)d, accumulate,
-                                                        static_cast<__nv_bfloat16*>(dh));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // few rows: a block column per 256 columns, so that their segments are read side by side
+    const dim3 grid((unsigned)cdiv(N, 4), few ? (unsigned)cdiv(d, 256) : 1u, 1);
+    e = launch_dependent(ce_dh_kernel, grid, 128, 0, st, u, rest, sg, wb, ldw, tcol, mul, tval, N, (int)d, accumulate,
+                         static_cast<__nv_bfloat16*>(dh));
+    if (e != cudaSuccess) return e;
   }
-  if (dw) {
-    for (int64_t c0 = 0; c0 < V; c0 += L.piece) {
-      const int64_t cols = V - c0 < L.piece ? V - c0 : L.piece;
-      HeadParams p = logits(c0, cols);
-      p.mul = mul;
-      p.tval = tval;
-      p.store_p = 1;
-      if ((e = launch_head<M_LOGITS>(th, tw, tps, p, QAD_K_CE_LOGITS, st)) != cudaSuccess) return e;
-      HeadParams q = base;
-      q.c0 = (int)c0;
-      q.cols = (int)cols;
-      q.mt = (int)cdiv(cols, kTile);
-      q.nt = (int)cdiv(d, kTile);
-      q.n_fast = 1;
-      q.num_kb = (int)cdiv(N, HCfg<M_DW>::BKE);
-      if ((e = launch_head<M_DW>(tp_mn, th_mn, tdw, q, QAD_K_CE_DW, st)) != cudaSuccess) return e;
-    }
+  for (int i = 0; dw && i < L.pieces; ++i) {
+    const int64_t c0 = (int64_t)i * L.piece, cols = V - c0 < L.piece ? V - c0 : L.piece;
+    if ((e = logits(i, nullptr, false, true, true)) != cudaSuccess) return e;
+    HeadParams q = base;
+    q.c0 = (int)c0;
+    q.cols = (int)cols;
+    q.mt = (int)cdiv(cols, kTile);
+    q.nt = (int)cdiv(d, kTile);
+    q.n_fast = 1;
+    q.num_kb = (int)cdiv(N, HCfg<M_DW>::BKE);
+    e = few ? launch_head<M_DW_T>(tm_ed, tm_hd, tm_dw, q, QAD_K_CE_DW, st)
+            : launch_head<M_DW>(tm_ed, tm_hd, tm_dw, q, QAD_K_CE_DW, st);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
