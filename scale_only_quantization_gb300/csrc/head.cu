@@ -244,11 +244,11 @@ __device__ __forceinline__ void epi_logits(const HeadParams& p, const CUtensorMa
   }
 }
 
-// Vocabulary row v's e for 64 of the tokens (32 at a time); sums[c], tops[c]: this lane's token of chunk c, over
-// all rows that this warp has seen
+// Vocabulary row v's e for 64 of the tokens, 8 at a time; sums[i], tops[i]: token 8 i + lane / 4 of these 64,
+// over all rows that this warp has seen
 __device__ __forceinline__ void epi_logits_t(const HeadParams& p, const float* tok, const HTile& ti, int rank,
-                                             uint32_t tbase, int q, int lane, int half, float (&sums)[2],
-                                             float (&tops)[2]) {
+                                             uint32_t tbase, int q, int lane, int half, float (&sums)[8],
+                                             float (&tops)[8]) {
   const int vr = ti.mb * kTile + rank * BM + 32 * q + lane;  // within the piece
   const bool live = vr < p.cols;
   const int v = p.c0 + vr;
@@ -258,52 +258,52 @@ __device__ __forceinline__ void epi_logits_t(const HeadParams& p, const float* t
   const int4* tgt = reinterpret_cast<const int4*>(tv + kFewRows / 4);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    const int n0 = 64 * half + 32 * c;
-    if (n0 >= p.N && !p.store_p) continue;  // tokens that are not there; their e (K of the next product) must be 0
+    if (64 * half + 32 * c >= p.N && !p.store_p) continue;  // tokens that are not there; if stored, their e must be 0
     uint32_t r[32];
-    tmem_ld32_issue(tbase + n0, r);
+    tmem_ld32_issue(tbase + 64 * half + 32 * c, r);
     tmem_wait32(r);
-    float x[32];
-    uint4 out[4];
-    uint32_t* o = reinterpret_cast<uint32_t*>(out);
 #pragma unroll
-    for (int i4 = 0; i4 < 8; ++i4) {
-      const float4 rf = ref[n0 / 4 + i4], mf = mul[n0 / 4 + i4], tf = tv[n0 / 4 + i4];
-      const int4 tg = tgt[n0 / 4 + i4];
-      const float rr[4] = {rf.x, rf.y, rf.z, rf.w}, mm[4] = {mf.x, mf.y, mf.z, mf.w}, tt[4] = {tf.x, tf.y, tf.z, tf.w};
-      const int gg[4] = {tg.x, tg.y, tg.z, tg.w};
-      float y[4];
+    for (int k = 0; k < 4; ++k) {
+      const int n0 = 64 * half + 32 * c + 8 * k;
+      if (n0 >= p.N && !p.store_p) continue;
+      float x[8], y[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = __expf(__uint_as_float(r[4 * i4 + i]) - rr[i]);
-        const bool none = !live || n0 + 4 * i4 + i >= p.N;
-        x[4 * i4 + i] = none || gg[i] == v ? 0.0f : e;
-        y[i] = none ? 0.0f : gg[i] == v ? tt[i] : e * mm[i];
-      }
-      o[2 * i4] = pack_bf16(y[0], y[1]);
-      o[2 * i4 + 1] = pack_bf16(y[2], y[3]);
-    }
-    if (p.store_p) {
-      uint4* to = reinterpret_cast<uint4*>(p.p + (int64_t)vr * kFewRows + n0);
+      for (int i4 = 0; i4 < 2; ++i4) {
+        const float4 rf = ref[n0 / 4 + i4], mf = mul[n0 / 4 + i4], tf = tv[n0 / 4 + i4];
+        const int4 tg = tgt[n0 / 4 + i4];
+        const float rr[4] = {rf.x, rf.y, rf.z, rf.w}, mm[4] = {mf.x, mf.y, mf.z, mf.w}, tt[4] = {tf.x, tf.y, tf.z, tf.w};
+        const int gg[4] = {tg.x, tg.y, tg.z, tg.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) to[i] = out[i];
-    }
-    if (p.psum) {
-      float z[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = live ? __uint_as_float(r[i]) : -INFINITY;
-      // over the warp's 32 rows: each step halves the tokens a lane carries, until it has its own
-#pragma unroll
-      for (int off = 16; off; off /= 2) {
-        const bool up = lane & off;
-#pragma unroll
-        for (int i = 0; i < off; ++i) {
-          x[i] = (up ? x[i + off] : x[i]) + __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + off], off);
-          z[i] = fmaxf(up ? z[i + off] : z[i], __shfl_xor_sync(0xffffffffu, up ? z[i] : z[i + off], off));
+        for (int i = 0; i < 4; ++i) {
+          const float e = __expf(__uint_as_float(r[8 * k + 4 * i4 + i]) - rr[i]);
+          const bool none = !live || n0 + 4 * i4 + i >= p.N;
+          x[4 * i4 + i] = none || gg[i] == v ? 0.0f : e;
+          y[4 * i4 + i] = none ? 0.0f : gg[i] == v ? tt[i] : e * mm[i];
         }
       }
-      sums[c] += x[0];
-      tops[c] = fmaxf(tops[c], z[0]);
+      if (p.store_p) *reinterpret_cast<uint4*>(p.p + (int64_t)vr * kFewRows + n0) = pack8(y);
+      if (p.psum && n0 < p.N) {
+        float z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = live ? __uint_as_float(r[8 * k + i]) : -INFINITY;
+        // over the warp's 32 rows: three steps halve the tokens a lane carries, until it has one
+#pragma unroll
+        for (int off = 16, n = 4; n; off /= 2, n /= 2) {
+          const bool up = lane & off;
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            x[i] = (up ? x[i + n] : x[i]) + __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + n], off);
+            z[i] = fmaxf(up ? z[i + n] : z[i], __shfl_xor_sync(0xffffffffu, up ? z[i] : z[i + n], off));
+          }
+        }
+#pragma unroll
+        for (int off = 2; off; off /= 2) {
+          x[0] += __shfl_xor_sync(0xffffffffu, x[0], off);
+          z[0] = fmaxf(z[0], __shfl_xor_sync(0xffffffffu, z[0], off));
+        }
+        sums[4 * c + k] += x[0];
+        tops[4 * c + k] = fmaxf(tops[4 * c + k], z[0]);
+      }
     }
   }
 }
@@ -331,6 +331,17 @@ __device__ __forceinline__ void epi_u_t(const HeadParams& p, const HTile& ti, in
   }
 }
 
+__device__ __forceinline__ void ld_f32x8(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p) : "memory");
+}
+__device__ __forceinline__ void st_f32x8(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // Row r's 128 columns of U += e W, this segment's partial sums, fp32 in global memory
 __device__ __forceinline__ void epi_u(const HeadParams& p, const HTile& ti, int seg, int pair, int rank, uint32_t tbase,
                                       int q, int lane, int half) {
@@ -342,21 +353,21 @@ __device__ __forceinline__ void epi_u(const HeadParams& p, const HTile& ti, int 
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32];
     tmem_ld32_issue(tbase + half * 128 + 32 * c, r);
-    tmem_wait32(r);
-    float4* u = reinterpret_cast<float4*>(to + 32 * c);
+    // one 32-byte sector of the row per access: the warp's lanes are 32 rows
+    float* u = to + 32 * c;
+    const bool live = row < p.N;
+    float before[4][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (row >= p.N || col0 + 32 * c + 4 * i >= p.d) continue;
-      float4 v = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
-                             __uint_as_float(r[4 * i + 3]));
-      if (p.add) {
-        const float4 w = u[i];
-        v.x += w.x;
-        v.y += w.y;
-        v.z += w.z;
-        v.w += w.w;
-      }
-      u[i] = v;
+    for (int i = 0; i < 4; ++i)
+      if (p.add && live && col0 + 32 * c + 8 * i < p.d) ld_f32x8(u + 8 * i, before[i]);
+    tmem_wait32(r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!live || col0 + 32 * c + 8 * i >= p.d) continue;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[8 * i + j]) + (p.add ? before[i][j] : 0.0f);
+      st_f32x8(u + 8 * i, v);
     }
     __syncwarp();  // the next tensor-memory load is the whole warp's
   }
@@ -543,7 +554,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     const uint32_t my_stage = stage_out + (uint32_t)(warp - 2) * 4096u;
     int acc = 0;
     uint32_t acc_phase = 0, buf = 0;
-    float sums[2] = {0.0f, 0.0f}, tops[2] = {-INFINITY, -INFINITY};
+    float sums[8], tops[8];  // M_LOGITS_T
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sums[i] = 0.0f;
+      tops[i] = -INFINITY;
+    }
     if constexpr (C::BOXES) tma_prefetch_desc(&tmC);
     while (wk.next(p)) {
       const HTile ti = htile(p, wk.tile);
@@ -566,13 +582,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
       if (lane == 0) bulk_wait_all();
     }
     if constexpr (MODE == M_LOGITS_T) {  // one part per CTA and lane quadrant
-      if (p.psum)
+      if (p.psum && (lane & 3) == 0)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int n = 64 * half + 32 * c + lane;
+        for (int i = 0; i < 8; ++i) {
+          const int n = 64 * half + 8 * i + lane / 4;
           const int64_t at = (int64_t)(p.part0 + (pair * 2 + (int)rank) * 4 + q) * kFewRows + n;
-          p.psum[at] = sums[c];
-          p.pmax[at] = tops[c];
+          p.psum[at] = sums[i];
+          p.pmax[at] = tops[i];
         }
     }
   }
