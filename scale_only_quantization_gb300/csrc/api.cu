@@ -420,7 +420,7 @@ static bool ok_rows(const void* p, int64_t ld, int64_t d) { return ok_ptr(p) && 
 
 size_t qad_rmsnorm_workspace_bytes(int64_t T, int64_t d) {
   if (T < 0 || d <= 0 || d % 16 || d > QAD_RMSNORM_MAX_D) return 0;
-  return up(4 * (size_t)norm_groups(T > 0 ? T : 1) * (size_t)d);
+  return up(4 * (size_t)norm_blocks(T > 0 ? T : 1) * (size_t)d);
 }
 
 int qad_rmsnorm_fwd(const void* x, const void* res, const void* gamma, float eps, int act, void* res_out, void* y,

@@ -126,7 +126,7 @@ cudaError_t gemm_wgrad_fc2(const GemmCtx& c, const void* w2, const float* s2, fl
 cudaError_t gemm_wgrad_fc1(const GemmCtx& c, const void* w13, const float* s13, float* ds13, int accumulate);
 
 // ---- residual RMSNorm (norm.cu); kind: kQNone, kQE4M3 or kQInt8 ----
-int norm_groups(int64_t T);  // partial dgamma rows of the backward's workspace
+int norm_blocks(int64_t T);  // partial dgamma rows of the backward's workspace at most
 cudaError_t launch_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* gamma, float eps,
                                int kind, void* r, void* y, void* y_hat, void* codes, float* scale, float* rstd,
                                int64_t T, int64_t d, cudaStream_t st);

@@ -14,6 +14,17 @@
 namespace qad {
 namespace {
 
+// unpack8 by byte moves.  The second use of a row's values unpacks them by other instructions than the
+// first: with the same ones the compiler keeps the unpacked values in between, twice the registers.
+__device__ __forceinline__ void unpack8_again(const uint4& u, float* f) {
+  const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(__byte_perm(x[i], 0, 0x1044));
+    f[2 * i + 1] = __uint_as_float(__byte_perm(x[i], 0, 0x3244));
+  }
+}
+
 struct NormFwd {
   const __nv_bfloat16 *x, *res, *gamma;
   __nv_bfloat16 *r, *y, *y_hat;
@@ -169,12 +180,14 @@ struct NormBwd {
   int nv, d;
 };
 
-// Rows are taken in turn by groups of W warps on a fixed grid; each lane keeps the norm-weight
-// gradient of its own columns in registers over all rows of its group, so the sum over rows
-// costs one fp32 row per group, added in a fixed order by rmsnorm_dgamma_kernel.
-template <int VPL, int W>
+// Rows are taken in turn by groups of W warps on a fixed grid, a row's loads issued before the row ahead
+// of it is worked on; each lane keeps the norm-weight gradient of its own columns in registers over
+// all rows of its group, so the sum over rows costs one fp32 row per block, added in a fixed order by
+// rmsnorm_dgamma_kernel.
+template <int VPL, int W, bool DRES>
 __global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(const NormBwd p) {
   constexpr int RB = 8 / W;
+  extern __shared__ float4 joined[];  // [RB - 1, d]
   __shared__ float red[RB][2][W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int grp = warp / W, wr = warp % W, t = wr * 32 + lane;
@@ -189,26 +202,31 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(const NormBwd p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
   }
-  int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RB + grp; row < p.T; row += step) {
+  uint4 n[VPL], g[VPL], e[DRES ? VPL : 1];
+  float rstd = 0.0f;
+  auto load = [&](int64_t row, uint4 (&nn)[VPL], uint4 (&gg)[VPL], uint4 (&ee)[DRES ? VPL : 1], float& rs) {
+    const bool in = row < p.T;
     const uint4* rr = reinterpret_cast<const uint4*>(p.r + row * p.ldr);
     const uint4* dyr = reinterpret_cast<const uint4*>(p.dy + row * p.d);
-    uint4 n[VPL], g[VPL], e[VPL];
+    const uint4* er = reinterpret_cast<const uint4*>(p.dres + row * p.d);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int c = i * 32 * W + t;
-      n[i] = c < p.nv ? __ldcs(rr + c) : zero;
-      g[i] = c < p.nv ? __ldcs(dyr + c) : zero;
+      const bool ok = in && c < p.nv;
+      nn[i] = ok ? __ldcs(rr + c) : zero;
+      gg[i] = ok ? __ldcs(dyr + c) : zero;
+      if constexpr (DRES) ee[i] = ok ? __ldcs(er + c) : zero;
     }
-    if (p.dres) {
-      const uint4* er = reinterpret_cast<const uint4*>(p.dres + row * p.d);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int c = i * 32 * W + t;
-        e[i] = c < p.nv ? __ldcs(er + c) : zero;
-      }
-    }
-    const float rstd = __ldg(p.rstd + row);
+    rs = in ? __ldg(p.rstd + row) : 0.0f;
+  };
+  int flip = 0;
+  int64_t row = (int64_t)blockIdx.x * RB + grp;
+  if constexpr (VPL <= 4) load(row, n, g, e, rstd);
+  for (; row < p.T; row += step) {
+    uint4 n2[VPL], g2[VPL], e2[DRES ? VPL : 1];
+    float rstd2 = 0.0f;
+    if constexpr (VPL <= 4) load(row + step, n2, g2, e2, rstd2);
+    else load(row, n, g, e, rstd);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -231,29 +249,56 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(const NormBwd p) {
     for (int i = 0; i < VPL; ++i) {
       const int c = i * 32 * W + t;
       float a[8], b[8], w[8], o[8];
-      unpack8(n[i], a);
-      unpack8(g[i], b);
-      unpack8(gm[i], w);
+      unpack8_again(n[i], a);
+      unpack8_again(g[i], b);
+      unpack8_again(gm[i], w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = rstd * (b[j] * w[j] - a[j] * rstd * m);
-      if (p.dres) {
+      if constexpr (DRES) {
         unpack8(e[i], a);
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] += a[j];
       }
       if (c < p.nv) out[c] = pack8(o);
     }
-  }
-  if (p.part) {
-    float* pr = p.part + ((int64_t)blockIdx.x * RB + grp) * p.d;
+    if constexpr (VPL <= 4) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int c = i * 32 * W + t;
-      if (c < p.nv) {
-        reinterpret_cast<float4*>(pr)[2 * c] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-        reinterpret_cast<float4*>(pr)[2 * c + 1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+      for (int i = 0; i < VPL; ++i) {
+        n[i] = n2[i];
+        g[i] = g2[i];
+        if constexpr (DRES) e[i] = e2[i];
       }
+      rstd = rstd2;
     }
+  }
+  if (!p.part) return;
+  if constexpr (RB > 1) {
+    if (grp > 0)
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int c = i * 32 * W + t;
+        if (c < p.nv) {
+          float4* to = joined + ((int64_t)(grp - 1) * p.nv + c) * 2;
+          to[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+          to[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+        }
+      }
+    __syncthreads();
+    if (grp > 0) return;
+  }
+  float4* pr = reinterpret_cast<float4*>(p.part + (int64_t)blockIdx.x * p.d);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = i * 32 * W + t;
+    if (c >= p.nv) continue;
+#pragma unroll
+    for (int q = 0; q < RB - 1; ++q) {
+      const float4 a = joined[((int64_t)q * p.nv + c) * 2], b = joined[((int64_t)q * p.nv + c) * 2 + 1];
+      dg[i][0] += a.x; dg[i][1] += a.y; dg[i][2] += a.z; dg[i][3] += a.w;
+      dg[i][4] += b.x; dg[i][5] += b.y; dg[i][6] += b.z; dg[i][7] += b.w;
+    }
+    pr[2 * c] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+    pr[2 * c + 1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
   }
 }
 
@@ -286,19 +331,20 @@ cudaError_t fwd_kind(const NormFwd& p, int kind, cudaStream_t st) {
 }
 
 template <int VPL, int W>
-cudaError_t bwd_launch(const NormBwd& p, int groups, cudaStream_t st) {
-  constexpr int RB = 8 / W;
-  rmsnorm_bwd_kernel<VPL, W><<<(unsigned)((groups + RB - 1) / RB), 256, 0, st>>>(p);
+cudaError_t bwd_launch(const NormBwd& p, int blocks, cudaStream_t st) {
+  const size_t smem = p.part ? (size_t)(8 / W - 1) * p.d * 4 : 0;
+  if (p.dres) rmsnorm_bwd_kernel<VPL, W, true><<<(unsigned)blocks, 256, smem, st>>>(p);
+  else rmsnorm_bwd_kernel<VPL, W, false><<<(unsigned)blocks, 256, smem, st>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Partial dgamma rows: a constant so that the workspace size needs no device query; 8 row groups
-// for each of 152 SMs.
-constexpr int kNormGroups = 1216;
+// Blocks of the backward, and so partial dgamma rows: a constant, so that the workspace size needs no device query.
+// (Bounding the registers for three or four blocks spills: 86 and 96 us against 50 for 16384 x 2048.)
+constexpr int kNormBlocks = 304;  // two per SM of 152, as many as the registers hold
 
-int norm_groups(int64_t T) { return (int)(T < kNormGroups ? (T + 7) / 8 * 8 : kNormGroups); }
+int norm_blocks(int64_t T) { return (int)(T < kNormBlocks ? T : kNormBlocks); }
 
 cudaError_t launch_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* gamma, float eps,
                                int kind, void* r, void* y, void* y_hat, void* codes, float* scale, float* rstd,
@@ -349,22 +395,23 @@ cudaError_t launch_rmsnorm_bwd(const void* dy, const void* dres, const void* r, 
   p.ldr = ldr;
   p.nv = (int)(d / 8);
   p.d = (int)d;
-  const int groups = norm_groups(T);
   const int lanes1 = (p.nv + 31) / 32;
+  const int w = lanes1 <= 2 ? 1 : lanes1 <= 4 ? 2 : lanes1 <= 12 ? 4 : 8;  // warps per row
+  const int blocks = norm_blocks((T + 8 / w - 1) / (8 / w));
   prof_begin(QAD_K_RMSNORM_BWD, st);
   cudaError_t e;
-  if (lanes1 <= 1) e = bwd_launch<1, 1>(p, groups, st);
-  else if (lanes1 <= 2) e = bwd_launch<2, 1>(p, groups, st);
-  else if (lanes1 <= 4) e = bwd_launch<2, 2>(p, groups, st);
-  else if (lanes1 <= 8) e = bwd_launch<2, 4>(p, groups, st);
-  else if (lanes1 <= 12) e = bwd_launch<3, 4>(p, groups, st);
-  else if (lanes1 <= 16) e = bwd_launch<2, 8>(p, groups, st);
-  else if (lanes1 <= 32) e = bwd_launch<4, 8>(p, groups, st);
-  else e = bwd_launch<8, 8>(p, groups, st);
+  if (lanes1 <= 1) e = bwd_launch<1, 1>(p, blocks, st);
+  else if (lanes1 <= 2) e = bwd_launch<2, 1>(p, blocks, st);
+  else if (lanes1 <= 4) e = bwd_launch<2, 2>(p, blocks, st);
+  else if (lanes1 <= 8) e = bwd_launch<2, 4>(p, blocks, st);
+  else if (lanes1 <= 12) e = bwd_launch<3, 4>(p, blocks, st);
+  else if (lanes1 <= 16) e = bwd_launch<2, 8>(p, blocks, st);
+  else if (lanes1 <= 32) e = bwd_launch<4, 8>(p, blocks, st);
+  else e = bwd_launch<8, 8>(p, blocks, st);
   prof_end(QAD_K_RMSNORM_BWD, st);
   if (e != cudaSuccess || !dgamma) return e;
   note_launches(1);
-  rmsnorm_dgamma_kernel<<<(unsigned)((d + 31) / 32), 1024, 0, st>>>(part, groups, (int)d, dgamma);
+  rmsnorm_dgamma_kernel<<<(unsigned)((d + 31) / 32), 1024, 0, st>>>(part, blocks, (int)d, dgamma);
   return cudaGetLastError();
 }
 
