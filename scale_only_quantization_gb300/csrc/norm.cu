@@ -32,7 +32,7 @@ struct NormFwd {
   float *scale, *rstd;
   int64_t T, ldx, ldres;
   int nv, d;  // 16-byte vectors of a row, and its elements
-  float eps;
+  float eps, inv_d;
 };
 
 // Sum (or maximum) over the W warps that share a row; every thread of the group returns it.
@@ -49,18 +49,137 @@ __device__ __forceinline__ float row_reduce(float v, float* smem, int warp_in_ro
   return v;
 }
 
-// W warps per row, each lane keeping VPL vectors of it; the block's other warps take other rows.
+// The layer's activation quantizer on 4 values of scale s: their codes, and code value * s in place
+template <int KIND>
+__device__ __forceinline__ void quantize4(float* a, float s, uint32_t& code) {
+  if constexpr (KIND == kQE4M3) {
+    uint32_t c[1];
+    fakequant_e4m3_codes<4, true>(a, s, c);
+    code = c[0];
+  } else {
+    float x[4];
+    act_quotients<4>(a, s, x);
+    code = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float q = q_int8(x[j]);
+      code |= ((uint32_t)(int)q & 0xffu) << (8 * j);
+      a[j] = __fmul_rn(copysignf(q, x[j]), s);
+    }
+  }
+}
+
+// Two bf16 pairs (8 bytes) <-> 4 floats
+__device__ __forceinline__ void unpack4(const uint2& u, float* f) {
+  f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
+}
+__device__ __forceinline__ uint2 pack4(const float* f) { return make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])); }
+
+// The squares of bf16 values are exact in fp32, so rstd depends on the order of their sum alone.  Up to 4096
+// elements it is that of an unfused fp32 row sum: 128 chains (element i in chain i % 128), the four of a
+// group one after the other, then the 32 groups pairwise.  rstd and y then have the unfused bits: a last place
+// of rstd moves y by a bf16 step now and then and with it, in the row's largest element, the scale.
+
+// Rows of up to 1024 elements: one warp per row, no barrier; lane l keeps the 4-element groups l, l + 32, ...
+template <int G, int KIND>
+__global__ void __launch_bounds__(128) rmsnorm_fwd_warp_kernel(const NormFwd p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int ng = p.d / 4;  // groups of a row
+  if (row >= p.T) return;
+  const uint2* xr = reinterpret_cast<const uint2*>(p.x + row * p.ldx);
+  const uint2 zero = make_uint2(0, 0);
+  uint2 v[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) v[i] = lane + 32 * i < ng ? __ldcs(xr + lane + 32 * i) : zero;
+  if (p.res) {
+    const uint2* rr = reinterpret_cast<const uint2*>(p.res + row * p.ldres);
+    uint2 u[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) u[i] = lane + 32 * i < ng ? __ldcs(rr + lane + 32 * i) : zero;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      float a[4], b[4];
+      unpack4(v[i], a);
+      unpack4(u[i], b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] += b[j];
+      v[i] = pack4(a);
+    }
+  }
+  if (p.r) {
+    uint2* ro = reinterpret_cast<uint2*>(p.r + row * p.d);
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (lane + 32 * i < ng) ro[lane + 32 * i] = v[i];
+  }
+  auto mean_square = [&](float f) {
+    float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      float a[4];
+      unpack4(v[i], a);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = fmaf(a[j] * f, a[j] * f, q[j]);
+    }
+    float s = ((q[0] + q[1]) + q[2]) + q[3];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s * p.inv_d;
+  };
+  float mean = mean_square(1.0f);
+  float rstd = __fdiv_rn(1.0f, __fsqrt_rn(mean + p.eps));
+  if (mean == INFINITY)  // the squares leave fp32's range (|r| > 1e19 / sqrt(d)): scaled by 2^-64 they do not, and
+    rstd = __fdiv_rn(1.0f, __fsqrt_rn(mean_square(0x1p-64f))) * 0x1p-64f;  // eps is below the last place
+  if (lane == 0 && p.rstd) p.rstd[row] = rstd;
+  const uint2* gr = reinterpret_cast<const uint2*>(p.gamma);
+  uint2* yo = reinterpret_cast<uint2*>(p.y + row * p.d);
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    float a[4], g[4];
+    unpack4(v[i], a);
+    unpack4(lane + 32 * i < ng ? __ldg(gr + lane + 32 * i) : zero, g);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = __fmul_rn(__fmul_rn(a[j], rstd), g[j]);
+    v[i] = pack4(a);
+    if (p.y && lane + 32 * i < ng) yo[lane + 32 * i] = v[i];
+    if constexpr (KIND != kQNone) {
+      unpack4(v[i], a);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fabsf(a[j]));
+    }
+  }
+  if constexpr (KIND != kQNone) {
+    const float s = __fdiv_rn(warp_max(amax), KIND == kQE4M3 ? 448.0f : 127.0f);
+    if (lane == 0 && p.scale) p.scale[row] = s;
+    if (!p.codes && !p.y_hat) return;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int c = lane + 32 * i;
+      if (c >= ng) continue;
+      float a[4];
+      uint32_t code;
+      unpack4(v[i], a);
+      quantize4<KIND>(a, s, code);
+      if (p.codes) reinterpret_cast<uint32_t*>(p.codes + row * p.d)[c] = code;
+      if (p.y_hat) reinterpret_cast<uint2*>(p.y_hat + row * p.d)[c] = pack4(a);
+    }
+  }
+}
+
+// Wider rows: W warps per row, each lane keeping VPL 16-byte vectors of it.  Up to 4096 elements the row also
+// passes through shared memory, where thread t of the 128 takes chain t (beyond, the order is the lanes' own).
+// For 16384 x 2048 with codes 49 us; a warp per row, which needs no barrier, takes 58: its 102 registers leave 20
+// warps per SM, and their loads do not cover each other's reductions.
 template <int VPL, int W, int KIND>
-__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) rmsnorm_fwd_kernel(const NormFwd p) {
-  constexpr int RB = W > 4 ? 1 : 4 / W;
-  __shared__ float red[RB][2][W];
+__global__ void __launch_bounds__(32 * W) rmsnorm_fwd_kernel(const NormFwd p) {
+  __shared__ float red[3][W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int grp = warp / W, wr = warp % W, t = wr * 32 + lane;
-  const int64_t row = (int64_t)blockIdx.x * RB + grp;
-  if (row >= p.T) return;  // a whole group leaves: its named barrier is its own
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x;
   const uint4* xr = reinterpret_cast<const uint4*>(p.x + row * p.ldx);
   uint4 v[VPL];
-  float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int c = i * 32 * W + t;
@@ -92,28 +211,46 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) rmsnorm_fwd_kernel(const
       if (c < p.nv) ro[c] = v[i];
     }
   }
+  constexpr bool CHAINS = W == 4 && VPL <= 4;
+  __shared__ __align__(16) __nv_bfloat16 row_copy[CHAINS ? VPL * 1024 : 8];
+  if constexpr (CHAINS) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    float a[8];
-    unpack8(v[i], a);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(a[j], a[j], sum);
+    for (int i = 0; i < VPL; ++i) reinterpret_cast<uint4*>(row_copy)[i * 128 + t] = v[i];  // zeros past the row
+    __syncthreads();
   }
-  sum = row_reduce<W, false>(sum, red[grp][0], wr, lane, 1 + grp);
-  float rstd = rsqrtf(sum / (float)p.d + p.eps);
-  if (sum == INFINITY) {  // the squares leave fp32's range (|r| > 1e19 / sqrt(d)): scaled by 2^-64 they do not
-    sum = 0.0f;
+  auto mean_square = [&](float f, float* smem) {
+    float sum = 0.0f;
+    if constexpr (CHAINS) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      float a[8];
-      unpack8(v[i], a);
+      for (int i = 0; i < VPL * 8; ++i) {
+        const float a = __bfloat162float(row_copy[i * 128 + t]) * f;
+        sum = fmaf(a, a, sum);
+      }
+      // the four chains of a group in turn (lanes 4 k .. 4 k + 3), then the warp's 8 groups pairwise, then the warps
+      const float q1 = __shfl_down_sync(0xffffffffu, sum, 1), q2 = __shfl_down_sync(0xffffffffu, sum, 2),
+                  q3 = __shfl_down_sync(0xffffffffu, sum, 3);
+      sum = ((sum + q1) + q2) + q3;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(a[j] * 0x1p-64f, a[j] * 0x1p-64f, sum);
+      for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) smem[warp] = sum;
+      __syncthreads();
+      sum = (smem[0] + smem[1]) + (smem[2] + smem[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        float a[8];
+        unpack8(v[i], a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(a[j] * f, a[j] * f, sum);
+      }
+      sum = row_reduce<W, false>(sum, smem, warp, lane, 1);
     }
-    if constexpr (W > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(32 * W) : "memory");
-    sum = row_reduce<W, false>(sum, red[grp][0], wr, lane, 1 + grp);
-    rstd = rsqrtf(sum / (float)p.d) * 0x1p-64f;  // eps is below the last place
-  }
+    return sum * p.inv_d;
+  };
+  const float mean = mean_square(1.0f, red[0]);
+  float rstd = __fdiv_rn(1.0f, __fsqrt_rn(mean + p.eps));
+  if (mean == INFINITY)  // the squares leave fp32's range (|r| > 1e19 / sqrt(d)): scaled by 2^-64 they do not, and
+    rstd = __fdiv_rn(1.0f, __fsqrt_rn(mean_square(0x1p-64f, red[2]))) * 0x1p-64f;  // eps is below the last place
   if (t == 0 && p.rstd) p.rstd[row] = rstd;
   const uint4* gr = reinterpret_cast<const uint4*>(p.gamma);
   float amax = 0.0f;
@@ -124,7 +261,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) rmsnorm_fwd_kernel(const
     unpack8(v[i], a);
     unpack8(c < p.nv ? __ldg(gr + c) : make_uint4(0, 0, 0, 0), g);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = a[j] * rstd * g[j];
+    for (int j = 0; j < 8; ++j) a[j] = __fmul_rn(__fmul_rn(a[j], rstd), g[j]);
     v[i] = pack8(a);
     if constexpr (KIND != kQNone) {
       unpack8(v[i], a);
@@ -141,7 +278,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) rmsnorm_fwd_kernel(const
     }
   }
   if constexpr (KIND != kQNone) {
-    amax = row_reduce<W, true>(amax, red[grp][1], wr, lane, 1 + grp);
+    amax = row_reduce<W, true>(amax, red[1], warp, lane, 1);
     const float s = __fdiv_rn(amax, KIND == kQE4M3 ? 448.0f : 127.0f);
     if (t == 0 && p.scale) p.scale[row] = s;
     if (!p.codes && !p.y_hat) return;
@@ -152,19 +289,8 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) rmsnorm_fwd_kernel(const
       float a[8];
       uint32_t code[2];
       unpack8(v[i], a);
-      if constexpr (KIND == kQE4M3) {
-        fakequant_e4m3_codes<8, true>(a, s, code);
-      } else {
-        float x[8];
-        act_quotients<8>(a, s, x);
-        code[0] = code[1] = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float q = q_int8(x[j]);
-          code[j / 4] |= ((uint32_t)(int)q & 0xffu) << (8 * (j % 4));
-          a[j] = __fmul_rn(copysignf(q, x[j]), s);
-        }
-      }
+      quantize4<KIND>(a, s, code[0]);
+      quantize4<KIND>(a + 4, s, code[1]);
       if (p.codes) reinterpret_cast<uint2*>(p.codes + row * p.d)[c] = make_uint2(code[0], code[1]);
       if (p.y_hat) reinterpret_cast<uint4*>(p.y_hat + row * p.d)[c] = pack8(a);
     }
@@ -319,14 +445,20 @@ __global__ void __launch_bounds__(1024) rmsnorm_dgamma_kernel(const float* __res
   if (lane == 0 && cw < d) dgamma[cw] = v;
 }
 
+template <int G>
+cudaError_t fwd_warp(const NormFwd& p, int kind, cudaStream_t st) {
+  const unsigned blocks = (unsigned)((p.T + 3) / 4);
+  if (kind == kQE4M3) rmsnorm_fwd_warp_kernel<G, kQE4M3><<<blocks, 128, 0, st>>>(p);
+  else if (kind == kQInt8) rmsnorm_fwd_warp_kernel<G, kQInt8><<<blocks, 128, 0, st>>>(p);
+  else rmsnorm_fwd_warp_kernel<G, kQNone><<<blocks, 128, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <int VPL, int W>
-cudaError_t fwd_kind(const NormFwd& p, int kind, cudaStream_t st) {
-  constexpr int RB = W > 4 ? 1 : 4 / W;
-  const int64_t blocks = (p.T + RB - 1) / RB;
-  const int threads = W > 4 ? 32 * W : 128;
-  if (kind == kQE4M3) rmsnorm_fwd_kernel<VPL, W, kQE4M3><<<(unsigned)blocks, threads, 0, st>>>(p);
-  else if (kind == kQInt8) rmsnorm_fwd_kernel<VPL, W, kQInt8><<<(unsigned)blocks, threads, 0, st>>>(p);
-  else rmsnorm_fwd_kernel<VPL, W, kQNone><<<(unsigned)blocks, threads, 0, st>>>(p);
+cudaError_t fwd_wide(const NormFwd& p, int kind, cudaStream_t st) {
+  if (kind == kQE4M3) rmsnorm_fwd_kernel<VPL, W, kQE4M3><<<(unsigned)p.T, 32 * W, 0, st>>>(p);
+  else if (kind == kQInt8) rmsnorm_fwd_kernel<VPL, W, kQInt8><<<(unsigned)p.T, 32 * W, 0, st>>>(p);
+  else rmsnorm_fwd_kernel<VPL, W, kQNone><<<(unsigned)p.T, 32 * W, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -365,17 +497,18 @@ cudaError_t launch_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int6
   p.nv = (int)(d / 8);
   p.d = (int)d;
   p.eps = eps;
+  p.inv_d = 1.0f / (float)d;
   prof_begin(QAD_K_RMSNORM, st);
-  const int lanes1 = (p.nv + 31) / 32;  // vectors per lane with one warp per row
+  const int groups = (int)((d + 127) / 128);  // 4-element groups per lane of a warp
   cudaError_t e;
-  if (lanes1 <= 1) e = fwd_kind<1, 1>(p, kind, st);
-  else if (lanes1 <= 2) e = fwd_kind<2, 1>(p, kind, st);
-  else if (lanes1 <= 4) e = fwd_kind<4, 1>(p, kind, st);
-  else if (lanes1 <= 8) e = fwd_kind<2, 4>(p, kind, st);
-  else if (lanes1 <= 12) e = fwd_kind<3, 4>(p, kind, st);
-  else if (lanes1 <= 16) e = fwd_kind<4, 4>(p, kind, st);
-  else if (lanes1 <= 32) e = fwd_kind<8, 4>(p, kind, st);
-  else e = fwd_kind<8, 8>(p, kind, st);
+  if (groups <= 2) e = fwd_warp<2>(p, kind, st);
+  else if (groups <= 4) e = fwd_warp<4>(p, kind, st);
+  else if (groups <= 8) e = fwd_warp<8>(p, kind, st);
+  else if (groups <= 16) e = fwd_wide<2, 4>(p, kind, st);
+  else if (groups <= 24) e = fwd_wide<3, 4>(p, kind, st);
+  else if (groups <= 32) e = fwd_wide<4, 4>(p, kind, st);
+  else if (groups <= 64) e = fwd_wide<8, 4>(p, kind, st);
+  else e = fwd_wide<8, 8>(p, kind, st);
   prof_end(QAD_K_RMSNORM, st);
   return e;
 }
