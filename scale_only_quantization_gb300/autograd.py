@@ -10,10 +10,16 @@ and ds13 / ds2 for the scales.
 Marshalling only: the forward is qad_moe_fwd, the backward qad_moe_bwd_dgrad followed by
 qad_moe_bwd_scalegrad, all on torch's current stream.  The workspace, which carries the
 stashed stages from the forward to the backward, lives in the autograd context.
+
+What stands around the layer in a training step: QADRMSNorm (residual addition, norm and the 8-bit
+form of its output) before it, QADHeadLoss (cross entropy and distillation on the frozen head) at the
+end.
 """
 import torch
 
-from . import (qad_moe_bwd_dgrad, qad_moe_bwd_scalegrad, qad_moe_fwd, qad_moe_workspace_bytes, shape)
+from . import (QAD_ACT_NONE, qad_distill_topk_fwd_bwd, qad_linear_ce_fwd_bwd, qad_linear_ce_workspace_bytes,
+               qad_moe_bwd_dgrad, qad_moe_bwd_scalegrad, qad_moe_fwd, qad_moe_workspace_bytes, qad_rmsnorm_bwd,
+               qad_rmsnorm_fwd, qad_rmsnorm_workspace_bytes, shape)
 
 
 class QADMoEFunction(torch.autograd.Function):
@@ -72,3 +78,159 @@ class QADMoE(torch.nn.Module):
     def forward(self, x, topk_idx, topk_w):
         return QADMoEFunction.apply(x.contiguous(), topk_idx.contiguous(), topk_w.contiguous(), self.w13, self.s13,
                                     self.w2, self.s2, self.fmt, self.flags)
+
+
+def _rows(t, d, what):
+    """t as [rows, d] bf16 rows that the library can read: unit column stride, 16-byte aligned rows."""
+    if t.dtype != torch.bfloat16 or t.shape[-1] != d:
+        raise ValueError("%s must be bf16 with %d columns, got %s %s" % (what, d, t.dtype, tuple(t.shape)))
+    t = t.reshape(-1, d)
+    if t.stride(1) != 1 or t.stride(0) % 8 or t.stride(0) < d or t.data_ptr() % 16:
+        t = t.contiguous()
+    return t
+
+
+class QADRMSNormFunction(torch.autograd.Function):
+    """(y, r, codes, scale) = residual addition + RMSNorm of x with the per-row activation quantizer `act`.
+
+    r = bf16(x + res) is the residual stream; y = bf16(r * rstd * gamma) is what the router and the layer
+    read; codes [.., d] uint8 and scale [rows] fp32 are its 8-bit form (None with QAD_ACT_NONE).  The
+    backward is straight through the quantizer: dx for x and res, dgamma.
+    """
+
+    @staticmethod
+    def forward(ctx, x, res, gamma, eps, act):
+        d = gamma.numel()
+        x2 = _rows(x, d, "x")
+        res2 = None if res is None else _rows(res, d, "res")
+        if res2 is not None and res2.shape != x2.shape:
+            raise ValueError("x and res differ in shape")
+        T = x2.shape[0]
+        dev = x.device
+        r = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+        y = torch.empty_like(r)
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        codes = torch.empty((T, d), dtype=torch.uint8, device=dev) if act != QAD_ACT_NONE else None
+        scale = torch.empty(T, dtype=torch.float32, device=dev) if act != QAD_ACT_NONE else None
+        gamma = gamma.contiguous()
+        qad_rmsnorm_fwd(x2, res2, gamma, eps, act, r, y, None, codes, scale, rstd, T, d, x2.stride(0) if T > 1 else d,
+                        res2.stride(0) if res2 is not None and T > 1 else d)
+        ctx.save_for_backward(r, gamma, rstd)
+        ctx.has_res = res is not None
+        ctx.shape = x.shape
+        if codes is not None:
+            ctx.mark_non_differentiable(codes, scale)
+            codes = codes.view(x.shape)
+        return y.view(x.shape), r.view(x.shape), codes, scale
+
+    @staticmethod
+    def backward(ctx, dy, dr, _codes, _scale):
+        r, gamma, rstd = ctx.saved_tensors
+        T, d = r.shape
+        dy2 = (torch.zeros_like(r) if dy is None else dy).reshape(T, d).contiguous()
+        dr2 = None if dr is None else dr.reshape(T, d).contiguous()
+        dx = torch.empty_like(r)
+        need = ctx.needs_input_grad[2]
+        dgamma = torch.empty(d, dtype=torch.float32, device=r.device) if need else None
+        ws = torch.empty(qad_rmsnorm_workspace_bytes(T, d), dtype=torch.uint8, device=r.device) if need else None
+        qad_rmsnorm_bwd(dy2, dr2, r, gamma, rstd, dx, dgamma, T, d, d, ws)
+        dx = dx.view(ctx.shape)
+        return dx, dx if ctx.has_res else None, dgamma.to(gamma.dtype) if need else None, None, None
+
+
+class QADRMSNorm(torch.nn.Module):
+    """RMSNorm before a quantized layer: forward(x, res=None) -> (y, r), or (y, r, codes, scale) with a per-row
+    activation grid (QAD_ACT_E4M3, QAD_ACT_INT8).  The weight is kept in high precision; frozen unless trained."""
+
+    def __init__(self, weight, eps=1e-6, act=QAD_ACT_NONE, trained=False):
+        super().__init__()
+        self.weight = torch.nn.Parameter(weight.to(torch.bfloat16).contiguous(), requires_grad=trained)
+        self.eps = float(eps)
+        self.act = int(act)
+
+    def forward(self, x, res=None):
+        y, r, codes, scale = QADRMSNormFunction.apply(x, res, self.weight, self.eps, self.act)
+        return (y, r) if self.act == QAD_ACT_NONE else (y, r, codes, scale)
+
+
+class QADHeadLossFunction(torch.autograd.Function):
+    """total = sum_i g_lm[i] * CE_i + sum_i g_kd[i] * KD_i of hidden states h against the frozen head w.
+
+    CE_i is the cross entropy over the whole vocabulary (rows with target < 0 carry none), KD_i the
+    divergence over the teacher's top tokens idx [N, K] with logits t [N, K], softened by tau, mixed
+    forward and reverse by mix [N] (None: forward).  Either part is left out when its target or idx is
+    None.  The hidden-state gradient is formed in the forward, where the logits are, and scaled by the
+    upstream gradient in the backward.  Returns (total, CE [N] or None, KD [N] or None).
+    """
+
+    @staticmethod
+    def forward(ctx, h, w, target, g_lm, idx, t, g_kd, tau, mix):
+        V, d = w.shape
+        if w.dtype != torch.bfloat16 or not w.is_contiguous():
+            raise ValueError("the head must be a contiguous bf16 [V, d]")
+        h2 = _rows(h, d, "h")
+        N, dev = h2.shape[0], h.device
+        ld = h2.stride(0) if N > 1 else d
+        dh = torch.empty((N, d), dtype=torch.bfloat16, device=dev)
+        total = torch.zeros((), dtype=torch.float32, device=dev)
+        ce = kd = None
+        if target is not None:
+            target = target.reshape(-1).to(torch.int32).contiguous()
+            g_lm = g_lm.to(torch.float32).contiguous()
+            if target.numel() != N or g_lm.numel() != N:
+                raise ValueError("one target and one weight per row of h")
+            ce, lse = torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev)
+            ws = torch.empty(qad_linear_ce_workspace_bytes(N, d, V, 1, 0), dtype=torch.uint8, device=dev)
+            qad_linear_ce_fwd_bwd(h2, ld, w, d, target, g_lm, ce, lse, dh, None, 0, N, d, V, ws)
+            total = total + torch.dot(ce, g_lm)
+        if idx is not None:
+            K = idx.shape[-1]
+            idx = idx.reshape(N, K).to(torch.int32).contiguous()
+            t = t.reshape(N, K).to(torch.float32).contiguous()
+            g_kd = g_kd.to(torch.float32).contiguous()
+            mix = None if mix is None else mix.to(torch.float32).contiguous()
+            if g_kd.numel() != N or (mix is not None and mix.numel() != N):
+                raise ValueError("one distillation weight (and mix) per row of h")
+            kd = torch.empty(N, dtype=torch.float32, device=dev)
+            qad_distill_topk_fwd_bwd(h2, ld, w, d, idx, t, mix, 1.0 / tau, g_kd, kd, dh, int(target is not None), N, d, V,
+                                     K)
+            total = total + torch.dot(kd, g_kd)
+        if target is None and idx is None:
+            raise ValueError("neither targets nor teacher logits")
+        ctx.save_for_backward(dh)
+        ctx.shape = h.shape
+        ctx.mark_non_differentiable(*[x for x in (ce, kd) if x is not None])
+        return total, ce, kd
+
+    @staticmethod
+    def backward(ctx, dtotal, _ce, _kd):
+        (dh,) = ctx.saved_tensors
+        return ((dh * dtotal).to(torch.bfloat16).view(ctx.shape), None, None, None, None, None, None, None, None)
+
+
+class QADHeadLoss(torch.nn.Module):
+    """The loss of a scale-only QAD step on the frozen output head (AngelSlim mcore_qad walkthrough,
+    section 二.5): total = lm_weight * lm + distill_weight * distill, each a mean over its tokens.
+
+    forward(h, target=None, teacher_idx=None, teacher_logits=None, mix=None) -> (total, lm, distill): lm is
+    the cross entropy over the rows with a target, distill the divergence over the teacher's top tokens.
+    """
+
+    def __init__(self, w, lm_weight=1.0, distill_weight=1.0, tau=1.0):
+        super().__init__()
+        self.register_buffer("w", w.to(torch.bfloat16).contiguous())
+        self.lm_weight, self.distill_weight, self.tau = float(lm_weight), float(distill_weight), float(tau)
+
+    def forward(self, h, target=None, teacher_idx=None, teacher_logits=None, mix=None):
+        N = h.numel() // h.shape[-1]
+        one = torch.ones(N, dtype=torch.float32, device=h.device)
+        g_lm = g_kd = None
+        if target is not None:
+            live = (target.reshape(-1) >= 0).to(torch.float32)
+            g_lm = live * (self.lm_weight / live.sum().clamp_min(1.0))
+        if teacher_idx is not None:
+            g_kd = one * (self.distill_weight / max(N, 1))
+        total, ce, kd = QADHeadLossFunction.apply(h, self.w, target, g_lm, teacher_idx, teacher_logits, g_kd, self.tau,
+                                                  mix)
+        lm = None if ce is None else ce.sum() / live.sum().clamp_min(1.0)
+        return total, lm, None if kd is None else kd.mean()

@@ -1,0 +1,153 @@
+"""The autograd views of the norm and the head loss, and the example that trains a small model with them."""
+import os
+import sys
+
+import pytest
+import torch
+
+import scale_only_quantization_gb300 as Q
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+
+
+def _build():
+    from scale_only_quantization_gb300 import build
+    build.build()
+
+
+def test_modules_hold_frozen_weights():
+    from scale_only_quantization_gb300.autograd import QADHeadLoss, QADRMSNorm
+    n = QADRMSNorm(torch.ones(64))
+    assert not n.weight.requires_grad and n.weight.dtype == torch.bfloat16
+    assert QADRMSNorm(torch.ones(64), trained=True).weight.requires_grad
+    h = QADHeadLoss(torch.randn(10, 64))
+    assert list(h.parameters()) == [] and h.w.dtype == torch.bfloat16
+
+
+def test_rows_are_checked():
+    from scale_only_quantization_gb300.autograd import _rows
+    x = torch.zeros((6, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        _rows(x.float(), 64, "x")
+    with pytest.raises(ValueError):
+        _rows(x, 32, "x")
+    assert _rows(x[:, 8:40], 32, "x").stride(0) == 64            # a slice of aligned rows is read in place
+    assert _rows(x[:, 1:33], 32, "x").is_contiguous()            # an unaligned one is copied
+    assert _rows(x.t()[:, :6], 6, "x").is_contiguous()
+    assert _rows(x.view(2, 3, 64), 64, "x").shape == (6, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [Q.QAD_ACT_NONE, Q.QAD_ACT_E4M3])
+def test_norm_gradients_equal_the_abi_calls(act):
+    from scale_only_quantization_gb300.autograd import QADRMSNorm
+    _build()
+    T, d = 50, 272
+    bf = torch.bfloat16
+    x, res, dy, dr = (torch.randn((2, T // 2, d), device="cuda").to(bf) for _ in range(4))
+    n = QADRMSNorm(1 + 0.1 * torch.randn(d, device="cuda"), act=act, trained=True)
+    x.requires_grad_(True)
+    res.requires_grad_(True)
+    out = n(x, res)
+    torch.autograd.backward([out[0], out[1]], [dy, dr])
+    r, y = torch.empty((T, d), dtype=bf, device="cuda"), torch.empty((T, d), dtype=bf, device="cuda")
+    rstd = torch.empty(T, device="cuda")
+    Q.qad_rmsnorm_fwd(x.detach(), res.detach(), n.weight.detach(), 1e-6, 0, r, y, None, None, None, rstd, T, d, d, d)
+    dx, dg = torch.empty_like(r), torch.empty(d, device="cuda")
+    ws = torch.empty(Q.qad_rmsnorm_workspace_bytes(T, d), dtype=torch.uint8, device="cuda")
+    Q.qad_rmsnorm_bwd(dy, dr, r, n.weight.detach(), rstd, dx, dg, T, d, d, ws)
+    assert torch.equal(out[0].view(T, d), y) and torch.equal(out[1].view(T, d), r)
+    assert torch.equal(x.grad.view(T, d), dx) and torch.equal(res.grad.view(T, d), dx)
+    assert torch.equal(n.weight.grad, dg.to(bf))
+    if act:
+        assert out[2].shape == x.shape and out[3].shape == (T,)
+
+
+@pytest.mark.gpu
+def test_head_loss_against_torch():
+    """total, its parts and dh against fp64 torch autograd of the same definition; dh within its bf16 roundings (of the
+    softmax, of each part's sum and of their total: 4 x 2^-8 of the terms' size)."""
+    from scale_only_quantization_gb300.autograd import QADHeadLoss
+    _build()
+    N, d, V, K = 60, 128, 900, 16
+    bf = torch.bfloat16
+    w = (torch.randn((V, d), device="cuda") * d ** -0.5).to(bf)
+    h = torch.randn((N, d), device="cuda").to(bf).requires_grad_(True)
+    target = torch.randint(0, V, (N,), device="cuda")
+    target[:7] = -1
+    idx = torch.stack([torch.randperm(V, device="cuda")[:K] for _ in range(N)]).to(torch.int32)
+    t = torch.randn((N, K), device="cuda") * 2
+    loss = QADHeadLoss(w, lm_weight=0.3, distill_weight=0.7, tau=2.0)
+    total, lm, kd = loss(h, target, idx, t)
+    (3.0 * total).backward()
+    h64 = h.detach().double().requires_grad_(True)
+    z = h64 @ w.double().T
+    live = target >= 0
+    lm64 = torch.nn.functional.cross_entropy(z[live], target[live])
+    lq = torch.log_softmax(z.gather(1, idx.long()) / 2, 1)
+    lp = torch.log_softmax(t.double() / 2, 1)
+    kd64 = (lp.exp() * (lp - lq)).sum(1).mean()
+    tot64 = 0.3 * lm64 + 0.7 * kd64
+    (3.0 * tot64).backward()
+    for a, b in ((lm, lm64), (kd, kd64), (total, tot64)):
+        assert abs(float((a - b).detach())) < 1e-5
+    size = (3 * (0.3 / 53 + 0.7 / N)) * w.double().abs().amax(0)
+    assert torch.all((h.grad.double() - h64.grad).abs() <= 4 * 2.0 ** -8 * (h64.grad.abs() + size))
+    # either part alone
+    only = QADHeadLoss(w)(h.detach(), target)
+    assert only[2] is None and abs(float((only[1] - lm64).detach())) < 1e-5
+    only = QADHeadLoss(w, tau=2.0)(h.detach(), None, idx, t)
+    assert only[1] is None and abs(float((only[2] - kd64).detach())) < 1e-5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [Q.QAD_FMT_NVFP4, Q.QAD_FMT_INT4_G128])
+def test_example_trains_the_scales(fmt):
+    """The divergence from the unquantized model falls when only the scales move (4-bit weights: 8-bit ones start
+    within the noise of a few tokens routed otherwise)."""
+    _build()
+    import qad_step
+    hist = qad_step.train(fmt, steps=12, tokens=256, log=None)
+    kd = [h[2] for h in hist]
+    assert all(x == x and x < 1e3 for h in hist for x in h)
+    assert kd[0] > 0 and min(kd[-3:]) < 0.95 * kd[0]
+
+
+@pytest.mark.gpu
+def test_norm_and_losses_in_a_cuda_graph():
+    """The calls allocate nothing and read nothing back: a captured step replays with the same results."""
+    _build()
+    N, d, V, K = 200, 256, 3000, 16
+    bf = torch.bfloat16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x, w, gamma = rand(N, d).to(bf), (rand(V, d) * d ** -0.5).to(bf), (1 + 0.1 * rand(d)).to(bf)
+    target = torch.randint(0, V, (N,), generator=g, device="cuda").to(torch.int32)
+    idx = torch.randint(0, V, (N, K), generator=g, device="cuda").to(torch.int32)
+    t = rand(N, K)
+    y, dh = torch.empty_like(x), torch.empty_like(x)
+    ce, lse, kd = (torch.empty(N, device="cuda") for _ in range(3))
+    ws = torch.empty(Q.qad_linear_ce_workspace_bytes(N, d, V, 1, 0), dtype=torch.uint8, device="cuda")
+
+    def step():
+        Q.qad_rmsnorm_fwd(x, None, gamma, 1e-6, 0, None, y, None, None, None, None, N, d, d, d)
+        Q.qad_linear_ce_fwd_bwd(y, d, w, d, target, None, ce, lse, dh, None, 0, N, d, V, ws)
+        Q.qad_distill_topk_fwd_bwd(y, d, w, d, idx, t, None, 1.0, None, kd, dh, 1, N, d, V, K)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    ref = [v.clone() for v in (y, ce, lse, kd, dh)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for v in (y, ce, lse, kd, dh):
+        v.fill_(0)
+    graph.replay()
+    torch.cuda.synchronize()
+    for v, r in zip((y, ce, lse, kd, dh), ref):
+        assert torch.equal(v, r)
