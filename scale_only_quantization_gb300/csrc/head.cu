@@ -44,7 +44,7 @@ struct HeadParams {
   int32_t* err;
   int mt, nt, num_kb;   // tiles along the output's rows and columns, K blocks
   int n_fast;           // tile order: columns fastest
-  int split;            // the pairs share out all K blocks evenly, tiles cut where a share ends (U)
+  int split;            // slabs of K blocks that are contracted apart (U; else 1)
   int a_row0, b_row0;   // first row of the A / B tensors of this piece
   int64_t N;            // token rows
   // logits: columns c0 .. c0 + cols of the vocabulary
@@ -56,9 +56,7 @@ struct HeadParams {
   int part0;                    // first part of this piece
   int store_p;
   __nv_bfloat16* p;             // transposed logits: e [piece, kFewRows]
-  // U [N, d]: a tile's first segment; its others in `rest`, a tile of 256 x TN per pair (only the first tile of a
-  // pair's share can have begun in another's)
-  float *u, *rest;
+  float* u;  // U: partial sums [slab, N, d]
   int d, add;
 };
 
@@ -96,54 +94,21 @@ __device__ __forceinline__ HTile htile(const HeadParams& p, int t) {
   return x;
 }
 
-// A split contraction.  As many whole rounds of tiles as there are, one tile per pair at a time and all
-// at the same K block (they share their operands in L2); the K blocks of the `rest` tiles that do not
-// fill a round are shared out evenly over the pairs (over as many as there are blocks): pair i takes
-// [i * all / pairs, (i + 1) * all / pairs) of all = rest * num_kb.  The segments of such a tile are numbered from the first pair that touches
-// it.  (Shared out evenly from the start, the pairs run at different K blocks and re-read the operands
-// from HBM: 6.75 against 6.43 ms for the 8192 x 2048 x 151936 step unsplit.)
-__host__ __device__ inline int64_t split_pairs(int64_t num_kb, int64_t rest, int64_t pairs) {
-  return rest * num_kb < pairs ? rest * num_kb : pairs;
-}
-__host__ __device__ inline int64_t split_first(int64_t rest_tile, int64_t num_kb, int64_t rest, int64_t pairs) {
-  return ((rest_tile * num_kb + 1) * pairs - 1) / (rest * num_kb);  // the largest pair whose share starts at or before it
-}
-__host__ __device__ inline int64_t split_last(int64_t rest_tile, int64_t num_kb, int64_t rest, int64_t pairs) {
-  return ((rest_tile + 1) * num_kb * pairs - 1) / (rest * num_kb);
-}
-
-// The tiles, or parts of tiles, of one pair: every role of the CTA walks the same sequence.
+// The tiles of one pair, or, where the contraction is split, its slabs of tiles: every role of the CTA walks
+// the same sequence.  Slab s covers the K blocks [s num_kb / split, (s + 1) num_kb / split); the pairs take
+// all tiles of a slab before the next one's, so that those running together read the same K blocks of
+// both operands from L2.
 struct Walk {
-  int tile, kb0, kb1, seg;
-  int next_tile, whole, pairs, pair, sharers;  // whole: tiles that are not split; sharers: pairs that share the others
-  int64_t at, end;                    // this pair's share of the rest, in K blocks
-  __device__ __forceinline__ Walk(const HeadParams& p, int pair_, int pairs_) : pairs(pairs_), pair(pair_) {
-    const int tiles = p.mt * p.nt, rest = p.split ? tiles % pairs : 0;
-    whole = tiles - rest;
-    next_tile = pair;
-    sharers = (int)split_pairs(p.num_kb, rest, pairs);
-    at = end = 0;
-    if (pair < sharers) {
-      at = (int64_t)pair * rest * p.num_kb / sharers;
-      end = (int64_t)(pair + 1) * rest * p.num_kb / sharers;
-    }
-  }
+  int tile, kb0, kb1, slab;
+  int at, step, tiles;
+  __device__ __forceinline__ Walk(const HeadParams& p, int pair, int pairs) : at(pair), step(pairs), tiles(p.mt * p.nt) {}
   __device__ __forceinline__ bool next(const HeadParams& p) {
-    if (next_tile < whole) {
-      tile = next_tile;
-      kb0 = 0;
-      kb1 = p.num_kb;
-      seg = 0;
-      next_tile += pairs;
-      return true;
-    }
-    if (at >= end) return false;
-    const int rt = (int)(at / p.num_kb);
-    tile = whole + rt;
-    kb0 = (int)(at - (int64_t)rt * p.num_kb);
-    kb1 = end - at < p.num_kb - kb0 ? kb0 + (int)(end - at) : p.num_kb;
-    seg = pair - (int)split_first(rt, p.num_kb, p.mt * p.nt - whole, sharers);
-    at += kb1 - kb0;
+    if (at >= tiles * p.split) return false;
+    slab = at / tiles;
+    tile = at - slab * tiles;
+    kb0 = (int)((int64_t)slab * p.num_kb / p.split);
+    kb1 = (int)((int64_t)(slab + 1) * p.num_kb / p.split);
+    at += step;
     return true;
   }
 };
@@ -308,12 +273,11 @@ __device__ __forceinline__ void epi_logits_t(const HeadParams& p, const float* t
   }
 }
 
-// Row dd (a column of U) of 64 tokens: U^T += W^T e, this segment's partial sums, fp32
-__device__ __forceinline__ void epi_u_t(const HeadParams& p, const HTile& ti, int seg, int pair, int rank,
-                                        uint32_t tbase, int q, int lane, int half) {
-  const int dt = rank * BM + 32 * q + lane, dd = ti.mb * kTile + dt;
-  float* u = seg == 0 ? p.u + dd : p.rest + (int64_t)pair * kTile * kFewRows + dt;
-  const int64_t pitch = seg == 0 ? p.d : kTile;
+// Row dd (a column of U) of 64 tokens: U^T += W^T e, this slab's partial sums, fp32
+__device__ __forceinline__ void epi_u_t(const HeadParams& p, const HTile& ti, int slab, int rank, uint32_t tbase, int q,
+                                        int lane, int half) {
+  const int dd = ti.mb * kTile + rank * BM + 32 * q + lane;
+  float* u = p.u + (int64_t)slab * p.N * p.d + dd;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int n0 = 64 * half + 32 * c;
@@ -324,7 +288,7 @@ __device__ __forceinline__ void epi_u_t(const HeadParams& p, const HTile& ti, in
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       if (n0 + i >= p.N || dd >= p.d) continue;
-      float* at = u + (n0 + i) * pitch;
+      float* at = u + (int64_t)(n0 + i) * p.d;
       *at = __uint_as_float(r[i]) + (p.add ? *at : 0.0f);
     }
     __syncwarp();  // the next tensor-memory load is the whole warp's
@@ -342,13 +306,12 @@ __device__ __forceinline__ void st_f32x8(float* p, const float (&v)[8]) {
                : "memory");
 }
 
-// Row r's 128 columns of U += e W, this segment's partial sums, fp32 in global memory
-__device__ __forceinline__ void epi_u(const HeadParams& p, const HTile& ti, int seg, int pair, int rank, uint32_t tbase,
-                                      int q, int lane, int half) {
-  const int rt = rank * BM + 32 * q + lane;
-  const int64_t row = (int64_t)ti.mb * kTile + rt;
+// Row r's 128 columns of U += e W, this slab's partial sums, fp32 in global memory
+__device__ __forceinline__ void epi_u(const HeadParams& p, const HTile& ti, int slab, int rank, uint32_t tbase, int q,
+                                      int lane, int half) {
+  const int64_t row = ti.mb * kTile + rank * BM + 32 * q + lane;
   const int col0 = ti.nb * kTile + half * 128;
-  float* to = seg == 0 ? p.u + row * p.d + col0 : p.rest + ((int64_t)pair * kTile + rt) * kTile + half * 128;
+  float* to = p.u + ((int64_t)slab * p.N + row) * p.d + col0;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32];
@@ -568,9 +531,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
       tc_fence_after();
       const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * TN);
       if constexpr (MODE == M_LOGITS) epi_logits(p, &tmC, ti, (int)rank, tbase, q, lane, half, my_stage, buf);
-      else if constexpr (MODE == M_U) epi_u(p, ti, wk.seg, pair, (int)rank, tbase, q, lane, half);
+      else if constexpr (MODE == M_U) epi_u(p, ti, wk.slab, (int)rank, tbase, q, lane, half);
       else if constexpr (MODE == M_LOGITS_T) epi_logits_t(p, tok, ti, (int)rank, tbase, q, lane, half, sums, tops);
-      else if constexpr (MODE == M_U_T) epi_u_t(p, ti, wk.seg, pair, (int)rank, tbase, q, lane, half);
+      else if constexpr (MODE == M_U_T) epi_u_t(p, ti, wk.slab, (int)rank, tbase, q, lane, half);
       else epi_dw(p, &tmC, ti, (int)rank, tbase, q, lane, half, my_stage, buf);
       tc_fence_before();
       __syncwarp();
@@ -685,17 +648,8 @@ __global__ void __launch_bounds__(1024) ce_stats_kernel(const int32_t* gate, con
   tval[row] = live ? -gi * (s / total) : 0.0f;
 }
 
-// How the product with the head was split: its K blocks, tiles (row-major over token rows and columns, or
-// over columns alone when it was taken transposed), those that are whole, and the pairs that share the rest
-struct Segments {
-  int64_t num_kb, tiles, whole, pairs;
-  int nt, transposed;
-};
-
-// dh_i = mul_i U_i + tval_i w_t (+ dh_i), U_i the sum of its segments: one warp per row, a tile's 256
-// columns at a time
-__global__ void __launch_bounds__(128) ce_dh_kernel(const float* __restrict__ u, const float* __restrict__ rest,
-                                                    const Segments sg,
+// dh_i = mul_i U_i + tval_i w_t (+ dh_i), U_i the sum over the slabs: one warp per row
+__global__ void __launch_bounds__(128) ce_dh_kernel(const float* __restrict__ u, int slabs,
                                                     const __nv_bfloat16* __restrict__ w, int64_t ldw,
                                                     const int32_t* __restrict__ tcol, const float* __restrict__ mul,
                                                     const float* __restrict__ tval, int64_t N, int d, int accumulate,
@@ -707,20 +661,13 @@ __global__ void __launch_bounds__(128) ce_dh_kernel(const float* __restrict__ u,
   const float a = __ldg(mul + row), b = __ldg(tval + row);
   const uint4* wr = reinterpret_cast<const uint4*>(w + (int64_t)__ldg(tcol + row) * ldw);
   uint4* out = reinterpret_cast<uint4*>(dh + row * d);
-  for (int i = blockIdx.y; i * 256 < d; i += gridDim.y) {
-    const int c = 32 * i + lane;
-    const int64_t tile = sg.transposed ? i : (row / kTile) * sg.nt + i;
-    const int64_t rt = tile - sg.whole, rest_tiles = sg.tiles - sg.whole;
-    const int p0 = rt < 0 ? 0 : (int)split_first(rt, sg.num_kb, rest_tiles, sg.pairs);
-    const int p1 = rt < 0 ? 0 : (int)split_last(rt, sg.num_kb, rest_tiles, sg.pairs);
-    if (c >= d / 8) continue;
+  for (int c = 32 * blockIdx.y + lane; c < d / 8; c += 32 * gridDim.y) {
+    const float* ur = u + row * d + 8 * c;
     float x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8];
 #pragma unroll 4
-    for (int pr = p0; pr <= p1; ++pr) {
-      const float* at = pr == p0         ? u + row * d + 8 * c
-                        : sg.transposed ? rest + ((int64_t)pr * kFewRows + row) * kTile + 8 * lane
-                                        : rest + ((int64_t)pr * kTile + row % kTile) * kTile + 8 * lane;
-      const float4 u0 = reinterpret_cast<const float4*>(at)[0], u1 = reinterpret_cast<const float4*>(at)[1];
+    for (int s = 0; s < slabs; ++s) {
+      const float4* at = reinterpret_cast<const float4*>(ur + (int64_t)s * N * d);
+      const float4 u0 = at[0], u1 = at[1];
       x[0] += u0.x; x[1] += u0.y; x[2] += u0.z; x[3] += u0.w;
       x[4] += u1.x; x[5] += u1.y; x[6] += u1.z; x[7] += u1.w;
     }
@@ -791,7 +738,7 @@ cudaError_t launch_head(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
   cudaError_t e = cudaSuccess;
   const int most = head_pairs<MODE>(&e);
   if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)p.mt * p.nt * (p.split ? p.num_kb : 1);
+  const int64_t units = (int64_t)p.mt * p.nt * p.split;
   const int pairs = (int)(units < most ? units : most);
   if (used) *used = pairs;
   if (pairs < 1) return cudaSuccess;
@@ -802,7 +749,27 @@ cudaError_t launch_head(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
   return e;
 }
 
-constexpr size_t kPieceBytes = size_t(1000) << 20;  // bound on the stored piece of exp(logits)
+constexpr size_t kPieceBytes = size_t(832) << 20;  // bound on the stored piece of exp(logits)
+constexpr size_t kSlabBytes = size_t(192) << 20;   // and on the partial sums of U beyond the first
+
+// Slabs that the product with the head is split into: fewer tiles than SM pairs, or a last round of tiles
+// that fills few of them, leave pairs idle, which more and smaller units of work avoid; each slab is one
+// more fp32 [N, d] written and read.  Costs in K blocks of one pair; a written and read tile is worth about
+// kSlabCost of them.
+int choose_slabs(int64_t tiles, int64_t num_kb, int64_t N, int64_t d) {
+  constexpr double kSlabCost = 24.0;
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= 2 * kMaxPairs && s <= num_kb && (s == 1 || (s - 1) * 4.0 * N * d <= (double)kSlabBytes); ++s) {
+    const double rounds = (double)((tiles * s + kMaxPairs - 1) / kMaxPairs);
+    const double cost = rounds * ((double)num_kb / s + kSlabCost);
+    if (s == 1 || cost < 0.99 * least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
+}
 
 size_t align_up(size_t v) { return (v + 1023) / 1024 * 1024; }
 
@@ -820,6 +787,9 @@ int ce_layout_of(int64_t N, int64_t d, int64_t V, int grad, int dw, CeLayout* L)
   L->pieces = (int)cdiv(vt, most);
   L->piece = (int)(cdiv(vt, L->pieces) * kTile);
   L->pieces = (int)cdiv(V, L->piece);
+  const int64_t tiles = (few ? 1 : cdiv(N, kTile)) * cdiv(d, kTile);
+  const int64_t bke = few ? HCfg<M_U_T>::BKE : HCfg<M_U>::BKE;
+  L->slabs = tiles ? choose_slabs(tiles, cdiv(L->pieces > 1 ? L->piece : V, bke), N, d) : 1;
   L->parts = few ? L->pieces * kMaxPairs * 8 : (int)(2 * vt);
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes); return at; };
@@ -831,8 +801,7 @@ int ce_layout_of(int64_t N, int64_t d, int64_t V, int grad, int dw, CeLayout* L)
   L->tval = take(4 * (size_t)N);
   L->psum = take(4 * (size_t)width * L->parts);
   L->pmax = take(4 * (size_t)width * L->parts);
-  L->u = take(grad ? 4 * (size_t)(N * d) : 0);
-  L->rest = take(grad ? 4 * (size_t)kMaxPairs * kTile * (few ? kFewRows : kTile) : 0);
+  L->u = take(grad ? 4 * (size_t)L->slabs * (size_t)(N * d) : 0);
   L->p = take(grad || dw ? 2 * (size_t)width * L->piece : 0);
   L->total = o;
   return QAD_OK;
@@ -850,7 +819,6 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   float* psum = reinterpret_cast<float*>(ws + L.psum);
   float* pmax = reinterpret_cast<float*>(ws + L.pmax);
   float* u = reinterpret_cast<float*>(ws + L.u);
-  float* rest = reinterpret_cast<float*>(ws + L.rest);
   void* ep = ws + L.p;
   const auto* hb = static_cast<const __nv_bfloat16*>(h);
   const auto* wb = static_cast<const __nv_bfloat16*>(w);
@@ -883,6 +851,7 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   base.d = (int)d;
   base.ref = ref;
   base.target = tcol;
+  base.split = 1;
   int parts = 0;  // partial sums of the sweep so far
   auto logits = [&](int piece, const int32_t* gate, bool sums, bool store, bool final) -> cudaError_t {
     const int64_t c0 = (int64_t)piece * L.piece, cols = V - c0 < L.piece ? V - c0 : L.piece;
@@ -917,34 +886,28 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
     parts += 2 * p.nt;
     return launch_head<M_LOGITS>(tm_h, tm_w, tm_es, p, QAD_K_CE_LOGITS, st);
   };
-  Segments sg = {};
   auto product = [&](int piece, const int32_t* gate) -> cudaError_t {
     const int64_t c0 = (int64_t)piece * L.piece;
-    // every piece is contracted over the same number of K blocks, so that their segments are the same: the
-    // last one's rows of the head past V read as zeros
+    // every piece is contracted over the same number of K blocks, so that its slabs are the same: the last
+    // one's rows of the head past V read as zeros
     const int64_t cols = L.pieces > 1 ? L.piece : V;
     HeadParams q = base;
     q.gate = gate;
     q.nt = few ? 1 : (int)cdiv(d, kTile);
     q.mt = few ? (int)cdiv(d, kTile) : (int)cdiv(N, kTile);
     q.n_fast = 1;
-    q.split = 1;
+    q.split = L.slabs;
     q.u = u;
-    q.rest = rest;
     q.add = c0 > 0;
     q.num_kb = (int)cdiv(cols, few ? HCfg<M_U_T>::BKE : HCfg<M_U>::BKE);
-    int pairs = 0;
     cudaError_t e;
     if (few) {
       q.a_row0 = (int)c0;
-      e = launch_head<M_U_T>(tm_wu, tm_e, tm_e, q, QAD_K_CE_DH, st, &pairs);
+      e = launch_head<M_U_T>(tm_wu, tm_e, tm_e, q, QAD_K_CE_DH, st);
     } else {
       q.b_row0 = (int)c0;
-      e = launch_head<M_U>(tm_e, tm_wu, tm_e, q, QAD_K_CE_DH, st, &pairs);
+      e = launch_head<M_U>(tm_e, tm_wu, tm_e, q, QAD_K_CE_DH, st);
     }
-    const int64_t tiles = (int64_t)q.mt * q.nt;
-    const int64_t rest = tiles % pairs;
-    sg = {q.num_kb, tiles, tiles - rest, split_pairs(q.num_kb, rest, pairs), q.nt, few ? 1 : 0};
     return e;
   };
   // the sweep: exp(logits) of a piece, then its product with the piece of the head
@@ -968,9 +931,9 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   if ((e = stats(hdr + 1, 1)) != cudaSuccess) return e;
   if (dh) {
     note_launches(1);
-    // few rows: a block column per 256 columns, so that their segments are read side by side
+    // few rows: a block column per 256 columns, so that their slabs are read side by side
     const dim3 grid((unsigned)cdiv(N, 4), few ? (unsigned)cdiv(d, 256) : 1u, 1);
-    e = launch_dependent(ce_dh_kernel, grid, 128, 0, st, u, rest, sg, wb, ldw, tcol, mul, tval, N, (int)d, accumulate,
+    e = launch_dependent(ce_dh_kernel, grid, 128, 0, st, u, L.slabs, wb, ldw, tcol, mul, tval, N, (int)d, accumulate,
                          static_cast<__nv_bfloat16*>(dh));
     if (e != cudaSuccess) return e;
   }

@@ -138,8 +138,8 @@ cudaError_t launch_rmsnorm_bwd(const void* dy, const void* dres, const void* r, 
 // Byte offsets of its workspace; `piece`: columns of the vocabulary per piece, `parts`: partial
 // sums per row of a sweep at most
 struct CeLayout {
-  int piece, pieces, parts;
-  size_t header, ref, zt, tcol, mul, tval, psum, pmax, u, rest, p, total;
+  int piece, pieces, slabs, parts;  // slabs: partial sums of the product with the head
+  size_t header, ref, zt, tcol, mul, tval, psum, pmax, u, p, total;
 };
 int ce_layout_of(int64_t N, int64_t d, int64_t V, int grad, int dw, CeLayout* L);
 // loss and lse; dh / dw may be null; header words: [0] device errors, [1] a second sweep is needed
