@@ -17,7 +17,6 @@
 namespace qad {
 namespace {
 
-constexpr int kFwdThreads = 128;
 constexpr int kMaxStages = 16;  // ring of stages per team
 constexpr int kSlots = 3;       // token rows a team holds: being prepared, streamed, and having its loss taken
 constexpr size_t kMaxSmem = 220 * 1024;
@@ -138,17 +137,25 @@ struct DistillGrid {
 //   dh = beta g ((1 - m - m sbar) A0 / S + m A1 / S - (1 - m) B),
 //   A0 = sum e_k w_k, A1 = sum e_k s_k w_k, B = sum p_k w_k, e_k = exp(beta z_k - M), S = sum e_k,
 //   s_k = beta (z_k - t_k) up to a constant of the row, sbar = sum e_k s_k / S
-// is accumulated in fp32 while the rows stream past (x_k - RKL = s_k - sbar).  M is the first logit,
-// replaced (and the sums scaled) only by one more than kMaxAbove nats higher: e may exceed 1.
+// is accumulated in fp32 while the rows stream past (x_k - RKL = s_k - sbar).  M is the first batch's
+// largest logit, replaced (and the sums scaled) only by one more than kMaxAbove nats higher: e may
+// exceed 1.
 //
-// A team of CW consumer warps takes a token row: lane l of warp w owns V 16-byte vectors of the columns, 32 CW
-// apart.  A producer warp per team runs ahead: it makes the teacher's probabilities of a row, brings its
-// head rows two at a time into a ring of shared memory (one bulk copy per row) and, when a row is
-// through, takes its loss from the logits that the consumers left.  Per stage the consumers take the
-// rows into registers and free the stage, join their dot products (one shuffle reduction for both
-// rows, one named barrier of the team, none for CW = 1) and add the weighted rows to their sums.  A
-// stage is a chain of some 2000 cycles of waits and reductions, so several teams share an SM, each
-// with few registers: nothing is shared between teams.
+// A team of CW consumer warps takes a token row: lane l of warp w owns V 16-byte vectors of the columns,
+// 32 CW apart.  A producer warp per team runs ahead: it makes the teacher's probabilities of a row,
+// brings its head rows, R at a time, into a ring of shared memory (one bulk copy per row) and, when a
+// row is through, takes its loss from the logits that the consumers left.  Per stage the consumers take
+// the R rows into registers and free the stage, join their dot products (one shuffle reduction for all
+// R, one named barrier of the team, none for CW = 1) and add the weighted rows to their sums.
+//
+// What bounds it: the gathered rows come from HBM (a head of 152k rows does not stay in L2), and a stage is
+// a chain of some 2000 cycles of waits, reductions and exponentials, so that the bytes that the SM's
+// registers hold at once set the rate: two teams of 4 warps with 8 rows each (64 KB) reach 6.0 TB/s of
+// head rows at d = 2048, K = 64 (178 us for 4096 token rows); batches of 4 rows 206 us, 8-warp teams with
+// half the columns per lane 206 us.  One team of 8 warps takes d = 4096; with both divergences its third
+// sum leaves it at 4.4 TB/s (967 us for 16384 token rows, K = 32).  Reading the rows a second time from L2
+// for the gradient instead took 305 and 1240 us; matrix instructions (mma.sync, 8 rows a fragment) for both
+// products 234 and 1358 us, their rate on this chip being a few times the FMA units' only.
 template <int CW, int V, int R, bool MIX>
 __global__ void __launch_bounds__(32 * (teams_of<CW, V>() * (CW + 1)), 1)
     distill_kernel(const Distill p, const DistillGrid q, const int64_t N) {
@@ -477,8 +484,8 @@ cudaError_t launch_one(const Distill& p, int64_t N, cudaStream_t st) {
 // The loss alone: one block per row, one warp per head row, 8 vectors of it in flight per lane; no stage,
 // no barrier until the logits are there.  The partial sums are those of the teams above, in their order,
 // so that the loss has the same bits: warp i's vectors are i * 32 + lane + 32 CW j.
-template <int CW, int V>
-__global__ void __launch_bounds__(kFwdThreads, 8) distill_fwd_kernel(const Distill p) {
+template <int CW, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_fwd_kernel(const Distill p) {
   extern __shared__ __align__(128) uint8_t sm[];
   const int nv = p.d / 8, K = p.K;
   uint4* hs = reinterpret_cast<uint4*>(sm);
@@ -488,8 +495,8 @@ __global__ void __launch_bounds__(kFwdThreads, 8) distill_fwd_kernel(const Disti
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x;
   const uint4* hr = reinterpret_cast<const uint4*>(p.h + row * p.ldh);
-  for (int c = tid; c < nv; c += kFwdThreads) hs[c] = __ldg(hr + c);
-  for (int k = tid; k < K; k += kFwdThreads) {
+  for (int c = tid; c < nv; c += THREADS) hs[c] = __ldg(hr + c);
+  for (int k = tid; k < K; k += THREADS) {
     int32_t v = __ldg(p.idx + row * K + k);
     float t = __ldg(p.t + row * K + k) * p.beta;
     if (v >= p.V) {
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(kFwdThreads, 8) distill_fwd_kernel(const Disti
     ts[k] = t;
   }
   __syncthreads();
-  for (int k = warp; k < K; k += kFwdThreads / 32) {
+  for (int k = warp; k < K; k += THREADS / 32) {
     const int32_t v = tok[k];
     if (v < 0) continue;
     const uint4* wr = reinterpret_cast<const uint4*>(p.w + (int64_t)v * p.ldw);
@@ -551,7 +558,11 @@ template <int CW, int V, int R>
 cudaError_t launch_team(const Distill& p, int64_t N, cudaStream_t st) {
   if (p.dh) return p.mix ? launch_one<CW, V, R, true>(p, N, st) : launch_one<CW, V, R, false>(p, N, st);
   const size_t smem = (size_t)p.d * 2 + (size_t)p.K * 12;
-  distill_fwd_kernel<CW, V><<<(unsigned)N, kFwdThreads, smem, st>>>(p);
+  // rows that do not fill the SMs: 32 warps share a row's head rows instead of 4 (64 rows of K = 64, d = 2048: 10 us;
+  // one of K = 128, d = 4096: 19 us, with 4 warps 39); with more rows small blocks cover each other's ends better
+  // (1000 rows of K = 100, d = 2880: 87 us with 4 warps, 96 with 16)
+  if (N <= num_sms() && p.K > 4) distill_fwd_kernel<CW, V, 1024><<<(unsigned)N, 1024, smem, st>>>(p);
+  else distill_fwd_kernel<CW, V, 128><<<(unsigned)N, 128, smem, st>>>(p);
   return cudaGetLastError();
 }
 

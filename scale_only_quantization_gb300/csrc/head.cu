@@ -18,6 +18,12 @@
 // The products run on SM pairs (tcgen05 cta_group::2, 256 x 256 tiles) with the roles and
 // barriers of the grouped GEMMs: warp 0 of each CTA loads, warp 1 of the leader issues the MMAs,
 // warps 2-9 run the epilogue of one accumulator while the other is filled.
+//
+// What bounds it: the tensor cores from a few hundred token rows on (8192 x 2048 x 151936 with dh: 4 N V d
+// flop in 5.8 ms, 1.76 PFLOP/s; the logits kernel at 90% of the tensor pipe's cycles, its epilogue of 5500
+// cycles a tile under the 16400 of the tile's MMAs); below that the head's one reading per product (8 rows'
+// loss 111 us, 5.6 TB/s; with dh the head is read twice, 240 us).  At d = 256 the epilogue is longer than
+// the MMAs, and the launches of the short kernels weigh as much (512 x 256 x 32000: 51 us).
 #include <utility>
 
 #include "internal.h"
@@ -55,7 +61,8 @@ struct HeadParams {
   float *psum, *pmax;           // partial sums without the target / maxima, or null
   int part0;                    // first part of this piece
   int store_p;
-  __nv_bfloat16* p;             // transposed logits: e [piece, kFewRows]
+  __nv_bfloat16* p;             // e: [N, ldp], transposed [piece, kFewRows]
+  int64_t ldp;
   float* u;  // U: partial sums [slab, N, d]
   int d, add;
 };
@@ -74,7 +81,7 @@ template <int MODE> struct HCfg {
   static constexpr int A_BYTES = ATOMS * A_ATOM, B_BYTES = ATOMS * B_ATOM;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = (192 * 1024) / STAGE;
-  static constexpr bool BOXES = MODE == M_LOGITS || MODE == M_DW || MODE == M_DW_T;  // stores through TMA
+  static constexpr bool BOXES = MODE == M_DW || MODE == M_DW_T;  // stores through TMA
   static constexpr int STAGING = BOXES ? kEpiWarps * 4096 : MODE == M_LOGITS_T ? 4 * kFewRows * 4 : 0;
   static constexpr int SMEM = STAGES * STAGE + 512 + 1024 + STAGING;
 };
@@ -132,13 +139,17 @@ __device__ __forceinline__ void store_box32(const CUtensorMap* tm, uint32_t stag
   buf ^= 1u;
 }
 
+__device__ __forceinline__ void st_b32x8(uint32_t* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // Row r's 128 columns of a logits tile: e = exp(z - ref) (x factor), its sum without the target,
 // the largest logit, and the bf16 piece for the product that follows.
-__device__ __forceinline__ void epi_logits(const HeadParams& p, const CUtensorMap* tm, const HTile& ti, int rank,
-                                           uint32_t tbase, int q, int lane, int half, uint32_t stage_base,
-                                           uint32_t& buf) {
-  const int y = ti.mb * kTile + rank * BM + 32 * q;
-  const int64_t row = y + lane;
+__device__ __forceinline__ void epi_logits(const HeadParams& p, const HTile& ti, int rank, uint32_t tbase, int q,
+                                           int lane, int half) {
+  const int64_t row = ti.mb * kTile + rank * BM + 32 * q + lane;
   const bool live = row < p.N;
   const float ref = live ? __ldg(p.ref + row) : 0.0f;
   const float mul = live && p.mul ? __ldg(p.mul + row) : 1.0f;
@@ -195,7 +206,12 @@ __device__ __forceinline__ void epi_logits(const HeadParams& p, const CUtensorMa
       for (int i = 0; i < 32; i += 2)
         o[i / 2] = pack_bf16(__expf(__uint_as_float(r[i]) - ref) * mul, __expf(__uint_as_float(r[i + 1]) - ref) * mul);
     }
-    if (p.store_p && y < p.N) store_box32(tm, stage_base, buf, lane, out, col0 + 32 * c, y);
+    if (p.store_p && live) {  // two 32-byte sectors of the row
+      uint32_t* to = reinterpret_cast<uint32_t*>(p.p + row * p.ldp + col0 + 32 * c);
+      st_b32x8(to, out[0], out[1]);
+      st_b32x8(to + 8, out[2], out[3]);
+    }
+    __syncwarp();  // the next tensor-memory load is the whole warp's
     if (c < 3) {
       tmem_wait32(next);
 #pragma unroll
@@ -530,7 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * TN);
-      if constexpr (MODE == M_LOGITS) epi_logits(p, &tmC, ti, (int)rank, tbase, q, lane, half, my_stage, buf);
+      if constexpr (MODE == M_LOGITS) epi_logits(p, ti, (int)rank, tbase, q, lane, half);
       else if constexpr (MODE == M_U) epi_u(p, ti, wk.slab, (int)rank, tbase, q, lane, half);
       else if constexpr (MODE == M_LOGITS_T) epi_logits_t(p, tok, ti, (int)rank, tbase, q, lane, half, sums, tops);
       else if constexpr (MODE == M_U_T) epi_u_t(p, ti, wk.slab, (int)rank, tbase, q, lane, half);
@@ -826,10 +842,8 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   const int64_t width = few ? kFewRows : N;
   cudaError_t e = cudaSuccess;
   // operands K-major for the logits; the head MN-major for U; e [token, piece] or, transposed, [piece, token]
-  CUtensorMap tm_h, tm_w, tm_es, tm_e, tm_wu, tm_hd, tm_ed, tm_dw;
+  CUtensorMap tm_h, tm_w, tm_e, tm_wu, tm_hd, tm_ed, tm_dw;
   bool ok = make_tmap(&tm_h, h, d, N, ldh, few ? kFewRows / 2 : BM) && make_tmap(&tm_w, w, d, V, ldw, BM);
-  tm_es = tm_h;
-  if (ok && (dh || dw) && !few) ok = make_store_tmap(&tm_es, ep, L.piece, N, L.piece);
   if (ok && dh) {
     ok = make_tmap(&tm_wu, w, d, V, ldw, few ? HCfg<M_U_T>::BKE : HCfg<M_U>::BKE) &&
          (few ? make_tmap(&tm_e, ep, kFewRows, L.piece, kFewRows, HCfg<M_U_T>::BKE)
@@ -861,6 +875,8 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
     p.cols = (int)cols;
     p.num_kb = (int)cdiv(d, HCfg<M_LOGITS>::BKE);
     p.store_p = store;
+    p.p = static_cast<__nv_bfloat16*>(ep);
+    p.ldp = L.piece;
     if (sums) {
       p.psum = psum;
       p.pmax = pmax;
@@ -874,9 +890,8 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
       p.a_row0 = (int)c0;
       p.mt = (int)cdiv(cols, kTile);
       p.nt = 1;
-      p.p = static_cast<__nv_bfloat16*>(ep);
       int pairs = 0;
-      const cudaError_t e = launch_head<M_LOGITS_T>(tm_w, tm_h, tm_es, p, QAD_K_CE_LOGITS, st, &pairs);
+      const cudaError_t e = launch_head<M_LOGITS_T>(tm_w, tm_h, tm_h, p, QAD_K_CE_LOGITS, st, &pairs);
       parts += pairs * 8;
       return e;
     }
@@ -884,7 +899,7 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
     p.mt = (int)cdiv(N, kTile);
     p.nt = (int)cdiv(cols, kTile);
     parts += 2 * p.nt;
-    return launch_head<M_LOGITS>(tm_h, tm_w, tm_es, p, QAD_K_CE_LOGITS, st);
+    return launch_head<M_LOGITS>(tm_h, tm_w, tm_h, p, QAD_K_CE_LOGITS, st);
   };
   auto product = [&](int piece, const int32_t* gate) -> cudaError_t {
     const int64_t c0 = (int64_t)piece * L.piece;
