@@ -12,6 +12,7 @@
 // (6.1 TB/s), backward with the residual's gradient and dgamma 50 us for 268 MB (5.4 TB/s).
 #include "common.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
 
 namespace qad {
 namespace {
@@ -299,6 +300,8 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_fwd_kernel(const NormFwd p) {
   }
 }
 
+constexpr int kRing = 4;  // rows of the backward's ring
+
 struct NormBwd {
   const __nv_bfloat16 *dy, *dres, *r, *gamma;
   const float* rstd;
@@ -430,6 +433,152 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(const NormBwd p) {
   }
 }
 
+__device__ __forceinline__ void unpack_pairs(const uint4& u, uint64_t* f) {
+  f[0] = f2pack(bf16lo(u.x), bf16hi(u.x));
+  f[1] = f2pack(bf16lo(u.y), bf16hi(u.y));
+  f[2] = f2pack(bf16lo(u.z), bf16hi(u.z));
+  f[3] = f2pack(bf16lo(u.w), bf16hi(u.w));
+}
+
+// The same for rows of 513 to 4096 elements, with the rows ahead in shared memory: each group has a ring
+// of kRing rows of r, dy and dres, filled by bulk copies that its first lane issues one row after the
+// stage's last use (a row's barrier says that every warp is through with the row before).
+template <int VPL, int W, bool DRES>
+__global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd p) {
+  constexpr int RB = 8 / W, PARTS = DRES ? 3 : 2;
+  extern __shared__ __align__(128) uint4 ring_all[];
+  __shared__ float red[RB][2][W];
+  __shared__ __align__(8) uint64_t bars[RB][kRing];
+  __shared__ int abort_flag, late;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp / W, wr = warp % W, t = wr * 32 + lane;
+  const int64_t step = (int64_t)gridDim.x * RB, first = (int64_t)blockIdx.x * RB + grp;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4* ring = ring_all + (size_t)grp * kRing * PARTS * p.nv;
+  const bool leader = t == 0;
+  if (threadIdx.x == 0) abort_flag = late = 0;
+  if (leader) {
+    for (int s = 0; s < kRing; ++s) mbar_init(smem_u32(&bars[grp][s]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t bytes = (uint32_t)p.d * 2u;
+  auto fill = [&](int stage, int64_t row) {  // the leader's
+    const uint32_t bar = smem_u32(&bars[grp][stage]);
+    mbar_expect_tx(bar, PARTS * bytes);
+    const __nv_bfloat16* src[3] = {p.r + row * p.ldr, p.dy + row * p.d, DRES ? p.dres + row * p.d : nullptr};
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              smem_u32(ring + (size_t)(stage * PARTS + i) * p.nv)),
+          "l"(reinterpret_cast<uint64_t>(src[i])), "r"(bytes), "r"(bar)
+          : "memory");
+  };
+  if (leader)
+    for (int s = 0; s < kRing; ++s)
+      if (first + s * step < p.T) fill(s, first + s * step);
+  uint64_t gm[VPL][4], dg[VPL][4];  // pairs of columns: packed fp32 arithmetic
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = i * 32 * W + t;
+    unpack_pairs(c < p.nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma) + c) : zero, gm[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dg[i][j] = f2pack(0.0f, 0.0f);
+  }
+  int stage = 0, flip = 0;
+  uint32_t phase = 0;
+  for (int64_t row = first; row < p.T; row += step) {
+    const float rstd = __ldg(p.rstd + row);
+    const uint4* at = ring + (size_t)stage * PARTS * p.nv;
+    // a wait that ran out leaves wrong values; the group's barriers stay in step
+    mbar_wait(smem_u32(&bars[grp][stage]), phase, &abort_flag, &late);
+    __syncwarp();
+    uint64_t n[VPL][4], dn[VPL][4], dot2 = f2pack(0.0f, 0.0f);
+    const uint64_t rs2 = f2pack(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = i * 32 * W + t;
+      uint64_t b[4];
+      unpack_pairs(c < p.nv ? at[c] : zero, n[i]);
+      unpack_pairs(c < p.nv ? at[p.nv + c] : zero, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        n[i][j] = f2mul(n[i][j], rs2);
+        dg[i][j] = f2fma(b[j], n[i][j], dg[i][j]);
+        dn[i][j] = f2mul(b[j], gm[i][j]);
+        dot2 = f2fma(dn[i][j], n[i][j], dot2);
+      }
+    }
+    const float2 dots = f2unpack(dot2);
+    float dot = dots.x + dots.y;
+    dot = row_reduce<W, false>(dot, red[grp][flip], wr, lane, 1 + grp);
+    flip ^= 1;  // the next row's partial sums must not overwrite what a slower warp still reads
+    if constexpr (W == 1) __syncwarp();
+    // every warp has passed this row's barrier, so all are through with the row before: its stage takes the row
+    // kRing - 1 ahead
+    const int64_t ahead = row + (int64_t)(kRing - 1) * step;
+    if (leader && row > first && ahead < p.T) fill(stage == 0 ? kRing - 1 : stage - 1, ahead);
+    const float m = -rstd * (dot / (float)p.d);
+    const uint64_t m2 = f2pack(m, m);
+    uint4* out = reinterpret_cast<uint4*>(p.dx + row * p.d);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = i * 32 * W + t;
+      if (c >= p.nv) continue;
+      uint64_t e[4];
+      if constexpr (DRES) unpack_pairs(at[2 * p.nv + c], e);
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // rstd dn - rstd mean(dn n) n (+ dres)
+        uint64_t v = DRES ? f2fma(dn[i][j], rs2, e[j]) : f2mul(dn[i][j], rs2);
+        const float2 x = f2unpack(f2fma(n[i][j], m2, v));
+        o[j] = pack_bf16(x.x, x.y);
+      }
+      out[c] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (++stage == kRing) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  if (!p.part) return;
+  float4* joined = reinterpret_cast<float4*>(ring_all);  // [RB - 1, d]: every copy has landed and been read
+  auto store = [&](float4* to, const uint64_t (&v)[4]) {
+    const float2 a = f2unpack(v[0]), b = f2unpack(v[1]), c = f2unpack(v[2]), d = f2unpack(v[3]);
+    to[0] = make_float4(a.x, a.y, b.x, b.y);
+    to[1] = make_float4(c.x, c.y, d.x, d.y);
+  };
+  if constexpr (RB > 1) {
+    __syncthreads();
+    if (grp > 0)
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int c = i * 32 * W + t;
+        if (c < p.nv) store(joined + ((int64_t)(grp - 1) * p.nv + c) * 2, dg[i]);
+      }
+    __syncthreads();
+    if (grp > 0) return;
+  }
+  float4* pr = reinterpret_cast<float4*>(p.part + (int64_t)blockIdx.x * p.d);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = i * 32 * W + t;
+    if (c >= p.nv) continue;
+#pragma unroll
+    for (int q = 0; q < RB - 1; ++q) {
+      const float4 a = joined[((int64_t)q * p.nv + c) * 2], b = joined[((int64_t)q * p.nv + c) * 2 + 1];
+      dg[i][0] = f2add(dg[i][0], f2pack(a.x, a.y));
+      dg[i][1] = f2add(dg[i][1], f2pack(a.z, a.w));
+      dg[i][2] = f2add(dg[i][2], f2pack(b.x, b.y));
+      dg[i][3] = f2add(dg[i][3], f2pack(b.z, b.w));
+    }
+    store(pr + 2 * c, dg[i]);
+  }
+}
+
 // dgamma[c] = sum over the partial rows, in a fixed order: 32 columns per block, each of 32 warps
 // adding every 32nd row.
 __global__ void __launch_bounds__(1024) rmsnorm_dgamma_kernel(const float* __restrict__ part, int parts, int d,
@@ -437,8 +586,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_dgamma_kernel(const float* __res
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched beside the backward's end: its partial rows are complete
   float v = 0.0f;
   if (c < d)
+#pragma unroll 10
     for (int i = warp; i < parts; i += 32) v += part[(int64_t)i * d + c];
   s[warp][lane] = v;
   __syncthreads();
@@ -464,8 +615,29 @@ cudaError_t fwd_wide(const NormFwd& p, int kind, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <int VPL, int W, bool DRES>
+cudaError_t bwd_ring(const NormBwd& p, int blocks, cudaStream_t st) {
+  auto kern = rmsnorm_bwd_ring_kernel<VPL, W, DRES>;
+  constexpr int kMax = 8 / W * kRing * 3 * 512 * W * VPL;  // bytes at the widest row
+  static bool ready[64] = {false};  // per device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (!ready[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  size_t smem = (size_t)(8 / W) * kRing * (DRES ? 3 : 2) * p.d * 2;
+  kern<<<(unsigned)blocks, 256, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <int VPL, int W>
 cudaError_t bwd_launch(const NormBwd& p, int blocks, cudaStream_t st) {
+  // rows of 512 elements or fewer stay with loads: their copies of 1 KB or less cost more than they hide (32768
+  // x 512: 29 against 33 us, x 256: 20 against 25); from 1024 on the ring wins (16000 x 4096: 84 against 91)
+  if constexpr (VPL <= 2 && W >= 2) return p.dres ? bwd_ring<VPL, W, true>(p, blocks, st) : bwd_ring<VPL, W, false>(p, blocks, st);
   const size_t smem = p.part ? (size_t)(8 / W - 1) * p.d * 4 : 0;
   if (p.dres) rmsnorm_bwd_kernel<VPL, W, true><<<(unsigned)blocks, 256, smem, st>>>(p);
   else rmsnorm_bwd_kernel<VPL, W, false><<<(unsigned)blocks, 256, smem, st>>>(p);
@@ -545,8 +717,16 @@ cudaError_t launch_rmsnorm_bwd(const void* dy, const void* dres, const void* r, 
   prof_end(QAD_K_RMSNORM_BWD, st);
   if (e != cudaSuccess || !dgamma) return e;
   note_launches(1);
-  rmsnorm_dgamma_kernel<<<(unsigned)((d + 31) / 32), 1024, 0, st>>>(part, blocks, (int)d, dgamma);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((d + 31) / 32), 1, 1);
+  cfg.blockDim = dim3(1024, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rmsnorm_dgamma_kernel, static_cast<const float*>(part), blocks, (int)d, dgamma);
 }
 
 }  // namespace qad
