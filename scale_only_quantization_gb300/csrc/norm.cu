@@ -637,12 +637,15 @@ cudaError_t bwd_ring(const NormBwd& p, int blocks, cudaStream_t st) {
 template <int VPL, int W>
 cudaError_t bwd_launch(const NormBwd& p, int blocks, cudaStream_t st) {
   // rows of 512 elements or fewer stay with loads: their copies of 1 KB or less cost more than they hide (32768
-  // x 512: 29 against 33 us, x 256: 20 against 25); from 1024 on the ring wins (16000 x 4096: 84 against 91)
-  if constexpr (VPL <= 2 && W >= 2) return p.dres ? bwd_ring<VPL, W, true>(p, blocks, st) : bwd_ring<VPL, W, false>(p, blocks, st);
-  const size_t smem = p.part ? (size_t)(8 / W - 1) * p.d * 4 : 0;
-  if (p.dres) rmsnorm_bwd_kernel<VPL, W, true><<<(unsigned)blocks, 256, smem, st>>>(p);
-  else rmsnorm_bwd_kernel<VPL, W, false><<<(unsigned)blocks, 256, smem, st>>>(p);
-  return cudaGetLastError();
+  // x 512: 29 against 33 us, x 256: 20 against 25); from 1024 on the ring wins (16000 x 4096: 83 against 91)
+  if constexpr (VPL <= 2 && W >= 2) {
+    return p.dres ? bwd_ring<VPL, W, true>(p, blocks, st) : bwd_ring<VPL, W, false>(p, blocks, st);
+  } else {
+    const size_t smem = p.part ? (size_t)(8 / W - 1) * p.d * 4 : 0;
+    if (p.dres) rmsnorm_bwd_kernel<VPL, W, true><<<(unsigned)blocks, 256, smem, st>>>(p);
+    else rmsnorm_bwd_kernel<VPL, W, false><<<(unsigned)blocks, 256, smem, st>>>(p);
+    return cudaGetLastError();
+  }
 }
 
 }  // namespace

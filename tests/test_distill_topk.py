@@ -203,3 +203,39 @@ def test_repeatable_on_another_stream():
     with torch.cuda.stream(torch.cuda.Stream()):
         b = run(c)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mixed", [False, True])
+@pytest.mark.parametrize("N, d, V, K", [(1, 2048, 500, 64), (152, 512, 600, 24), (153, 512, 600, 24), (2000, 64, 200, 9), (700, 1024, 900, 40)])
+def test_row_counts_below_and_above_the_sms(N, d, V, K, mixed):
+    _lib()
+    check(make(N, d, V, K, seed=N, mixed=mixed))
+
+
+@pytest.mark.gpu
+def test_a_later_logit_far_above_the_first():
+    """The sums' reference is the first batch's largest logit; one 100 nats above it replaces it."""
+    _lib()
+    c = make(30, 256, 400, 24, seed=21, mixed=True)
+    for i in range(30):  # make slot 5 + i % 19 the row's own direction, so that its logit is the largest by far
+        c["w"][int(c["idx"][i, 5 + i % 19])] = c["h"][i] * 0.5
+    check(c)
+
+
+@pytest.mark.gpu
+def test_nan_in_a_head_row_reaches_the_rows_that_name_it_only():
+    _lib()
+    c = make(12, 256, 400, 16, seed=22)
+    c["idx"] = torch.stack([torch.arange(16, device="cuda", dtype=torch.int32) + 16 * (i % 6) for i in range(12)])
+    c["idx"][3, 4] = -1
+    loss, dh = run(c)
+    c["w"][17] = float("nan")            # named by rows 1 and 7
+    c["w"][16 * 3 + 4] = float("nan")    # row 9's, and in row 3 a slot that does not count
+    c["w"][399] = float("inf")           # nobody's
+    l2, d2 = run(c)
+    for i in range(12):
+        if i in (1, 7, 9):
+            assert torch.isnan(l2[i])
+        else:
+            assert torch.equal(loss[i], l2[i]) and torch.equal(dh[i], d2[i])

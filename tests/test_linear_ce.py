@@ -289,3 +289,47 @@ def test_repeatable_on_another_stream():
     torch.cuda.synchronize()
     for n in ("loss", "lse", "dh", "dw"):
         assert torch.equal(a[n], b[n])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N, d, V", [(64, 512, 700), (127, 272, 3001), (128, 256, 5000), (129, 256, 5000), (700, 320, 40000)])
+def test_row_counts_around_the_transposed_products(N, d, V):
+    """Up to 128 rows the products are taken transposed; many words for few columns split the contraction into many slabs."""
+    _lib()
+    check(make(N, d, V, seed=N, drop=0.1), dw=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 40, 128])
+def test_large_logits_of_few_rows(N):
+    """The second sweep of the transposed products: targets hundreds of nats below the largest logit."""
+    _lib()
+    c = make(N, 256, 2000, seed=15, boost=0.0, size=200.0)
+    o = run(c, dw=True)
+    ref, tol = exact(c)
+    assert float(ref["loss"].max()) > 100.0
+    for n in ("loss", "lse", "dh", "dw"):
+        assert torch.isfinite(o[n]).all()
+        assert torch.all((o[n].double() - ref[n]).abs() <= tol[n]), n
+
+
+@pytest.mark.gpu
+def test_neighbouring_calls_share_a_workspace():
+    """Calls of different sizes follow each other on one workspace without a wait between them."""
+    _lib()
+    cs = [make(N, 256, V, seed=N, drop=0.1) for N, V in ((300, 5000), (20, 9000), (600, 777), (1, 9000))]
+    want = [run(c) for c in cs]
+    ws = torch.empty(max(Q.qad_linear_ce_workspace_bytes(c["N"], 256, c["V"], 1, 0) for c in cs), dtype=torch.uint8,
+                     device="cuda")
+    outs = []
+    for c in cs:
+        N = c["N"]
+        o = dict(loss=torch.empty(N, device="cuda"), lse=torch.empty(N, device="cuda"),
+                 dh=torch.empty((N, 256), dtype=torch.bfloat16, device="cuda"))
+        Q.qad_linear_ce_fwd_bwd(c["h"], 256, c["w"], 256, c["target"], c["g"], o["loss"], o["lse"], o["dh"], None, 0, N,
+                                256, c["V"], ws)
+        outs.append(o)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for n in o:
+            assert torch.equal(o[n], w[n])

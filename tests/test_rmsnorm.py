@@ -241,3 +241,37 @@ def test_on_another_stream():
     Q.qad_rmsnorm_fwd(x, None, gamma, EPS, 0, None, y2, None, None, None, None, 64, 256, 256, 0)
     torch.cuda.synchronize()
     assert torch.equal(y, y2)
+
+
+@pytest.mark.gpu
+def test_no_rows_give_a_zero_weight_gradient():
+    _lib()
+    e = torch.empty(0, device="cuda")
+    dg = torch.full((64,), float("nan"), device="cuda")
+    Q.qad_rmsnorm_bwd(e, None, e, e, e, e, dg, 0, 64, 64)
+    torch.cuda.synchronize()
+    assert torch.all(dg == 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [256, 272, 2048, 2880, 4096])
+def test_statistics_have_the_unfused_bits(d):
+    """rstd and y are those of elementary fp32 operations, bit for bit: 128 chains of squares (element i in chain i %
+    128), the four chains of a group one after the other, the 32 groups pairwise, then one product with 1 / d, one root,
+    one reciprocal and two products."""
+    _lib()
+    x, res, gamma, o = _run(200, d, 0, seed=d)
+    r = (x.float() + res.float()).to(torch.bfloat16).float()
+    sq = torch.zeros((200, -(-d // 128) * 128), device="cuda")
+    sq[:, :d] = r * r
+    chains = torch.zeros((200, 128), device="cuda")
+    for part in sq.split(128, dim=1):
+        chains = chains + part
+    c = chains.view(200, 32, 4)
+    s = ((c[:, :, 0] + c[:, :, 1]) + c[:, :, 2]) + c[:, :, 3]
+    while s.shape[1] > 1:
+        s = s[:, 0::2] + s[:, 1::2]
+    inv = torch.tensor(1.0, device="cuda") / d
+    rstd = 1 / torch.sqrt(s[:, 0] * inv + EPS)
+    y = (r * rstd[:, None] * gamma.float()).to(torch.bfloat16)
+    assert torch.equal(o["rstd"], rstd) and torch.equal(o["y"], y)
