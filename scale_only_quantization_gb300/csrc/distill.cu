@@ -153,7 +153,9 @@ struct DistillGrid {
 // registers hold at once set the rate: two teams of 4 warps with 8 rows each (64 KB) reach 6.0 TB/s of
 // head rows at d = 2048, K = 64 (178 us for 4096 token rows); batches of 4 rows 206 us, 8-warp teams with
 // half the columns per lane 206 us.  One team of 8 warps takes d = 4096; with both divergences its third
-// sum leaves it at 4.4 TB/s (967 us for 16384 token rows, K = 32).  Reading the rows a second time from L2
+// sum leaves it at 4.4 TB/s (967 us for 16384 token rows, K = 32).  Two teams on an SM there, with batches of 4
+// rows or 2 that are read a second time from shared memory instead of held in registers, spill and hold each
+// stage for its whole chain: 1670 to 2400 us.  Reading the rows a second time from L2
 // for the gradient instead took 305 and 1240 us; matrix instructions (mma.sync, 8 rows a fragment) for both
 // products 234 and 1358 us, their rate on this chip being a few times the FMA units' only.
 template <int CW, int V, int R, bool MIX>
