@@ -39,19 +39,27 @@ struct NormFwd {
   float eps, inv_d;
 };
 
-// Sum (or maximum) over the W warps that share a row; every thread of the group returns it.
-template <int W, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* smem, int warp_in_row, int lane, int bar) {
-  v = MAX ? warp_max(v) : warp_sum(v);
+// Sum over the W warps that share a row; every thread of the group returns it.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float* smem, int warp_in_row, int lane, int bar) {
+  v = warp_sum(v);
   if constexpr (W > 1) {
     if (lane == 0) smem[warp_in_row] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * W) : "memory");
     v = smem[0];
 #pragma unroll
-    for (int i = 1; i < W; ++i) v = MAX ? fmaxf(v, smem[i]) : v + smem[i];
+    for (int i = 1; i < W; ++i) v += smem[i];
   }
   return v;
 }
+
+// max |y| of a row from its bf16 bits: without their signs, magnitudes compare as integers, two per word, and a NaN
+// is above infinity, so that neither is lost on the way to the scale (fmaxf would drop a NaN).
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t pair) { return __vmaxu2(m, pair & 0x7fff7fffu); }
+__device__ __forceinline__ uint32_t warp_max_bits(uint32_t m) {
+  return __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+}
+__device__ __forceinline__ float magnitude(uint32_t bits) { return __uint_as_float(bits << 16); }
 
 // The layer's activation quantizer on 4 values of scale s: their codes, and code value * s in place
 template <int KIND>
@@ -63,12 +71,13 @@ __device__ __forceinline__ void quantize4(float* a, float s, uint32_t& code) {
   } else {
     float x[4];
     act_quotients<4>(a, s, x);
+    const float by = s < INFINITY ? s : NAN;  // no INT8 code stands for a NaN quotient: its y_hat says it
     code = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float q = q_int8(x[j]);
       code |= ((uint32_t)(int)q & 0xffu) << (8 * j);
-      a[j] = __fmul_rn(copysignf(q, x[j]), s);
+      a[j] = __fmul_rn(copysignf(q, x[j]), by);
     }
   }
 }
@@ -138,7 +147,7 @@ __global__ void __launch_bounds__(128) rmsnorm_fwd_warp_kernel(const NormFwd p) 
   if (lane == 0 && p.rstd) p.rstd[row] = rstd;
   const uint2* gr = reinterpret_cast<const uint2*>(p.gamma);
   uint2* yo = reinterpret_cast<uint2*>(p.y + row * p.d);
-  float amax = 0.0f;
+  uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < G; ++i) {
     float a[4], g[4];
@@ -148,14 +157,10 @@ __global__ void __launch_bounds__(128) rmsnorm_fwd_warp_kernel(const NormFwd p) 
     for (int j = 0; j < 4; ++j) a[j] = __fmul_rn(__fmul_rn(a[j], rstd), g[j]);
     v[i] = pack4(a);
     if (p.y && lane + 32 * i < ng) yo[lane + 32 * i] = v[i];
-    if constexpr (KIND != kQNone) {
-      unpack4(v[i], a);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fabsf(a[j]));
-    }
+    if constexpr (KIND != kQNone) amax = max_bits(max_bits(amax, v[i].x), v[i].y);
   }
   if constexpr (KIND != kQNone) {
-    const float s = __fdiv_rn(warp_max(amax), KIND == kQE4M3 ? 448.0f : 127.0f);
+    const float s = __fdiv_rn(magnitude(warp_max_bits(amax)), KIND == kQE4M3 ? 448.0f : 127.0f);
     if (lane == 0 && p.scale) p.scale[row] = s;
     if (!p.codes && !p.y_hat) return;
 #pragma unroll
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_fwd_kernel(const NormFwd p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fmaf(a[j] * f, a[j] * f, sum);
       }
-      sum = row_reduce<W, false>(sum, smem, warp, lane, 1);
+      sum = row_sum<W>(sum, smem, warp, lane, 1);
     }
     return sum * p.inv_d;
   };
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_fwd_kernel(const NormFwd p) {
     rstd = __fdiv_rn(1.0f, __fsqrt_rn(mean_square(0x1p-64f, red[2]))) * 0x1p-64f;  // eps is below the last place
   if (t == 0 && p.rstd) p.rstd[row] = rstd;
   const uint4* gr = reinterpret_cast<const uint4*>(p.gamma);
-  float amax = 0.0f;
+  uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int c = i * 32 * W + t;
@@ -267,11 +272,7 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_fwd_kernel(const NormFwd p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = __fmul_rn(__fmul_rn(a[j], rstd), g[j]);
     v[i] = pack8(a);
-    if constexpr (KIND != kQNone) {
-      unpack8(v[i], a);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(a[j]));
-    }
+    if constexpr (KIND != kQNone) amax = max_bits(max_bits(max_bits(max_bits(amax, v[i].x), v[i].y), v[i].z), v[i].w);
   }
   if (p.y) {
     uint4* yo = reinterpret_cast<uint4*>(p.y + row * p.d);
@@ -282,8 +283,13 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_fwd_kernel(const NormFwd p) {
     }
   }
   if constexpr (KIND != kQNone) {
-    amax = row_reduce<W, true>(amax, red[1], warp, lane, 1);
-    const float s = __fdiv_rn(amax, KIND == kQE4M3 ? 448.0f : 127.0f);
+    amax = warp_max_bits(amax);
+    uint32_t* tops = reinterpret_cast<uint32_t*>(red[1]);
+    if (lane == 0) tops[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) amax = max(amax, tops[i]);
+    const float s = __fdiv_rn(magnitude(amax), KIND == kQE4M3 ? 448.0f : 127.0f);
     if (t == 0 && p.scale) p.scale[row] = s;
     if (!p.codes && !p.y_hat) return;
 #pragma unroll
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(const NormBwd p) {
         dot = fmaf(b[j] * w[j], nn, dot);
       }
     }
-    dot = row_reduce<W, false>(dot, red[grp][flip], wr, lane, 1 + grp);
+    dot = row_sum<W>(dot, red[grp][flip], wr, lane, 1 + grp);
     flip ^= 1;  // the next row's partial sums must not overwrite what a slower warp still reads
     const float m = dot / (float)p.d;
     uint4* out = reinterpret_cast<uint4*>(p.dx + row * p.d);
@@ -515,7 +521,7 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd 
     }
     const float2 dots = f2unpack(dot2);
     float dot = dots.x + dots.y;
-    dot = row_reduce<W, false>(dot, red[grp][flip], wr, lane, 1 + grp);
+    dot = row_sum<W>(dot, red[grp][flip], wr, lane, 1 + grp);
     flip ^= 1;  // the next row's partial sums must not overwrite what a slower warp still reads
     if constexpr (W == 1) __syncwarp();
     // every warp has passed this row's barrier, so all are through with the row before: its stage takes the row

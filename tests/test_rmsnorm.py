@@ -275,3 +275,37 @@ def test_statistics_have_the_unfused_bits(d):
     rstd = 1 / torch.sqrt(s[:, 0] * inv + EPS)
     y = (r * rstd[:, None] * gamma.float()).to(torch.bfloat16)
     assert torch.equal(o["rstd"], rstd) and torch.equal(o["y"], y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [Q.QAD_ACT_E4M3, Q.QAD_ACT_INT8])
+@pytest.mark.parametrize("d", [48, 512, 1024, 2048, 4112, 8208])
+def test_nan_and_infinity_reach_the_8bit_outputs(d, act):
+    """A row whose y holds a NaN has no 8-bit form: scale NaN, and with it every y_hat and E4M3 code; an infinite y
+    makes the scale infinite and its own code NaN.  Rows beside it keep their bits."""
+    _lib()
+    x = torch.randn((7, d), device="cuda").to(torch.bfloat16)
+    clean = _run(7, d, act, res=False, x=x.clone())[3]
+    x[2, d // 3] = float("nan")
+    x[4, d - 1] = float("inf")
+    x[5, 0] = -float("inf")
+    o = _run(7, d, act, res=False, x=x)[3]
+    for i in (0, 1, 3, 6):
+        for n in ("y", "y_hat", "codes", "scale", "rstd"):
+            assert torch.equal(o[n][i], clean[n][i])
+    for i in (2, 4, 5):
+        assert torch.isnan(o["y"][i]).any()
+        assert torch.isnan(o["scale"][i]) and torch.isnan(o["y_hat"][i]).all()
+        if act == Q.QAD_ACT_E4M3:
+            assert torch.isnan(o["codes"][i].view(torch.float8_e4m3fn).float()).all()
+    # finite r, a norm weight that carries y past bf16's range
+    x = torch.ones((2, d), device="cuda", dtype=torch.bfloat16)
+    x[1, 5] = 2.0
+    gamma = torch.ones(d, device="cuda", dtype=torch.bfloat16)
+    gamma[5] = 3.3e38
+    y, yh = torch.empty_like(x), torch.empty_like(x)
+    codes, scale = torch.empty((2, d), dtype=torch.uint8, device="cuda"), torch.empty(2, device="cuda")
+    Q.qad_rmsnorm_fwd(x, None, gamma, EPS, act, None, y, yh, codes, scale, None, 2, d, d, d)
+    torch.cuda.synchronize()
+    assert torch.isfinite(y[0]).all() and torch.isfinite(scale[0]) and torch.isfinite(yh[0, 0])
+    assert torch.isinf(y[1, 5]) and torch.isinf(scale[1]) and torch.isnan(yh[1]).all()
