@@ -61,6 +61,20 @@ __device__ __forceinline__ uint32_t warp_max_bits(uint32_t m) {
 }
 __device__ __forceinline__ float magnitude(uint32_t bits) { return __uint_as_float(bits << 16); }
 
+// rstd from the row's mean square; scaled_mean(f) is that of f r.  Squares that leave fp32's range, at the top (|r| >
+// 1e19 / sqrt(d)) or, where next to no eps covers it, at the bottom, are taken again of scaled values: 2^-64 r or 2^100 r.
+// A row of zeros without eps has rstd 0, so that y and the gradient are 0; below an rms of 3e-39, whose reciprocal fp32
+// does not hold, rstd stays at fp32's largest value.
+template <typename F>
+__device__ __forceinline__ float inverse_rms(float mean, float eps, F scaled_mean) {
+  if (mean == INFINITY || mean + eps < 0x1p-100f) {
+    const float f = mean == INFINITY ? 0x1p-64f : 0x1p100f;
+    const float s = scaled_mean(f) + eps * f * f;
+    return s == 0.0f ? 0.0f : fminf(__fdiv_rn(1.0f, __fsqrt_rn(s)) * f, 3.402823466e38f);
+  }
+  return __fdiv_rn(1.0f, __fsqrt_rn(mean + eps));
+}
+
 // The layer's activation quantizer on 4 values of scale s: their codes, and code value * s in place
 template <int KIND>
 __device__ __forceinline__ void quantize4(float* a, float s, uint32_t& code) {
@@ -140,10 +154,7 @@ __global__ void __launch_bounds__(128) rmsnorm_fwd_warp_kernel(const NormFwd p) 
     for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s * p.inv_d;
   };
-  float mean = mean_square(1.0f);
-  float rstd = __fdiv_rn(1.0f, __fsqrt_rn(mean + p.eps));
-  if (mean == INFINITY)  // the squares leave fp32's range (|r| > 1e19 / sqrt(d)): scaled by 2^-64 they do not, and
-    rstd = __fdiv_rn(1.0f, __fsqrt_rn(mean_square(0x1p-64f))) * 0x1p-64f;  // eps is below the last place
+  const float rstd = inverse_rms(mean_square(1.0f), p.eps, mean_square);
   if (lane == 0 && p.rstd) p.rstd[row] = rstd;
   const uint2* gr = reinterpret_cast<const uint2*>(p.gamma);
   uint2* yo = reinterpret_cast<uint2*>(p.y + row * p.d);
@@ -256,10 +267,8 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_fwd_kernel(const NormFwd p) {
     }
     return sum * p.inv_d;
   };
-  const float mean = mean_square(1.0f, red[0]);
-  float rstd = __fdiv_rn(1.0f, __fsqrt_rn(mean + p.eps));
-  if (mean == INFINITY)  // the squares leave fp32's range (|r| > 1e19 / sqrt(d)): scaled by 2^-64 they do not, and
-    rstd = __fdiv_rn(1.0f, __fsqrt_rn(mean_square(0x1p-64f, red[2]))) * 0x1p-64f;  // eps is below the last place
+  const float rstd =
+      inverse_rms(mean_square(1.0f, red[0]), p.eps, [&](float f) { return mean_square(f, red[2]); });
   if (t == 0 && p.rstd) p.rstd[row] = rstd;
   const uint4* gr = reinterpret_cast<const uint4*>(p.gamma);
   uint32_t amax = 0;

@@ -309,3 +309,34 @@ def test_nan_and_infinity_reach_the_8bit_outputs(d, act):
     torch.cuda.synchronize()
     assert torch.isfinite(y[0]).all() and torch.isfinite(scale[0]) and torch.isfinite(yh[0, 0])
     assert torch.isinf(y[1, 5]) and torch.isinf(scale[1]) and torch.isnan(yh[1]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [48, 1024, 2048, 4112, 8208])
+def test_no_epsilon(d):
+    """eps = 0 (or one far below the row): a row of zeros gives y = 0, rows whose squares leave fp32's range at the
+    bottom keep their norm, down to where 1 / rms itself does; the backward of such rows is finite."""
+    _lib()
+    bf = torch.bfloat16
+    x = torch.randn((6, d), device="cuda").to(bf)
+    x[0] = 0
+    for i, e in ((1, -50), (2, -70), (3, -100), (4, 70)):
+        x[i] = (x[i].float() * 2.0 ** e).to(bf)
+    gamma = (1 + 0.2 * torch.randn(d, device="cuda")).to(bf)
+    for eps in (0.0, 1e-38):
+        y, rstd, scale = torch.empty_like(x), torch.empty(6, device="cuda"), torch.empty(6, device="cuda")
+        codes = torch.empty((6, d), dtype=torch.uint8, device="cuda")
+        Q.qad_rmsnorm_fwd(x, None, gamma, eps, Q.QAD_ACT_E4M3, None, y, None, codes, scale, rstd, 6, d, d, d)
+        torch.cuda.synchronize()
+        assert torch.all(y[0] == 0) and float(scale[0]) == 0 and torch.all(codes[0] & 0x7F == 0)
+        assert torch.isfinite(rstd).all()
+        eps32 = float(torch.tensor(eps))
+        want = (x.double().square().mean(1) + eps32).rsqrt()
+        rows = slice(1, 6) if eps == 0 else slice(0, 6)
+        assert torch.all((rstd.double() - want).abs()[rows] <= 1e-5 * want[rows])
+        ref = x.double() * torch.where(torch.isinf(want), 0.0, want)[:, None] * gamma.double()
+        assert torch.all((y.double() - ref).abs() <= (2.0 ** -8 + 2e-5) * ref.abs() + 1e-38)
+        dy, dx = torch.randn((6, d), device="cuda").to(bf), torch.empty_like(x)
+        Q.qad_rmsnorm_bwd(dy, None, x, gamma, rstd, dx, None, 6, d, d)
+        torch.cuda.synchronize()
+        assert torch.isfinite(dx).all()
