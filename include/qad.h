@@ -268,7 +268,10 @@ int qad_rmsnorm_fwd(const void* x, const void* res, const void* gamma, float eps
  *   dy     bf16 [T, d]         dres bf16 [T, d] or NULL: the gradient arriving at res_out
  *   r      bf16 [T, d], ldr between rows: the forward's res_out (x without res)    rstd fp32 [T]
  *   dx     bf16 [T, d] (may be dy or dres)          dgamma fp32 [d] or NULL (overwritten)
- *   ws     needed with dgamma: 256-byte aligned, ws_bytes >= qad_rmsnorm_workspace_bytes(T, d)
+ *   ws     needed with dgamma: 256-byte aligned, ws_bytes >= qad_rmsnorm_workspace_bytes(T, d).  Its first word
+ *          is the device error word (qad_check_device_error), written by each call with T > 0 and dgamma.
+ * Should a pipeline wait time out, the rows of its thread block are NaN in dx, and dgamma is NaN: without
+ * a workspace that is the only sign.
  */
 size_t qad_rmsnorm_workspace_bytes(int64_t T, int64_t d);
 int qad_rmsnorm_bwd(const void* dy, const void* dres, const void* r, const void* gamma, const float* rstd, void* dx,
@@ -443,6 +446,13 @@ int qad_route_permute_noalloc(const int32_t* topk_idx, int64_t T, int32_t topk, 
  * QAD_DEV_TIMEOUT into *err_word (device int32) when it gives up.
  */
 int qad_debug_wait_timeout(int32_t* err_word, int64_t budget_cycles, qad_stream_t stream);
+
+/*
+ * The same for the kernels that stream token rows through a ring of bulk copies (qad_rmsnorm_bwd,
+ * 512 < d <= 4096): until it is called again with row < 0, calls of this process leave out the copies of
+ * token row `row` (and of the rows after it that the same warps work on), and their waits give up after `budget_cycles` SM clock cycles (0 to 2e9).
+ */
+int qad_debug_stuck_copy(int64_t row, int64_t budget_cycles);
 
 /*
  * Self-check of the division inside the quantizers (not an operation of the method).

@@ -32,8 +32,8 @@ QAD_RMSNORM_MAX_D, QAD_DISTILL_MAX_D, QAD_DISTILL_MAX_K = 16384, 16384, 1024
 EXPORTS = ["qad_fakequant_fwd", "qad_moe_workspace_bytes", "qad_moe_fwd", "qad_moe_bwd_dgrad",
            "qad_moe_bwd_scalegrad", "qad_check_device_error", "qad_status_string", "qad_moe_debug_view",
            "qad_profile_enable", "qad_profile_reset", "qad_profile_read", "qad_kernel_name", "qad_launch_count",
-           "qad_debug_quotient", "qad_route_permute_noalloc", "qad_debug_wait_timeout", "qad_moe_combine",
-           "qad_nvfp4_deploy_scales", "qad_rmsnorm_workspace_bytes", "qad_rmsnorm_fwd", "qad_rmsnorm_bwd",
+           "qad_debug_quotient", "qad_route_permute_noalloc", "qad_debug_wait_timeout", "qad_debug_stuck_copy",
+           "qad_moe_combine", "qad_nvfp4_deploy_scales", "qad_rmsnorm_workspace_bytes", "qad_rmsnorm_fwd", "qad_rmsnorm_bwd",
            "qad_linear_ce_workspace_bytes", "qad_linear_ce_fwd", "qad_linear_ce_fwd_bwd", "qad_distill_topk_fwd",
            "qad_distill_topk_fwd_bwd"]
 
@@ -84,6 +84,7 @@ def lib():
             "qad_launch_count": (ctypes.c_int64, []),
             "qad_debug_quotient": (ctypes.c_int, [_P, _P, _P, _P, _I64, ctypes.c_int32, _P]),
             "qad_debug_wait_timeout": (ctypes.c_int, [_P, _I64, _P]),
+            "qad_debug_stuck_copy": (ctypes.c_int, [_I64, _I64]),
             "qad_route_permute_noalloc": (ctypes.c_int, [_P, _I64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P,
                                                          _P, _P, _P]),
             "qad_moe_combine": (ctypes.c_int, [_P, _P, _P, _P, _I64, ctypes.c_int32, _I64, _P]),
@@ -296,6 +297,10 @@ def qad_distill_topk_fwd_bwd(h, ldh, w, ldw, idx, t_logit, mix, inv_temp, g, los
 def qad_debug_wait_timeout(err_word, budget_cycles, stream=None):
     return _check(lib().qad_debug_wait_timeout(_ptr(err_word), int(budget_cycles), _stream(stream)),
                   "qad_debug_wait_timeout")
+
+
+def qad_debug_stuck_copy(row, budget_cycles=0):
+    return _check(lib().qad_debug_stuck_copy(int(row), int(budget_cycles)), "qad_debug_stuck_copy")
 
 
 def workspace_view(ws, s, which, dtype):

@@ -54,6 +54,8 @@ cudaEvent_t take_event() {
 
 int g_sms[64] = {0};
 
+std::atomic<int64_t> g_stuck_row{-1}, g_stuck_budget{0};
+
 }  // namespace
 
 int num_sms() {
@@ -67,6 +69,8 @@ int num_sms() {
   }
   return g_sms[dev];
 }
+
+StuckCopy stuck_copy() { return {g_stuck_row.load(), g_stuck_budget.load()}; }
 
 void prof_begin(int id, cudaStream_t st) {
   g_launch_total.fetch_add(1, std::memory_order_relaxed);
@@ -420,7 +424,7 @@ static bool ok_rows(const void* p, int64_t ld, int64_t d) { return ok_ptr(p) && 
 
 size_t qad_rmsnorm_workspace_bytes(int64_t T, int64_t d) {
   if (T < 0 || d <= 0 || d % 16 || d > QAD_RMSNORM_MAX_D) return 0;
-  return up(4 * (size_t)norm_blocks(T > 0 ? T : 1) * (size_t)d);
+  return up(norm_workspace(T > 0 ? T : 1, d));
 }
 
 int qad_rmsnorm_fwd(const void* x, const void* res, const void* gamma, float eps, int act, void* res_out, void* y,
@@ -455,7 +459,7 @@ int qad_rmsnorm_bwd(const void* dy, const void* dres, const void* r, const void*
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return QAD_ERR_INVALID_ARG;
     if (ws_bytes < qad_rmsnorm_workspace_bytes(T, d)) return QAD_ERR_WORKSPACE;
   }
-  return to_status(launch_rmsnorm_bwd(dy, dres, r, ldr, gamma, rstd, dx, dgamma, static_cast<float*>(ws), T, d, st));
+  return to_status(launch_rmsnorm_bwd(dy, dres, r, ldr, gamma, rstd, dx, dgamma, static_cast<uint8_t*>(ws), T, d, st));
 }
 
 size_t qad_linear_ce_workspace_bytes(int64_t N, int64_t d, int64_t V, int dh, int dw) {
@@ -631,6 +635,13 @@ int64_t qad_launch_count(void) { return g_launch_total.load(); }
 int qad_debug_wait_timeout(int32_t* err_word, int64_t budget_cycles, qad_stream_t stream) {
   if (!err_word || budget_cycles < 0 || budget_cycles > 2000000000LL) return QAD_ERR_INVALID_ARG;
   return to_status(launch_wait_selftest(err_word, budget_cycles, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qad_debug_stuck_copy(int64_t row, int64_t budget_cycles) {
+  if (row >= 0 && (budget_cycles < 0 || budget_cycles > 2000000000LL)) return QAD_ERR_INVALID_ARG;
+  g_stuck_budget.store(budget_cycles);
+  g_stuck_row.store(row < 0 ? -1 : row);
+  return QAD_OK;
 }
 
 int qad_debug_quotient(const float* w, const float* s, float* x_fast, float* x_ieee, int64_t n, int32_t mode,

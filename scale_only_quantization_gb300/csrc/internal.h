@@ -41,6 +41,12 @@ void prof_end(int kernel_id, cudaStream_t st);
 void note_launches(int n);  // extra kernels launched inside one profiled region
 int num_sms();
 
+// qad_debug_stuck_copy: the token row whose copies the rings leave out (-1: none) and their waits' budget
+struct StuckCopy {
+  int64_t row, budget;
+};
+StuckCopy stuck_copy();
+
 // ---- kernels (each returns the launch's cudaError_t) ----
 // codes (E4M3 weights only, may be null): the E4M3 code byte of every element, [rows, K]
 cudaError_t launch_fakequant(int fmt, const void* w, const float* s, void* out, int64_t rows, int64_t K,
@@ -126,12 +132,12 @@ cudaError_t gemm_wgrad_fc2(const GemmCtx& c, const void* w2, const float* s2, fl
 cudaError_t gemm_wgrad_fc1(const GemmCtx& c, const void* w13, const float* s13, float* ds13, int accumulate);
 
 // ---- residual RMSNorm (norm.cu); kind: kQNone, kQE4M3 or kQInt8 ----
-int norm_blocks(int64_t T);  // partial dgamma rows of the backward's workspace at most
+size_t norm_workspace(int64_t T, int64_t d);  // bytes of the backward's workspace (T > 0)
 cudaError_t launch_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* gamma, float eps,
                                int kind, void* r, void* y, void* y_hat, void* codes, float* scale, float* rstd,
                                int64_t T, int64_t d, cudaStream_t st);
 cudaError_t launch_rmsnorm_bwd(const void* dy, const void* dres, const void* r, int64_t ldr, const void* gamma,
-                               const float* rstd, void* dx, float* dgamma, float* part, int64_t T, int64_t d,
+                               const float* rstd, void* dx, float* dgamma, uint8_t* ws, int64_t T, int64_t d,
                                cudaStream_t st);
 
 // ---- linear cross entropy (head.cu) ----

@@ -322,8 +322,11 @@ struct NormBwd {
   const __nv_bfloat16 *dy, *dres, *r, *gamma;
   const float* rstd;
   __nv_bfloat16* dx;
-  float* part;  // [gridDim.x * rows per block, d] partial dgamma, or null
+  float* part;      // [gridDim.x, d] partial dgamma, or null
+  int32_t* status;  // [gridDim.x] device error bits of each block (the ring's waits), with part
   int64_t T, ldr;
+  int64_t stuck;     // a row whose copies are left out (the failure path's self-check), -1: none
+  long long budget;  // clock cycles that a wait of the ring may take
   int nv, d;
 };
 
@@ -458,7 +461,11 @@ __device__ __forceinline__ void unpack_pairs(const uint4& u, uint64_t* f) {
 
 // The same for rows of 513 to 4096 elements, with the rows ahead in shared memory: each group has a ring
 // of kRing rows of r, dy and dres, filled by bulk copies that its first lane issues one row after the
-// stage's last use (a row's barrier says that every warp is through with the row before).
+// stage's last use (a row's barrier says that every warp is through with the row before).  When a wait
+// runs out the leaders issue no more copies, those under way land before the block gives its memory back,
+// and the block makes all its rows of dx and its part of the weight gradient NaN and sets its status word:
+// nothing of it is in the loop but the leader's look at its wait (a row made NaN where its wait failed cost 2 us
+// of 49 for 16384 x 2048).
 template <int VPL, int W, bool DRES>
 __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd p) {
   constexpr int RB = 8 / W, PARTS = DRES ? 3 : 2;
@@ -472,6 +479,7 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd 
   const uint4 zero = make_uint4(0, 0, 0, 0);
   uint4* ring = ring_all + (size_t)grp * kRing * PARTS * p.nv;
   const bool leader = t == 0;
+  int fills = 0;  // the leader's copies so far, in rows
   if (threadIdx.x == 0) abort_flag = late = 0;
   if (leader) {
     for (int s = 0; s < kRing; ++s) mbar_init(smem_u32(&bars[grp][s]), 1);
@@ -482,6 +490,7 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t bytes = (uint32_t)p.d * 2u;
   auto fill = [&](int stage, int64_t row) {  // the leader's
+    ++fills;
     const uint32_t bar = smem_u32(&bars[grp][stage]);
     mbar_expect_tx(bar, PARTS * bytes);
     const __nv_bfloat16* src[3] = {p.r + row * p.ldr, p.dy + row * p.d, DRES ? p.dres + row * p.d : nullptr};
@@ -493,9 +502,11 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd 
           "l"(reinterpret_cast<uint64_t>(src[i])), "r"(bytes), "r"(bar)
           : "memory");
   };
+  // a row whose copies never come, in the failure path's self-check, ends its group's copies
+  const int64_t end = p.stuck >= 0 && p.stuck % step == first ? p.stuck : p.T;
   if (leader)
     for (int s = 0; s < kRing; ++s)
-      if (first + s * step < p.T) fill(s, first + s * step);
+      if (first + s * step < end) fill(s, first + s * step);
   uint64_t gm[VPL][4], dg[VPL][4];  // pairs of columns: packed fp32 arithmetic
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -509,8 +520,8 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd 
   for (int64_t row = first; row < p.T; row += step) {
     const float rstd = __ldg(p.rstd + row);
     const uint4* at = ring + (size_t)stage * PARTS * p.nv;
-    // a wait that ran out leaves wrong values; the group's barriers stay in step
-    mbar_wait(smem_u32(&bars[grp][stage]), phase, &abort_flag, &late);
+    // a wait that ran out leaves wrong values, replaced below; the group's barriers stay in step
+    const bool ok = mbar_wait(smem_u32(&bars[grp][stage]), phase, &abort_flag, &late, p.budget);
     __syncwarp();
     uint64_t n[VPL][4], dn[VPL][4], dot2 = f2pack(0.0f, 0.0f);
     const uint64_t rs2 = f2pack(rstd, rstd);
@@ -536,7 +547,7 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd 
     // every warp has passed this row's barrier, so all are through with the row before: its stage takes the row
     // kRing - 1 ahead
     const int64_t ahead = row + (int64_t)(kRing - 1) * step;
-    if (leader && row > first && ahead < p.T) fill(stage == 0 ? kRing - 1 : stage - 1, ahead);
+    if (leader && row > first && ahead < end && ok) fill(stage == 0 ? kRing - 1 : stage - 1, ahead);
     const float m = -rstd * (dot / (float)p.d);
     const uint64_t m2 = f2pack(m, m);
     uint4* out = reinterpret_cast<uint4*>(p.dx + row * p.d);
@@ -560,7 +571,23 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd 
       phase ^= 1u;
     }
   }
+  __syncthreads();
+  if (abort_flag) {  // alike in the whole block: no wait is left
+    volatile int none = 0;
+    for (int s = 0; leader && s < kRing; ++s)
+      if (fills > s) mbar_wait(smem_u32(&bars[grp][s]), (uint32_t)((fills - 1 - s) / kRing) & 1u, &none, &late);
+    const uint32_t nans = 0x7fff7fffu;
+    for (int64_t row = first; row < p.T; row += step)
+      for (int c = t; c < p.nv; c += 32 * W)
+        reinterpret_cast<uint4*>(p.dx + row * p.d)[c] = make_uint4(nans, nans, nans, nans);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dg[i][j] = f2pack(NAN, NAN);
+    __syncthreads();
+  }
   if (!p.part) return;
+  if (threadIdx.x == 0) p.status[blockIdx.x] = late;
   float4* joined = reinterpret_cast<float4*>(ring_all);  // [RB - 1, d]: every copy has landed and been read
   auto store = [&](float4* to, const uint64_t (&v)[4]) {
     const float2 a = f2unpack(v[0]), b = f2unpack(v[1]), c = f2unpack(v[2]), d = f2unpack(v[3]);
@@ -568,7 +595,6 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd 
     to[1] = make_float4(c.x, c.y, d.x, d.y);
   };
   if constexpr (RB > 1) {
-    __syncthreads();
     if (grp > 0)
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
@@ -596,19 +622,22 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd 
 }
 
 // dgamma[c] = sum over the partial rows, in a fixed order: 32 columns per block, each of 32 warps
-// adding every 32nd row.
+// adding every 32nd row.  Block 0 joins the status words (null: the backward waits for nothing) into the error word.
 __global__ void __launch_bounds__(1024) rmsnorm_dgamma_kernel(const float* __restrict__ part, int parts, int d,
-                                                              float* __restrict__ dgamma) {
+                                                              float* __restrict__ dgamma, const int32_t* status,
+                                                              int32_t* err) {
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched beside the backward's end: its partial rows are complete
+  const int late = blockIdx.x == 0 && status && threadIdx.x < parts ? status[threadIdx.x] : 0;
   float v = 0.0f;
   if (c < d)
 #pragma unroll 10
     for (int i = warp; i < parts; i += 32) v += part[(int64_t)i * d + c];
   s[warp][lane] = v;
-  __syncthreads();
+  const int bad = __syncthreads_or(late);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *err = bad ? QAD_DEV_TIMEOUT : 0;
   v = warp_sum(s[lane][warp]);
   const int cw = blockIdx.x * 32 + warp;
   if (lane == 0 && cw < d) dgamma[cw] = v;
@@ -671,6 +700,11 @@ constexpr int kNormBlocks = 304;  // two per SM of 152, as many as the registers
 
 int norm_blocks(int64_t T) { return (int)(T < kNormBlocks ? T : kNormBlocks); }
 
+// The workspace: the error word, the blocks' status words from kNormStatus on, and the partial dgamma rows
+constexpr size_t kNormStatus = 256, kNormHeader = 2048;
+static_assert(kNormStatus + 4 * kNormBlocks <= kNormHeader, "a status word per block");
+size_t norm_workspace(int64_t T, int64_t d) { return kNormHeader + 4 * (size_t)norm_blocks(T) * (size_t)d; }
+
 cudaError_t launch_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* gamma, float eps,
                                int kind, void* r, void* y, void* y_hat, void* codes, float* scale, float* rstd,
                                int64_t T, int64_t d, cudaStream_t st) {
@@ -707,7 +741,7 @@ cudaError_t launch_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int6
 }
 
 cudaError_t launch_rmsnorm_bwd(const void* dy, const void* dres, const void* r, int64_t ldr, const void* gamma,
-                               const float* rstd, void* dx, float* dgamma, float* part, int64_t T, int64_t d,
+                               const float* rstd, void* dx, float* dgamma, uint8_t* ws, int64_t T, int64_t d,
                                cudaStream_t st) {
   NormBwd p = {};
   p.dy = static_cast<const __nv_bfloat16*>(dy);
@@ -716,7 +750,11 @@ cudaError_t launch_rmsnorm_bwd(const void* dy, const void* dres, const void* r, 
   p.gamma = static_cast<const __nv_bfloat16*>(gamma);
   p.rstd = rstd;
   p.dx = static_cast<__nv_bfloat16*>(dx);
-  p.part = dgamma ? part : nullptr;
+  p.part = dgamma ? reinterpret_cast<float*>(ws + kNormHeader) : nullptr;
+  p.status = dgamma ? reinterpret_cast<int32_t*>(ws + kNormStatus) : nullptr;
+  const StuckCopy stuck = stuck_copy();
+  p.stuck = stuck.row;
+  p.budget = stuck.row < 0 ? kWaitCycles : stuck.budget;
   p.T = T;
   p.ldr = ldr;
   p.nv = (int)(d / 8);
@@ -745,7 +783,9 @@ cudaError_t launch_rmsnorm_bwd(const void* dy, const void* dres, const void* r, 
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rmsnorm_dgamma_kernel, static_cast<const float*>(part), blocks, (int)d, dgamma);
+  const bool ring = lanes1 > 2 && lanes1 <= 16;  // the others write no status
+  return cudaLaunchKernelEx(&cfg, rmsnorm_dgamma_kernel, static_cast<const float*>(p.part), blocks, (int)d, dgamma,
+                            static_cast<const int32_t*>(ring ? p.status : nullptr), reinterpret_cast<int32_t*>(ws));
 }
 
 }  // namespace qad

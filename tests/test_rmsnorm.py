@@ -340,3 +340,37 @@ def test_no_epsilon(d):
         Q.qad_rmsnorm_bwd(dy, None, x, gamma, rstd, dx, None, 6, d, d)
         torch.cuda.synchronize()
         assert torch.isfinite(dx).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T, d, row", [(6000, 528, 4000), (6000, 1040, 5), (3000, 4096, 2999), (700, 2880, 0)])
+def test_a_copy_that_never_comes_is_reported(T, d, row):
+    """The backward's ring with one row's copies left out: its wait gives up (0.5 ms here), the rows of its block and
+    the weight gradient are NaN, the error word says timeout, other rows have their bits, and the next call on the same
+    workspace is clean."""
+    _lib()
+    clean = _bwd(T, d, True, seed=T)
+    r, dy, e, gamma, rstd = clean[:5]
+    ws = torch.full((Q.qad_rmsnorm_workspace_bytes(T, d),), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def call(with_ws=True):
+        dx = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
+        dg = torch.zeros(d, device="cuda") if with_ws else None
+        Q.qad_rmsnorm_bwd(dy, e, r, gamma, rstd, dx, dg, T, d, d, ws if with_ws else None)
+        return (Q.qad_check_device_error(ws) if with_ws else torch.cuda.synchronize()), dx, dg
+
+    with pytest.raises(Q.QADError):
+        Q.qad_debug_stuck_copy(0, -1)
+    Q.qad_debug_stuck_copy(row, 1_000_000)
+    try:
+        err, dx, dg = call()
+        _, dx2, _ = call(with_ws=False)
+    finally:
+        Q.qad_debug_stuck_copy(-1)
+    assert err == Q.QAD_DEV_TIMEOUT and torch.isnan(dg).all()
+    for out in (dx, dx2):
+        gone = torch.isnan(out).any(1)
+        assert gone[row] and torch.isnan(out[row]).all()
+        assert int(gone.sum()) <= -(-T // 304) + 8 and torch.equal(out[~gone], clean[5][~gone])
+    err, dx, dg = call()
+    assert err == 0 and torch.equal(dx, clean[5]) and torch.equal(dg, clean[6])
