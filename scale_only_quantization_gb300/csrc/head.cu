@@ -68,7 +68,10 @@ struct HeadParams {
 };
 
 // The kernels of a call are launched as dependents of one another: each is set up while the one before it
-// ends, and touches memory only after this wait, which the whole grid before it has completed by.
+// ends, and touches memory only after this wait, which the whole grid before it has completed by.  What those
+// before it wrote (ref, mul, tval, tcol, zt, psum, pmax, u, the header) is read by ordinary loads: the non-coherent
+// path of __ldg and of const __restrict__ is for memory that nobody writes while the kernel is resident, and such a
+// load could be moved above the wait.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -151,11 +154,11 @@ __device__ __forceinline__ void epi_logits(const HeadParams& p, const HTile& ti,
                                            int lane, int half) {
   const int64_t row = ti.mb * kTile + rank * BM + 32 * q + lane;
   const bool live = row < p.N;
-  const float ref = live ? __ldg(p.ref + row) : 0.0f;
-  const float mul = live && p.mul ? __ldg(p.mul + row) : 1.0f;
-  const float tv = live && p.tval ? __ldg(p.tval + row) : 0.0f;
+  const float ref = live ? p.ref[row] : 0.0f;
+  const float mul = live && p.mul ? p.mul[row] : 1.0f;
+  const float tv = live && p.tval ? p.tval[row] : 0.0f;
   const int col0 = ti.nb * kTile + half * 128;  // within the piece
-  const int target = live ? __ldg(p.target + row) - p.c0 - col0 : -1;  // within these 128 columns
+  const int target = live ? p.target[row] - p.c0 - col0 : -1;  // within these 128 columns
   const bool edge = col0 + 128 > p.cols;
   float sum = 0.0f, top = -INFINITY;
   uint32_t r[32], next[32];
@@ -616,13 +619,12 @@ __global__ void __launch_bounds__(128) ce_ref_kernel(const __nv_bfloat16* __rest
 // Per row, from the sweep's partial sums [parts, np]: the loss, lse and the factors of the gradients.
 // A row whose largest logit lies over kMaxAbove above its reference asks for the second sweep (again =
 // 0).  One block per 32 rows, its 32 warps taking the parts in turn.
-__global__ void __launch_bounds__(1024) ce_stats_kernel(const int32_t* gate, const float* __restrict__ psum,
-                                                        const float* __restrict__ pmax, int parts, int np, int64_t N,
+__global__ void __launch_bounds__(1024) ce_stats_kernel(const int32_t* gate, const float* psum, const float* pmax,
+                                                        int parts, int np, int64_t N,
                                                         const int32_t* __restrict__ target, int64_t V,
-                                                        const float* __restrict__ g, const float* __restrict__ zt,
-                                                        float* __restrict__ ref, float* __restrict__ mul,
-                                                        float* __restrict__ tval, float* __restrict__ loss,
-                                                        float* __restrict__ lse, int again, int32_t* hdr) {
+                                                        const float* __restrict__ g, const float* zt, float* ref,
+                                                        float* mul, float* tval, float* loss, float* lse, int again,
+                                                        int32_t* hdr) {
   let_next_start();
   wait_for_previous();
   if (gate && *gate == 0) return;
@@ -665,17 +667,16 @@ __global__ void __launch_bounds__(1024) ce_stats_kernel(const int32_t* gate, con
 }
 
 // dh_i = mul_i U_i + tval_i w_t (+ dh_i), U_i the sum over the slabs: one warp per row
-__global__ void __launch_bounds__(128) ce_dh_kernel(const float* __restrict__ u, int slabs,
-                                                    const __nv_bfloat16* __restrict__ w, int64_t ldw,
-                                                    const int32_t* __restrict__ tcol, const float* __restrict__ mul,
-                                                    const float* __restrict__ tval, int64_t N, int d, int accumulate,
+__global__ void __launch_bounds__(128) ce_dh_kernel(const float* u, int slabs, const __nv_bfloat16* __restrict__ w,
+                                                    int64_t ldw, const int32_t* tcol, const float* mul,
+                                                    const float* tval, int64_t N, int d, int accumulate,
                                                     __nv_bfloat16* dh) {
   wait_for_previous();
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= N) return;
-  const float a = __ldg(mul + row), b = __ldg(tval + row);
-  const uint4* wr = reinterpret_cast<const uint4*>(w + (int64_t)__ldg(tcol + row) * ldw);
+  const float a = mul[row], b = tval[row];
+  const uint4* wr = reinterpret_cast<const uint4*>(w + (int64_t)tcol[row] * ldw);
   uint4* out = reinterpret_cast<uint4*>(dh + row * d);
   for (int c = 32 * blockIdx.y + lane; c < d / 8; c += 32 * gridDim.y) {
     const float* ur = u + row * d + 8 * c;

@@ -623,9 +623,10 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_bwd_ring_kernel(const NormBwd 
 
 // dgamma[c] = sum over the partial rows, in a fixed order: 32 columns per block, each of 32 warps
 // adding every 32nd row.  Block 0 joins the status words (null: the backward waits for nothing) into the error word.
-__global__ void __launch_bounds__(1024) rmsnorm_dgamma_kernel(const float* __restrict__ part, int parts, int d,
-                                                              float* __restrict__ dgamma, const int32_t* status,
-                                                              int32_t* err) {
+// part and status are written while this kernel is already resident: ordinary loads after the wait, not the
+// non-coherent ones that const __restrict__ allows.
+__global__ void __launch_bounds__(1024) rmsnorm_dgamma_kernel(const float* part, int parts, int d, float* dgamma,
+                                                              const int32_t* status, int32_t* err) {
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
