@@ -324,7 +324,8 @@ int qad_linear_ce_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t ldw
  *   loss fp32 [N] (written)
  *   dh  bf16 [N, d]; added to when accumulate != 0 (after qad_linear_ce_fwd_bwd: the total loss's
  *       gradient), else overwritten
- *   err int32 [1] or NULL: a device error word of the caller's, OR-ed into (qad_check_device_error)
+ *   err int32 [1] or NULL: a device error word of the caller's, OR-ed into (qad_check_device_error).  Should
+ *       a pipeline wait time out, the rows of its thread block are NaN in loss and dh: without err the only sign.
  * Requires d % 16 == 0, d <= QAD_DISTILL_MAX_D, 1 <= K <= QAD_DISTILL_MAX_K, ldh, ldw >= d and multiples
  * of 8, inv_temp > 0 and finite.
  */
@@ -449,8 +450,8 @@ int qad_debug_wait_timeout(int32_t* err_word, int64_t budget_cycles, qad_stream_
 
 /*
  * The same for the kernels that stream token rows through a ring of bulk copies (qad_rmsnorm_bwd,
- * 512 < d <= 4096): until it is called again with row < 0, calls of this process leave out the copies of
- * token row `row` (and of the rows after it that the same warps work on), and their waits give up after `budget_cycles` SM clock cycles (0 to 2e9).
+ * 512 < d <= 4096, and qad_distill_topk_fwd_bwd): until it is called again with row < 0, calls of this process leave out the copies of
+ * token row `row` (and maybe of the rows after it that the same warps work on), and their waits give up after `budget_cycles` SM clock cycles (0 to 2e9).
  */
 int qad_debug_stuck_copy(int64_t row, int64_t budget_cycles);
 

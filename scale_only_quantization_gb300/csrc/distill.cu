@@ -30,6 +30,8 @@ struct Distill {
   __nv_bfloat16* dh;
   int32_t* err;
   int64_t ldh, ldw, V;
+  int64_t stuck;     // a row whose copies are left out (the failure path's self-check), -1: none
+  long long budget;  // clock cycles that a wait of the producers may take
   float beta;
   int K, d, accumulate;
 };
@@ -129,6 +131,16 @@ __device__ __forceinline__ uint4 ld_nc(const uint4* ptr) {
   return v;
 }
 
+// loss and dh of every step-th row from first on (one warp): a pipeline wait of their block ran out
+__device__ __forceinline__ void make_nan(const Distill& p, int64_t first, int64_t step, int64_t N, int lane) {
+  const uint32_t nans = 0x7fff7fffu;
+  for (int64_t row = first; row < N; row += step) {
+    if (lane == 0) p.loss[row] = NAN;
+    for (int c = lane; c < p.d / 8; c += 32)
+      reinterpret_cast<uint4*>(p.dh + row * p.d)[c] = make_uint4(nans, nans, nans, nans);
+  }
+}
+
 struct DistillGrid {
   int stages, teams;  // ring depth, teams per block
 };
@@ -146,7 +158,9 @@ struct DistillGrid {
 // brings its head rows, R at a time, into a ring of shared memory (one bulk copy per row) and, when a
 // row is through, takes its loss from the logits that the consumers left.  Per stage the consumers take
 // the R rows into registers and free the stage, join their dot products (one shuffle reduction for all
-// R, one named barrier of the team, none for CW = 1) and add the weighted rows to their sums.
+// R, one named barrier of the team, none for CW = 1) and add the weighted rows to their sums.  When a wait runs
+// out the producers arm no stage any more, the copies under way land, and the block's producers make the losses and dh of
+// all its rows NaN: the sign where the caller gave no error word.
 //
 // What bounds it: the gathered rows come from HBM (a head of 152k rows does not stay in L2), and a stage is
 // a chain of some 2000 cycles of waits, reductions and exponentials, so that the bytes that the SM's
@@ -218,7 +232,7 @@ __global__ void __launch_bounds__(32 * (teams_of<CW, V>() * (CW + 1)), 1)
     int64_t i = 0;
     auto finish = [&](int64_t j) {  // the loss of this team's j-th row, once its consumers are through
       const int s = (int)(j % kSlots);
-      const bool got = __all_sync(0xffffffffu, mbar_wait(done(s), (uint32_t)(j / kSlots) & 1u, &abort_flag, err));
+      const bool got = __all_sync(0xffffffffu, mbar_wait(done(s), (uint32_t)(j / kSlots) & 1u, &abort_flag, err, p.budget));
       if (got) {
         const float l = row_divergence(p, first + j * step, zz(s), ts(s), lane);
         if (lane == 0) p.loss[first + j * step] = l;
@@ -261,20 +275,23 @@ __global__ void __launch_bounds__(32 * (teams_of<CW, V>() * (CW + 1)), 1)
       for (int k = lane; k < K; k += 32) pk(slot)[k] *= rt;
       __syncwarp();
       for (int b = 0; b < groups; ++b) {
-        ok = __all_sync(0xffffffffu, mbar_wait(empty(stage), phase ^ 1u, &abort_flag, err));
+        // a consumer whose wait ran out has raised the flag before it freed the stage: no stage is armed after that
+        ok = __all_sync(0xffffffffu, mbar_wait(empty(stage), phase ^ 1u, &abort_flag, err, p.budget) &&
+                                         !*static_cast<volatile int*>(&abort_flag));
         if (!ok) break;
         const int k = b * R + lane;
         const int32_t v = lane < R && k < K ? tok[k] : -1;
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, v >= 0)), bytes = (uint32_t)nv * 16u;
-        if (lane == 0) mbar_expect_tx(full(stage), n * bytes);
+        const bool stuck = row == p.stuck;
+        if (lane == 0 && !stuck) mbar_expect_tx(full(stage), n * bytes);
         __syncwarp();
-        if (v >= 0)
+        if (v >= 0 && !stuck)
           asm volatile(
               "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                   smem_u32(ring + (size_t)(stage * R + lane) * nv)),
               "l"(reinterpret_cast<uint64_t>(p.w + (int64_t)v * p.ldw)), "r"(bytes), "r"(full(stage))
               : "memory");
-        armed |= 1u << stage;
+        if (!stuck) armed |= 1u << stage;
         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == stages) {
           stage = 0;
@@ -284,11 +301,13 @@ __global__ void __launch_bounds__(32 * (teams_of<CW, V>() * (CW + 1)), 1)
       if (++slot == kSlots) slot = 0;
     }
     for (int64_t j = i > kSlots ? i - kSlots : 0; ok && j < i; ++j) ok = finish(j);
-    if (abort_flag) {  // copies may be under way: they land (bounded wait) before shared memory is given back
-      volatile int none = 0;
+    if (*static_cast<volatile int*>(&abort_flag)) {
+      volatile int none = 0;  // copies may be under way: they land (bounded wait) before shared memory is given back
       for (int s = 0; s < stages; ++s)
         if (armed & (1u << s)) mbar_wait(full(s), (armed_parity >> s) & 1u, &none, &late);
     }
+    __syncthreads();  // the consumers' stores are over
+    if (abort_flag) make_nan(p, first, step, N, lane);
     return;
   }
 
@@ -311,7 +330,7 @@ __global__ void __launch_bounds__(32 * (teams_of<CW, V>() * (CW + 1)), 1)
     float M = 0.0f, S = 0.0f, S1 = 0.0f, soff = 0.0f;
     bool some = false;
     for (int b = 0; b < groups; ++b) {
-      // a wait that ran out leaves wrong values and the error bit; the team's barriers stay in step
+      // a wait that ran out leaves the error bit and wrong values, replaced below; the team's barriers stay in step
       mbar_wait(full(stage), phase, &abort_flag, err);
       __syncwarp();
       const int k = b * R + (lane & (R - 1));  // this lane's head row of the stage
@@ -452,6 +471,7 @@ __global__ void __launch_bounds__(32 * (teams_of<CW, V>() * (CW + 1)), 1)
       out[c] = pack8(v);
     }
   }
+  __syncthreads();  // with the producers
 }
 
 // As many teams as a block holds, with the deepest ring; fewer teams where the rows' arrays (many kept
@@ -591,6 +611,9 @@ cudaError_t launch_distill_topk(const void* h, int64_t ldh, const void* w, int64
   p.K = (int)K;
   p.d = (int)d;
   p.accumulate = accumulate;
+  const StuckCopy stuck = stuck_copy();
+  p.stuck = stuck.row;
+  p.budget = stuck.row < 0 ? kWaitCycles : stuck.budget;
   // a team as wide as the row needs, each lane with 16 of its columns and their three sums
   prof_begin(QAD_K_DISTILL, st);
   cudaError_t e;

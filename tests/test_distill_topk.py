@@ -239,3 +239,29 @@ def test_nan_in_a_head_row_reaches_the_rows_that_name_it_only():
             assert torch.isnan(l2[i])
         else:
             assert torch.equal(loss[i], l2[i]) and torch.equal(dh[i], d2[i])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mixed", [False, True])
+@pytest.mark.parametrize("N, d, K, row", [(400, 2048, 20, 250), (200, 4096, 9, 0), (1500, 256, 40, 1499), (40, 8192, 5, 3)])
+def test_a_copy_that_never_comes_is_reported(N, d, K, row, mixed):
+    """One token row's copies left out: the wait gives up (0.5 ms here), the rows of its block are NaN in loss and dh, with
+    or without an error word to say so, other rows have their bits, and the next call is clean."""
+    _lib()
+    c = make(N, d, 300, K, seed=40, mixed=mixed)
+    loss, dh = run(c)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    Q.qad_debug_stuck_copy(row, 1_000_000)
+    try:
+        got = [run(c, err=err), run(c)]
+    finally:
+        Q.qad_debug_stuck_copy(-1)
+    assert Q.qad_check_device_error(err) == Q.QAD_DEV_TIMEOUT
+    for l2, d2 in got:
+        gone = torch.isnan(l2)
+        assert gone[row] and torch.equal(gone, torch.isnan(d2).all(1)) and torch.equal(gone, torch.isnan(d2).any(1))
+        assert int(gone.sum()) <= 8 * -(-N // 152) + 8
+        assert torch.equal(l2[~gone], loss[~gone]) and torch.equal(d2[~gone], dh[~gone])
+    err.zero_()
+    l2, d2 = run(c, err=err)
+    assert Q.qad_check_device_error(err) == 0 and torch.equal(l2, loss) and torch.equal(d2, dh)
