@@ -292,7 +292,7 @@ int qad_rmsnorm_bwd(const void* dy, const void* dres, const void* r, const void*
  *          e.g. lm_weight / tokens; loss itself is not scaled by it
  *   loss, lse fp32 [N] (written)
  *   dh     bf16 [N, d] or NULL; added to when accumulate != 0, else overwritten
- *   dw     bf16 [V, d] or NULL (overwritten); one of dh and dw must be given.  Every row of h, also
+ *   dw     bf16 [V, d] or NULL (overwritten); one of dh and dw must be given unless N = 0.  Every row of h, also
  *          one without a target, must be finite when dw is asked for.
  *   ws     256-byte aligned, ws_bytes >= qad_linear_ce_workspace_bytes(N, d, V, dh != NULL, dw != NULL).
  *          Its first word is the device error word (qad_check_device_error), cleared by each call.

@@ -333,3 +333,14 @@ def test_neighbouring_calls_share_a_workspace():
     for o, w in zip(outs, want):
         for n in o:
             assert torch.equal(o[n], w[n])
+
+
+@pytest.mark.gpu
+def test_no_rows_with_a_hidden_gradient_only():
+    """N = 0 with dh alone: an empty tensor has no address, and the call has nothing to write."""
+    _lib()
+    w = torch.randn((300, 64), device="cuda").to(torch.bfloat16)
+    e = torch.empty(0, device="cuda")
+    ws = torch.full((Q.qad_linear_ce_workspace_bytes(0, 64, 300, 1, 0),), 0xFF, dtype=torch.uint8, device="cuda")
+    Q.qad_linear_ce_fwd_bwd(e, 64, w, 64, e, None, e, e, e, None, 0, 0, 64, 300, ws)
+    assert Q.qad_check_device_error(ws) == 0

@@ -151,3 +151,14 @@ def test_norm_and_losses_in_a_cuda_graph():
     torch.cuda.synchronize()
     for v, r in zip((y, ce, lse, kd, dh), ref):
         assert torch.equal(v, r)
+
+
+@pytest.mark.gpu
+def test_head_loss_of_no_rows():
+    from scale_only_quantization_gb300.autograd import QADHeadLoss
+    _build()
+    head = QADHeadLoss(torch.randn((100, 64), device="cuda"))
+    h = torch.empty((0, 64), device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    total, lm, _ = head(h, torch.empty(0, dtype=torch.int64, device="cuda"))
+    total.backward()
+    assert float(total.detach()) == 0 and float(lm.detach()) == 0 and h.grad.shape == (0, 64)
