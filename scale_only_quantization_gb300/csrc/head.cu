@@ -656,11 +656,12 @@ __global__ void __launch_bounds__(1024) ce_stats_kernel(const int32_t* gate, con
   }
   const float et = expf(z - r);  // 1 unless the row's reference was replaced
   const float total = s + et;
-  const float l = (r - z) + (r == z ? log1pf(s) : logf(total));
+  const float log_sum = r == z ? log1pf(s) : logf(total);
+  const float l = (r - z) + log_sum;
   const bool live = t >= 0 && t < V;
   const float gi = live ? (g ? g[row] : 1.0f) : 0.0f;
   loss[row] = live ? l : 0.0f;
-  lse[row] = z + l;
+  lse[row] = r + log_sum;  // not by way of the target's logit, which may be far below
   // a row that carries no loss has a zero gradient whatever its logits are
   mul[row] = live ? gi / total : 0.0f;
   tval[row] = live ? -gi * (s / total) : 0.0f;

@@ -344,3 +344,32 @@ def test_no_rows_with_a_hidden_gradient_only():
     ws = torch.full((Q.qad_linear_ce_workspace_bytes(0, 64, 300, 1, 0),), 0xFF, dtype=torch.uint8, device="cuda")
     Q.qad_linear_ce_fwd_bwd(e, 64, w, 64, e, None, e, e, e, None, 0, 0, 64, 300, ws)
     assert Q.qad_check_device_error(ws) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [3, 150])
+def test_normaliser_of_a_target_far_below(N):
+    """lse does not pass through the target's logit: with logits 0, 1, 2, ... and a target at -2^20 (all products exact
+    in fp32) it keeps its precision, whose ulp at 2^20 would be 1/8; a target at -inf leaves it finite."""
+    _lib()
+    V, d = 300, 16
+    w = torch.zeros((V, d), device="cuda", dtype=torch.bfloat16)
+    w[:, 0] = torch.arange(V, device="cuda") % 8
+    w[7, 0], w[7, 1] = 0.0, -(2.0 ** 20)
+    w[9, 0], w[9, 2] = 0.0, -3e38
+    h = torch.zeros((N, d), device="cuda", dtype=torch.bfloat16)
+    h[:, 0] = 1.0
+    h[0::3, 1] = 1.0     # the target's logit is -2^20
+    h[1::3, 2] = 8.0     # ... below fp32's range
+    target = torch.full((N,), 7, dtype=torch.int32, device="cuda")
+    target[1::3] = 9
+    target[2::3] = 8
+    c = dict(h=h, w=w, target=target, g=torch.ones(N, device="cuda"), N=N, d=d, V=V)
+    o = run(c)
+    z = h.double() @ w.double().T
+    lse = torch.logsumexp(z, 1)
+    assert torch.all((o["lse"].double() - lse).abs() <= 2e-6 * (1 + lse.abs()))
+    want = lse - z.gather(1, target.long()[:, None])[:, 0]
+    assert torch.isinf(o["loss"][1::3]).all()
+    ok = torch.arange(N, device="cuda") % 3 != 1
+    assert torch.all((o["loss"].double() - want).abs()[ok] <= 2e-6 * (1 + want.abs()[ok]))
