@@ -318,7 +318,8 @@ int qad_linear_ce_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t ldw
  *   h bf16 [N, d], ldh between rows     w bf16 [V, d], ldw between rows (no gradient: the head is frozen)
  *   idx int32 [N, K], t_logit fp32 [N, K] (logits or log-probabilities: a row's common offset does not
  *       matter).  A slot with idx < 0 or t_logit = -inf does not count; idx >= V neither, and
- *       QAD_DEV_BAD_INDEX is set in *err.  A row that keeps no slot has loss 0 and dh 0.
+ *       QAD_DEV_BAD_INDEX is set in *err.  A row that keeps no slot has loss 0 and dh 0.  A finite logit counts
+ *       however low it is: with p = 0 there, the reverse divergence grows with its distance.
  *   mix fp32 [N] or NULL (0: forward KL; 1: reverse KL)
  *   g   fp32 [N] or NULL (1): the derivative of the total loss with respect to each row's loss
  *   loss fp32 [N] (written)

@@ -36,6 +36,13 @@ struct Distill {
   int K, d, accumulate;
 };
 
+// beta t of a slot: -inf says that the slot does not count, so a finite logit of the lowest values, whose product leaves
+// fp32's range, stays finite (its probability is 0 all the same)
+__device__ __forceinline__ float softened(float t, float beta) {
+  const float b = t * beta;
+  return b == -INFINITY && t != -INFINITY ? -3.402823466e38f : b;
+}
+
 // p f(x), with q = p e^x: a Taylor sum where e^x - 1 - x would cancel (|x| < 1/2: the first
 // omitted term is below 2^-29 of the sum), the difference of the two probabilities elsewhere.
 __device__ __forceinline__ float div_term(float p, float q, float x) {
@@ -85,7 +92,8 @@ __device__ __forceinline__ float row_divergence(const Distill& p, int64_t row, c
   kl = warp_sum(kl);
   rkl = warp_sum(rkl);
   const float m = p.mix ? p.mix[row] : 0.0f;
-  return (1.0f - m) * kl + m * rkl;
+  // a part without a share is left out: it may be infinite (RKL, where the teacher's logit is the lowest value)
+  return (m != 1.0f ? (1.0f - m) * kl : 0.0f) + (m != 0.0f ? m * rkl : 0.0f);
 }
 
 // Sums of R values over the warp's 32 lanes (R a power of two): lane l returns the sum of value
@@ -246,7 +254,7 @@ __global__ void __launch_bounds__(32 * (teams_of<CW, V>() * (CW + 1)), 1)
       if (!ok) break;
       float mt = -INFINITY;
       auto take = [&](int k, int32_t v, float t) {
-        t *= p.beta;
+        t = softened(t, p.beta);
         if (v >= p.V) {
           if (p.err) atomicOr(p.err, QAD_DEV_BAD_INDEX);
           v = -1;
@@ -444,7 +452,8 @@ __global__ void __launch_bounds__(32 * (teams_of<CW, V>() * (CW + 1)), 1)
     const float scale = p.beta * (p.g ? __ldg(p.g + row) : 1.0f);
     const float m = MIX ? __ldg(p.mix + row) : 0.0f;
     const float rs = some ? scale / S : 0.0f;
-    const float ka = ((1.0f - m) - (MIX && some ? m * (S1 / S) : 0.0f)) * rs, k1 = m * rs, kb = -(1.0f - m) * scale;
+    const bool reverse = MIX && some && m != 0.0f;  // else its sums are left out: they may be infinite
+    const float ka = ((1.0f - m) - (reverse ? m * (S1 / S) : 0.0f)) * rs, k1 = m * rs, kb = -(1.0f - m) * scale;
     uint4* out = reinterpret_cast<uint4*>(p.dh + row * p.d);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -458,8 +467,10 @@ __global__ void __launch_bounds__(32 * (teams_of<CW, V>() * (CW + 1)), 1)
         v[2 * i + 1] = ka * x.y + kb * y.y;
         if constexpr (MIX) {
           const float2 u = f2unpack(a1[j][i]);
-          v[2 * i] += k1 * u.x;
-          v[2 * i + 1] += k1 * u.y;
+          if (reverse) {
+            v[2 * i] += k1 * u.x;
+            v[2 * i + 1] += k1 * u.y;
+          }
         }
       }
       if (p.accumulate) {
@@ -520,7 +531,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) distill_fwd_kernel(co
   for (int c = tid; c < nv; c += THREADS) hs[c] = __ldg(hr + c);
   for (int k = tid; k < K; k += THREADS) {
     int32_t v = __ldg(p.idx + row * K + k);
-    float t = __ldg(p.t + row * K + k) * p.beta;
+    float t = softened(__ldg(p.t + row * K + k), p.beta);
     if (v >= p.V) {
       if (p.err) atomicOr(p.err, QAD_DEV_BAD_INDEX);
       v = -1;

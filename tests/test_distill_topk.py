@@ -265,3 +265,27 @@ def test_a_copy_that_never_comes_is_reported(N, d, K, row, mixed):
     err.zero_()
     l2, d2 = run(c, err=err)
     assert Q.qad_check_device_error(err) == 0 and torch.equal(l2, loss) and torch.equal(d2, dh)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("beta", [0.5, 1.0, 2.0])
+@pytest.mark.parametrize("low", [-1e4, -1e30, torch.finfo(torch.float32).min])
+def test_teacher_logits_of_the_lowest_value(low, beta):
+    """A finite teacher logit counts however low it is and whatever the temperature: p = 0 there, the student's
+    probability is taken over it.  With the forward divergence alone, and in rows of a mix whose share of the reverse
+    one is 0, loss and gradient stay finite and are those of the definition."""
+    _lib()
+    c = make(24, 256, 400, 12, seed=31, mixed=True)
+    c["t"][::2, 7:] = low
+    c["t"][1::4, :3] = low
+    for mix in (None, torch.zeros(24, device="cuda")):
+        e = {**c, "mix": mix}
+        loss, dh = run(e, beta)
+        l64, d64, _, _ = exact(e, beta)
+        assert torch.isfinite(loss).all() and torch.isfinite(dh.float()).all()
+        # a logit is 4 packed products, a sum and 5 steps of a reduction: 10 roundings of at most sum |h w|
+        w = c["w"][c["idx"].long()].double().abs()
+        err = 10 * U * (w @ c["h"].double().abs()[:, :, None])[:, :, 0].amax(1)
+        assert torch.all((loss.double() - l64).abs() <= 2 * beta * err + 4e-6 * (1 + l64.abs()))
+        assert torch.all((dh.double() - d64).norm(dim=1) <= 1e-2 * d64.norm(dim=1))  # bf16: 2^-8 of an element
+        assert torch.equal(run(e, beta, grad=False)[0], loss)
