@@ -160,11 +160,12 @@ class QADHeadLossFunction(torch.autograd.Function):
     divergence over the teacher's top tokens idx [N, K] with logits t [N, K], softened by tau, mixed
     forward and reverse by mix [N] (None: forward).  Either part is left out when its target or idx is
     None.  The hidden-state gradient is formed in the forward, where the logits are, and scaled by the
-    upstream gradient in the backward.  Returns (total, CE [N] or None, KD [N] or None).
+    upstream gradient in the backward.  err int32 [1]: a device error word that the calls' is OR-ed into.
+    Returns (total, CE [N] or None, KD [N] or None).
     """
 
     @staticmethod
-    def forward(ctx, h, w, target, g_lm, idx, t, g_kd, tau, mix):
+    def forward(ctx, h, w, target, g_lm, idx, t, g_kd, tau, mix, err):
         V, d = w.shape
         if w.dtype != torch.bfloat16 or not w.is_contiguous():
             raise ValueError("the head must be a contiguous bf16 [V, d]")
@@ -182,6 +183,7 @@ class QADHeadLossFunction(torch.autograd.Function):
             ce, lse = torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev)
             ws = torch.empty(qad_linear_ce_workspace_bytes(N, d, V, 1, 0), dtype=torch.uint8, device=dev)
             qad_linear_ce_fwd_bwd(h2, ld, w, d, target, g_lm, ce, lse, dh, None, 0, N, d, V, ws)
+            err.bitwise_or_(ws[:4].view(torch.int32))
             total = total + torch.dot(ce, g_lm)
         if idx is not None:
             K = idx.shape[-1]
@@ -193,7 +195,7 @@ class QADHeadLossFunction(torch.autograd.Function):
                 raise ValueError("one distillation weight (and mix) per row of h")
             kd = torch.empty(N, dtype=torch.float32, device=dev)
             qad_distill_topk_fwd_bwd(h2, ld, w, d, idx, t, mix, 1.0 / tau, g_kd, kd, dh, int(target is not None), N, d, V,
-                                     K)
+                                     K, err)
             total = total + torch.dot(kd, g_kd)
         if target is None and idx is None:
             raise ValueError("neither targets nor teacher logits")
@@ -205,7 +207,7 @@ class QADHeadLossFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dtotal, _ce, _kd):
         (dh,) = ctx.saved_tensors
-        return ((dh * dtotal).to(torch.bfloat16).view(ctx.shape), None, None, None, None, None, None, None, None)
+        return ((dh * dtotal).to(torch.bfloat16).view(ctx.shape), None, None, None, None, None, None, None, None, None)
 
 
 class QADHeadLoss(torch.nn.Module):
@@ -214,23 +216,32 @@ class QADHeadLoss(torch.nn.Module):
 
     forward(h, target=None, teacher_idx=None, teacher_logits=None, mix=None) -> (total, lm, distill): lm is
     the cross entropy over the rows with a target, distill the divergence over the teacher's top tokens.
+    A target or teacher token past the vocabulary carries nothing, as a negative one does, and sets a bit that
+    device_error() returns.
     """
 
     def __init__(self, w, lm_weight=1.0, distill_weight=1.0, tau=1.0):
         super().__init__()
         self.register_buffer("w", w.to(torch.bfloat16).contiguous())
+        self.register_buffer("err", torch.zeros(1, dtype=torch.int32, device=w.device), persistent=False)
         self.lm_weight, self.distill_weight, self.tau = float(lm_weight), float(distill_weight), float(tau)
+
+    def device_error(self):
+        """The QAD_DEV_* bits of the calls since it was last read (0: none), and clears them; waits for the device."""
+        code = int(self.err.item())
+        self.err.zero_()
+        return code
 
     def forward(self, h, target=None, teacher_idx=None, teacher_logits=None, mix=None):
         N = h.numel() // h.shape[-1]
         one = torch.ones(N, dtype=torch.float32, device=h.device)
         g_lm = g_kd = None
         if target is not None:
-            live = (target.reshape(-1) >= 0).to(torch.float32)
+            live = ((target >= 0) & (target < self.w.shape[0])).reshape(-1).to(torch.float32)
             g_lm = live * (self.lm_weight / live.sum().clamp_min(1.0))
         if teacher_idx is not None:
             g_kd = one * (self.distill_weight / max(N, 1))
         total, ce, kd = QADHeadLossFunction.apply(h, self.w, target, g_lm, teacher_idx, teacher_logits, g_kd, self.tau,
-                                                  mix)
+                                                  mix, self.err)
         lm = None if ce is None else ce.sum() / live.sum().clamp_min(1.0)
         return total, lm, None if kd is None else kd.mean()

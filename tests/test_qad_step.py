@@ -162,3 +162,38 @@ def test_head_loss_of_no_rows():
     total, lm, _ = head(h, torch.empty(0, dtype=torch.int64, device="cuda"))
     total.backward()
     assert float(total.detach()) == 0 and float(lm.detach()) == 0 and h.grad.shape == (0, 64)
+
+
+@pytest.mark.gpu
+def test_head_loss_reports_tokens_past_the_vocabulary():
+    """A target or teacher token that is not in the vocabulary: its row carries nothing, the mean is over the others, and
+    the module's error word says so until it is read."""
+    from scale_only_quantization_gb300.autograd import QADHeadLoss
+    _build()
+    N, d, V, K = 40, 64, 300, 8
+    w = (torch.randn((V, d), device="cuda") * d ** -0.5).to(torch.bfloat16)
+    h = torch.randn((N, d), device="cuda").to(torch.bfloat16).requires_grad_(True)
+    target = torch.randint(0, V, (N,), device="cuda")
+    idx = torch.randint(0, V, (N, K), device="cuda", dtype=torch.int32)
+    t = torch.randn((N, K), device="cuda")
+    head = QADHeadLoss(w)
+    for want in (0, Q.QAD_DEV_BAD_INDEX, 0):
+        tg, ix = target.clone(), idx.clone()
+        if want:
+            tg[3], tg[9] = V, 2 ** 30
+        total, lm, kd = head(h, tg, ix, t)
+        assert head.device_error() == want
+        z = h.detach().double() @ w.double().T
+        live = tg < V
+        ref = torch.nn.functional.cross_entropy(z[live], tg[live])
+        assert abs(float(lm.detach()) - float(ref)) < 1e-5
+        if want:
+            total.backward()
+            assert torch.isfinite(h.grad.float()).all()
+    ix = idx.clone()
+    ix[5, 2] = V
+    head(h, None, ix, t)
+    with torch.no_grad():
+        head(h, target, idx, t)          # a clean call does not clear what an earlier one reported
+    assert head.device_error() == Q.QAD_DEV_BAD_INDEX
+    assert head.device_error() == 0      # read and cleared
