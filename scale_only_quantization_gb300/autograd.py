@@ -80,13 +80,19 @@ class QADMoE(torch.nn.Module):
                                     self.w2, self.s2, self.fmt, self.flags)
 
 
+def _packed(t):
+    """t, contiguous and on a 16-byte boundary: contiguous() alone returns a view such as ids[1:] where it lies."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def _rows(t, d, what):
     """t as [rows, d] bf16 rows that the library can read: unit column stride, 16-byte aligned rows."""
     if t.dtype != torch.bfloat16 or t.shape[-1] != d:
         raise ValueError("%s must be bf16 with %d columns, got %s %s" % (what, d, t.dtype, tuple(t.shape)))
     t = t.reshape(-1, d)
     if t.stride(1) != 1 or t.stride(0) % 8 or t.stride(0) < d or t.data_ptr() % 16:
-        t = t.contiguous()
+        t = _packed(t)
     return t
 
 
@@ -112,7 +118,7 @@ class QADRMSNormFunction(torch.autograd.Function):
         rstd = torch.empty(T, dtype=torch.float32, device=dev)
         codes = torch.empty((T, d), dtype=torch.uint8, device=dev) if act != QAD_ACT_NONE else None
         scale = torch.empty(T, dtype=torch.float32, device=dev) if act != QAD_ACT_NONE else None
-        gamma = gamma.contiguous()
+        gamma = _packed(gamma)
         qad_rmsnorm_fwd(x2, res2, gamma, eps, act, r, y, None, codes, scale, rstd, T, d, x2.stride(0) if T > 1 else d,
                         res2.stride(0) if res2 is not None and T > 1 else d)
         ctx.save_for_backward(r, gamma, rstd)
@@ -127,8 +133,8 @@ class QADRMSNormFunction(torch.autograd.Function):
     def backward(ctx, dy, dr, _codes, _scale):
         r, gamma, rstd = ctx.saved_tensors
         T, d = r.shape
-        dy2 = (torch.zeros_like(r) if dy is None else dy).reshape(T, d).contiguous()
-        dr2 = None if dr is None else dr.reshape(T, d).contiguous()
+        dy2 = _packed((torch.zeros_like(r) if dy is None else dy).reshape(T, d))
+        dr2 = None if dr is None else _packed(dr.reshape(T, d))
         dx = torch.empty_like(r)
         need = ctx.needs_input_grad[2]
         dgamma = torch.empty(d, dtype=torch.float32, device=r.device) if need else None
@@ -144,7 +150,7 @@ class QADRMSNorm(torch.nn.Module):
 
     def __init__(self, weight, eps=1e-6, act=QAD_ACT_NONE, trained=False):
         super().__init__()
-        self.weight = torch.nn.Parameter(weight.to(torch.bfloat16).contiguous(), requires_grad=trained)
+        self.weight = torch.nn.Parameter(_packed(weight.to(torch.bfloat16)), requires_grad=trained)
         self.eps = float(eps)
         self.act = int(act)
 
@@ -176,8 +182,8 @@ class QADHeadLossFunction(torch.autograd.Function):
         total = torch.zeros((), dtype=torch.float32, device=dev)
         ce = kd = None
         if target is not None:
-            target = target.reshape(-1).to(torch.int32).contiguous()
-            g_lm = g_lm.to(torch.float32).contiguous()
+            target = _packed(target.reshape(-1).to(torch.int32))
+            g_lm = _packed(g_lm.to(torch.float32))
             if target.numel() != N or g_lm.numel() != N:
                 raise ValueError("one target and one weight per row of h")
             ce, lse = torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev)
@@ -187,10 +193,10 @@ class QADHeadLossFunction(torch.autograd.Function):
             total = total + torch.dot(ce, g_lm)
         if idx is not None:
             K = idx.shape[-1]
-            idx = idx.reshape(N, K).to(torch.int32).contiguous()
-            t = t.reshape(N, K).to(torch.float32).contiguous()
-            g_kd = g_kd.to(torch.float32).contiguous()
-            mix = None if mix is None else mix.to(torch.float32).contiguous()
+            idx = _packed(idx.reshape(N, K).to(torch.int32))
+            t = _packed(t.reshape(N, K).to(torch.float32))
+            g_kd = _packed(g_kd.to(torch.float32))
+            mix = None if mix is None else _packed(mix.to(torch.float32))
             if g_kd.numel() != N or (mix is not None and mix.numel() != N):
                 raise ValueError("one distillation weight (and mix) per row of h")
             kd = torch.empty(N, dtype=torch.float32, device=dev)
@@ -222,7 +228,7 @@ class QADHeadLoss(torch.nn.Module):
 
     def __init__(self, w, lm_weight=1.0, distill_weight=1.0, tau=1.0):
         super().__init__()
-        self.register_buffer("w", w.to(torch.bfloat16).contiguous())
+        self.register_buffer("w", _packed(w.to(torch.bfloat16)))
         self.register_buffer("err", torch.zeros(1, dtype=torch.int32, device=w.device), persistent=False)
         self.lm_weight, self.distill_weight, self.tau = float(lm_weight), float(distill_weight), float(tau)
 

@@ -197,3 +197,51 @@ def test_head_loss_reports_tokens_past_the_vocabulary():
         head(h, target, idx, t)          # a clean call does not clear what an earlier one reported
     assert head.device_error() == Q.QAD_DEV_BAD_INDEX
     assert head.device_error() == 0      # read and cleared
+
+
+def test_views_off_a_16_byte_boundary_are_copied():
+    """contiguous() returns a contiguous view as it is, wherever it starts."""
+    from scale_only_quantization_gb300.autograd import _packed, _rows
+    ids = torch.arange(41, dtype=torch.int32)
+    for v in (ids[1:], torch.arange(9.0)[3:], torch.arange(16, dtype=torch.uint8)[5:].view(torch.uint8)):
+        p = _packed(v)
+        assert p.data_ptr() % 16 == 0 and p.is_contiguous() and torch.equal(p, v)
+    assert _packed(ids).data_ptr() == ids.data_ptr()             # an aligned one is read in place
+    flat = torch.arange(6 * 64 + 8, dtype=torch.float32).to(torch.bfloat16)
+    x = flat[1: 1 + 6 * 64].view(6, 64)
+    r = _rows(x, 64, "x")
+    assert x.is_contiguous() and x.data_ptr() % 16 and r.data_ptr() % 16 == 0 and torch.equal(r, x)
+
+
+@pytest.mark.gpu
+def test_shifted_targets_and_other_misaligned_views():
+    """target = ids[1:] in int32, and every other input as a view that starts off a 16-byte boundary."""
+    from scale_only_quantization_gb300.autograd import QADHeadLoss, QADRMSNorm
+    _build()
+    N, d, V, K = 33, 64, 300, 8
+    bf = torch.bfloat16
+
+    def off(t):  # the same values, one element into a buffer of their own
+        b = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        b[1:] = t.reshape(-1)
+        return b[1:].view(t.shape)
+
+    w = (torch.randn((V, d), device="cuda") * d ** -0.5).to(bf)
+    h = torch.randn((N, d), device="cuda").to(bf)
+    ids = torch.randint(0, V, (N + 1,), device="cuda", dtype=torch.int32)
+    idx = torch.randint(0, V, (N, K), device="cuda", dtype=torch.int32)
+    t, mix = torch.randn((N, K), device="cuda"), torch.rand(N, device="cuda")
+    head = QADHeadLoss(w)
+    a, b = h.clone().requires_grad_(True), off(h).requires_grad_(True)
+    ta = head(a, ids[1:].clone(), idx, t, mix)
+    tb = QADHeadLoss(off(w))(b, ids[1:], off(idx), off(t), off(mix))
+    ta[0].backward()
+    tb[0].backward()
+    assert all(torch.equal(x, y) for x, y in zip(ta, tb)) and torch.equal(a.grad, b.grad)
+    norm = QADRMSNorm(1 + 0.1 * torch.randn(d, device="cuda"), trained=True)
+    norm2 = QADRMSNorm(off(norm.weight.detach()), trained=True)
+    a, b, g = h.clone().requires_grad_(True), off(h).requires_grad_(True), torch.randn((N, d), device="cuda").to(bf)
+    ya, yb = norm(a, h), norm2(b, off(h))
+    torch.autograd.backward([ya[0], ya[1]], [g, h])
+    torch.autograd.backward([yb[0], yb[1]], [off(g), off(h)])
+    assert torch.equal(ya[0], yb[0]) and torch.equal(a.grad, b.grad) and torch.equal(norm.weight.grad, norm2.weight.grad)
