@@ -221,7 +221,8 @@ class QADHeadLoss(torch.nn.Module):
     section 二.5): total = lm_weight * lm + distill_weight * distill, each a mean over its tokens.
 
     forward(h, target=None, teacher_idx=None, teacher_logits=None, mix=None) -> (total, lm, distill): lm is
-    the cross entropy over the rows with a target, distill the divergence over the teacher's top tokens.
+    the cross entropy over the rows with a target, distill the divergence over the teacher's top tokens, over the
+    rows that keep one (a teacher_idx in the vocabulary whose logit is not -inf): padding does not dilute either mean.
     A target or teacher token past the vocabulary carries nothing, as a negative one does, and sets a bit that
     device_error() returns.
     """
@@ -240,14 +241,17 @@ class QADHeadLoss(torch.nn.Module):
 
     def forward(self, h, target=None, teacher_idx=None, teacher_logits=None, mix=None):
         N = h.numel() // h.shape[-1]
-        one = torch.ones(N, dtype=torch.float32, device=h.device)
         g_lm = g_kd = None
         if target is not None:
             live = ((target >= 0) & (target < self.w.shape[0])).reshape(-1).to(torch.float32)
             g_lm = live * (self.lm_weight / live.sum().clamp_min(1.0))
         if teacher_idx is not None:
-            g_kd = one * (self.distill_weight / max(N, 1))
+            K = teacher_idx.shape[-1]
+            teacher_idx, teacher_logits = teacher_idx.reshape(N, K), teacher_logits.reshape(N, K)
+            kept = (teacher_idx >= 0) & (teacher_idx < self.w.shape[0]) & (teacher_logits != -torch.inf)
+            kept = kept.any(1).to(torch.float32)
+            g_kd = kept * (self.distill_weight / kept.sum().clamp_min(1.0))
         total, ce, kd = QADHeadLossFunction.apply(h, self.w, target, g_lm, teacher_idx, teacher_logits, g_kd, self.tau,
                                                   mix, self.err)
         lm = None if ce is None else ce.sum() / live.sum().clamp_min(1.0)
-        return total, lm, None if kd is None else kd.mean()
+        return total, lm, None if kd is None else kd.sum() / kept.sum().clamp_min(1.0)

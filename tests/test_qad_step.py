@@ -245,3 +245,30 @@ def test_shifted_targets_and_other_misaligned_views():
     torch.autograd.backward([ya[0], ya[1]], [g, h])
     torch.autograd.backward([yb[0], yb[1]], [off(g), off(h)])
     assert torch.equal(ya[0], yb[0]) and torch.equal(a.grad, b.grad) and torch.equal(norm.weight.grad, norm2.weight.grad)
+
+
+@pytest.mark.gpu
+def test_distillation_mean_is_over_the_rows_that_keep_a_token():
+    """Padding rows (no teacher token) neither shrink the distillation loss nor its gradient."""
+    from scale_only_quantization_gb300.autograd import QADHeadLoss
+    _build()
+    N, d, V, K = 30, 64, 300, 8
+    w = (torch.randn((V, d), device="cuda") * d ** -0.5).to(torch.bfloat16)
+    h = torch.randn((N, d), device="cuda").to(torch.bfloat16)
+    idx = torch.randint(0, V, (N, K), device="cuda", dtype=torch.int32)
+    t = torch.randn((N, K), device="cuda") * 2
+    idx[20:25] = -1
+    t[25:28] = -float("inf")
+    idx[28:, :] = V          # not in the vocabulary: not kept either
+    head = QADHeadLoss(w, distill_weight=0.5)
+    a, b = h.clone().requires_grad_(True), h[:20].clone().requires_grad_(True)
+    ta, tb = head(a, None, idx, t), head(b, None, idx[:20], t[:20])
+    ta[0].backward()
+    tb[0].backward()
+    assert abs(float(ta[2] - tb[2])) <= 1e-6 * float(tb[2]) and abs(float((ta[0] - tb[0]).detach())) <= 1e-6
+    assert torch.all(a.grad[20:] == 0)
+    assert torch.all((a.grad[:20].double() - b.grad.double()).abs() <= 2.0 ** -7 * b.grad.double().abs())
+    none = head(h, None, torch.full_like(idx, -1), t)
+    assert float(none[0]) == 0 and float(none[2]) == 0
+    other = head(h.view(5, 6, d), None, idx.view(5, 6, K), t)       # the same rows in other shapes
+    assert torch.equal(other[0], ta[0].detach())
