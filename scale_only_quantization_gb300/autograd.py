@@ -213,7 +213,9 @@ class QADHeadLossFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dtotal, _ce, _kd):
         (dh,) = ctx.saved_tensors
-        return ((dh * dtotal).to(torch.bfloat16).view(ctx.shape), None, None, None, None, None, None, None, None, None)
+        # as a 1 x 1 tensor the factor stays fp32 (a scalar tensor would be rounded to dh's bf16 first); one rounding
+        dh = torch.mul(dh, dtotal.to(torch.float32).view(1, 1), out=torch.empty_like(dh))
+        return (dh.view(ctx.shape), None, None, None, None, None, None, None, None, None)
 
 
 class QADHeadLoss(torch.nn.Module):

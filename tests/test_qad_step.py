@@ -272,3 +272,20 @@ def test_distillation_mean_is_over_the_rows_that_keep_a_token():
     assert float(none[0]) == 0 and float(none[2]) == 0
     other = head(h.view(5, 6, d), None, idx.view(5, 6, K), t)       # the same rows in other shapes
     assert torch.equal(other[0], ta[0].detach())
+
+
+@pytest.mark.gpu
+def test_upstream_gradient_is_applied_in_fp32():
+    """(loss / 3).backward(): the stored gradient times 1/3 in fp32, rounded to bf16 once."""
+    from scale_only_quantization_gb300.autograd import QADHeadLoss
+    _build()
+    N, d, V = 50, 128, 500
+    w = (torch.randn((V, d), device="cuda") * d ** -0.5).to(torch.bfloat16)
+    h = torch.randn((N, d), device="cuda").to(torch.bfloat16)
+    target = torch.randint(0, V, (N,), device="cuda")
+    head = QADHeadLoss(w)
+    a, b = h.clone().requires_grad_(True), h.clone().requires_grad_(True)
+    head(a, target)[0].backward()
+    (head(b, target)[0] / 3).backward()
+    assert torch.equal(b.grad, (a.grad.float() * (torch.ones((), device="cuda") / 3)).to(torch.bfloat16))
+    assert b.grad.dtype == torch.bfloat16
