@@ -16,6 +16,7 @@ form of its output) before it, QADHeadLoss (cross entropy and distillation on th
 end.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (QAD_ACT_NONE, qad_distill_topk_fwd_bwd, qad_linear_ce_fwd_bwd, qad_linear_ce_workspace_bytes,
                qad_moe_bwd_dgrad, qad_moe_bwd_scalegrad, qad_moe_fwd, qad_moe_workspace_bytes, qad_rmsnorm_bwd,
@@ -130,6 +131,7 @@ class QADRMSNormFunction(torch.autograd.Function):
         return y.view(x.shape), r.view(x.shape), codes, scale
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dr, _codes, _scale):
         r, gamma, rstd = ctx.saved_tensors
         T, d = r.shape
@@ -211,6 +213,7 @@ class QADHeadLossFunction(torch.autograd.Function):
         return total, ce, kd
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dtotal, _ce, _kd):
         (dh,) = ctx.saved_tensors
         # as a 1 x 1 tensor the factor stays fp32 (a scalar tensor would be rounded to dh's bf16 first); one rounding

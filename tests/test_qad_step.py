@@ -289,3 +289,19 @@ def test_upstream_gradient_is_applied_in_fp32():
     (head(b, target)[0] / 3).backward()
     assert torch.equal(b.grad, (a.grad.float() * (torch.ones((), device="cuda") / 3)).to(torch.bfloat16))
     assert b.grad.dtype == torch.bfloat16
+
+
+@pytest.mark.gpu
+def test_second_derivatives_are_refused():
+    """The gradients are kernels' outputs: asking to differentiate them again raises instead of returning a gradient
+    that does not depend on the hidden states."""
+    from scale_only_quantization_gb300.autograd import QADHeadLoss, QADRMSNorm
+    _build()
+    d, V = 64, 100
+    h = torch.randn((5, d), device="cuda").to(torch.bfloat16).requires_grad_(True)
+    w = torch.randn((V, d), device="cuda") * d ** -0.5
+    target = torch.randint(0, V, (5,), device="cuda")
+    for loss in (QADHeadLoss(w)(h, target)[0].square(), QADRMSNorm(torch.ones(d, device="cuda"))(h)[0].float().square().sum()):
+        (g,) = torch.autograd.grad(loss, h, create_graph=True)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(g.float().sum(), h)
