@@ -123,7 +123,8 @@ class QADRMSNormFunction(torch.autograd.Function):
         qad_rmsnorm_fwd(x2, res2, gamma, eps, act, r, y, None, codes, scale, rstd, T, d, x2.stride(0) if T > 1 else d,
                         res2.stride(0) if res2 is not None and T > 1 else d)
         ctx.save_for_backward(r, gamma, rstd)
-        ctx.has_res = res is not None
+        ctx.set_materialize_grads(False)  # an output that nothing reads costs the backward nothing
+        ctx.res_shape = None if res is None else res.shape
         ctx.shape = x.shape
         if codes is not None:
             ctx.mark_non_differentiable(codes, scale)
@@ -135,15 +136,19 @@ class QADRMSNormFunction(torch.autograd.Function):
     def backward(ctx, dy, dr, _codes, _scale):
         r, gamma, rstd = ctx.saved_tensors
         T, d = r.shape
-        dy2 = _packed((torch.zeros_like(r) if dy is None else dy).reshape(T, d))
-        dr2 = None if dr is None else _packed(dr.reshape(T, d))
-        dx = torch.empty_like(r)
         need = ctx.needs_input_grad[2]
-        dgamma = torch.empty(d, dtype=torch.float32, device=r.device) if need else None
-        ws = torch.empty(qad_rmsnorm_workspace_bytes(T, d), dtype=torch.uint8, device=r.device) if need else None
-        qad_rmsnorm_bwd(dy2, dr2, r, gamma, rstd, dx, dgamma, T, d, d, ws)
-        dx = dx.view(ctx.shape)
-        return dx, dx if ctx.has_res else None, dgamma.to(gamma.dtype) if need else None, None, None
+        if dy is None and dr is None:
+            return None, None, None, None, None
+        if dy is None:  # only the residual stream goes on
+            dx, dgamma = dr, torch.zeros_like(gamma) if need else None
+        else:
+            dx = torch.empty_like(r)
+            dgamma = torch.empty(d, dtype=torch.float32, device=r.device) if need else None
+            ws = torch.empty(qad_rmsnorm_workspace_bytes(T, d), dtype=torch.uint8, device=r.device) if need else None
+            qad_rmsnorm_bwd(_packed(dy.reshape(T, d)), None if dr is None else _packed(dr.reshape(T, d)), r, gamma, rstd, dx,
+                            dgamma, T, d, d, ws)
+            dgamma = dgamma.to(gamma.dtype) if need else None
+        return (dx.reshape(ctx.shape), None if ctx.res_shape is None else dx.reshape(ctx.res_shape), dgamma, None, None)
 
 
 class QADRMSNorm(torch.nn.Module):

@@ -305,3 +305,36 @@ def test_second_derivatives_are_refused():
         (g,) = torch.autograd.grad(loss, h, create_graph=True)
         with pytest.raises(RuntimeError):
             torch.autograd.grad(g.float().sum(), h)
+
+
+@pytest.mark.gpu
+def test_norm_with_one_output_unused(monkeypatch):
+    """A gradient that does not arrive is not made up as zeros and read: with r unused the call gets none, with y unused
+    dx is r's gradient as it came."""
+    from scale_only_quantization_gb300 import autograd as A
+    _build()
+    calls = []
+    bwd = A.qad_rmsnorm_bwd
+    monkeypatch.setattr(A, "qad_rmsnorm_bwd", lambda *a, **k: (calls.append(a), bwd(*a, **k)))
+    d = 272
+    x, res, g = (torch.randn((2, 20, d), device="cuda").to(torch.bfloat16) for _ in range(3))
+    norm = A.QADRMSNorm(1 + 0.1 * torch.randn(d, device="cuda"), trained=True)
+
+    def grads(which):
+        a, b = x.clone().requires_grad_(True), res.clone().requires_grad_(True)
+        norm.weight.grad = None
+        out = norm(a, b)
+        if which == "both":
+            torch.autograd.backward([out[0], out[1]], [g, torch.zeros_like(g)])
+        else:
+            out[which].backward(g)
+        return a.grad, b.grad, norm.weight.grad
+
+    only_y, both, only_r = grads(0), grads("both"), grads(1)
+    assert all(torch.equal(p, q) for p, q in zip(only_y, both))
+    assert calls[0][1] is None and calls[1][1] is not None and len(calls) == 2
+    assert torch.equal(only_r[0], g) and torch.equal(only_r[1], g) and torch.all(only_r[2] == 0)
+    # the residual may come in another view of the same rows
+    a, b = x.clone().requires_grad_(True), res.reshape(40, d).clone().requires_grad_(True)
+    norm(a, b)[0].backward(g)
+    assert torch.equal(a.grad, only_y[0]) and torch.equal(b.grad.view_as(res), only_y[1])
