@@ -18,9 +18,9 @@ end.
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (QAD_ACT_NONE, qad_distill_topk_fwd_bwd, qad_linear_ce_fwd_bwd, qad_linear_ce_workspace_bytes,
-               qad_moe_bwd_dgrad, qad_moe_bwd_scalegrad, qad_moe_fwd, qad_moe_workspace_bytes, qad_rmsnorm_bwd,
-               qad_rmsnorm_fwd, qad_rmsnorm_workspace_bytes, shape)
+from . import (QAD_ACT_NONE, qad_distill_topk_fwd, qad_distill_topk_fwd_bwd, qad_linear_ce_fwd, qad_linear_ce_fwd_bwd,
+               qad_linear_ce_workspace_bytes, qad_moe_bwd_dgrad, qad_moe_bwd_scalegrad, qad_moe_fwd,
+               qad_moe_workspace_bytes, qad_rmsnorm_bwd, qad_rmsnorm_fwd, qad_rmsnorm_workspace_bytes, shape)
 
 
 class QADMoEFunction(torch.autograd.Function):
@@ -173,7 +173,7 @@ class QADHeadLossFunction(torch.autograd.Function):
     divergence over the teacher's top tokens idx [N, K] with logits t [N, K], softened by tau, mixed
     forward and reverse by mix [N] (None: forward).  Either part is left out when its target or idx is
     None.  The hidden-state gradient is formed in the forward, where the logits are, and scaled by the
-    upstream gradient in the backward.  err int32 [1]: a device error word that the calls' is OR-ed into.
+    upstream gradient in the backward; an h that needs none (detach it under no_grad) costs the losses alone.  err int32 [1]: a device error word that the calls' is OR-ed into.
     Returns (total, CE [N] or None, KD [N] or None).
     """
 
@@ -185,7 +185,8 @@ class QADHeadLossFunction(torch.autograd.Function):
         h2 = _rows(h, d, "h")
         N, dev = h2.shape[0], h.device
         ld = h2.stride(0) if N > 1 else d
-        dh = torch.empty((N, d), dtype=torch.bfloat16, device=dev)
+        grad = ctx.needs_input_grad[0]
+        dh = torch.empty((N, d), dtype=torch.bfloat16, device=dev) if grad else None
         total = torch.zeros((), dtype=torch.float32, device=dev)
         ce = kd = None
         if target is not None:
@@ -194,8 +195,11 @@ class QADHeadLossFunction(torch.autograd.Function):
             if target.numel() != N or g_lm.numel() != N:
                 raise ValueError("one target and one weight per row of h")
             ce, lse = torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev)
-            ws = torch.empty(qad_linear_ce_workspace_bytes(N, d, V, 1, 0), dtype=torch.uint8, device=dev)
-            qad_linear_ce_fwd_bwd(h2, ld, w, d, target, g_lm, ce, lse, dh, None, 0, N, d, V, ws)
+            ws = torch.empty(qad_linear_ce_workspace_bytes(N, d, V, grad, 0), dtype=torch.uint8, device=dev)
+            if grad:
+                qad_linear_ce_fwd_bwd(h2, ld, w, d, target, g_lm, ce, lse, dh, None, 0, N, d, V, ws)
+            else:
+                qad_linear_ce_fwd(h2, ld, w, d, target, ce, lse, N, d, V, ws)
             err.bitwise_or_(ws[:4].view(torch.int32))
             total = total + torch.dot(ce, g_lm)
         if idx is not None:
@@ -207,12 +211,16 @@ class QADHeadLossFunction(torch.autograd.Function):
             if g_kd.numel() != N or (mix is not None and mix.numel() != N):
                 raise ValueError("one distillation weight (and mix) per row of h")
             kd = torch.empty(N, dtype=torch.float32, device=dev)
-            qad_distill_topk_fwd_bwd(h2, ld, w, d, idx, t, mix, 1.0 / tau, g_kd, kd, dh, int(target is not None), N, d, V,
-                                     K, err)
+            if grad:
+                qad_distill_topk_fwd_bwd(h2, ld, w, d, idx, t, mix, 1.0 / tau, g_kd, kd, dh, int(target is not None), N,
+                                         d, V, K, err)
+            else:
+                qad_distill_topk_fwd(h2, ld, w, d, idx, t, mix, 1.0 / tau, kd, N, d, V, K, err)
             total = total + torch.dot(kd, g_kd)
         if target is None and idx is None:
             raise ValueError("neither targets nor teacher logits")
-        ctx.save_for_backward(dh)
+        if grad:
+            ctx.save_for_backward(dh)
         ctx.shape = h.shape
         ctx.mark_non_differentiable(*[x for x in (ce, kd) if x is not None])
         return total, ce, kd
@@ -261,6 +269,8 @@ class QADHeadLoss(torch.nn.Module):
             kept = (teacher_idx >= 0) & (teacher_idx < self.w.shape[0]) & (teacher_logits != -torch.inf)
             kept = kept.any(1).to(torch.float32)
             g_kd = kept * (self.distill_weight / kept.sum().clamp_min(1.0))
+        if not torch.is_grad_enabled():
+            h = h.detach()
         total, ce, kd = QADHeadLossFunction.apply(h, self.w, target, g_lm, teacher_idx, teacher_logits, g_kd, self.tau,
                                                   mix, self.err)
         lm = None if ce is None else ce.sum() / live.sum().clamp_min(1.0)

@@ -338,3 +338,30 @@ def test_norm_with_one_output_unused(monkeypatch):
     a, b = x.clone().requires_grad_(True), res.reshape(40, d).clone().requires_grad_(True)
     norm(a, b)[0].backward(g)
     assert torch.equal(a.grad, only_y[0]) and torch.equal(b.grad.view_as(res), only_y[1])
+
+
+@pytest.mark.gpu
+def test_no_gradient_asked_none_computed(monkeypatch):
+    """Under no_grad, or with hidden states that need none, the head loss makes the forward calls; the numbers are the
+    same bits."""
+    from scale_only_quantization_gb300 import autograd as A
+    _build()
+    N, d, V, K = 40, 64, 300, 8
+    w = (torch.randn((V, d), device="cuda") * d ** -0.5).to(torch.bfloat16)
+    h = torch.randn((N, d), device="cuda").to(torch.bfloat16)
+    target = torch.randint(0, V, (N,), device="cuda")
+    target[:3] = -1
+    idx = torch.randint(0, V, (N, K), device="cuda", dtype=torch.int32)
+    t = torch.randn((N, K), device="cuda")
+    head = A.QADHeadLoss(w, 0.3, 0.7)
+    want = [v.detach() for v in head(h.clone().requires_grad_(True), target, idx, t)]
+
+    def refuse(*a, **k):
+        raise AssertionError("a gradient was computed")
+    monkeypatch.setattr(A, "qad_linear_ce_fwd_bwd", refuse)
+    monkeypatch.setattr(A, "qad_distill_topk_fwd_bwd", refuse)
+    got = head(h, target, idx, t)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with torch.no_grad():
+        got = head(h.clone().requires_grad_(True), target, idx, t)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and not got[0].requires_grad
