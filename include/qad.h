@@ -297,7 +297,8 @@ int qad_rmsnorm_bwd(const void* dy, const void* dres, const void* r, const void*
  *   ws     256-byte aligned, ws_bytes >= qad_linear_ce_workspace_bytes(N, d, V, dh != NULL, dw != NULL).
  *          Its first word is the device error word (qad_check_device_error), cleared by each call.
  * The logits exist one piece of the vocabulary at a time (at most 1 GB of exp(logits) in bf16, and
- * only when a gradient is asked for); sums and gradients are accumulated in fp32.
+ * only when a gradient is asked for); sums and gradients are accumulated in fp32.  The rest of the workspace:
+ * a few words per row and at most 32 MB of partial sums, and with dh fp32 [N, d] (and up to 192 MB of slabs).
  * Requires d % 16 == 0, ldh, ldw >= d and multiples of 8, N, V < 2^30, d <= 65536.
  */
 size_t qad_linear_ce_workspace_bytes(int64_t N, int64_t d, int64_t V, int dh, int dw);

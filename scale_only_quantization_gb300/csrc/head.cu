@@ -59,7 +59,7 @@ struct HeadParams {
   const float* tval;            // per row: what the target's column holds (null: 0)
   const int32_t* target;        // per row: the target's column
   float *psum, *pmax;           // partial sums without the target / maxima, or null
-  int part0;                    // first part of this piece
+  int join;                     // add to the parts, which an earlier piece has written
   int store_p;
   __nv_bfloat16* p;             // e: [N, ldp], transposed [piece, kFewRows]
   int64_t ldp;
@@ -222,9 +222,9 @@ __device__ __forceinline__ void epi_logits(const HeadParams& p, const HTile& ti,
     }
   }
   if (p.psum && live) {
-    const int64_t at = (int64_t)(p.part0 + 2 * ti.nb + half) * p.N + row;
-    p.psum[at] = sum;
-    p.pmax[at] = top;
+    const int64_t at = (int64_t)(2 * ti.nb + half) * p.N + row;
+    p.psum[at] = p.join ? p.psum[at] + sum : sum;
+    p.pmax[at] = p.join ? fmaxf(p.pmax[at], top) : top;
   }
 }
 
@@ -568,9 +568,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int n = 64 * half + 8 * i + lane / 4;
-          const int64_t at = (int64_t)(p.part0 + (pair * 2 + (int)rank) * 4 + q) * kFewRows + n;
-          p.psum[at] = sums[i];
-          p.pmax[at] = tops[i];
+          const int64_t at = (int64_t)((pair * 2 + (int)rank) * 4 + q) * kFewRows + n;
+          p.psum[at] = p.join ? p.psum[at] + sums[i] : sums[i];
+          p.pmax[at] = p.join ? fmaxf(p.pmax[at], tops[i]) : tops[i];
         }
     }
   }
@@ -808,7 +808,8 @@ int ce_layout_of(int64_t N, int64_t d, int64_t V, int grad, int dw, CeLayout* L)
   const int64_t tiles = (few ? 1 : cdiv(N, kTile)) * cdiv(d, kTile);
   const int64_t bke = few ? HCfg<M_U_T>::BKE : HCfg<M_U>::BKE;
   L->slabs = tiles ? choose_slabs(tiles, cdiv(L->pieces > 1 ? L->piece : V, bke), N, d) : 1;
-  L->parts = few ? L->pieces * kMaxPairs * 8 : (int)(2 * vt);
+  // two parts per tile of a piece (transposed: eight per pair), which the pieces after the first add to
+  L->parts = few ? kMaxPairs * 8 : 2 * (L->piece / kTile);
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes); return at; };
   L->header = take(256);
@@ -868,7 +869,7 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   base.ref = ref;
   base.target = tcol;
   base.split = 1;
-  int parts = 0;  // partial sums of the sweep so far
+  int parts = 0;  // partial sums of the sweep
   auto logits = [&](int piece, const int32_t* gate, bool sums, bool store, bool final) -> cudaError_t {
     const int64_t c0 = (int64_t)piece * L.piece, cols = V - c0 < L.piece ? V - c0 : L.piece;
     HeadParams p = base;
@@ -882,7 +883,7 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
     if (sums) {
       p.psum = psum;
       p.pmax = pmax;
-      p.part0 = parts;
+      p.join = piece > 0;
     }
     if (final) {  // normalised, with the target's column
       p.mul = mul;
@@ -894,13 +895,13 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
       p.nt = 1;
       int pairs = 0;
       const cudaError_t e = launch_head<M_LOGITS_T>(tm_w, tm_h, tm_h, p, QAD_K_CE_LOGITS, st, &pairs);
-      parts += pairs * 8;
+      if (piece == 0) parts = pairs * 8;  // no later piece has more tiles
       return e;
     }
     p.b_row0 = (int)c0;
     p.mt = (int)cdiv(N, kTile);
     p.nt = (int)cdiv(cols, kTile);
-    parts += 2 * p.nt;
+    parts = L.parts;
     return launch_head<M_LOGITS>(tm_h, tm_w, tm_h, p, QAD_K_CE_LOGITS, st);
   };
   auto product = [&](int piece, const int32_t* gate) -> cudaError_t {
@@ -929,7 +930,6 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   };
   // the sweep: exp(logits) of a piece, then its product with the piece of the head
   auto sweep = [&](const int32_t* gate) -> cudaError_t {
-    parts = 0;
     for (int i = 0; i < L.pieces; ++i) {
       cudaError_t e = logits(i, gate, true, dh != nullptr, false);
       if (e == cudaSuccess && dh) e = product(i, gate);

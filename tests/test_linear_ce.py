@@ -373,3 +373,22 @@ def test_normaliser_of_a_target_far_below(N):
     assert torch.isinf(o["loss"][1::3]).all()
     ok = torch.arange(N, device="cuda") % 3 != 1
     assert torch.all((o["loss"].double() - want).abs()[ok] <= 2e-6 * (1 + want.abs()[ok]))
+
+
+def test_partial_sums_are_bounded_in_the_vocabulary():
+    """What the loss alone needs besides a few words per row does not grow with tokens times words."""
+    for N, V in [(1, 1), (128, 1 << 20), (128, (1 << 30) - 1), (8192, 151936), (32768, 151936), (100000, 256000), (1 << 20, 256000)]:
+        assert Q.qad_linear_ce_workspace_bytes(N, 2048, V, 0, 0) <= (32 << 20) + 64 * N + 16384
+
+
+@pytest.mark.gpu
+def test_pieces_of_few_rows():
+    """A vocabulary that 128 rows take in two pieces, the second one short: the sums of both, and some of the gradient."""
+    _lib()
+    N, d, V = 20, 16, 3500001
+    c = make(N, d, V, seed=3, drop=0.1)
+    o = run(c)
+    ref, tol = exact(c)
+    assert o["err"] == 0
+    for n in ("loss", "lse", "dh"):
+        assert torch.all((o[n].double() - ref[n]).abs() <= tol[n]), n
