@@ -10,9 +10,9 @@
 // once and accumulated in fp32, and the row's 1 / sum e is applied at the end.  So the logits are
 // computed once, not once for the normaliser and once for the gradient.  With the target as the
 // reference, sum_{v != t} e is the loss's own argument (no cancellation however sure the model is)
-// and (q_t - 1) w_t is added in fp32.  e may be far above 1 (bf16 has fp32's range): only a row
-// whose largest logit is over kMaxAbove nats above its target's is swept again, with the largest
-// as its reference (the second sweep's kernels leave at once when no row asked for it).
+// and (q_t - 1) w_t is added in fp32.  e may be far above 1 (bf16 has fp32's range): only the row
+// tiles in which some row's largest logit is over kMaxAbove nats above its target's are swept again, that row
+// with the largest as its reference (the second sweep's kernels leave at once when no row asked for it).
 // dW needs the final normaliser, so its pieces are computed from the logits a second time.
 //
 // The products run on SM pairs (tcgen05 cta_group::2, 256 x 256 tiles) with the roles and
@@ -46,7 +46,8 @@ constexpr int kFewRows = 128;
 constexpr int kMaxPairs = 76;  // SM pairs of the grid at most: bounds the partial sums of a split contraction
 
 struct HeadParams {
-  const int32_t* gate;  // null, or a word: 0 = nothing to do
+  const int32_t* gate;  // null, or a word: 0 = nothing to do, else (LISTED) the row tiles to do
+  const int32_t* list;  // those row tiles
   int32_t* err;
   int mt, nt, num_kb;   // tiles along the output's rows and columns, K blocks
   int n_fast;           // tile order: columns fastest
@@ -92,15 +93,18 @@ template <int MODE> struct HCfg {
 struct HTile {
   int mb, nb;
 };
-__device__ __forceinline__ HTile htile(const HeadParams& p, int t) {
+// LISTED: of the row tiles in p.list only, mt of them
+template <bool LISTED>
+__device__ __forceinline__ HTile htile(const HeadParams& p, int mt, int t) {
   HTile x;
   if (p.n_fast) {
     x.mb = t / p.nt;
     x.nb = t - x.mb * p.nt;
   } else {
-    x.nb = t / p.mt;
-    x.mb = t - x.nb * p.mt;
+    x.nb = t / mt;
+    x.mb = t - x.nb * mt;
   }
+  if constexpr (LISTED) x.mb = p.list[x.mb];
   return x;
 }
 
@@ -108,10 +112,11 @@ __device__ __forceinline__ HTile htile(const HeadParams& p, int t) {
 // the same sequence.  Slab s covers the K blocks [s num_kb / split, (s + 1) num_kb / split); the pairs take
 // all tiles of a slab before the next one's, so that those running together read the same K blocks of
 // both operands from L2.
-struct Walk {
+template <bool LISTED> struct Walk {
   int tile, kb0, kb1, slab;
-  int at, step, tiles;
-  __device__ __forceinline__ Walk(const HeadParams& p, int pair, int pairs) : at(pair), step(pairs), tiles(p.mt * p.nt) {}
+  int at, step, mt, tiles;
+  __device__ __forceinline__ Walk(const HeadParams& p, int pair, int pairs)
+      : at(pair), step(pairs), mt(LISTED ? *p.gate : p.mt), tiles(mt * p.nt) {}
   __device__ __forceinline__ bool next(const HeadParams& p) {
     if (at >= tiles * p.split) return false;
     slab = at / tiles;
@@ -376,7 +381,7 @@ __device__ __forceinline__ void epi_dw(const HeadParams& p, const CUtensorMap* t
   }
 }
 
-template <int MODE>
+template <int MODE, bool LISTED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const HeadParams p) {
@@ -441,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int pair = (int)cluster_id(), pairs = (int)cluster_count();
-  Walk wk(p, pair, pairs);
+  Walk<LISTED> wk(p, pair, pairs);
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------------ TMA producer (both CTAs)
@@ -452,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     bool ok = true;
     const int half = (int)rank * BM, half_n = (int)rank * (TN / 2);
     while (ok && wk.next(p)) {
-      const HTile ti = htile(p, wk.tile);
+      const HTile ti = htile<LISTED>(p, LISTED ? wk.mt : p.mt, wk.tile);
       for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
         if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
           ok = false;
@@ -544,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsH, 1)
     }
     if constexpr (C::BOXES) tma_prefetch_desc(&tmC);
     while (wk.next(p)) {
-      const HTile ti = htile(p, wk.tile);
+      const HTile ti = htile<LISTED>(p, LISTED ? wk.mt : p.mt, wk.tile);
       const bool got = mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.err);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
@@ -590,9 +595,10 @@ __global__ void __launch_bounds__(128) ce_ref_kernel(const __nv_bfloat16* __rest
                                                      const __nv_bfloat16* __restrict__ w, int64_t ldw,
                                                      const int32_t* __restrict__ target, int64_t N, int d, int64_t V,
                                                      float* __restrict__ ref, float* __restrict__ zt,
-                                                     int32_t* __restrict__ tcol, int32_t* hdr) {
+                                                     int32_t* __restrict__ tcol, int32_t* hdr, int32_t* asked) {
   let_next_start();
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (threadIdx.x == 0 && row % kTile == 0) asked[row / kTile] = 0;
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x < 64) hdr[threadIdx.x] = 0;  // nothing of this call has written it yet
   if (row >= N) return;
@@ -618,19 +624,21 @@ __global__ void __launch_bounds__(128) ce_ref_kernel(const __nv_bfloat16* __rest
 
 // Per row, from the sweep's partial sums [parts, np]: the loss, lse and the factors of the gradients.
 // A row whose largest logit lies over kMaxAbove above its reference asks for the second sweep (again =
-// 0).  One block per 32 rows, its 32 warps taking the parts in turn.
+// 0) of its tile: the first one to ask appends the tile to the list (asked: a word per tile, 0 or 1, then the list),
+// whose order changes no result.  One block per 32 rows, its 32 warps taking the parts in turn.
 __global__ void __launch_bounds__(1024) ce_stats_kernel(const int32_t* gate, const float* psum, const float* pmax,
                                                         int parts, int np, int64_t N,
                                                         const int32_t* __restrict__ target, int64_t V,
                                                         const float* __restrict__ g, const float* zt, float* ref,
                                                         float* mul, float* tval, float* loss, float* lse, int again,
-                                                        int32_t* hdr) {
+                                                        int32_t* hdr, int32_t* asked) {
   let_next_start();
   wait_for_previous();
   if (gate && *gate == 0) return;
   __shared__ float ss[32][33], sm[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t first = (int64_t)blockIdx.x * 32;
+  if (again && !asked[first / kTile]) return;  // its results stand
   float s = 0.0f, m = -INFINITY;
   if (first + lane < N)
 #pragma unroll 4
@@ -651,7 +659,7 @@ __global__ void __launch_bounds__(1024) ce_stats_kernel(const int32_t* gate, con
   const float r = ref[row], z = zt[row];
   if (!again && m - r > kMaxAbove && m < INFINITY) {  // an infinite logit gains nothing from it
     ref[row] = m;
-    atomicOr(hdr + 1, 1);
+    if (atomicExch(asked + row / kTile, 1) == 0) asked[(N + kTile - 1) / kTile + atomicAdd(hdr + 1, 1)] = (int32_t)(row / kTile);
     return;
   }
   const float et = expf(z - r);  // 1 unless the row's reference was replaced
@@ -706,9 +714,9 @@ __global__ void __launch_bounds__(128) ce_dh_kernel(const float* u, int slabs, c
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // SM pairs that can run the kernel at the same time (its persistent grid)
-template <int MODE>
+template <int MODE, bool LISTED>
 int head_pairs(cudaError_t* err) {
-  auto kern = head_gemm_kernel<MODE>;
+  auto kern = head_gemm_kernel<MODE, LISTED>;
   constexpr int SMEM = HCfg<MODE>::SMEM;
   static int max_pairs[64] = {0};  // per device
   int dev = 0;
@@ -750,18 +758,18 @@ cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t 
 }
 
 // *used (may be null): the pairs launched
-template <int MODE>
+template <int MODE, bool LISTED = false>
 cudaError_t launch_head(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const HeadParams& p,
                         int kid, cudaStream_t st, int* used = nullptr) {
   cudaError_t e = cudaSuccess;
-  const int most = head_pairs<MODE>(&e);
+  const int most = head_pairs<MODE, LISTED>(&e);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)p.mt * p.nt * p.split;
   const int pairs = (int)(units < most ? units : most);
   if (used) *used = pairs;
   if (pairs < 1) return cudaSuccess;
   prof_begin(kid, st);
-  e = launch_dependent(head_gemm_kernel<MODE>, dim3((unsigned)(2 * pairs), 1, 1), kThreadsH, HCfg<MODE>::SMEM, st, ta, tb,
+  e = launch_dependent(head_gemm_kernel<MODE, LISTED>, dim3((unsigned)(2 * pairs), 1, 1), kThreadsH, HCfg<MODE>::SMEM, st, ta, tb,
                        tc, p);
   prof_end(kid, st);
   return e;
@@ -813,6 +821,7 @@ int ce_layout_of(int64_t N, int64_t d, int64_t V, int grad, int dw, CeLayout* L)
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes); return at; };
   L->header = take(256);
+  L->asked = take(8 * (size_t)cdiv(N, kTile));
   L->ref = take(4 * (size_t)N);
   L->zt = take(4 * (size_t)N);
   L->tcol = take(4 * (size_t)N);
@@ -830,6 +839,7 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
                       const float* g, float* loss, float* lse, void* dh, void* dw, int accumulate, int64_t N, int64_t d,
                       int64_t V, uint8_t* ws, cudaStream_t st) {
   int32_t* hdr = reinterpret_cast<int32_t*>(ws + L.header);
+  int32_t* asked = reinterpret_cast<int32_t*>(ws + L.asked);
   float* ref = reinterpret_cast<float*>(ws + L.ref);
   float* zt = reinterpret_cast<float*>(ws + L.zt);
   int32_t* tcol = reinterpret_cast<int32_t*>(ws + L.tcol);
@@ -859,7 +869,8 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   }
   if (!ok) return cudaErrorInvalidValue;
   note_launches(1);
-  ce_ref_kernel<<<(unsigned)cdiv(N, 4), 128, 0, st>>>(hb, ldh, wb, ldw, target, N, (int)d, V, ref, zt, tcol, hdr);
+  ce_ref_kernel<<<(unsigned)cdiv(N, 4), 128, 0, st>>>(hb, ldh, wb, ldw, target, N, (int)d, V, ref, zt, tcol, hdr,
+                                                    asked);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
   HeadParams base = {};
@@ -874,6 +885,7 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
     const int64_t c0 = (int64_t)piece * L.piece, cols = V - c0 < L.piece ? V - c0 : L.piece;
     HeadParams p = base;
     p.gate = gate;
+    p.list = asked + cdiv(N, kTile);
     p.c0 = (int)c0;
     p.cols = (int)cols;
     p.num_kb = (int)cdiv(d, HCfg<M_LOGITS>::BKE);
@@ -902,7 +914,8 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
     p.mt = (int)cdiv(N, kTile);
     p.nt = (int)cdiv(cols, kTile);
     parts = L.parts;
-    return launch_head<M_LOGITS>(tm_h, tm_w, tm_h, p, QAD_K_CE_LOGITS, st);
+    return gate ? launch_head<M_LOGITS, true>(tm_h, tm_w, tm_h, p, QAD_K_CE_LOGITS, st)
+                : launch_head<M_LOGITS>(tm_h, tm_w, tm_h, p, QAD_K_CE_LOGITS, st);
   };
   auto product = [&](int piece, const int32_t* gate) -> cudaError_t {
     const int64_t c0 = (int64_t)piece * L.piece;
@@ -911,6 +924,7 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
     const int64_t cols = L.pieces > 1 ? L.piece : V;
     HeadParams q = base;
     q.gate = gate;
+    q.list = asked + cdiv(N, kTile);
     q.nt = few ? 1 : (int)cdiv(d, kTile);
     q.mt = few ? (int)cdiv(d, kTile) : (int)cdiv(N, kTile);
     q.n_fast = 1;
@@ -924,7 +938,8 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
       e = launch_head<M_U_T>(tm_wu, tm_e, tm_e, q, QAD_K_CE_DH, st);
     } else {
       q.b_row0 = (int)c0;
-      e = launch_head<M_U>(tm_e, tm_wu, tm_e, q, QAD_K_CE_DH, st);
+      e = gate ? launch_head<M_U, true>(tm_e, tm_wu, tm_e, q, QAD_K_CE_DH, st)
+               : launch_head<M_U>(tm_e, tm_wu, tm_e, q, QAD_K_CE_DH, st);
     }
     return e;
   };
@@ -940,7 +955,7 @@ cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void*
   auto stats = [&](const int32_t* gate, int again) {
     note_launches(1);
     return launch_dependent(ce_stats_kernel, dim3((unsigned)cdiv(N, 32), 1, 1), 1024, 0, st, gate, psum, pmax, parts,
-                            (int)width, N, target, V, g, zt, ref, mul, tval, loss, lse, again, hdr);
+                            (int)width, N, target, V, g, zt, ref, mul, tval, loss, lse, again, hdr, asked);
   };
   if ((e = sweep(nullptr)) != cudaSuccess) return e;
   if ((e = stats(nullptr, 0)) != cudaSuccess) return e;

@@ -145,10 +145,10 @@ cudaError_t launch_rmsnorm_bwd(const void* dy, const void* dres, const void* r, 
 // sums per row of a sweep at most
 struct CeLayout {
   int piece, pieces, slabs, parts;  // slabs: partial sums of the product with the head
-  size_t header, ref, zt, tcol, mul, tval, psum, pmax, u, p, total;
+  size_t header, asked, ref, zt, tcol, mul, tval, psum, pmax, u, p, total;
 };
 int ce_layout_of(int64_t N, int64_t d, int64_t V, int grad, int dw, CeLayout* L);
-// loss and lse; dh / dw may be null; header words: [0] device errors, [1] a second sweep is needed
+// loss and lse; dh / dw may be null; header words: [0] device errors, [1] row tiles that need a second sweep
 cudaError_t linear_ce(const CeLayout& L, const void* h, int64_t ldh, const void* w, int64_t ldw, const int32_t* target,
                       const float* g, float* loss, float* lse, void* dh, void* dw, int accumulate, int64_t N, int64_t d,
                       int64_t V, uint8_t* ws, cudaStream_t st);

@@ -10,7 +10,7 @@ import pytest
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "scale_only_quantization_gb300", "csrc")
 WAIT = r"wait_for_previous\(\)|griddepcontrol\.wait"
 # what an earlier kernel of a chain writes, by the names it goes by in the dependent kernels
-CHAIN = {"head.cu": ("ref", "mul", "tval", "tcol", "target", "zt", "psum", "pmax", "u", "ur", "at", "p", "gate"),
+CHAIN = {"head.cu": ("ref", "mul", "tval", "tcol", "target", "zt", "psum", "pmax", "u", "ur", "at", "p", "gate", "list", "asked"),
          "norm.cu": ("part", "status")}
 OF_THE_CALLER = ("target", "g", "w", "h")  # parameters of plain kernels: inputs, read-only during the whole call
 

@@ -392,3 +392,82 @@ def test_pieces_of_few_rows():
     assert o["err"] == 0
     for n in ("loss", "lse", "dh"):
         assert torch.all((o[n].double() - ref[n]).abs() <= tol[n]), n
+
+
+def _one_row_far_below(N, d, V, row, seed):
+    """Inputs in which exactly one row's target lies more than 60 nats below its largest logit."""
+    c = make(N, d, V, seed=seed, drop=0.1)
+    c["h"][row] = (c["h"][row].float() * 40).to(torch.bfloat16)
+    z = c["h"][row].double() @ c["w"].double().T
+    c["target"][row] = int(z.argmin())
+    assert float(z.max() - z.min()) > 100
+    return c
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N, row", [(1000, 700), (1000, 999), (300, 0), (2600, 1300)])
+def test_second_sweep_of_one_tile_of_rows(N, row):
+    """One row asks for the second sweep: it and the rows of its tile are right, the others keep the bits that they have
+    when nobody asks; a second such row in another tile changes nothing for the first."""
+    _lib()
+    d, V = 256, 3001
+    c = _one_row_far_below(N, d, V, row, seed=N + row)
+    o = run(c, dw=True)
+    ref, tol = exact(c)
+    assert o["err"] == 0
+    for n in ("loss", "lse", "dh", "dw"):
+        assert torch.all((o[n].double() - ref[n]).abs() <= tol[n]), n
+    calm = {**c, "target": c["target"].clone()}
+    calm["target"][row] = int((c["h"][row].double() @ c["w"].double().T).argmax())
+    a = run(calm)
+    rest = torch.arange(N, device="cuda") != row
+    for n in ("loss", "lse", "dh"):
+        assert torch.equal(a[n][rest], o[n][rest]), n
+    again = _one_row_far_below(N, d, V, (row + 300) % N, seed=N + row)
+    two = {**c, "h": again["h"].clone(), "target": again["target"].clone()}
+    two["h"][row], two["target"][row] = c["h"][row], c["target"][row]
+    b = run(two)
+    assert torch.equal(b["loss"][row], o["loss"][row]) and torch.equal(b["dh"][row], o["dh"][row])
+    ref, tol = exact(two)
+    for n in ("loss", "lse", "dh"):
+        assert torch.all((b[n].double() - ref[n]).abs() <= tol[n]), n
+
+
+@pytest.mark.gpu
+def test_second_sweep_of_many_pieces():
+    """The tiles that ask, over three pieces of the vocabulary."""
+    _lib()
+    N, d, V, row = 20000, 64, 60001, 12345
+    c = _one_row_far_below(N, d, V, row, seed=2)
+    o = run(c)
+    at = slice(row - 40, row + 40)
+    part = {**c, "N": 80, "h": c["h"][at], "target": c["target"][at], "g": c["g"][at]}
+    ref, tol = exact(part)
+    for n in ("loss", "lse", "dh"):
+        assert torch.all((o[n][at].double() - ref[n]).abs() <= tol[n]), n
+
+
+@pytest.mark.gpu
+def test_one_row_does_not_double_the_step():
+    """The second sweep is of the row's tile only: with 16 tiles of rows the call takes well under half as long again
+    (twice, were all rows swept)."""
+    _lib()
+    N, d, V = 4096, 512, 50000
+    slow = _one_row_far_below(N, d, V, 2000, seed=1)
+    fast = {**slow, "target": slow["target"].clone()}
+    fast["target"][2000] = int((slow["h"][2000].double() @ slow["w"].double().T).argmax())
+    ws = torch.empty(Q.qad_linear_ce_workspace_bytes(N, d, V, 1, 0), dtype=torch.uint8, device="cuda")
+    loss, lse = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+    dh = torch.empty((N, d), dtype=torch.bfloat16, device="cuda")
+
+    def time(c):
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        e[0].record()
+        for _ in range(10):
+            Q.qad_linear_ce_fwd_bwd(c["h"], d, c["w"], d, c["target"], c["g"], loss, lse, dh, None, 0, N, d, V, ws)
+        e[1].record()
+        torch.cuda.synchronize()
+        return e[0].elapsed_time(e[1])
+
+    both = [(time(fast), time(slow)) for _ in range(8)][1:]
+    assert min(b for _, b in both) < 1.5 * min(a for a, _ in both), both
