@@ -289,3 +289,93 @@ def test_teacher_logits_of_the_lowest_value(low, beta):
         assert torch.all((loss.double() - l64).abs() <= 2 * beta * err + 4e-6 * (1 + l64.abs()))
         assert torch.all((dh.double() - d64).norm(dim=1) <= 1e-2 * d64.norm(dim=1))  # bf16: 2^-8 of an element
         assert torch.equal(run(e, beta, grad=False)[0], loss)
+
+
+def bounds(c, beta):
+    """exact()'s loss and dh with each slot's error weighted by its own probability.  A logit is at most 16 packed products,
+    a sum, 5 steps of a reduction and 16 warps' sums: 38 roundings of sum |h w|, 40 here (e).  x moves by 2 b e and the
+    roundings of z, t and their differences (dx); KL's derivative with respect to x_k is q - p, RKL's q (x - RKL), and
+    terms with |x| >= 1/2 are differences of probabilities.  dz's factors: exp by the intrinsic (2 ulp and 1.2 ulp per
+    unit of its argument), K fp32 additions of the three sums, whose own references are the first slot's x."""
+    d, V, K = c["d"], c["V"], c["K"]
+    idx, t = c["idx"].long(), c["t"].double() * beta
+    keep = (idx >= 0) & (idx < V) & (t > -float("inf"))
+    wk = c["w"][idx.clamp(0, V - 1), :d].double() * keep[:, :, None]
+    h = c["h"][:, :d].double()
+    z = (wk @ h[:, :, None])[:, :, 0] * beta
+    e = 40 * U * (wk.abs() @ h.abs()[:, :, None])[:, :, 0].amax(1, keepdim=True) * beta
+    ninf = torch.full_like(z, -1e300)
+    lq = torch.log_softmax(torch.where(keep, z, ninf), 1)
+    lp = torch.log_softmax(torch.where(keep, t, ninf), 1)
+    zero = torch.zeros_like(z)
+    q, p, x = (torch.where(keep, v, zero) for v in (lq.exp(), lp.exp(), lq - lp))
+    rkl = (q * x).sum(1, keepdim=True)
+    m = torch.zeros_like(rkl) if c["mix"] is None else c["mix"].double()[:, None]
+    big = lambda v: torch.where(keep, v.abs(), zero).amax(1, keepdim=True)  # noqa: E731
+    dx = 2 * e + 16 * U * (big(z) + big(t) + big(x) + 1)
+    kl = -(p * x).sum(1, keepdim=True)
+    loss = (1 - m) * kl + m * rkl
+    tol_loss = (1 - m) * ((q - p).abs() * dx + (p + q) * dx * dx) + m * q * ((x - rkl).abs() * dx + dx * dx * (1 + x.abs()))
+    tol_loss = tol_loss + torch.where(x.abs() > 0.4, (p + q) * (1 + x.abs()) * (dx + 2e-6), zero)
+    tol_loss = tol_loss.sum(1) + 2e-5 * loss[:, 0].abs() + 1e-12
+    first = x.gather(1, keep.to(torch.int8).argmax(1, keepdim=True))
+    eps = 2 * e + 4e-6 + 2e-7 * (z - torch.where(keep, z, ninf).amax(1, keepdim=True)).abs() + (K + 10) * U
+    gb = beta * c["g"].double()[:, None]
+    dz = gb * ((1 - m) * (q - p) + m * q * (x - rkl))
+    tol_dz = gb * ((1 - m) * (q * eps + p * (4e-6 + K * U)) + m * q * (eps * ((x - first).abs() + (rkl - first).abs()) + 2 * dx))
+    dh, slack = (dz[:, None, :] @ wk)[:, 0], (tol_dz[:, None, :] @ wk.abs())[:, 0]
+    return loss[:, 0], dh, tol_loss, slack
+
+
+def check_closely(c, beta=1.0, gradient=True):
+    """Every row's loss and gradient within bounds() (bf16: 2^-8 of an element more), and bounds that would reject a
+    missing or a turned gradient in every row."""
+    loss, dh = run(c, beta)
+    l64, d64, tl, slack = bounds(c, beta)
+    tol = 2.0 ** -8 * d64.abs() + slack
+    if gradient:
+        assert torch.all((d64.abs() > tol).any(1)) and torch.all(slack.norm(dim=1) < 0.5 * d64.norm(dim=1))
+    assert torch.all((loss.double() - l64).abs() <= tl), float(((loss.double() - l64).abs() / tl).max())
+    assert torch.all((dh.double() - d64).abs() <= tol), float(((dh.double() - d64).abs() / tol).max())
+    assert torch.all((dh.double() - d64).norm(dim=1) <= 2.0 ** -8 * d64.norm(dim=1) + slack.norm(dim=1))
+    assert torch.equal(run(c, beta, grad=False)[0], loss)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("beta", [1.0, 0.5])
+@pytest.mark.parametrize("mixed", [False, True])
+@pytest.mark.parametrize("N, d, V, K", [(3, 272, 777, 33), (65, 2048, 4096, 64), (9, 2880, 999, 100), (2, 4096, 2000, 128), (2, 8192, 300, 300),
+                                        (4, 64, 2000, 1024), (2, 16384, 64, 17)])
+def test_closely_against_64_bits(N, d, V, K, mixed, beta):
+    _lib()
+    check_closely(make(N, d, V, K, seed=N + d + K, mixed=mixed), beta)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("near, size", [(0.01, 1.0), (0.1, 1.0), (3.0, 1.0), (30.0, 1.0), (1.0, 40.0), (0.0, 1.0)])
+def test_near_far_and_equal_distributions_closely(near, size):
+    """The loss keeps its relative precision down to a teacher a hundredth of a nat away; where the distributions are
+    equal, or both one token's, there is no gradient to hold apart from its bounds."""
+    _lib()
+    check_closely(make(33, 256, 500, 16, seed=3, mixed=True, near=near, size=size), gradient=near > 0 and size == 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mixed", [False, True])
+def test_a_later_logit_far_above_the_first_closely(mixed):
+    """The sums' reference is replaced and the sums scaled: all of the student's weight is on the later slot."""
+    _lib()
+    c = make(30, 256, 400, 24, seed=21, mixed=mixed)
+    for i in range(30):
+        c["w"][int(c["idx"][i, 5 + i % 19])] = c["h"][i] * 0.5
+    check_closely(c, gradient=not mixed)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mixed", [False, True])
+@pytest.mark.parametrize("N, d, K", [(9800, 256, 11), (6100, 512, 11), (4900, 1024, 11), (2450, 2048, 11), (1230, 4096, 11), (1230, 8192, 5),
+                                     (1230, 16384, 5)])
+def test_teams_with_many_rows(N, d, K, mixed):
+    """Eight rows or more for every team of every width: the rows' slots and the ring's stages are used again and again."""
+    _lib()
+    check_closely(make(N, d, 300, K, seed=N, mixed=mixed))

@@ -374,3 +374,39 @@ def test_a_copy_that_never_comes_is_reported(T, d, row):
         assert int(gone.sum()) <= -(-T // 304) + 8 and torch.equal(out[~gone], clean[5][~gone])
     err, dx, dg = call()
     assert err == 0 and torch.equal(dx, clean[5]) and torch.equal(dg, clean[6])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dres", [False, True])
+@pytest.mark.parametrize("T, d", [(12000, 528), (12000, 768), (12000, 1024), (6000, 1040), (6000, 2048), (3000, 2064), (3000, 2880), (3000, 4096),
+                                  (3000, 4112), (3000, 8208)])
+def test_backward_of_many_rows(T, d, dres):
+    """Nine rows or more for every group of warps: the ring's stages are filled again and its phases turn over.  Bounds
+    as above, and a relative one per row, which bf16's rounding takes half of."""
+    _lib()
+    r, dy, e, gamma, rstd, dx, dg = _bwd(T, d, dres, seed=T + d)
+    r, dy, gamma, rstd = r.double(), dy.double(), gamma.double(), rstd.double()[:, None]
+    n, dn = r * rstd, dy * gamma
+    ref = rstd * (dn - n * (dn * n).mean(1, keepdim=True))
+    size = rstd * (dn.abs() + n.abs() * (dn * n).abs().mean(1, keepdim=True))
+    if dres:
+        ref, size = ref + e.double(), size + e.double().abs()
+    assert torch.all((dx.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2e-5 * size)
+    assert torch.all((dx.double() - ref).norm(dim=1) <= 2.0 ** -7 * ref.norm(dim=1))
+    terms = dy * n
+    assert torch.all((dg.double() - terms.sum(0)).abs() <= 2e-5 * terms.abs().sum(0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T, d", [(1000, 256), (6000, 1024), (3000, 4096), (700, 8192)])
+def test_backward_in_place(T, d):
+    """dx may be dy or dres: the same bits as in a buffer of its own."""
+    _lib()
+    r, dy, e, gamma, rstd, dx, dg = _bwd(T, d, True, seed=T)
+    for which in (0, 1):
+        a = [dy.clone(), e.clone()]
+        dg2 = torch.empty_like(dg)
+        ws = torch.empty(Q.qad_rmsnorm_workspace_bytes(T, d), dtype=torch.uint8, device="cuda")
+        Q.qad_rmsnorm_bwd(a[0], a[1], r, gamma, rstd, a[which], dg2, T, d, d, ws)
+        assert Q.qad_check_device_error(ws) == 0
+        assert torch.equal(a[which], dx) and torch.equal(dg2, dg) and torch.equal(a[1 - which], (e, dy)[which])
