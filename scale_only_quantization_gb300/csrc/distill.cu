@@ -173,13 +173,15 @@ struct DistillGrid {
 // What bounds it: the gathered rows come from HBM (a head of 152k rows does not stay in L2), and a stage is
 // a chain of some 2000 cycles of waits, reductions and exponentials, so that the bytes that the SM's
 // registers hold at once set the rate: two teams of 4 warps with 8 rows each (64 KB) reach 6.0 TB/s of
-// head rows at d = 2048, K = 64 (178 us for 4096 token rows); batches of 4 rows 206 us, 8-warp teams with
+// head rows at d = 2048, K = 64 (178 to 182 us for 4096 token rows); batches of 4 rows 206 us, 8-warp teams with
 // half the columns per lane 206 us.  One team of 8 warps takes d = 4096; with both divergences its third
-// sum leaves it at 4.4 TB/s (967 us for 16384 token rows, K = 32).  Two teams on an SM there, with batches of 4
-// rows or 2 that are read a second time from shared memory instead of held in registers, spill and hold each
-// stage for its whole chain: 1670 to 2400 us.  Reading the rows a second time from L2
+// sum leaves it at 4.4 TB/s (967 to 976 us for 16384 token rows, K = 32; 746 us without it).  Two teams on an SM
+// there, with batches of 4 rows or 2 that are read a second time from shared memory instead of held in registers,
+// spill and hold each stage for its whole chain: 1670 to 2400 us.  Reading the rows a second time from L2
 // for the gradient instead took 305 and 1240 us; matrix instructions (mma.sync, 8 rows a fragment) for both
-// products 234 and 1358 us, their rate on this chip being a few times the FMA units' only.
+// products 234 and 1358 us, their rate on this chip being a few times the FMA units' only.  Wider rows take one team of
+// 16 warps with batches of 2 head rows, or of 1: 4096 token rows of d = 8192, K = 32 515 us (4.2 TB/s), mixed 880;
+// 2048 of d = 16384 1455 us (1.5 TB/s), mixed 3020, where the sums spill (0.5 and 1.6 KB).
 template <int CW, int V, int R, bool MIX>
 __global__ void __launch_bounds__(32 * (teams_of<CW, V>() * (CW + 1)), 1)
     distill_kernel(const Distill p, const DistillGrid q, const int64_t N) {

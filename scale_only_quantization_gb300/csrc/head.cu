@@ -20,10 +20,16 @@
 // warps 2-9 run the epilogue of one accumulator while the other is filled.
 //
 // What bounds it: the tensor cores from a few hundred token rows on (8192 x 2048 x 151936 with dh: 4 N V d
-// flop in 5.8 ms, 1.76 PFLOP/s; the logits kernel at 90% of the tensor pipe's cycles, its epilogue of 5500
-// cycles a tile under the 16400 of the tile's MMAs); below that the head's one reading per product (8 rows'
-// loss 111 us, 5.6 TB/s; with dh the head is read twice, 240 us).  At d = 256 the epilogue is longer than
-// the MMAs, and the launches of the short kernels weigh as much (512 x 256 x 32000: 51 us).
+// flop in 6.0 to 6.3 ms as the power cap allows, 1.62 to 1.70 PFLOP/s; the logits kernel at 88% of the tensor pipe's
+// cycles, its epilogue of 5500 cycles a tile under the 16400 of the tile's MMAs, the product with the head at 97%);
+// below that the head's one reading per product (8 rows' loss 111 to 114 us, 5.5 TB/s; with dh the head is read twice,
+// 234 us: one piece is the whole vocabulary, so the second product finds none of it in L2).  At d = 256 the
+// epilogue is longer than the MMAs, and the launches of the short kernels weigh as much (512 x 256 x 32000: 51 us).
+//
+// Roundings to bf16: e before the product with the head (2^-8 of a term, below dh's own rounding: dh is as far from
+// the 64-bit value as with fp32 probabilities, 1.7e-3), and the normalised residual g (q - 1) before the product with h,
+// which raises dW's error from 1.7e-3 to 2.4e-3: the tensor cores take bf16 operands.  exp is the intrinsic (2
+// ulp and 1.2 ulp per nat of its argument): the loss is off by 1.7e-7 instead of 7.5e-8.
 #include <utility>
 
 #include "internal.h"

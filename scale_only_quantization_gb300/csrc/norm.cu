@@ -9,8 +9,10 @@
 //   dx = rstd * (dn - n * mean(dn * n)) + dres,   dgamma = sum over rows of dy * n
 // All sums are fp32.  One pass over the data: a row stays in registers between its reductions, so
 // both directions are bound by HBM.  16384 x 2048: forward with residual, y and E4M3 codes 49 us for 302 MB
-// (6.1 TB/s), backward with the residual's gradient and dgamma 50 us for 268 MB: 6.9 TB/s between 8192 and 16384
-// rows, 6 us of launch and first rows, 4.5 us for the sum of the partial weight gradients.
+// (6.1 TB/s), backward with the residual's gradient and dgamma 49.4 us for 268 MB: 6.9 TB/s between 8192 and 16384
+// rows, 6 us of launch and first rows, 4.5 us for the sum of the partial weight gradients.  Rows wider than 4096 go
+// without the ring, one block of the backward per SM: 8192 x 8192 takes 99.6 us (5.4 TB/s), 4096 x 16384 155 us
+// (3.5 TB/s, with 76 to 228 bytes of spills); their forward 53.6 us for 4096 x 8192 (5.6 TB/s).
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -103,9 +105,11 @@ __device__ __forceinline__ void unpack4(const uint2& u, float* f) {
 __device__ __forceinline__ uint2 pack4(const float* f) { return make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])); }
 
 // The squares of bf16 values are exact in fp32, so rstd depends on the order of their sum alone.  Up to 4096
-// elements it is that of an unfused fp32 row sum: 128 chains (element i in chain i % 128), the four of a
-// group one after the other, then the 32 groups pairwise.  rstd and y then have the unfused bits: a last place
-// of rstd moves y by a bf16 step now and then and with it, in the row's largest element, the scale.
+// elements that order is fixed: 128 chains (element i in chain i % 128), the four of a group one after the
+// other, then the 32 groups pairwise, whatever the kernel that takes the row (and as an evaluation in elementary fp32
+// operations sums a row on this GPU); wider rows are summed in their lanes' own order.  A last place of rstd moves y by
+// a bf16 step now and then and with it, in the row's largest element, the scale.  The scale is the quotient by
+// 448 or 127, as the layer's is: a product with the rounded reciprocal differs in the last place for half the rows.
 
 // Rows of up to 1024 elements: one warp per row, no barrier; lane l keeps the 4-element groups l, l + 32, ...
 template <int G, int KIND>
@@ -697,7 +701,7 @@ cudaError_t bwd_launch(const NormBwd& p, int blocks, cudaStream_t st) {
 
 // Blocks of the backward, and so partial dgamma rows: a constant, so that the workspace size needs no device query.
 // (Bounding the registers for three or four blocks spills: 86 and 96 us against 50 for 16384 x 2048.)
-constexpr int kNormBlocks = 304;  // two per SM of 152, as many as the registers hold
+constexpr int kNormBlocks = 304;  // two per SM of 152: as many as the registers hold up to 4096 elements, twice as many above
 
 int norm_blocks(int64_t T) { return (int)(T < kNormBlocks ? T : kNormBlocks); }
 
