@@ -248,13 +248,15 @@ class QADHeadLoss(torch.nn.Module):
     def __init__(self, w, lm_weight=1.0, distill_weight=1.0, tau=1.0):
         super().__init__()
         self.register_buffer("w", _packed(w.to(torch.bfloat16)))
-        self.register_buffer("err", torch.zeros(1, dtype=torch.int32, device=w.device), persistent=False)
+        self._err = {}  # device -> error word; not a buffer, which data parallelism would overwrite with rank 0's
         self.lm_weight, self.distill_weight, self.tau = float(lm_weight), float(distill_weight), float(tau)
 
     def device_error(self):
         """The QAD_DEV_* bits of the calls since it was last read (0: none), and clears them; waits for the device."""
-        code = int(self.err.item())
-        self.err.zero_()
+        code = 0
+        for err in self._err.values():
+            code |= int(err.item())
+            err.zero_()
         return code
 
     def forward(self, h, target=None, teacher_idx=None, teacher_logits=None, mix=None):
@@ -271,7 +273,9 @@ class QADHeadLoss(torch.nn.Module):
             g_kd = kept * (self.distill_weight / kept.sum().clamp_min(1.0))
         if not torch.is_grad_enabled():
             h = h.detach()
+        if h.device not in self._err:
+            self._err[h.device] = torch.zeros(1, dtype=torch.int32, device=h.device)
         total, ce, kd = QADHeadLossFunction.apply(h, self.w, target, g_lm, teacher_idx, teacher_logits, g_kd, self.tau,
-                                                  mix, self.err)
+                                                  mix, self._err[h.device])
         lm = None if ce is None else ce.sum() / live.sum().clamp_min(1.0)
         return total, lm, None if kd is None else kd.sum() / kept.sum().clamp_min(1.0)

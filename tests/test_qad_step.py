@@ -365,3 +365,11 @@ def test_no_gradient_asked_none_computed(monkeypatch):
     with torch.no_grad():
         got = head(h.clone().requires_grad_(True), target, idx, t)
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and not got[0].requires_grad
+
+
+def test_the_error_word_is_the_rank_s_own():
+    """Data parallelism broadcasts a module's buffers from rank 0 before each forward: the error word is none."""
+    from scale_only_quantization_gb300.autograd import QADHeadLoss
+    h = QADHeadLoss(torch.randn(10, 64))
+    assert [n for n, _ in h.named_buffers()] == ["w"] and list(h.state_dict()) == ["w"]
+    assert h.device_error() == 0
