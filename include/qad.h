@@ -244,7 +244,7 @@ int qad_moe_combine(const void* rows, const int32_t* row_of, const float* p, voi
  *   y     = bf16(r * rstd * gamma)              for the router, or as the layer's x
  *   scale = fp32(max |y| / 448) (E4M3) or / 127 (INT8), per row
  *   codes = E4M3 or INT8 code of fp32(y / scale); y_hat = bf16(code value * scale)
- * -- the same bits as the layer's own activation quantizer gives for y.
+ * -- the same bits as the layer's own activation quantizer gives for a finite y.
  *   x     bf16 [T, d], ldx elements between rows     res    bf16 [T, d], ldres between rows, or NULL
  *   gamma bf16 [d]                                   res_out bf16 [T, d] or NULL: r (may be res itself
  *                                                           when ldres == d, or x when ldx == d)
@@ -252,8 +252,9 @@ int qad_moe_combine(const void* rows, const int32_t* row_of, const float* p, voi
  *   y, y_hat and codes must be given, and codes need scale; y_hat, codes and scale must be NULL with
  *   QAD_ACT_NONE.  Outputs other than res_out may not overlap inputs.
  * Requires d % 16 == 0, d <= QAD_RMSNORM_MAX_D (else QAD_ERR_UNSUPPORTED), ldx, ldres >= d and multiples
- * of 8, eps >= 0.  A row of zeros gives y = 0, scale 0 and codes of +-0 (rstd 0 without eps).  A NaN or an infinity in y is one in scale, and
- * makes the row's y_hat and E4M3 codes NaN (an infinity: its own code, the others are 0; INT8 codes have no NaN).
+ * of 8, eps >= 0.  A row of zeros gives y = 0, scale 0 and codes of +-0 (rstd 0 without eps).  A NaN or an
+ * infinity in y is one in scale and makes the row's y_hat NaN, and its E4M3 codes (an infinity: its own code, the
+ * others are 0; INT8 codes have no NaN).
  */
 typedef enum { QAD_ACT_NONE = 0, QAD_ACT_E4M3 = 1, QAD_ACT_INT8 = 2 } qad_act;
 enum { QAD_RMSNORM_MAX_D = 16384 };
