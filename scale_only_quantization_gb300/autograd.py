@@ -166,6 +166,11 @@ class QADRMSNorm(torch.nn.Module):
         return (y, r) if self.act == QAD_ACT_NONE else (y, r, codes, scale)
 
 
+def _tokens(t, V):
+    """t as int32: a 64-bit token keeps its side of the vocabulary [0, V) instead of wrapping into it."""
+    return t if t.dtype == torch.int32 else t.clamp(-1, V).to(torch.int32)
+
+
 class QADHeadLossFunction(torch.autograd.Function):
     """total = sum_i g_lm[i] * CE_i + sum_i g_kd[i] * KD_i of hidden states h against the frozen head w.
 
@@ -173,8 +178,8 @@ class QADHeadLossFunction(torch.autograd.Function):
     divergence over the teacher's top tokens idx [N, K] with logits t [N, K], softened by tau, mixed
     forward and reverse by mix [N] (None: forward).  Either part is left out when its target or idx is
     None.  The hidden-state gradient is formed in the forward, where the logits are, and scaled by the
-    upstream gradient in the backward; an h that needs none (detach it under no_grad) costs the losses alone.  err int32 [1]: a device error word that the calls' is OR-ed into.
-    Returns (total, CE [N] or None, KD [N] or None).
+    upstream gradient in the backward; an h that needs none (detach it under no_grad) costs the losses alone.
+    err int32 [1]: a device error word that the calls' is OR-ed into.  Returns (total, CE [N] or None, KD [N] or None).
     """
 
     @staticmethod
@@ -190,7 +195,7 @@ class QADHeadLossFunction(torch.autograd.Function):
         total = torch.zeros((), dtype=torch.float32, device=dev)
         ce = kd = None
         if target is not None:
-            target = _packed(target.reshape(-1).to(torch.int32))
+            target = _packed(_tokens(target.reshape(-1), V))
             g_lm = _packed(g_lm.to(torch.float32))
             if target.numel() != N or g_lm.numel() != N:
                 raise ValueError("one target and one weight per row of h")
@@ -204,7 +209,7 @@ class QADHeadLossFunction(torch.autograd.Function):
             total = total + torch.dot(ce, g_lm)
         if idx is not None:
             K = idx.shape[-1]
-            idx = _packed(idx.reshape(N, K).to(torch.int32))
+            idx = _packed(_tokens(idx.reshape(N, K), V))
             t = _packed(t.reshape(N, K).to(torch.float32))
             g_kd = _packed(g_kd.to(torch.float32))
             mix = None if mix is None else _packed(mix.to(torch.float32))

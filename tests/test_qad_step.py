@@ -373,3 +373,31 @@ def test_the_error_word_is_the_rank_s_own():
     h = QADHeadLoss(torch.randn(10, 64))
     assert [n for n, _ in h.named_buffers()] == ["w"] and list(h.state_dict()) == ["w"]
     assert h.device_error() == 0
+
+
+def test_wide_tokens_do_not_wrap_into_the_vocabulary():
+    from scale_only_quantization_gb300.autograd import _tokens
+    t = torch.tensor([0, 99, 100, -1, -100, 2 ** 32 + 5, -(2 ** 32) + 5, 2 ** 62])
+    assert _tokens(t, 100).tolist() == [0, 99, 100, -1, -1, 100, -1, 100] and _tokens(t, 100).dtype == torch.int32
+    t = t[:5].to(torch.int32)
+    assert _tokens(t, 100) is t
+
+
+@pytest.mark.gpu
+def test_head_loss_of_wide_tokens():
+    """A 64-bit token whose low word names a word of the vocabulary is past it all the same."""
+    from scale_only_quantization_gb300.autograd import QADHeadLoss
+    _build()
+    N, d, V, K = 20, 64, 300, 8
+    h = torch.randn((N, d), device="cuda").to(torch.bfloat16)
+    target = torch.randint(0, V, (N,), device="cuda")
+    idx = torch.randint(0, V, (N, K), device="cuda")
+    t = torch.randn((N, K), device="cuda")
+    head = QADHeadLoss(torch.randn((V, d), device="cuda") * d ** -0.5)
+    a = [target.clone(), idx.clone()]
+    a[0][4], a[1][6, 2] = -1, -1
+    want = head(h, a[0], a[1], t)
+    assert head.device_error() == 0
+    a[0][4], a[1][6, 2] = 2 ** 32 + 5, 2 ** 32 + 5
+    got = head(h, a[0], a[1], t)
+    assert all(torch.equal(x, y) for x, y in zip(want, got)) and head.device_error() == Q.QAD_DEV_BAD_INDEX
