@@ -192,21 +192,20 @@ class QADHeadLossFunction(torch.autograd.Function):
         ld = h2.stride(0) if N > 1 else d
         grad = ctx.needs_input_grad[0]
         dh = torch.empty((N, d), dtype=torch.bfloat16, device=dev) if grad else None
-        total = torch.zeros((), dtype=torch.float32, device=dev)
-        ce = kd = None
+        total = ce = kd = None
         if target is not None:
             target = _packed(_tokens(target.reshape(-1), V))
             g_lm = _packed(g_lm.to(torch.float32))
             if target.numel() != N or g_lm.numel() != N:
                 raise ValueError("one target and one weight per row of h")
             ce, lse = torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev)
-            ws = torch.empty(qad_linear_ce_workspace_bytes(N, d, V, grad, 0), dtype=torch.uint8, device=dev)
+            ws = torch.empty(qad_linear_ce_workspace_bytes(N, d, V, grad, 0) // 4, dtype=torch.int32, device=dev)
             if grad:
                 qad_linear_ce_fwd_bwd(h2, ld, w, d, target, g_lm, ce, lse, dh, None, 0, N, d, V, ws)
             else:
                 qad_linear_ce_fwd(h2, ld, w, d, target, ce, lse, N, d, V, ws)
-            err.bitwise_or_(ws[:4].view(torch.int32))
-            total = total + torch.dot(ce, g_lm)
+            err.bitwise_or_(ws[:1])
+            total = torch.dot(ce, g_lm)
         if idx is not None:
             K = idx.shape[-1]
             idx = _packed(_tokens(idx.reshape(N, K), V))
@@ -221,8 +220,8 @@ class QADHeadLossFunction(torch.autograd.Function):
                                          d, V, K, err)
             else:
                 qad_distill_topk_fwd(h2, ld, w, d, idx, t, mix, 1.0 / tau, kd, N, d, V, K, err)
-            total = total + torch.dot(kd, g_kd)
-        if target is None and idx is None:
+            total = torch.dot(kd, g_kd) if total is None else total + torch.dot(kd, g_kd)
+        if total is None:
             raise ValueError("neither targets nor teacher logits")
         if grad:
             ctx.save_for_backward(dh)
@@ -265,22 +264,28 @@ class QADHeadLoss(torch.nn.Module):
         return code
 
     def forward(self, h, target=None, teacher_idx=None, teacher_logits=None, mix=None):
-        N = h.numel() // h.shape[-1]
+        N, V = h.numel() // h.shape[-1], self.w.shape[0]
         g_lm = g_kd = None
+        # few operations: small steps wait for their launches
         if target is not None:
-            live = ((target >= 0) & (target < self.w.shape[0])).reshape(-1).to(torch.float32)
-            g_lm = live * (self.lm_weight / live.sum().clamp_min(1.0))
+            target = _tokens(target.reshape(-1), V)
+            live = target.clamp(0, V - 1) == target
+            lm_rows = live.sum().clamp_min_(1)
+            g_lm = live / lm_rows
+            if self.lm_weight != 1.0:
+                g_lm.mul_(self.lm_weight)
         if teacher_idx is not None:
             K = teacher_idx.shape[-1]
-            teacher_idx, teacher_logits = teacher_idx.reshape(N, K), teacher_logits.reshape(N, K)
-            kept = (teacher_idx >= 0) & (teacher_idx < self.w.shape[0]) & (teacher_logits != -torch.inf)
-            kept = kept.any(1).to(torch.float32)
-            g_kd = kept * (self.distill_weight / kept.sum().clamp_min(1.0))
+            teacher_idx, teacher_logits = _tokens(teacher_idx.reshape(N, K), V), teacher_logits.reshape(N, K)
+            kept = ((teacher_idx.clamp(0, V - 1) == teacher_idx) & (teacher_logits != -torch.inf)).any(1)
+            kd_rows = kept.sum().clamp_min_(1)
+            g_kd = kept / kd_rows
+            if self.distill_weight != 1.0:
+                g_kd.mul_(self.distill_weight)
         if not torch.is_grad_enabled():
             h = h.detach()
         if h.device not in self._err:
             self._err[h.device] = torch.zeros(1, dtype=torch.int32, device=h.device)
         total, ce, kd = QADHeadLossFunction.apply(h, self.w, target, g_lm, teacher_idx, teacher_logits, g_kd, self.tau,
                                                   mix, self._err[h.device])
-        lm = None if ce is None else ce.sum() / live.sum().clamp_min(1.0)
-        return total, lm, None if kd is None else kd.sum() / kept.sum().clamp_min(1.0)
+        return total, None if ce is None else ce.sum() / lm_rows, None if kd is None else kd.sum() / kd_rows
