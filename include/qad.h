@@ -341,6 +341,111 @@ int qad_distill_topk_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t 
                              void* dh, int accumulate, int64_t N, int64_t d, int64_t V, int64_t K, int32_t* err,
                              qad_stream_t stream);
 
+/*
+ * The layer for a few tokens: generation, where qad_moe_fwd would fake-quantize every expert to serve one token.
+ * The same definition as qad_moe_fwd (A1, Z1, H, H_hat, Y and out are rounded where that call rounds them), on the
+ * weights of the experts that some token names, each read once and fake-quantized on its way to the tensor cores; no
+ * copy of the weights is made and nothing is kept for a backward pass.  Only the order of the sums differs.
+ *   x, topk_idx, topk_w, w13, s13, w2, s2, out as in qad_moe_fwd.  With QAD_FMT_NVFP4_E4M3, s13 and s2 are the deployed
+ *           scales that qad_nvfp4_deploy_scales makes (per_mat = 2F * d / 16 and d * F / 16): a generating program
+ *           makes them once.
+ *   ws      256-byte aligned, ws_bytes >= qad_moe_few_workspace_bytes(s); its first word is the device error word
+ *           (QAD_DEV_BAD_INDEX, QAD_DEV_DUP_INDEX: that (token, slot) pair is dropped), written by each call.
+ * Supported: T <= QAD_MOE_FEW_MAX_T, d and F at most QAD_MOE_FEW_MAX_D, and what qad_moe_fwd supports; flags 0 or
+ * QAD_FLAG_NO_QUANT (others: QAD_ERR_INVALID_ARG).  32-byte aligned weights are read with one 256-bit load per 16, others
+ * with two 16-byte loads; the results are the same bits.
+ */
+enum { QAD_MOE_FEW_MAX_T = 64, QAD_MOE_FEW_MAX_D = 8192 };
+size_t qad_moe_few_workspace_bytes(const qad_moe_shape* s); /* 0 if the shape is not supported; host-only */
+int qad_moe_few_fwd(const qad_moe_shape* s, const void* x, const int32_t* topk_idx, const float* topk_w,
+                    const void* w13, const float* s13, const void* w2, const float* s2, void* out, void* ws,
+                    size_t ws_bytes, qad_stream_t stream);
+
+/*
+ * Log probabilities of given tokens, entropy and top alternatives of logits the caller holds, in one reading of them:
+ * the teacher's side of the distillation loss ("MCoreQAD Backend", distill_topk), scoring, and the terms of a policy
+ * gradient.  b = inv_temp, p = softmax(b * z):
+ *   lse[i]     = log(sum_v exp(b * z[i, v]))
+ *   logp[i]    = b * z[i, token[i]] - lse[i]  (0 for token < 0)
+ *   entropy[i] = -sum_v p log p
+ *   top_idx[i, :], top_logit[i, :]: the K largest logits in falling order, equal ones by rising index (-0 equals +0)
+ *   z      fp32 or bf16 (dtype: qad_dtype) [N, V], ldz >= V elements between rows (any: rows need no alignment)
+ *   token  int32 [N] or NULL; >= V: logp 0 and QAD_DEV_BAD_INDEX is set in *err
+ *   logp (needs token), lse, entropy fp32 [N]; top_idx int32 [N, K], top_logit fp32 [N, K] (z itself, not scaled:
+ *          qad_distill_topk's idx and t_logit): each may be NULL, but one must be given; K = 0 without the last two
+ *   err    int32 [1] or NULL: a device error word of the caller's, OR-ed into
+ * Masked logits (-inf) have probability 0 and stand last among the alternatives.  A row of nothing else has lse -inf,
+ * entropy 0 and logp -inf.  A NaN or +inf makes lse, logp and entropy NaN; a NaN is never an alternative (slots left
+ * over hold -1 and -inf).  Finite logits count however low they are.
+ * Requires 0 <= K <= min(V, QAD_LOGPROBS_MAX_K), N, V < 2^30, ldz < 2^31, 0 < inv_temp <= 2^100; z 16-byte aligned,
+ * token, err and the outputs 4-byte aligned.
+ */
+typedef enum { QAD_F32 = 0, QAD_BF16 = 1 } qad_dtype;
+enum { QAD_LOGPROBS_MAX_K = 1024 };
+int qad_token_logprobs(const void* z, int dtype, int64_t ldz, const int32_t* token, float inv_temp, float* logp,
+                       float* lse, float* entropy, int32_t* top_idx, float* top_logit, int64_t N, int64_t V, int64_t K,
+                       int32_t* err, qad_stream_t stream);
+
+/*
+ * Gradient of qad_token_logprobs' logp and entropy with respect to the logits:
+ *   dz[i, v] = b * (g_logp[i] * (1[v = token[i]] - p) - g_entropy[i] * p * (log p + entropy[i]))
+ *   token, lse, entropy as the forward took and wrote them (lse is always needed, token with g_logp, entropy with
+ *          g_entropy); a row with token < 0 or >= V has no g_logp part
+ *   g_logp, g_entropy fp32 [N]: the gradients arriving; one may be NULL (none)
+ *   dz     [N, V] of z's type, lddz >= V between rows (written; may be z when lddz == ldz)
+ * A masked logit (-inf) has gradient 0, and so has a whole row of them.  Rows whose z and dz lie alike relative to
+ * 16 bytes are read and written 16 bytes at a time.  Sizes and alignment as in the forward.
+ */
+int qad_token_logprobs_bwd(const void* z, int dtype, int64_t ldz, const int32_t* token, float inv_temp,
+                           const float* lse, const float* entropy, const float* g_logp, const float* g_entropy,
+                           void* dz, int64_t lddz, int64_t N, int64_t V, qad_stream_t stream);
+
+/*
+ * The optimizer's side of a step, over lists of tensors ("MCoreQAD Backend", YAML optim: lr, betas, weight decay,
+ * grad_clip).  A list is an array in HOST memory, read before the call returns; the tensors are contiguous, in any
+ * number and of any size (0 too), and do not overlap one another.
+ */
+typedef struct {
+  void* data;     /* 16-byte aligned device pointer (may be NULL when numel is 0) */
+  int64_t numel;
+  int32_t dtype;  /* qad_dtype */
+  int32_t reserved; /* must be 0 */
+} qad_tensor;
+
+/*
+ * norm[0] = sqrt(sum over all n tensors of g^2), n >= 0.  Squares are summed in fp32 over 16 values, and those sums in
+ * 64 bits (values whose squares leave fp32's range as well), in a fixed order: the same bits from call to call.
+ *   norm  fp32 [1] (written)      ws  256-byte aligned, ws_bytes >= qad_grad_norm_workspace_bytes()
+ */
+size_t qad_grad_norm_workspace_bytes(void);
+int qad_grad_norm(const qad_tensor* grads, int64_t n, float* norm, void* ws, size_t ws_bytes, qad_stream_t stream);
+
+/*
+ * out = g * min(1, max_norm / (norm[0] + 1e-6)), tensor by tensor; out may be NULL or hold the same pointers (in place:
+ * gradients within the norm are then not touched).  out's sizes and types are the gradients'.  A NaN norm makes every
+ * gradient NaN, an infinite one makes the finite ones 0.  Requires max_norm >= 0.
+ */
+int qad_grad_clip(const qad_tensor* grads, const qad_tensor* out, int64_t n, const float* norm, float max_norm,
+                  qad_stream_t stream);
+
+/*
+ * One step of AdamW with clipping by the global norm, t = steps[0] + 1, c = min(1, max_norm / (norm[0] + 1e-6)):
+ *   m = beta1 m + (1 - beta1) c g,    v = beta2 v + (1 - beta2) (c g)^2
+ *   p = max(floor, p - lr decay p - lr m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps)),   steps[0] = t
+ *   params, exp_avg, exp_avg_sq  lists of fp32 tensors, updated in place; grads of fp32 or bf16 tensors (read): n each,
+ *           with the same sizes
+ *   lr      fp32 [n] on the device: a rate for each tensor (a schedule rewrites it, a captured step reads it again)
+ *   floor   lower bound of the parameters (a quantizer's scale must stay positive); -inf: none
+ *   norm    fp32 [1] or NULL (c = 1).  A norm that is not finite leaves everything as it was, steps too.
+ *   steps   int64 [1] on the device: steps done so far
+ *   ws      256-byte aligned, ws_bytes >= qad_grad_norm_workspace_bytes() (it may be qad_grad_norm's)
+ * Requires 0 <= beta < 1, eps >= 0, decay >= 0, floor not NaN, max_norm >= 0.
+ */
+int qad_adamw_step(const qad_tensor* params, const qad_tensor* grads, const qad_tensor* exp_avg,
+                   const qad_tensor* exp_avg_sq, int64_t n, const float* lr, double beta1, double beta2, float eps,
+                   float decay, float floor, const float* norm, float max_norm, int64_t* steps, void* ws,
+                   size_t ws_bytes, qad_stream_t stream);
+
 /* Synchronises `stream`, copies the device error word of `ws` into *code (host
  * pointer, may be NULL) and returns QAD_OK if it is zero, QAD_ERR_DEVICE otherwise. */
 int qad_check_device_error(void* ws, qad_stream_t stream, int32_t* code);
@@ -397,7 +502,9 @@ enum {
   QAD_K_DEPLOY_SCALES = 15,      /* QAD_FMT_NVFP4_E4M3: the deployed weight scales */
   QAD_K_RMSNORM = 16, QAD_K_RMSNORM_BWD = 17,
   QAD_K_CE_LOGITS = 18, QAD_K_CE_DH = 19, QAD_K_CE_DW = 20, QAD_K_DISTILL = 21,
-  QAD_K_COUNT = 22
+  QAD_K_MOE_FEW = 22, QAD_K_LOGPROBS = 23, QAD_K_LOGPROBS_BWD = 24, QAD_K_GRAD_NORM = 25, QAD_K_GRAD_CLIP = 26,
+  QAD_K_ADAMW = 27,
+  QAD_K_COUNT = 28
 };
 int qad_profile_enable(int on);
 int qad_profile_reset(void);

@@ -25,9 +25,12 @@ VIEWS = ["HEADER", "OFFSETS", "COUNTS", "ROW_TOKEN", "ROW_SLOT", "ROW_OF", "W13_
          "H_HAT", "Y", "DY", "DZ1", "DA1", "XQ", "W13_CODES", "W2_CODES", "A1_CODES", "H_CODES", "A_SCALE",
          "H_SCALE", "S13_DEPLOYED", "S2_DEPLOYED"]
 VIEW = {n: i for i, n in enumerate(VIEWS)}
-KERNELS = 22
+KERNELS = 28
 QAD_ACT_NONE, QAD_ACT_E4M3, QAD_ACT_INT8 = range(3)
 QAD_RMSNORM_MAX_D, QAD_DISTILL_MAX_D, QAD_DISTILL_MAX_K = 16384, 16384, 1024
+QAD_MOE_FEW_MAX_T, QAD_MOE_FEW_MAX_D = 64, 8192
+QAD_F32, QAD_BF16 = range(2)
+QAD_LOGPROBS_MAX_K = 1024
 
 EXPORTS = ["qad_fakequant_fwd", "qad_moe_workspace_bytes", "qad_moe_fwd", "qad_moe_bwd_dgrad",
            "qad_moe_bwd_scalegrad", "qad_check_device_error", "qad_status_string", "qad_moe_debug_view",
@@ -35,7 +38,8 @@ EXPORTS = ["qad_fakequant_fwd", "qad_moe_workspace_bytes", "qad_moe_fwd", "qad_m
            "qad_debug_quotient", "qad_route_permute_noalloc", "qad_debug_wait_timeout", "qad_debug_stuck_copy",
            "qad_moe_combine", "qad_nvfp4_deploy_scales", "qad_rmsnorm_workspace_bytes", "qad_rmsnorm_fwd", "qad_rmsnorm_bwd",
            "qad_linear_ce_workspace_bytes", "qad_linear_ce_fwd", "qad_linear_ce_fwd_bwd", "qad_distill_topk_fwd",
-           "qad_distill_topk_fwd_bwd"]
+           "qad_distill_topk_fwd_bwd", "qad_moe_few_workspace_bytes", "qad_moe_few_fwd", "qad_token_logprobs",
+           "qad_token_logprobs_bwd", "qad_grad_norm_workspace_bytes", "qad_grad_norm", "qad_grad_clip", "qad_adamw_step"]
 
 
 class QADError(RuntimeError):
@@ -51,10 +55,38 @@ class MoEShape(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class Tensor(ctypes.Structure):
+    """qad_tensor: one entry of a list of tensors."""
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class TensorList:
+    """Tensors as the optimizer calls take them (qad_tensor[]); holds the tensors, so that their memory stays."""
+
+    def __init__(self, tensors):
+        import torch
+        kinds = {torch.float32: QAD_F32, torch.bfloat16: QAD_BF16}
+        self.tensors = list(tensors)
+        self.n = len(self.tensors)
+        self.array = (Tensor * max(1, self.n))()
+        for a, t in zip(self.array, self.tensors):
+            if t.dtype not in kinds or not t.is_contiguous():
+                raise ValueError("a list takes contiguous fp32 and bf16 tensors, got %s %s with strides %s" % (
+                    t.dtype, tuple(t.shape), t.stride()))
+            a.data, a.numel, a.dtype = t.data_ptr(), t.numel(), kinds[t.dtype]
+
+
+def tensor_list(tensors):
+    """A TensorList of `tensors`: made once where the tensors stay (a captured step, preallocated gradients)."""
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
 _SHAPE = ctypes.POINTER(MoEShape)
 
 
@@ -101,6 +133,15 @@ def lib():
                                                     _P, _P]),
             "qad_distill_topk_fwd_bwd": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _F32, _P, _P, _P, ctypes.c_int,
                                                         _I64, _I64, _I64, _I64, _P, _P]),
+            "qad_moe_few_workspace_bytes": (ctypes.c_size_t, [_SHAPE]),
+            "qad_moe_few_fwd": (ctypes.c_int, [_SHAPE] + [_P] * 9 + [ctypes.c_size_t, _P]),
+            "qad_token_logprobs": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _F32] + [_P] * 5 + [_I64] * 3 + [_P, _P]),
+            "qad_token_logprobs_bwd": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _F32] + [_P] * 5 + [_I64] * 3 + [_P]),
+            "qad_grad_norm_workspace_bytes": (ctypes.c_size_t, []),
+            "qad_grad_norm": (ctypes.c_int, [_P, _I64, _P, _P, ctypes.c_size_t, _P]),
+            "qad_grad_clip": (ctypes.c_int, [_P, _P, _I64, _P, _F32, _P]),
+            "qad_adamw_step": (ctypes.c_int, [_P] * 4 + [_I64, _P, _F64, _F64, _F32, _F32, _F32, _P, _F32, _P, _P,
+                                              ctypes.c_size_t, _P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -292,6 +333,62 @@ def qad_distill_topk_fwd_bwd(h, ldh, w, ldw, idx, t_logit, mix, inv_temp, g, los
                                                  _ptr(mix), float(inv_temp), _ptr(g), _ptr(loss), _ptr(dh),
                                                  int(accumulate), int(N), int(d), int(V), int(K), _ptr(err),
                                                  _stream(stream)), "qad_distill_topk_fwd_bwd")
+
+
+def qad_moe_few_workspace_bytes(s):
+    return int(lib().qad_moe_few_workspace_bytes(ctypes.byref(s)))
+
+
+def qad_moe_few_fwd(s, x, topk_idx, topk_w, w13, s13, w2, s2, out, ws, stream=None):
+    """The layer's forward for at most QAD_MOE_FEW_MAX_T tokens, nothing kept for a backward (see include/qad.h)."""
+    return _check(lib().qad_moe_few_fwd(ctypes.byref(s), _ptr(x), _ptr(topk_idx), _ptr(topk_w), _ptr(w13), _ptr(s13),
+                                        _ptr(w2), _ptr(s2), _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream)),
+                  "qad_moe_few_fwd")
+
+
+def qad_token_logprobs(z, dtype, ldz, token, inv_temp, logp, lse, entropy, top_idx, top_logit, N, V, K, err=None,
+                       stream=None):
+    """Log probabilities of given tokens, entropy and top alternatives of logits (see include/qad.h)."""
+    return _check(lib().qad_token_logprobs(_ptr(z), int(dtype), int(ldz), _ptr(token), float(inv_temp), _ptr(logp),
+                                           _ptr(lse), _ptr(entropy), _ptr(top_idx), _ptr(top_logit), int(N), int(V),
+                                           int(K), _ptr(err), _stream(stream)), "qad_token_logprobs")
+
+
+def qad_token_logprobs_bwd(z, dtype, ldz, token, inv_temp, lse, entropy, g_logp, g_entropy, dz, lddz, N, V, stream=None):
+    return _check(lib().qad_token_logprobs_bwd(_ptr(z), int(dtype), int(ldz), _ptr(token), float(inv_temp), _ptr(lse),
+                                               _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(dz), int(lddz), int(N),
+                                               int(V), _stream(stream)), "qad_token_logprobs_bwd")
+
+
+def qad_grad_norm_workspace_bytes():
+    return int(lib().qad_grad_norm_workspace_bytes())
+
+
+def qad_grad_norm(grads, norm, ws, stream=None):
+    """The norm over all tensors of a list (a TensorList, or the tensors themselves)."""
+    g = tensor_list(grads)
+    return _check(lib().qad_grad_norm(g.array, g.n, _ptr(norm), _ptr(ws), _nbytes(ws), _stream(stream)), "qad_grad_norm")
+
+
+def qad_grad_clip(grads, out, norm, max_norm, stream=None):
+    """Gradients times min(1, max_norm / (norm + 1e-6)); out None: in place."""
+    g, o = tensor_list(grads), None if out is None else tensor_list(out)
+    if o is not None and o.n != g.n:
+        raise ValueError("%d gradients and %d outputs" % (g.n, o.n))
+    return _check(lib().qad_grad_clip(g.array, None if o is None else o.array, g.n, _ptr(norm), float(max_norm),
+                                      _stream(stream)), "qad_grad_clip")
+
+
+def qad_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, beta1, beta2, eps, decay, floor, norm, max_norm, steps, ws,
+                   stream=None):
+    """One AdamW step over lists of tensors, clipped by the norm if one is given (see include/qad.h)."""
+    p, g, m, v = (tensor_list(a) for a in (params, grads, exp_avg, exp_avg_sq))
+    if not p.n == g.n == m.n == v.n or (lr is not None and lr.numel() != g.n):
+        raise ValueError("the lists differ in length: %d parameters, %d gradients, %d and %d moments, %s rates" % (
+            p.n, g.n, m.n, v.n, None if lr is None else lr.numel()))
+    return _check(lib().qad_adamw_step(p.array, g.array, m.array, v.array, g.n, _ptr(lr), float(beta1), float(beta2),
+                                       float(eps), float(decay), float(floor), _ptr(norm), float(max_norm), _ptr(steps),
+                                       _ptr(ws), _nbytes(ws), _stream(stream)), "qad_adamw_step")
 
 
 def qad_debug_wait_timeout(err_word, budget_cycles, stream=None):

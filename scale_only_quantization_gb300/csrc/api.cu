@@ -530,6 +530,122 @@ int qad_distill_topk_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t 
   return distill_call(h, ldh, w, ldw, idx, t_logit, mix, inv_temp, g, loss, dh, accumulate, N, d, V, K, err, stream);
 }
 
+size_t qad_moe_few_workspace_bytes(const qad_moe_shape* s) {
+  if (!s) return 0;
+  FewLayout L;
+  return few_layout_of(*s, &L) == QAD_OK ? L.total : 0;
+}
+
+int qad_moe_few_fwd(const qad_moe_shape* s, const void* x, const int32_t* topk_idx, const float* topk_w,
+                    const void* w13, const float* s13, const void* w2, const float* s2, void* out, void* ws,
+                    size_t ws_bytes, qad_stream_t stream) {
+  if (!s) return QAD_ERR_INVALID_ARG;
+  FewLayout L;
+  const int rc = few_layout_of(*s, &L);
+  if (rc != QAD_OK) return rc;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return QAD_ERR_INVALID_ARG;
+  if (ws_bytes < L.total) return QAD_ERR_WORKSPACE;
+  if (!ok_ptr(w13) || !ok_ptr(s13) || !ok_ptr(w2) || !ok_ptr(s2)) return QAD_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (s->T == 0) return to_status(cudaMemsetAsync(ws, 0, 4, st));
+  if (!ok_ptr(x) || !ok_ptr(topk_idx) || !ok_ptr(topk_w) || !ok_ptr(out)) return QAD_ERR_INVALID_ARG;
+  return to_status(launch_moe_few(*s, L, x, topk_idx, topk_w, w13, s13, w2, s2, out, static_cast<uint8_t*>(ws), st));
+}
+
+static bool ok_words(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static int check_logits(const void* z, int dtype, int64_t ldz, float inv_temp, int64_t N, int64_t V) {
+  if ((dtype != QAD_F32 && dtype != QAD_BF16) || N < 0 || V <= 0 || ldz < V) return QAD_ERR_INVALID_ARG;
+  if (!(inv_temp > 0.0f) || !(inv_temp <= 0x1p100f)) return QAD_ERR_INVALID_ARG;
+  if (N >= (int64_t(1) << 30) || V >= (int64_t(1) << 30) || ldz >= (int64_t(1) << 31)) return QAD_ERR_UNSUPPORTED;
+  return N > 0 && !ok_ptr(z) ? QAD_ERR_INVALID_ARG : QAD_OK;
+}
+
+int qad_token_logprobs(const void* z, int dtype, int64_t ldz, const int32_t* token, float inv_temp, float* logp,
+                       float* lse, float* entropy, int32_t* top_idx, float* top_logit, int64_t N, int64_t V, int64_t K,
+                       int32_t* err, qad_stream_t stream) {
+  if (const int rc = check_logits(z, dtype, ldz, inv_temp, N, V)) return rc;
+  if (K < 0 || (K > 0) != (top_idx || top_logit) || (logp && !token)) return QAD_ERR_INVALID_ARG;
+  if (K > V || K > QAD_LOGPROBS_MAX_K) return QAD_ERR_UNSUPPORTED;
+  if (!logp && !lse && !entropy && !K && N > 0) return QAD_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)token, (const void*)logp, (const void*)lse, (const void*)entropy,
+                        (const void*)top_idx, (const void*)top_logit, (const void*)err})
+    if (!ok_words(p)) return QAD_ERR_INVALID_ARG;
+  if (N == 0) return QAD_OK;
+  return to_status(launch_logprobs(z, dtype, ldz, token, inv_temp, logp, lse, entropy, top_idx, top_logit, N, V, K, err,
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qad_token_logprobs_bwd(const void* z, int dtype, int64_t ldz, const int32_t* token, float inv_temp,
+                           const float* lse, const float* entropy, const float* g_logp, const float* g_entropy,
+                           void* dz, int64_t lddz, int64_t N, int64_t V, qad_stream_t stream) {
+  if (const int rc = check_logits(z, dtype, ldz, inv_temp, N, V)) return rc;
+  if (lddz < V || lddz >= (int64_t(1) << 31)) return lddz < V ? QAD_ERR_INVALID_ARG : QAD_ERR_UNSUPPORTED;
+  if (N == 0) return QAD_OK;
+  if (!ok_ptr(dz) || !lse || (!g_logp && !g_entropy) || (g_logp && !token) || (g_entropy && !entropy) ||
+      (dz == z && lddz != ldz))
+    return QAD_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)token, (const void*)lse, (const void*)entropy, (const void*)g_logp,
+                        (const void*)g_entropy})
+    if (!ok_words(p)) return QAD_ERR_INVALID_ARG;
+  return to_status(launch_logprobs_bwd(z, dtype, ldz, token, inv_temp, lse, entropy, g_logp, g_entropy, dz, lddz, N, V,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// A list of tensors; with `like`, its sizes (and types) are those of that list.
+static int check_list(const qad_tensor* list, int64_t n, const qad_tensor* like, bool same_type, bool f32) {
+  if (n < 0 || (n > 0 && !list)) return QAD_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < n; ++i) {
+    const qad_tensor& t = list[i];
+    if (t.numel < 0 || t.reserved != 0 || (t.dtype != QAD_F32 && t.dtype != QAD_BF16) || (f32 && t.dtype != QAD_F32))
+      return QAD_ERR_INVALID_ARG;
+    if (t.numel > 0 && !ok_ptr(t.data)) return QAD_ERR_INVALID_ARG;
+    if (t.numel >= (int64_t(1) << 40)) return QAD_ERR_UNSUPPORTED;
+    if (like && (t.numel != like[i].numel || (same_type && t.dtype != like[i].dtype))) return QAD_ERR_INVALID_ARG;
+  }
+  return QAD_OK;
+}
+
+static int check_optim_ws(const void* ws, size_t ws_bytes) {
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return QAD_ERR_INVALID_ARG;
+  return ws_bytes < optim_workspace() ? QAD_ERR_WORKSPACE : QAD_OK;
+}
+
+size_t qad_grad_norm_workspace_bytes(void) { return optim_workspace(); }
+
+int qad_grad_norm(const qad_tensor* grads, int64_t n, float* norm, void* ws, size_t ws_bytes, qad_stream_t stream) {
+  if (const int rc = check_list(grads, n, nullptr, false, false)) return rc;
+  if (!norm || !ok_words(norm)) return QAD_ERR_INVALID_ARG;
+  if (const int rc = check_optim_ws(ws, ws_bytes)) return rc;
+  return to_status(launch_grad_norm(grads, n, norm, static_cast<uint8_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qad_grad_clip(const qad_tensor* grads, const qad_tensor* out, int64_t n, const float* norm, float max_norm,
+                  qad_stream_t stream) {
+  if (const int rc = check_list(grads, n, nullptr, false, false)) return rc;
+  if (out)
+    if (const int rc = check_list(out, n, grads, true, false)) return rc;
+  if (!norm || !ok_words(norm) || !(max_norm >= 0.0f)) return QAD_ERR_INVALID_ARG;
+  return to_status(launch_grad_clip(grads, out ? out : grads, n, norm, max_norm, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qad_adamw_step(const qad_tensor* params, const qad_tensor* grads, const qad_tensor* exp_avg,
+                   const qad_tensor* exp_avg_sq, int64_t n, const float* lr, double beta1, double beta2, float eps,
+                   float decay, float floor, const float* norm, float max_norm, int64_t* steps, void* ws,
+                   size_t ws_bytes, qad_stream_t stream) {
+  if (const int rc = check_list(grads, n, nullptr, false, false)) return rc;
+  for (const qad_tensor* list : {params, exp_avg, exp_avg_sq})
+    if (const int rc = check_list(list, n, grads, false, true)) return rc;
+  if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) || !(decay >= 0) || floor != floor)
+    return QAD_ERR_INVALID_ARG;
+  if ((n > 0 && !lr) || !ok_words(lr) || !ok_words(norm) || (norm && !(max_norm >= 0)) || !steps ||
+      (reinterpret_cast<uintptr_t>(steps) & 7u))
+    return QAD_ERR_INVALID_ARG;
+  if (const int rc = check_optim_ws(ws, ws_bytes)) return rc;
+  return to_status(launch_adamw(params, grads, exp_avg, exp_avg_sq, n, lr, beta1, beta2, eps, decay, floor, norm,
+                                max_norm, steps, static_cast<uint8_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int qad_check_device_error(void* ws, qad_stream_t stream, int32_t* code) {
   if (!ws) return QAD_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -626,7 +742,8 @@ const char* qad_kernel_name(int id) {
                                            "gemm_dgrad_fc2_swiglu_bwd", "gemm_dgrad_fc1", "dx_combine",
                                            "gemm_wgrad_fc2_scalegrad", "gemm_wgrad_fc1_scalegrad", "scale_reduce",
                                            "gemm_fc1_recompute", "deploy_scales", "rmsnorm", "rmsnorm_bwd",
-                                           "ce_logits", "ce_dh", "ce_dw", "distill_topk"};
+                                           "ce_logits", "ce_dh", "ce_dw", "distill_topk", "moe_few", "token_logprobs",
+                                           "token_logprobs_bwd", "grad_norm", "grad_clip", "adamw"};
   return (id >= 0 && id < QAD_K_COUNT) ? names[id] : "unknown";
 }
 

@@ -159,4 +159,30 @@ cudaError_t launch_distill_topk(const void* h, int64_t ldh, const void* w, int64
                                 int accumulate, int64_t N, int64_t d, int64_t V, int64_t K, int32_t* err,
                                 cudaStream_t st);
 
+// ---- the layer for a few tokens (few.cu) ----
+struct FewLayout {  // byte offsets of its workspace; the error word comes first
+  size_t arrivals, h, y, total;
+};
+int few_layout_of(const qad_moe_shape& s, FewLayout* L);
+cudaError_t launch_moe_few(const qad_moe_shape& s, const FewLayout& L, const void* x, const int32_t* idx, const float* p,
+                           const void* w13, const float* s13, const void* w2, const float* s2, void* out, uint8_t* ws,
+                           cudaStream_t st);
+
+// ---- log probabilities, entropy and top alternatives of logits, and their gradient (logprobs.cu) ----
+cudaError_t launch_logprobs(const void* z, int dtype, int64_t ldz, const int32_t* token, float inv_temp, float* logp,
+                            float* lse, float* entropy, int32_t* top_idx, float* top_logit, int64_t N, int64_t V,
+                            int64_t K, int32_t* err, cudaStream_t st);
+cudaError_t launch_logprobs_bwd(const void* z, int dtype, int64_t ldz, const int32_t* token, float inv_temp,
+                                const float* lse, const float* entropy, const float* g_logp, const float* g_entropy,
+                                void* dz, int64_t lddz, int64_t N, int64_t V, cudaStream_t st);
+
+// ---- lists of tensors: norm, clipping, AdamW (optim.cu); lists are checked by the caller ----
+size_t optim_workspace();
+cudaError_t launch_grad_norm(const qad_tensor* grads, int64_t n, float* norm, uint8_t* ws, cudaStream_t st);
+cudaError_t launch_grad_clip(const qad_tensor* grads, const qad_tensor* out, int64_t n, const float* norm,
+                             float max_norm, cudaStream_t st);
+cudaError_t launch_adamw(const qad_tensor* params, const qad_tensor* grads, const qad_tensor* m, const qad_tensor* v,
+                         int64_t n, const float* lr, double beta1, double beta2, float eps, float decay, float floor,
+                         const float* norm, float max_norm, int64_t* steps, uint8_t* ws, cudaStream_t st);
+
 }  // namespace qad
