@@ -2,11 +2,13 @@
 
   embedding -> [residual RMSNorm -> router -> routed experts, fake-quantized] x layers -> residual RMSNorm
   -> cross entropy on the frozen head + distillation from the unquantized model's top logits -> scale gradients
+  -> clipping by the global norm and AdamW over all scales
 
 Only the quantizer scales are trained; the teacher is the same frozen model with the quantizers off
-("MCoreQAD Backend", opening section).
+("MCoreQAD Backend", opening section).  With --rollout N the tokens are the quantized model's own: up to 64 sequences
+of N tokens, written one token a step by the layer's form for few tokens.
 
-    python examples/qad_step.py [--fmt N] [--steps N] [--d N] [--layers N] [--vocab N] [--tokens N] [--topk N]
+    python examples/qad_step.py [--fmt N] [--steps N] [--d N] [--layers N] [--vocab N] [--tokens N] [--topk N] [--rollout N]
 """
 import argparse
 import os
@@ -18,7 +20,8 @@ import torch  # noqa: E402
 
 import scale_only_quantization_gb300 as Q  # noqa: E402
 import synth  # noqa: E402
-from scale_only_quantization_gb300.autograd import QADHeadLoss, QADMoE, QADMoEFunction, QADRMSNorm  # noqa: E402
+from scale_only_quantization_gb300.autograd import (QADAdamW, QADHeadLoss, QADMoE, QADMoEFunction, QADRMSNorm,  # noqa: E402
+                                                    QADTokenLogprobs)
 
 
 class Model(torch.nn.Module):
@@ -46,13 +49,15 @@ class Model(torch.nn.Module):
             self.experts.append(QADMoE(w13, synth.init_scales(w13, fmt, g), w2, synth.init_scales(w2, fmt, g), fmt))
         self.head = QADHeadLoss((rand(vocab, d) * 2 * d ** -0.5).to(bf), lm_weight=lm_weight, distill_weight=1.0)
 
-    def hidden(self, tokens, quantized=True):
+    def hidden(self, tokens, quantized=True, few=False):
         x, res = self.embed[tokens], None
         for norm, router, moe in zip(self.norms, self.routers, self.experts):
             y, res = norm(x, res)
             p, idx = torch.topk(y.float() @ router.float().T, self.topk, dim=1)
             p, idx = torch.softmax(p, dim=1), idx.to(torch.int32).contiguous()
-            if quantized:
+            if few:
+                x = moe.few(y, idx, p, quantized)
+            elif quantized:
                 x = moe(y, idx, p)
             else:
                 x = QADMoEFunction.apply(y, idx, p, moe.w13, moe.s13, moe.w2, moe.s2, moe.fmt, Q.QAD_FLAG_NO_QUANT)
@@ -62,21 +67,37 @@ class Model(torch.nn.Module):
     def teacher(self, tokens, k):
         """The unquantized model's top k logits and their tokens."""
         z = self.hidden(tokens, quantized=False).float() @ self.head.w.float().T
-        t, idx = torch.topk(z, k, dim=1)
-        return idx.to(torch.int32).contiguous(), t.contiguous()
+        _, _, _, idx, t = QADTokenLogprobs(top=k)(z)
+        return idx, t
+
+    @torch.no_grad()
+    def rollout(self, start, length, generator):
+        """Sequences [len(start), length] that the quantized model writes, sampled token by token, and each token's log
+        probability under it."""
+        read = QADTokenLogprobs()
+        tokens, logps = [start], []
+        for _ in range(length - 1):
+            z = self.hidden(tokens[-1], few=True).float() @ self.head.w.float().T
+            u = torch.rand(z.shape, generator=generator, device=z.device)
+            tokens.append((z - torch.log(-torch.log(u.clamp_min(1e-20)).clamp_min(1e-20))).argmax(1))
+            logps.append(read(z, tokens[-1])[0])
+        return torch.stack(tokens, 1), torch.stack(logps, 1) if logps else None
 
 
-def train(fmt=Q.QAD_FMT_NVFP4, steps=20, tokens=512, topk=32, lr=0.005, log=print, **model):
-    """Trains the scales for `steps` steps on random tokens; returns the (total, lm, distill) of every step."""
+def train(fmt=Q.QAD_FMT_NVFP4, steps=20, tokens=512, topk=32, lr=0.005, log=print, rollout=0, **model):
+    """Trains the scales for `steps` steps on random tokens, or on sequences of `rollout` tokens that the model writes
+    before the first step; returns the (total, lm, distill) of every step."""
     m = Model(fmt, **model)
     scales = [p for p in m.parameters() if p.requires_grad]
     # a step of Adam moves a parameter by about its rate: `lr` is a fraction of the tensor's typical scale
-    opt = torch.optim.AdamW([dict(params=[s], lr=lr * float(s.detach().mean())) for s in scales], weight_decay=0.0,
-                            betas=(0.9, 0.95))
+    opt = QADAdamW([dict(params=[s], lr=lr * float(s.detach().mean()), floor=1e-8) for s in scales], max_norm=1.0)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     vocab = m.embed.shape[0]
     x = torch.randint(0, vocab, (tokens,), generator=g, device="cuda")
+    if rollout:
+        x = m.rollout(x[:max(1, min(Q.QAD_MOE_FEW_MAX_T, tokens // rollout))], rollout, g)[0].reshape(-1)
+        tokens = x.numel()
     idx, t = m.teacher(x, topk)
     target = idx[:, 0].clone()  # no corpus here: the token that the unquantized model would write
     target[: tokens // 8] = -1  # a prompt: no language-model loss
@@ -85,7 +106,6 @@ def train(fmt=Q.QAD_FMT_NVFP4, steps=20, tokens=512, topk=32, lr=0.005, log=prin
         opt.zero_grad(set_to_none=True)
         total, lm, kd = m.head(m.hidden(x), target, idx, t)
         total.backward()
-        torch.nn.utils.clip_grad_norm_(scales, 1.0)
         opt.step()
         history.append(tuple(float(v.detach()) for v in (total, lm, kd)))
         if log:
@@ -102,7 +122,8 @@ if __name__ == "__main__":
     ap.add_argument("--d", type=int, default=256)
     ap.add_argument("--layers", type=int, default=2)
     ap.add_argument("--vocab", type=int, default=4001)
+    ap.add_argument("--rollout", type=int, default=0, help="tokens of each sequence that the model writes itself")
     a = ap.parse_args()
     from scale_only_quantization_gb300 import build
     build.build()
-    train(a.fmt, a.steps, a.tokens, a.topk, d=a.d, layers=a.layers, vocab=a.vocab)
+    train(a.fmt, a.steps, a.tokens, a.topk, rollout=a.rollout, d=a.d, layers=a.layers, vocab=a.vocab)

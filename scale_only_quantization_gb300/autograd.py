@@ -13,14 +13,20 @@ stashed stages from the forward to the backward, lives in the autograd context.
 
 What stands around the layer in a training step: QADRMSNorm (residual addition, norm and the 8-bit
 form of its output) before it, QADHeadLoss (cross entropy and distillation on the frozen head) at the
-end.
+end, QADTokenLogprobs for what is read off logits the caller holds (the teacher's top alternatives), and
+QADAdamW for the step of the scales.  QADMoE.few is the layer's forward for a few tokens (generation).
 """
+import math
+
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import (QAD_ACT_NONE, qad_distill_topk_fwd, qad_distill_topk_fwd_bwd, qad_linear_ce_fwd, qad_linear_ce_fwd_bwd,
-               qad_linear_ce_workspace_bytes, qad_moe_bwd_dgrad, qad_moe_bwd_scalegrad, qad_moe_fwd,
-               qad_moe_workspace_bytes, qad_rmsnorm_bwd, qad_rmsnorm_fwd, qad_rmsnorm_workspace_bytes, shape)
+               qad_linear_ce_workspace_bytes, qad_moe_bwd_dgrad, qad_moe_bwd_scalegrad, qad_moe_few_fwd,
+               qad_moe_few_workspace_bytes, qad_moe_fwd, qad_moe_workspace_bytes, qad_nvfp4_deploy_scales,
+               qad_rmsnorm_bwd, qad_rmsnorm_fwd, qad_rmsnorm_workspace_bytes, qad_adamw_step, qad_grad_norm,
+               qad_grad_norm_workspace_bytes, qad_token_logprobs, qad_token_logprobs_bwd, shape, tensor_list, QAD_BF16,
+               QAD_F32, QAD_FLAG_NO_QUANT, QAD_FMT_NVFP4_E4M3)
 
 
 class QADMoEFunction(torch.autograd.Function):
@@ -79,6 +85,27 @@ class QADMoE(torch.nn.Module):
     def forward(self, x, topk_idx, topk_w):
         return QADMoEFunction.apply(x.contiguous(), topk_idx.contiguous(), topk_w.contiguous(), self.w13, self.s13,
                                     self.w2, self.s2, self.fmt, self.flags)
+
+    @torch.no_grad()
+    def few(self, x, topk_idx, topk_w, quant=True):
+        """The layer's output for at most QAD_MOE_FEW_MAX_T tokens, without a gradient: what a generation loop calls.
+        quant False: the unquantized teacher."""
+        E, two_f, d = self.w13.shape
+        T, k = topk_idx.shape
+        if x.dtype != torch.bfloat16 or topk_idx.dtype != torch.int32 or topk_w.dtype != torch.float32 or \
+                x.shape != (T, d) or topk_w.shape != (T, k):
+            raise ValueError("x bf16 [T, %d], topk_idx int32 [T, k] and topk_w fp32 [T, k], got %s %s, %s %s, %s %s" % (
+                d, x.dtype, tuple(x.shape), topk_idx.dtype, tuple(topk_idx.shape), topk_w.dtype, tuple(topk_w.shape)))
+        s = shape(T, d, two_f // 2, E, k, self.fmt, 0 if quant else QAD_FLAG_NO_QUANT)
+        s13, s2 = self.s13, self.s2
+        if quant and self.fmt == QAD_FMT_NVFP4_E4M3:  # a program that generates much keeps these between updates
+            s13, s2 = torch.empty_like(self.s13), torch.empty_like(self.s2)
+            for a, b in ((self.s13, s13), (self.s2, s2)):
+                qad_nvfp4_deploy_scales(a, b, E, a.numel() // E)
+        ws = torch.empty(max(1, qad_moe_few_workspace_bytes(s)), dtype=torch.uint8, device=x.device)
+        out = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+        qad_moe_few_fwd(s, _packed(x), _packed(topk_idx), _packed(topk_w), self.w13, s13, self.w2, s2, out, ws)
+        return out
 
 
 def _packed(t):
@@ -289,3 +316,150 @@ class QADHeadLoss(torch.nn.Module):
         total, ce, kd = QADHeadLossFunction.apply(h, self.w, target, g_lm, teacher_idx, teacher_logits, g_kd, self.tau,
                                                   mix, self._err[h.device])
         return total, None if ce is None else ce.sum() / lm_rows, None if kd is None else kd.sum() / kd_rows
+
+
+class QADTokenLogprobsFunction(torch.autograd.Function):
+    """(logp, entropy, lse, top_idx, top_logit) of logits z [N, V] at temperature tau; the gradient is that of logp and
+    entropy."""
+
+    @staticmethod
+    def forward(ctx, z, token, tau, top, err):
+        N, V = z.shape
+        kinds = {torch.bfloat16: QAD_BF16, torch.float32: QAD_F32}
+        if z.dtype not in kinds:
+            raise ValueError("logits must be bf16 or fp32, got %s" % z.dtype)
+        if N and V and (z.stride(1) != 1 or z.stride(0) < V or z.data_ptr() % 16):
+            z = _packed(z)
+        if token is not None:
+            token = _packed(_tokens(token.reshape(-1), V))
+            if token.numel() != N:
+                raise ValueError("one token per row of z")
+        ld = z.stride(0) if N > 1 else V
+        lse, entropy = (torch.empty(N, dtype=torch.float32, device=z.device) for _ in range(2))
+        logp = None if token is None else torch.empty_like(lse)
+        top_idx = torch.empty((N, top), dtype=torch.int32, device=z.device) if top else None
+        top_logit = torch.empty((N, top), dtype=torch.float32, device=z.device) if top else None
+        qad_token_logprobs(z, kinds[z.dtype], ld, token, 1.0 / tau, logp, lse, entropy, top_idx, top_logit, N, V, top, err)
+        ctx.save_for_backward(z, lse, entropy, *(() if token is None else (token,)))
+        ctx.tau, ctx.ld, ctx.kind = tau, ld, kinds[z.dtype]
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(lse, *((top_idx, top_logit) if top else ()))
+        return logp, entropy, lse, top_idx, top_logit
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_logp, g_entropy, _lse, _idx, _logit):
+        if g_logp is None and g_entropy is None:
+            return None, None, None, None, None
+        z, lse, entropy, *token = ctx.saved_tensors
+        N, V = z.shape
+        dz = torch.empty((N, V), dtype=z.dtype, device=z.device)
+        g_logp, g_entropy = (None if g is None else g.to(torch.float32).contiguous() for g in (g_logp, g_entropy))
+        qad_token_logprobs_bwd(z, ctx.kind, ctx.ld, token[0] if token else None, 1.0 / ctx.tau, lse, entropy, g_logp,
+                               g_entropy, dz, V, N, V)
+        return dz, None, None, None, None
+
+
+class QADTokenLogprobs(torch.nn.Module):
+    """What is read off logits: forward(z, token=None) -> (logp, entropy, lse, top_idx, top_logit).
+
+    logp [N] is the log probability of each row's token at temperature tau (None without tokens, 0 where the token is
+    negative); top_idx and top_logit [N, top] the row's largest logits, which are teacher_idx and teacher_logits of
+    QADHeadLoss (None with top 0).  logp and entropy have a gradient.  A token past the vocabulary sets a bit that
+    device_error() returns.
+    """
+
+    def __init__(self, tau=1.0, top=0):
+        super().__init__()
+        self.tau, self.top = float(tau), int(top)
+        self._err = {}  # device -> error word, as QADHeadLoss keeps it
+
+    device_error = QADHeadLoss.device_error
+
+    def forward(self, z, token=None):
+        if z.device not in self._err:
+            self._err[z.device] = torch.zeros(1, dtype=torch.int32, device=z.device)
+        return QADTokenLogprobsFunction.apply(z, token, self.tau, self.top, self._err[z.device])
+
+
+class QADAdamW(torch.optim.Optimizer):
+    """AdamW of the quantizer scales with clipping by the norm over all gradients, in three launches for any number of
+    tensors ("MCoreQAD Backend", YAML optim: lr, betas, weight decay, grad_clip).
+
+    Parameters are fp32; groups may set lr, betas, eps, weight_decay and floor, the lower bound that keeps a scale
+    positive (-inf: none).  max_norm None: no clipping.  Every parameter needs a gradient (fp32 or bf16) at each step; a
+    step whose norm is not finite changes nothing, the count of steps neither.  last_norm [1] is the norm before
+    clipping.  State: exp_avg, exp_avg_sq and step (an int64 on the device that the parameters of a group share).
+    """
+
+    def __init__(self, params, lr=2e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, floor=-math.inf, max_norm=1.0):
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, floor=floor))
+        self.max_norm = max_norm
+        self.last_norm = None
+        self._ws = self._plan = None
+
+    def _make_plan(self):
+        """Groups of equal settings step together: (settings, parameters, their lists, rates, steps)."""
+        sets = {}
+        for group in self.param_groups:
+            key = (*group["betas"], group["eps"], group["weight_decay"], group["floor"])
+            sets.setdefault(key, []).extend((p, group) for p in group["params"])
+        plan = []
+        for key, members in sets.items():
+            ps = [p for p, _ in members]
+            dev = ps[0].device
+            for p in ps:
+                if p.dtype != torch.float32 or not p.is_contiguous() or p.device != dev:
+                    raise ValueError("parameters are contiguous fp32 tensors of one device")
+                st = self.state[p]
+                if "exp_avg" not in st:
+                    st["exp_avg"], st["exp_avg_sq"] = torch.zeros_like(p), torch.zeros_like(p)
+            steps = next((self.state[p]["step"] for p in ps if "step" in self.state[p]), None)
+            steps = torch.zeros(1, dtype=torch.int64, device=dev) if steps is None else steps.to(dev, torch.int64).view(1)
+            for p in ps:
+                self.state[p]["step"] = steps
+            lists = [tensor_list(x) for x in ([p.detach() for p in ps], [self.state[p]["exp_avg"] for p in ps],
+                                              [self.state[p]["exp_avg_sq"] for p in ps])]
+            plan.append(dict(key=key, members=members, lists=lists, steps=steps, lr=None, rates=None))
+        if self._ws is None and plan:
+            self._ws = torch.empty(qad_grad_norm_workspace_bytes(), dtype=torch.uint8, device=plan[0]["steps"].device)
+            self.last_norm = torch.zeros(1, device=self._ws.device)
+        return plan
+
+    def load_state_dict(self, state_dict):
+        super().load_state_dict(state_dict)
+        self._plan = None
+
+    def add_param_group(self, group):
+        super().add_param_group(group)
+        self._plan = None
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        # a plan holds as long as the settings and the parameters' memory stay
+        settings = [(*g["betas"], g["eps"], g["weight_decay"], g["floor"], *[p.data_ptr() for p in g["params"]])
+                    for g in self.param_groups]
+        if self._plan is None or settings != self._settings:
+            self._plan, self._settings = self._make_plan(), settings
+        grads = []
+        for part in self._plan:
+            if any(p.grad is None for p, _ in part["members"]):
+                raise ValueError("every parameter needs a gradient")
+            grads.append([_packed(p.grad) for p, _ in part["members"]])
+        norm = None
+        if self.max_norm is not None and grads:
+            norm = self.last_norm
+            qad_grad_norm([g for part in grads for g in part], norm, self._ws)
+        for part, gs in zip(self._plan, grads):
+            lr = [float(group["lr"]) for _, group in part["members"]]
+            if lr != part["lr"]:
+                part["lr"], part["rates"] = lr, torch.tensor(lr, dtype=torch.float32).to(part["steps"].device)
+            b1, b2, eps, decay, floor = part["key"]
+            p, m, v = part["lists"]
+            qad_adamw_step(p, gs, m, v, part["rates"], b1, b2, eps, decay, floor, norm,
+                           0.0 if norm is None else self.max_norm, part["steps"], self._ws)
+        return loss

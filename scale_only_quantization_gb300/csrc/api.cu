@@ -565,13 +565,14 @@ int qad_token_logprobs(const void* z, int dtype, int64_t ldz, const int32_t* tok
                        float* lse, float* entropy, int32_t* top_idx, float* top_logit, int64_t N, int64_t V, int64_t K,
                        int32_t* err, qad_stream_t stream) {
   if (const int rc = check_logits(z, dtype, ldz, inv_temp, N, V)) return rc;
-  if (K < 0 || (K > 0) != (top_idx || top_logit) || (logp && !token)) return QAD_ERR_INVALID_ARG;
+  if (K < 0) return QAD_ERR_INVALID_ARG;
   if (K > V || K > QAD_LOGPROBS_MAX_K) return QAD_ERR_UNSUPPORTED;
-  if (!logp && !lse && !entropy && !K && N > 0) return QAD_ERR_INVALID_ARG;
+  if (N == 0) return QAD_OK;  // tensors without elements have no address
+  if ((K > 0) != (top_idx || top_logit) || (logp && !token)) return QAD_ERR_INVALID_ARG;
+  if (!logp && !lse && !entropy && !K) return QAD_ERR_INVALID_ARG;
   for (const void* p : {(const void*)token, (const void*)logp, (const void*)lse, (const void*)entropy,
                         (const void*)top_idx, (const void*)top_logit, (const void*)err})
     if (!ok_words(p)) return QAD_ERR_INVALID_ARG;
-  if (N == 0) return QAD_OK;
   return to_status(launch_logprobs(z, dtype, ldz, token, inv_temp, logp, lse, entropy, top_idx, top_logit, N, V, K, err,
                                    reinterpret_cast<cudaStream_t>(stream)));
 }
