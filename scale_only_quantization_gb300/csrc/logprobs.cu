@@ -6,12 +6,14 @@
 //   dz = b (g (1[v = t] - p) - h p (log p + H)),   p = exp(b z - lse)
 //
 // Each thread keeps m, S and U of the logits it has seen (a new maximum rescales S and U); the block joins them at the
-// end.  The alternatives: a logit enters the block's candidates when it is above a threshold that at least K logits
-// reach.  The threshold is the K-th largest of the threads' maxima, found by bisection on the bits with block-wide
-// counts; with K well below the number of threads few more than K logits reach it, so that a row of 151936 leaves some
-// hundred candidates, which are sorted once.  Candidates are ordered by (value, index) as one 64-bit key: equal logits
-// stand by rising index.  Rows are split over the blocks of a cluster when there are too few to fill the GPU; the
-// cluster's first block joins the others' sums and candidates out of their shared memory.
+// end.  The alternatives: while it streams, a thread only notes the largest of each 16 logits (16 bits of its order, in
+// shared memory).  At the row's end each warp takes its q-th largest lane, a lane counting by its r-th largest note, with
+// 16 q r >= K: at least K logits reach the least of the 16 warps' values, and not many more than that do, so that few of
+// the groups have to be read again (they are still in L2).  Their logits that reach the bound are the candidates, ordered
+// by (value, index) as one 64-bit key: equal logits stand by rising index.  Taking candidates while streaming, under a
+// bound renewed at steps 0, 1, 2, 4, ..., cost more than the whole softmax (500 against 230 us for 4096 x 151936).
+// Rows are split over the blocks of a cluster when there are too few to fill the GPU; the cluster's first block joins
+// the others' sums and candidates out of their shared memory.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -25,7 +27,8 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kPer = 16;                  // logits of a thread per step
 constexpr int kStep = kThreads * kPer;    // of a block
-constexpr int kCap = 2048;                // candidates of a block
+constexpr int kCap = 4096;                // candidates of a block
+constexpr int kNotes = 32;                // steps whose largest logits are noted before candidates are taken
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float ex2(float v) {
@@ -66,12 +69,14 @@ struct Step {
   static constexpr int kVec = 16 / sizeof(ZT), kVecs = kPer / kVec;
   uint4 raw[kVecs];
 
-  __device__ __forceinline__ static int place(int step, int i) { return (step * kVecs * kThreads + i * kThreads + (int)threadIdx.x) * kVec; }
+  __device__ __forceinline__ static int place(int step, int i, int thread) {
+    return (step * kVecs * kThreads + i * kThreads + thread) * kVec;
+  }
 
   __device__ __forceinline__ void load(const ZT* base, int step, int to) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int at = place(step, i);
+      const int at = place(step, i, threadIdx.x);
       if (at + kVec <= to) {
         raw[i] = __ldg(reinterpret_cast<const uint4*>(base + at));
       } else {
@@ -108,8 +113,15 @@ struct Step {
       }
     }
   }
-  // the element's place of f[j]
-  __device__ __forceinline__ static int at_of(int step, int j) { return place(step, j / kVec) + j % kVec; }
+  // the place of a thread's f[j]
+  __device__ __forceinline__ static int at_of(int step, int j, int thread) {
+    return place(step, j / kVec, thread) + j % kVec;
+  }
+  // the logit at a place, read again
+  __device__ __forceinline__ static float one(const ZT* base, int at) {
+    if constexpr (sizeof(ZT) == 4) return __ldg(reinterpret_cast<const float*>(base) + at);
+    else return bf16lo(__ldg(reinterpret_cast<const unsigned short*>(base) + at));
+  }
 };
 
 // Sorts s_key[0, n2) in falling order, n2 a power of two.
@@ -130,31 +142,152 @@ __device__ __forceinline__ void sort_keys(uint64_t* s_key, int n2) {
   __syncthreads();
 }
 
-// Orders the candidates and keeps the K best; returns how many are left.
+// Orders the n candidates and keeps the K best; returns how many are left.  Up to kThreads of them each thread counts the
+// keys above its own (all differ); more are sorted.
 __device__ __forceinline__ int keep_best(uint64_t* s_key, int n, int K) {
-  int n2 = 32;
-  while (n2 < n) n2 *= 2;
   __syncthreads();
-  for (int i = n + threadIdx.x; i < n2; i += kThreads) s_key[i] = 0;
-  sort_keys(s_key, n2);
+  if (n <= kThreads) {
+    const int i = threadIdx.x;
+    const uint64_t mine = i < n ? s_key[i] : 0;
+    int rank = 0;
+    if ((i & ~31) < n) {
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) rank += s_key[j] > mine;
+    }
+    __syncthreads();
+    if (i < n) s_key[rank] = mine;
+    __syncthreads();
+  } else {
+    int n2 = 2 * kThreads;
+    while (n2 < n) n2 *= 2;
+    for (int i = n + threadIdx.x; i < n2; i += kThreads) s_key[i] = 0;
+    sort_keys(s_key, n2);
+  }
   return min(n, K);
 }
 
-// The largest t (in its upper bits) that at least K of the block's values reach.
-__device__ __forceinline__ uint32_t reached_by(uint32_t mine, int K, int bits) {
-  uint32_t t = 0;
-  for (int b = 31; b >= 32 - bits; --b) {
-    const uint32_t trial = t | (1u << b);
-    if (__syncthreads_count(mine >= trial) >= K) t = trial;
+// The q-th largest (q = 1 .. 32) of a warp's values: a bitonic sort of the lanes, falling.
+__device__ __forceinline__ uint32_t warp_qth(uint32_t v, int q, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+    for (int half = size / 2; half; half /= 2) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, v, half);
+      v = ((lane & half) == 0) == ((lane & size) == 0) ? max(v, o) : min(v, o);
+    }
   }
-  return t;
+  return __shfl_sync(0xffffffffu, v, q - 1);
 }
+
+// The r-th largest of a thread's n notes (0 if there are fewer).
+template <int R>
+__device__ __forceinline__ uint32_t rth_note(const uint16_t* notes, int n, int r) {
+  uint32_t best[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) best[i] = 0;
+  for (int s = 0; s < n; ++s) {
+    uint32_t v = notes[s * kThreads];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const uint32_t hi = max(best[i], v);
+      v = min(best[i], v);
+      best[i] = hi;
+    }
+  }
+  uint32_t v = best[0];
+#pragma unroll
+  for (int i = 1; i < R; ++i) v = i == r - 1 ? best[i] : v;
+  return v;
+}
+
+struct TopSmem {  // dynamic shared memory
+  uint64_t key[kCap];
+  uint16_t note[kNotes][kThreads];
+  uint16_t group[kCap];  // groups to read again: step * kThreads + thread
+  uint32_t bound[kWarps];
+  int n, groups;
+};
+
+// What a block knows of its part of a row, and the candidates it takes from it.
+template <typename ZT>
+struct Top {
+  using St = Step<ZT>;
+  TopSmem& s;
+  const ZT* base;
+  int lo, from, to, K;
+  uint64_t above;  // a candidate's key is larger: K better ones are listed
+
+  __device__ __forceinline__ uint64_t key_at(int at) const {
+    const float v = St::one(base, at);
+    return v == v ? ((uint64_t)order_of(v) << 32) | (0xffffffffu - (uint32_t)(lo + at - from)) : 0;
+  }
+  // cuts the list to the K best; the caller has passed a barrier since the last candidate
+  __device__ __forceinline__ void cut(int n) {
+    n = keep_best(s.key, n, K);
+    if (n == K && s.key[n - 1] > above) above = s.key[n - 1];
+    __syncthreads();
+    if (threadIdx.x == 0) s.n = n;
+    __syncthreads();
+  }
+  // the candidates of the steps [first, first + steps) behind the `held` listed ones
+  __device__ __forceinline__ void take(int first, int steps, int held) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    // warps all of whose lanes have logits; q lanes of each of them, r notes of a lane
+    const int full = min(kWarps, max(1, to / (32 * St::kVec)));
+    const int quota = (K + full - 1) / full, r = (quota + 7) / 8, q = (quota + r - 1) / r;
+    const uint16_t* mine = &s.note[0][tid];
+    uint32_t w = 0;
+    if (r <= 8) w = warp_qth(r == 1 ? rth_note<1>(mine, steps, 1) : rth_note<8>(mine, steps, r), q, lane);
+    if (lane == 0) s.bound[warp] = w;
+    if (tid == 0) s.groups = 0;
+    __syncthreads();
+    w = __reduce_min_sync(0xffffffffu, s.bound[min(lane, full - 1)]);
+    const uint32_t bound = max(w << 16, (uint32_t)(above >> 32));
+    for (int i = 0; i < steps; ++i) {
+      if (mine[i * kThreads] >= bound >> 16) {
+        const int slot = atomicAdd(&s.groups, 1);
+        if (slot < kCap) s.group[slot] = (uint16_t)(i * kThreads + tid);
+      }
+    }
+    __syncthreads();
+    const int groups = s.groups;
+    if (groups <= kCap) {
+      for (int i = tid; i < groups * kPer; i += kThreads) {
+        const int g = s.group[i / kPer];
+        const int at = St::at_of(first + g / kThreads, i % kPer, g % kThreads);
+        if (at < from || at >= to) continue;
+        const uint64_t key = key_at(at);
+        if (key > above && (uint32_t)(key >> 32) >= bound) {
+          const int slot = atomicAdd(&s.n, 1);
+          if (slot < kCap) s.key[slot] = key;
+        }
+      }
+      __syncthreads();
+      if (s.n <= kCap) return;
+    }
+    // very many reach the bound (equal logits, or fewer groups than K): all logits of these steps, kThreads at a time,
+    // and the list is cut whenever the next ones might not fit
+    __syncthreads();
+    if (tid == 0) s.n = held;
+    __syncthreads();
+    for (int i = 0; i < steps * kPer; ++i) {
+      const int n = s.n;
+      __syncthreads();  // read by everybody before anybody adds
+      if (n > kCap - kThreads) cut(n);
+      const int at = St::at_of(first + i / kPer, i % kPer, tid);
+      if (at >= from && at < to) {
+        const uint64_t key = key_at(at);
+        if (key > above && (uint32_t)(key >> 32) >= bound) s.key[atomicAdd(&s.n, 1)] = key;
+      }
+      __syncthreads();
+    }
+  }
+};
 
 template <typename ZT, bool TOP, bool ENT>
 __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int parts) {
   using St = Step<ZT>;
-  __shared__ uint64_t s_key[TOP ? kCap : 1];
-  __shared__ int s_n;
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float s_m[kWarps], s_s[kWarps], s_u[kWarps];
   __shared__ float s_sum[3];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
@@ -169,8 +302,9 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int p
   const int steps = (to + kStep - 1) / kStep;
   const float b2 = q.b * kLog2e;
   float m = -INFINITY, S = 0.0f, U = 0.0f;
-  uint64_t above = 0;  // a candidate's key is larger
-  if (TOP && tid == 0) s_n = 0;
+  TopSmem& ts = *reinterpret_cast<TopSmem*>(smem);
+  Top<ZT> alt = {ts, base, lo, from, to, q.K, 0};
+  if (TOP && tid == 0) ts.n = 0;
 
   St now, next;
   if (steps > 0) now.load(base, 0, to);
@@ -202,55 +336,22 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int p
     }
     S += f2unpack(s2).x + f2unpack(s2).y;
     if constexpr (ENT) U += f2unpack(u2).x + f2unpack(u2).y;
-
     if constexpr (TOP) {
-      const uint32_t mine = order_of(top);
-      int passing = __syncthreads_count(mine >= (uint32_t)(above >> 32));
-      if (passing) {
-        // a higher threshold from the maxima so far: at the first steps, and when the candidates would not fit
-        if (q.K <= kThreads && ((step & (step + 1)) == 0 || passing * kPer + s_n > kCap)) {
-          const uint32_t t = reached_by(order_of(m), q.K, sizeof(ZT) == 2 ? 16 : 22);
-          const uint64_t up = t ? ((uint64_t)t << 32) - 1 : 0;
-          if (up > above) {
-            above = up;
-            passing = __syncthreads_count(mine >= (uint32_t)(above >> 32));
-          }
-        }
-        const bool fits = passing * kPer + s_n <= kCap;
-        __syncthreads();  // everybody has read s_n
-        if (fits) {
-          if (mine >= (uint32_t)(above >> 32)) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-              const int at = St::at_of(step, j);
-              const uint64_t key = ((uint64_t)order_of(f[j]) << 32) | (0xffffffffu - (uint32_t)(lo + at - from));
-              if (key > above && f[j] == f[j] && at >= from && at < to) s_key[atomicAdd(&s_n, 1)] = key;
-            }
-          }
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < kPer; ++j) {
-            const int held = s_n;
-            __syncthreads();  // read by everybody before anybody adds
-            if (held > kCap - kThreads) {
-              const int n = keep_best(s_key, held, q.K);
-              if (n == q.K && s_key[n - 1] > above) above = s_key[n - 1];
-              __syncthreads();
-              if (tid == 0) s_n = n;
-              __syncthreads();
-            }
-            float v = f[0];
-#pragma unroll
-            for (int i = 1; i < kPer; ++i) v = i == j ? f[i] : v;
-            const int at = St::at_of(step, j);
-            const uint64_t key = ((uint64_t)order_of(v) << 32) | (0xffffffffu - (uint32_t)(lo + at - from));
-            if (key > above && v == v && at >= from && at < to) s_key[atomicAdd(&s_n, 1)] = key;
-            __syncthreads();
-          }
-        }
+      ts.note[step % kNotes][tid] = (uint16_t)(order_of(top) >> 16);
+      if (step % kNotes == kNotes - 1 && step + 1 < steps) {
+        __syncthreads();
+        if (step >= kNotes) alt.cut(ts.n);
+        alt.take(step - (kNotes - 1), kNotes, ts.n);
       }
     }
     now = next;
+  }
+  int n = 0;
+  if constexpr (TOP) {
+    __syncthreads();
+    if (steps > kNotes) alt.cut(ts.n);
+    if (steps > 0) alt.take((steps - 1) / kNotes * kNotes, (steps - 1) % kNotes + 1, ts.n);
+    n = keep_best(ts.key, ts.n, q.K);
   }
 
   // the block's sums
@@ -268,13 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int p
       s_u[warp] = U;
     }
   }
-  int n = 0;
-  if constexpr (TOP) {
-    __syncthreads();
-    n = keep_best(s_key, s_n, q.K);
-  } else {
-    __syncthreads();
-  }
+  __syncthreads();
   if (tid == 0) {
     float M = s_m[0];
     for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
@@ -287,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int p
     s_sum[0] = M;
     s_sum[1] = s;
     s_sum[2] = u;
-    s_n = n;
+    if constexpr (TOP) ts.n = n;
   }
   if (parts > 1) {
     cg::cluster_group cluster = cg::this_cluster();
@@ -309,12 +404,12 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int p
       }
       if constexpr (TOP) {
         for (int r = 1; r < parts; ++r) {
-          const int more = *cluster.map_shared_rank(&s_n, r);
-          const uint64_t* keys = cluster.map_shared_rank(s_key, r);
-          for (int i = tid; i < more; i += kThreads) s_key[n + i] = keys[i];
+          const int more = *cluster.map_shared_rank(&ts.n, r);
+          const uint64_t* keys = cluster.map_shared_rank(ts.key, r);
+          for (int i = tid; i < more; i += kThreads) ts.key[n + i] = keys[i];
           n += more;
         }
-        n = keep_best(s_key, n, q.K);
+        n = keep_best(ts.key, n, q.K);
       }
     }
     cluster.sync();  // the others' shared memory has been read
@@ -351,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int p
   }
   if constexpr (TOP) {
     for (int i = tid; i < q.K; i += kThreads) {
-      const uint64_t key = i < n ? s_key[i] : 0;
+      const uint64_t key = i < n ? ts.key[i] : 0;
       if (q.top_idx) q.top_idx[row * q.K + i] = i < n ? (int32_t)(0xffffffffu - (uint32_t)key) : -1;
       if (q.top_logit) q.top_logit[row * q.K + i] = i < n ? value_of((uint32_t)(key >> 32)) : -INFINITY;
     }
@@ -369,6 +464,12 @@ cudaError_t launch(const Logprobs& q, int64_t N, cudaStream_t st) {
   cfg.gridDim = dim3((unsigned)(N * parts), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = st;
+  if (TOP) {
+    cfg.dynamicSmemBytes = sizeof(TopSmem);
+    if (cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<ZT, TOP, ENT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)sizeof(TopSmem)))
+      return e;
+  }
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeClusterDimension;
   a[0].val.clusterDim.x = (unsigned)parts;
