@@ -1,7 +1,7 @@
 // Log probabilities of given tokens, entropy and top alternatives of logits in one reading of them, and the gradient
 // with respect to the logits.
 //
-//   y_v = (z_v - m) b log2(e),  S = sum 2^y,  U = sum 2^y y      m: the running maximum, per thread
+//   y_v = b log2(e) (z_v - m),  S = sum 2^y,  U = sum 2^y y      m: the running maximum, per thread
 //   lse = b m + ln S,   H = ln S - ln2 U / S,   logp = b (z_t - m) - ln S
 //   dz = b (g (1[v = t] - p) - h p (log p + H)),   p = exp(b z - lse)
 //
@@ -24,11 +24,12 @@ namespace cg = cooperative_groups;
 namespace qad {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kPer = 16;                  // logits of a thread per step
 constexpr int kStep = kThreads * kPer;    // of a block
-constexpr int kCap = 4096;                // candidates of a block
-constexpr int kNotes = 32;                // steps whose largest logits are noted before candidates are taken
+constexpr int kNotes = 40;                // steps whose largest logits are noted before candidates are taken
+// candidates of a block: about twice K logits reach the bound
+constexpr int kCapSmall = 1024, kCapLarge = 4096, kSmallK = 256;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float ex2(float v) {
@@ -52,13 +53,20 @@ __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o ^ 0x80000000u) : ~o);
 }
 
+// v, rounded down to the logits' type
+template <typename ZT>
+__device__ __forceinline__ float floor_of(float v) {
+  if constexpr (sizeof(ZT) == 4) return v;
+  else return __bfloat162float(__float2bfloat16_rd(v));
+}
+
 struct Logprobs {
   const void* z;
   const int32_t* token;
   float *logp, *lse, *entropy, *top_logit;
   int32_t *top_idx, *err;
   int64_t ldz;
-  int V, K;
+  int V, K, cap;
   float b;
 };
 
@@ -73,12 +81,19 @@ struct Step {
     return (step * kVecs * kThreads + i * kThreads + thread) * kVec;
   }
 
-  __device__ __forceinline__ void load(const ZT* base, int step, int to) {
+  // a step all of which lies before `to`
+  __device__ __forceinline__ void load(const uint4* at) {
 #pragma unroll
+    for (int i = 0; i < kVecs; ++i) raw[i] = __ldg(at + i * kThreads);
+  }
+  // the last one: what lies behind `to` is not read and counts as -inf
+  __device__ __forceinline__ void load_last(const ZT* base, int step, int to) {
+#pragma unroll 1
     for (int i = 0; i < kVecs; ++i) {
       const int at = place(step, i, threadIdx.x);
+      uint4 v;
       if (at + kVec <= to) {
-        raw[i] = __ldg(reinterpret_cast<const uint4*>(base + at));
+        v = __ldg(reinterpret_cast<const uint4*>(base + at));
       } else {
         uint32_t w[4];
 #pragma unroll
@@ -91,11 +106,61 @@ struct Step {
             w[j] = a | (b << 16);
           }
         }
-        raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        v = make_uint4(w[0], w[1], w[2], w[3]);
       }
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+        if (j == i) raw[j] = v;
     }
   }
-  __device__ __forceinline__ void unpack(float* f, int step, int from) const {
+  // what lies before `from` (in the first vector of the first thread) becomes -inf
+  __device__ __forceinline__ void cut_front(int from) {
+    if (threadIdx.x == 0 && from > 0) {
+      uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (j < from) {
+          if constexpr (sizeof(ZT) == 4) w[j] = 0xff800000u;
+          else w[j / 2] = j % 2 ? (w[j / 2] & 0xffffu) | 0xff800000u : (w[j / 2] & 0xffff0000u) | 0xff80u;
+        }
+      raw[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  // the largest; a NaN does not count
+  __device__ __forceinline__ float largest() const {
+    if constexpr (sizeof(ZT) == 4) {
+      float top = __uint_as_float(raw[0].x);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        top = fmaxf(top, fmaxf(__uint_as_float(raw[i].x), __uint_as_float(raw[i].y)));
+        top = fmaxf(top, fmaxf(__uint_as_float(raw[i].z), __uint_as_float(raw[i].w)));
+      }
+      return top;
+    } else {
+      auto pair = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); };
+      __nv_bfloat162 top = pair(raw[0].x);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        top = __hmax2(top, __hmax2(pair(raw[i].x), pair(raw[i].y)));
+        top = __hmax2(top, __hmax2(pair(raw[i].z), pair(raw[i].w)));
+      }
+      return fmaxf(__low2float(top), __high2float(top));
+    }
+  }
+  // max(z, least) of all; a NaN stays
+  __device__ __forceinline__ void raise(float least) {
+    auto up = [&](uint32_t v) {
+      if constexpr (sizeof(ZT) == 4) {
+        return __float_as_uint(floor_nan(__uint_as_float(v), least));
+      } else {
+        const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(least));
+        return *reinterpret_cast<const uint32_t*>(&r);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) raw[i] = make_uint4(up(raw[i].x), up(raw[i].y), up(raw[i].z), up(raw[i].w));
+  }
+  __device__ __forceinline__ void unpack(float* f) const {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       if constexpr (sizeof(ZT) == 4) {
@@ -105,11 +170,6 @@ struct Step {
         f[4 * i + 3] = __uint_as_float(raw[i].w);
       } else {
         unpack8(raw[i], f + 8 * i);
-      }
-      if (step == 0 && i == 0 && threadIdx.x == 0) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-          if (j < from) f[j] = -INFINITY;
       }
     }
   }
@@ -124,11 +184,14 @@ struct Step {
   }
 };
 
-// Sorts s_key[0, n2) in falling order, n2 a power of two.
+// Sorts s_key[0, n2) in falling order, n2 a power of two.  Exchanges over up to 32 keys stay within a warp's 64.
 __device__ __forceinline__ void sort_keys(uint64_t* s_key, int n2) {
+  bool wide = true;
   for (int size = 2; size <= n2; size *= 2) {
     for (int half = size / 2; half; half /= 2) {
-      __syncthreads();
+      if (wide || half > 32) __syncthreads();
+      else __syncwarp();
+      wide = half > 32;
       for (int i = threadIdx.x; i < n2 / 2; i += kThreads) {
         const int a = 2 * half * (i / half) + i % half, b = a + half;
         const uint64_t x = s_key[a], y = s_key[b];
@@ -200,12 +263,10 @@ __device__ __forceinline__ uint32_t rth_note(const uint16_t* notes, int n, int r
   return v;
 }
 
-struct TopSmem {  // dynamic shared memory
-  uint64_t key[kCap];
+struct TopSmem {  // in front of `cap` keys (8 bytes) and groups (2 bytes) in dynamic shared memory
   uint16_t note[kNotes][kThreads];
-  uint16_t group[kCap];  // groups to read again: step * kThreads + thread
   uint32_t bound[kWarps];
-  int n, groups;
+  int n, groups, pad[2];
 };
 
 // What a block knows of its part of a row, and the candidates it takes from it.
@@ -213,8 +274,10 @@ template <typename ZT>
 struct Top {
   using St = Step<ZT>;
   TopSmem& s;
+  uint64_t* key;    // the candidates
+  uint16_t* group;  // groups of 16 to read again: step * kThreads + thread
   const ZT* base;
-  int lo, from, to, K;
+  int lo, from, to, K, cap;
   uint64_t above;  // a candidate's key is larger: K better ones are listed
 
   __device__ __forceinline__ uint64_t key_at(int at) const {
@@ -223,8 +286,8 @@ struct Top {
   }
   // cuts the list to the K best; the caller has passed a barrier since the last candidate
   __device__ __forceinline__ void cut(int n) {
-    n = keep_best(s.key, n, K);
-    if (n == K && s.key[n - 1] > above) above = s.key[n - 1];
+    n = keep_best(key, n, K);
+    if (n == K && key[n - 1] > above) above = key[n - 1];
     __syncthreads();
     if (threadIdx.x == 0) s.n = n;
     __syncthreads();
@@ -237,7 +300,9 @@ struct Top {
     const int quota = (K + full - 1) / full, r = (quota + 7) / 8, q = (quota + r - 1) / r;
     const uint16_t* mine = &s.note[0][tid];
     uint32_t w = 0;
-    if (r <= 8) w = warp_qth(r == 1 ? rth_note<1>(mine, steps, 1) : rth_note<8>(mine, steps, r), q, lane);
+    if (r == 1) w = warp_qth(rth_note<1>(mine, steps, 1), q, lane);
+    else if (r <= 4) w = warp_qth(rth_note<4>(mine, steps, r), q, lane);
+    else if (r <= 16) w = warp_qth(rth_note<16>(mine, steps, r), q, lane);
     if (lane == 0) s.bound[warp] = w;
     if (tid == 0) s.groups = 0;
     __syncthreads();
@@ -246,24 +311,24 @@ struct Top {
     for (int i = 0; i < steps; ++i) {
       if (mine[i * kThreads] >= bound >> 16) {
         const int slot = atomicAdd(&s.groups, 1);
-        if (slot < kCap) s.group[slot] = (uint16_t)(i * kThreads + tid);
+        if (slot < cap) group[slot] = (uint16_t)(i * kThreads + tid);
       }
     }
     __syncthreads();
     const int groups = s.groups;
-    if (groups <= kCap) {
+    if (groups <= cap) {
       for (int i = tid; i < groups * kPer; i += kThreads) {
-        const int g = s.group[i / kPer];
+        const int g = group[i / kPer];
         const int at = St::at_of(first + g / kThreads, i % kPer, g % kThreads);
         if (at < from || at >= to) continue;
-        const uint64_t key = key_at(at);
-        if (key > above && (uint32_t)(key >> 32) >= bound) {
+        const uint64_t k = key_at(at);
+        if (k > above && (uint32_t)(k >> 32) >= bound) {
           const int slot = atomicAdd(&s.n, 1);
-          if (slot < kCap) s.key[slot] = key;
+          if (slot < cap) key[slot] = k;
         }
       }
       __syncthreads();
-      if (s.n <= kCap) return;
+      if (s.n <= cap) return;
     }
     // very many reach the bound (equal logits, or fewer groups than K): all logits of these steps, kThreads at a time,
     // and the list is cut whenever the next ones might not fit
@@ -273,11 +338,11 @@ struct Top {
     for (int i = 0; i < steps * kPer; ++i) {
       const int n = s.n;
       __syncthreads();  // read by everybody before anybody adds
-      if (n > kCap - kThreads) cut(n);
+      if (n > cap - kThreads) cut(n);
       const int at = St::at_of(first + i / kPer, i % kPer, tid);
       if (at >= from && at < to) {
-        const uint64_t key = key_at(at);
-        if (key > above && (uint32_t)(key >> 32) >= bound) s.key[atomicAdd(&s.n, 1)] = key;
+        const uint64_t k = key_at(at);
+        if (k > above && (uint32_t)(k >> 32) >= bound) key[atomicAdd(&s.n, 1)] = k;
       }
       __syncthreads();
     }
@@ -285,7 +350,7 @@ struct Top {
 };
 
 template <typename ZT, bool TOP, bool ENT>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int parts) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int parts) {
   using St = Step<ZT>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float s_m[kWarps], s_s[kWarps], s_u[kWarps];
@@ -301,67 +366,111 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int p
   const int to = from + len;
   const int steps = (to + kStep - 1) / kStep;
   const float b2 = q.b * kLog2e;
-  float m = -INFINITY, S = 0.0f, U = 0.0f;
+  // S = sum of 2^y and U = sum of 2^y y with y = b2 z - R, R = fp32(b2 m): one instruction for two logits.  R is off b2 m
+  // by `lo` (exact), which is taken out when sums join.  A logit below `least` (y <= -200, 2^y = 0) counts as `least`, so
+  // that -inf gives 0 * y and not NaN.  `wild`: products of logits of 10^36 and more would leave fp32's range; there
+  // y = b2 (z - m), clamped.
+  float m = -INFINITY, R = 0.0f, lo2 = 0.0f, S = 0.0f, U = 0.0f;
+  const float span = 200.0f / b2;
+  float least = -span;
+  bool wild = !(span < 3e38f);
   TopSmem& ts = *reinterpret_cast<TopSmem*>(smem);
-  Top<ZT> alt = {ts, base, lo, from, to, q.K, 0};
+  uint64_t* keys = reinterpret_cast<uint64_t*>(smem + sizeof(TopSmem));
   if (TOP && tid == 0) ts.n = 0;
 
-  St now, next;
-  if (steps > 0) now.load(base, 0, to);
-  for (int step = 0; step < steps; ++step) {
-    if (step + 1 < steps) next.load(base, step + 1, to);
-    float f[kPer];
-    now.unpack(f, step, from);
-    float top = f[0];
-#pragma unroll
-    for (int i = 1; i < kPer; ++i) top = fmaxf(top, f[i]);
+  uint16_t* note = &ts.note[0][tid];
+  auto see = [&](St& now) {
+    const float top = now.largest();
     if (top > m) {
+      R = top * b2;
+      least = __fsub_rd(top, span);
+      wild = !(fabsf(fmaf(floor_of<ZT>(least), b2, -R)) < 3e38f);
+      const float off = wild ? 0.0f : fmaf(top, b2, -R);
       if (m > -INFINITY) {
-        const float d = (m - top) * b2, c = ex2(d);
+        const float d = (m - top) * b2 - lo2 + off, c = ex2(d);
         if constexpr (ENT) U = c == 0.0f ? 0.0f : c * fmaf(S, d, U);
         S *= c;
       }
       m = top;
+      lo2 = off;
     }
-    const float ref = m == -INFINITY ? 0.0f : m;
-    const uint64_t nref = f2pack(-ref, -ref), bb = f2pack(b2, b2);
     uint64_t s2 = f2pack(0.0f, 0.0f), u2 = s2;
+    const uint64_t nr = f2pack(-R, -R), bb = f2pack(b2, b2);
+    float f[kPer];
+    if (!wild) {
+      now.raise(floor_of<ZT>(least));
+      now.unpack(f);
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-      const float2 y = f2unpack(f2mul(f2add(f2pack(f[i], f[i + 1]), nref), bb));
-      const float y0 = floor_nan(y.x, -200.0f), y1 = floor_nan(y.y, -200.0f);  // 2^-200 is 0 in fp32
-      const uint64_t e2 = f2pack(ex2(y0), ex2(y1));
-      s2 = f2add(s2, e2);
-      if constexpr (ENT) u2 = f2fma(e2, f2pack(y0, y1), u2);
+      for (int i = 0; i < kPer; i += 2) {
+        const uint64_t y2 = f2fma(f2pack(f[i], f[i + 1]), bb, nr);
+        const float2 y = f2unpack(y2);
+        const uint64_t e2 = f2pack(ex2(y.x), ex2(y.y));
+        s2 = f2add(s2, e2);
+        if constexpr (ENT) u2 = f2fma(e2, y2, u2);
+      }
+    } else {
+      now.unpack(f);
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        const float ref = m == -INFINITY ? 0.0f : m;
+        const float y0 = floor_nan((f[i] - ref) * b2, -200.0f), y1 = floor_nan((f[i + 1] - ref) * b2, -200.0f);
+        const uint64_t e2 = f2pack(ex2(y0), ex2(y1));
+        s2 = f2add(s2, e2);
+        if constexpr (ENT) u2 = f2fma(e2, f2pack(y0, y1), u2);
+      }
     }
     S += f2unpack(s2).x + f2unpack(s2).y;
     if constexpr (ENT) U += f2unpack(u2).x + f2unpack(u2).y;
     if constexpr (TOP) {
-      ts.note[step % kNotes][tid] = (uint16_t)(order_of(top) >> 16);
-      if (step % kNotes == kNotes - 1 && step + 1 < steps) {
-        __syncthreads();
-        if (step >= kNotes) alt.cut(ts.n);
-        alt.take(step - (kNotes - 1), kNotes, ts.n);
+      *note = (uint16_t)(order_of(top) >> 16);
+      note += kThreads;
+    }
+  };
+  // two steps in flight behind the one that is worked on; candidates are taken every kNotes steps
+  const int whole = to / kStep;
+  const uint4* ahead = reinterpret_cast<const uint4*>(base) + tid;
+  auto fetch = [&](St& v, int step, int end) {
+    if (step >= end) return;
+    if (step < whole) v.load(ahead + (int64_t)step * (St::kVecs * kThreads));
+    else v.load_last(base, step, to);
+  };
+  uint64_t above = 0;
+  for (int first = 0; first < steps; first += kNotes) {
+    const int end = min(steps, first + kNotes);
+    St even, odd;
+    fetch(even, first, end);
+    fetch(odd, first + 1, end);
+    if (first == 0) even.cut_front(from);
+    note = &ts.note[0][tid];
+    for (int step = first; step < end; step += 2) {
+      see(even);
+      fetch(even, step + 2, end);
+      if (step + 1 < end) {
+        see(odd);
+        fetch(odd, step + 3, end);
       }
     }
-    now = next;
+    if constexpr (TOP) {
+      Top<ZT> alt = {ts, keys, reinterpret_cast<uint16_t*>(keys + q.cap), base, lo, from, to, q.K, q.cap, above};
+      __syncthreads();
+      if (first > 0) alt.cut(ts.n);
+      alt.take(first, end - first, ts.n);
+      above = alt.above;
+    }
   }
   int n = 0;
   if constexpr (TOP) {
     __syncthreads();
-    if (steps > kNotes) alt.cut(ts.n);
-    if (steps > 0) alt.take((steps - 1) / kNotes * kNotes, (steps - 1) % kNotes + 1, ts.n);
-    n = keep_best(ts.key, ts.n, q.K);
+    n = keep_best(keys, ts.n, q.K);
   }
 
   // the block's sums
   {
     const float wm = warp_max(m);
-    const float c = m == -INFINITY ? 0.0f : ex2((m - wm) * b2);
-    if constexpr (ENT) U = c == 0.0f ? 0.0f : c * fmaf(S, (m - wm) * b2, U);
-    // a NaN stays one: where nothing but NaN and -inf was seen m is -inf, and S says which
-    S = m == -INFINITY ? S : S * c;
-    S = warp_sum(S);
+    const float d = m == -INFINITY ? 0.0f : (m - wm) * b2 - lo2, c = ex2(d);
+    // a thread that saw nothing but -inf and NaN has m = -inf, and S = 0 or NaN
+    if constexpr (ENT) U = c == 0.0f || m == -INFINITY ? 0.0f : c * fmaf(S, d, U);
+    S = warp_sum(S * c);
     if constexpr (ENT) U = warp_sum(U);
     if (lane == 0) {
       s_m[warp] = wm;
@@ -405,11 +514,11 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int p
       if constexpr (TOP) {
         for (int r = 1; r < parts; ++r) {
           const int more = *cluster.map_shared_rank(&ts.n, r);
-          const uint64_t* keys = cluster.map_shared_rank(ts.key, r);
-          for (int i = tid; i < more; i += kThreads) ts.key[n + i] = keys[i];
+          const uint64_t* theirs = cluster.map_shared_rank(keys, r);
+          for (int i = tid; i < more; i += kThreads) keys[n + i] = theirs[i];
           n += more;
         }
-        n = keep_best(ts.key, n, q.K);
+        n = keep_best(keys, n, q.K);
       }
     }
     cluster.sync();  // the others' shared memory has been read
@@ -424,9 +533,9 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int p
   if (tid == 0) {
     const float M = s_sum[0], s = s_sum[1];
     const bool empty = M == -INFINITY && s == 0.0f;
-    const float ls = logf(s);
+    const float l2 = log2f(s), ls = kLn2 * l2;
     if (q.lse) q.lse[row] = empty ? -INFINITY : M == -INFINITY ? s + NAN : fmaf(M, q.b, ls);
-    if (ENT) q.entropy[row] = empty ? 0.0f : M == -INFINITY ? NAN : fmaxf(ls - kLn2 * s_sum[2] / s, 0.0f) + 0.0f * s;
+    if (ENT) q.entropy[row] = empty ? 0.0f : M == -INFINITY ? NAN : fmaxf(kLn2 * (l2 - s_sum[2] / s), 0.0f) + 0.0f * s;
     if (q.logp) {
       const int t = q.token[row];
       float lp = 0.0f;
@@ -446,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(Logprobs q, int p
   }
   if constexpr (TOP) {
     for (int i = tid; i < q.K; i += kThreads) {
-      const uint64_t key = i < n ? ts.key[i] : 0;
+      const uint64_t key = i < n ? keys[i] : 0;
       if (q.top_idx) q.top_idx[row * q.K + i] = i < n ? (int32_t)(0xffffffffu - (uint32_t)key) : -1;
       if (q.top_logit) q.top_logit[row * q.K + i] = i < n ? value_of((uint32_t)(key >> 32)) : -INFINITY;
     }
@@ -457,17 +566,17 @@ template <typename ZT, bool TOP, bool ENT>
 cudaError_t launch(const Logprobs& q, int64_t N, cudaStream_t st) {
   // as many blocks for a row as fill the GPU twice, while each has a whole step and their candidates fit one block's list
   int parts = 1;
-  while (parts < 8 && 2 * parts * N <= 2 * (int64_t)num_sms() && q.V / (2 * parts) >= kStep / 4 &&
-         (!TOP || 2 * parts * q.K <= kCap))
+  while (parts < 8 && 2 * parts * N <= 2 * (int64_t)num_sms() && q.V / (2 * parts) >= kStep / 2 &&
+         (!TOP || 2 * parts * q.K <= q.cap))
     parts *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(N * parts), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = st;
   if (TOP) {
-    cfg.dynamicSmemBytes = sizeof(TopSmem);
+    cfg.dynamicSmemBytes = sizeof(TopSmem) + 10 * (size_t)q.cap;
     if (cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<ZT, TOP, ENT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)sizeof(TopSmem)))
+                                             (int)(sizeof(TopSmem) + 10 * kCapLarge)))
       return e;
   }
   cudaLaunchAttribute a[1];
@@ -598,6 +707,7 @@ cudaError_t launch_logprobs(const void* z, int dtype, int64_t ldz, const int32_t
   q.ldz = ldz;
   q.V = (int)V;
   q.K = (int)K;
+  q.cap = K <= kSmallK ? kCapSmall : kCapLarge;
   q.b = inv_temp;
   prof_begin(QAD_K_LOGPROBS, st);
   const cudaError_t e =
