@@ -177,7 +177,23 @@ struct Step {
   __device__ __forceinline__ static int at_of(int step, int j, int thread) {
     return place(step, j / kVec, thread) + j % kVec;
   }
-  // the logit at a place, read again
+  // the logits at a place, read again: one, or a vector (what lies behind `to` is not read)
+  __device__ __forceinline__ static void vector(const ZT* base, int at, int to, float* f) {
+    if (at + kVec <= to) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(base + at));
+      if constexpr (sizeof(ZT) == 4) {
+        f[0] = __uint_as_float(u.x);
+        f[1] = __uint_as_float(u.y);
+        f[2] = __uint_as_float(u.z);
+        f[3] = __uint_as_float(u.w);
+      } else {
+        unpack8(u, f);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) f[j] = at + j < to ? one(base, at + j) : -INFINITY;
+    }
+  }
   __device__ __forceinline__ static float one(const ZT* base, int at) {
     if constexpr (sizeof(ZT) == 4) return __ldg(reinterpret_cast<const float*>(base) + at);
     else return bf16lo(__ldg(reinterpret_cast<const unsigned short*>(base) + at));
@@ -248,6 +264,7 @@ __device__ __forceinline__ uint32_t rth_note(const uint16_t* notes, int n, int r
   uint32_t best[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) best[i] = 0;
+#pragma unroll 8
   for (int s = 0; s < n; ++s) {
     uint32_t v = notes[s * kThreads];
 #pragma unroll
@@ -280,8 +297,7 @@ struct Top {
   int lo, from, to, K, cap;
   uint64_t above;  // a candidate's key is larger: K better ones are listed
 
-  __device__ __forceinline__ uint64_t key_at(int at) const {
-    const float v = St::one(base, at);
+  __device__ __forceinline__ uint64_t key_of(float v, int at) const {
     return v == v ? ((uint64_t)order_of(v) << 32) | (0xffffffffu - (uint32_t)(lo + at - from)) : 0;
   }
   // cuts the list to the K best; the caller has passed a barrier since the last candidate
@@ -308,6 +324,7 @@ struct Top {
     __syncthreads();
     w = __reduce_min_sync(0xffffffffu, s.bound[min(lane, full - 1)]);
     const uint32_t bound = max(w << 16, (uint32_t)(above >> 32));
+#pragma unroll 8
     for (int i = 0; i < steps; ++i) {
       if (mine[i * kThreads] >= bound >> 16) {
         const int slot = atomicAdd(&s.groups, 1);
@@ -317,14 +334,20 @@ struct Top {
     __syncthreads();
     const int groups = s.groups;
     if (groups <= cap) {
-      for (int i = tid; i < groups * kPer; i += kThreads) {
-        const int g = group[i / kPer];
-        const int at = St::at_of(first + g / kThreads, i % kPer, g % kThreads);
-        if (at < from || at >= to) continue;
-        const uint64_t k = key_at(at);
-        if (k > above && (uint32_t)(k >> 32) >= bound) {
-          const int slot = atomicAdd(&s.n, 1);
-          if (slot < cap) key[slot] = k;
+      const float bound_f = bound <= 0x007fffffu ? -INFINITY : value_of(bound);
+      for (int i = tid; i < groups * St::kVecs; i += kThreads) {
+        const int g = group[i / St::kVecs];
+        const int at = St::place(first + g / kThreads, i % St::kVecs, g % kThreads);
+        float f[St::kVec];
+        St::vector(base, at, to, f);
+#pragma unroll
+        for (int j = 0; j < St::kVec; ++j) {
+          if (!(f[j] >= bound_f) || at + j < from || at + j >= to) continue;
+          const uint64_t k = key_of(f[j], at + j);
+          if (k > above && (uint32_t)(k >> 32) >= bound) {
+            const int slot = atomicAdd(&s.n, 1);
+            if (slot < cap) key[slot] = k;
+          }
         }
       }
       __syncthreads();
@@ -341,7 +364,7 @@ struct Top {
       if (n > cap - kThreads) cut(n);
       const int at = St::at_of(first + i / kPer, i % kPer, tid);
       if (at >= from && at < to) {
-        const uint64_t k = key_at(at);
+        const uint64_t k = key_of(St::one(base, at), at);
         if (k > above && (uint32_t)(k >> 32) >= bound) key[atomicAdd(&s.n, 1)] = k;
       }
       __syncthreads();
