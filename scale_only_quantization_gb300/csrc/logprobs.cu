@@ -25,8 +25,7 @@ namespace qad {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPer = 16;                  // logits of a thread per step
-constexpr int kStep = kThreads * kPer;    // of a block
+constexpr int kVecs = 4;                  // 16-byte vectors of a thread per step
 constexpr int kNotes = 40;                // steps whose largest logits are noted before candidates are taken
 // candidates of a block: about twice K logits reach the bound
 constexpr int kCapSmall = 1024, kCapLarge = 4096, kSmallK = 256;
@@ -74,7 +73,7 @@ struct Logprobs {
 // boundary at or before the range; what lies outside [from, to) counts as -inf and is not read past `to`.
 template <typename ZT>
 struct Step {
-  static constexpr int kVec = 16 / sizeof(ZT), kVecs = kPer / kVec;
+  static constexpr int kVec = 16 / sizeof(ZT), kPer = kVec * kVecs, kStep = kThreads * kPer;  // of a thread and a block
   uint4 raw[kVecs];
 
   __device__ __forceinline__ static int place(int step, int i, int thread) {
@@ -147,31 +146,31 @@ struct Step {
       return fmaxf(__low2float(top), __high2float(top));
     }
   }
-  // max(z, least) of all; a NaN stays
-  __device__ __forceinline__ void raise(float least) {
+  // a lower bound of the logits as raise() takes it
+  __device__ __forceinline__ static uint32_t packed(float low) {
+    if constexpr (sizeof(ZT) == 4) return __float_as_uint(low);
+    else return pack_bf16(low, low);
+  }
+  // max(z, low) of all; a NaN stays
+  __device__ __forceinline__ void raise(uint32_t low) {
     auto up = [&](uint32_t v) {
       if constexpr (sizeof(ZT) == 4) {
-        return __float_as_uint(floor_nan(__uint_as_float(v), least));
+        return __float_as_uint(floor_nan(__uint_as_float(v), __uint_as_float(low)));
       } else {
-        const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(least));
-        return *reinterpret_cast<const uint32_t*>(&r);
+        uint32_t r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(low));
+        return r;
       }
     };
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) raw[i] = make_uint4(up(raw[i].x), up(raw[i].y), up(raw[i].z), up(raw[i].w));
   }
-  __device__ __forceinline__ void unpack(float* f) const {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      if constexpr (sizeof(ZT) == 4) {
-        f[4 * i] = __uint_as_float(raw[i].x);
-        f[4 * i + 1] = __uint_as_float(raw[i].y);
-        f[4 * i + 2] = __uint_as_float(raw[i].z);
-        f[4 * i + 3] = __uint_as_float(raw[i].w);
-      } else {
-        unpack8(raw[i], f + 8 * i);
-      }
-    }
+  // logits i and i + 1 (i even)
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    const uint4& v = raw[i / kVec];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(ZT) == 4) return f2pack(__uint_as_float(w[i % 4]), __uint_as_float(w[i % 4 + 1]));
+    else return f2pack(bf16lo(w[i % 8 / 2]), bf16hi(w[i % 8 / 2]));
   }
   // the place of a thread's f[j]
   __device__ __forceinline__ static int at_of(int step, int j, int thread) {
@@ -313,12 +312,11 @@ struct Top {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     // warps all of whose lanes have logits; q lanes of each of them, r notes of a lane
     const int full = min(kWarps, max(1, to / (32 * St::kVec)));
-    const int quota = (K + full - 1) / full, r = (quota + 7) / 8, q = (quota + r - 1) / r;
+    const int quota = (K + full - 1) / full, r = (quota + 15) / 16, q = (quota + r - 1) / r;
     const uint16_t* mine = &s.note[0][tid];
     uint32_t w = 0;
     if (r == 1) w = warp_qth(rth_note<1>(mine, steps, 1), q, lane);
-    else if (r <= 4) w = warp_qth(rth_note<4>(mine, steps, r), q, lane);
-    else if (r <= 16) w = warp_qth(rth_note<16>(mine, steps, r), q, lane);
+    else if (r <= 8) w = warp_qth(rth_note<8>(mine, steps, r), q, lane);
     if (lane == 0) s.bound[warp] = w;
     if (tid == 0) s.groups = 0;
     __syncthreads();
@@ -335,9 +333,9 @@ struct Top {
     const int groups = s.groups;
     if (groups <= cap) {
       const float bound_f = bound <= 0x007fffffu ? -INFINITY : value_of(bound);
-      for (int i = tid; i < groups * St::kVecs; i += kThreads) {
-        const int g = group[i / St::kVecs];
-        const int at = St::place(first + g / kThreads, i % St::kVecs, g % kThreads);
+      for (int i = tid; i < groups * kVecs; i += kThreads) {
+        const int g = group[i / kVecs];
+        const int at = St::place(first + g / kThreads, i % kVecs, g % kThreads);
         float f[St::kVec];
         St::vector(base, at, to, f);
 #pragma unroll
@@ -358,11 +356,11 @@ struct Top {
     __syncthreads();
     if (tid == 0) s.n = held;
     __syncthreads();
-    for (int i = 0; i < steps * kPer; ++i) {
+    for (int i = 0; i < steps * St::kPer; ++i) {
       const int n = s.n;
       __syncthreads();  // read by everybody before anybody adds
       if (n > cap - kThreads) cut(n);
-      const int at = St::at_of(first + i / kPer, i % kPer, tid);
+      const int at = St::at_of(first + i / St::kPer, i % St::kPer, tid);
       if (at >= from && at < to) {
         const uint64_t k = key_of(St::one(base, at), at);
         if (k > above && (uint32_t)(k >> 32) >= bound) key[atomicAdd(&s.n, 1)] = k;
@@ -387,15 +385,17 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int p
   const int from = (int)((reinterpret_cast<uintptr_t>(zrow + lo) & 15u) / sizeof(ZT));
   const ZT* base = zrow + lo - from;
   const int to = from + len;
-  const int steps = (to + kStep - 1) / kStep;
+  const int steps = (to + St::kStep - 1) / St::kStep;
   const float b2 = q.b * kLog2e;
   // S = sum of 2^y and U = sum of 2^y y with y = b2 z - R, R = fp32(b2 m): one instruction for two logits.  R is off b2 m
-  // by `lo` (exact), which is taken out when sums join.  A logit below `least` (y <= -200, 2^y = 0) counts as `least`, so
+  // by `off` (exact), which is taken out when sums join.  A logit below `least` (y <= -200, 2^y = 0) counts as `least`, so
   // that -inf gives 0 * y and not NaN.  `wild`: products of logits of 10^36 and more would leave fp32's range; there
   // y = b2 (z - m), clamped.
-  float m = -INFINITY, R = 0.0f, lo2 = 0.0f, S = 0.0f, U = 0.0f;
+  float m = -INFINITY, off = 0.0f;
   const float span = 200.0f / b2;
-  float least = -span;
+  uint64_t s2 = f2pack(0.0f, 0.0f), u2 = s2, nr = s2;  // S and U of the even and odd logits; -R twice
+  const uint64_t bb = f2pack(b2, b2);
+  uint32_t least = St::packed(floor_of<ZT>(-span));
   bool wild = !(span < 3e38f);
   TopSmem& ts = *reinterpret_cast<TopSmem*>(smem);
   uint64_t* keys = reinterpret_cast<uint64_t*>(smem + sizeof(TopSmem));
@@ -405,56 +405,52 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int p
   auto see = [&](St& now) {
     const float top = now.largest();
     if (top > m) {
-      R = top * b2;
-      least = __fsub_rd(top, span);
-      wild = !(fabsf(fmaf(floor_of<ZT>(least), b2, -R)) < 3e38f);
-      const float off = wild ? 0.0f : fmaf(top, b2, -R);
+      const float R = top * b2, low = floor_of<ZT>(__fsub_rd(top, span));
+      wild = !(fabsf(fmaf(low, b2, -R)) < 3e38f);
+      const float off2 = wild ? 0.0f : fmaf(top, b2, -R);
       if (m > -INFINITY) {
-        const float d = (m - top) * b2 - lo2 + off, c = ex2(d);
-        if constexpr (ENT) U = c == 0.0f ? 0.0f : c * fmaf(S, d, U);
-        S *= c;
+        const float d = (m - top) * b2 - off + off2, c = ex2(d);
+        const uint64_t cc = f2pack(c, c);
+        if constexpr (ENT) u2 = c == 0.0f ? 0 : f2mul(cc, f2fma(s2, f2pack(d, d), u2));
+        s2 = f2mul(s2, cc);
       }
       m = top;
-      lo2 = off;
+      off = off2;
+      nr = f2pack(-R, -R);
+      least = St::packed(low);
     }
-    uint64_t s2 = f2pack(0.0f, 0.0f), u2 = s2;
-    const uint64_t nr = f2pack(-R, -R), bb = f2pack(b2, b2);
-    float f[kPer];
     if (!wild) {
-      now.raise(floor_of<ZT>(least));
-      now.unpack(f);
+      now.raise(least);
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        const uint64_t y2 = f2fma(f2pack(f[i], f[i + 1]), bb, nr);
+      for (int i = 0; i < St::kPer; i += 2) {
+        const uint64_t y2 = f2fma(now.pair(i), bb, nr);
         const float2 y = f2unpack(y2);
         const uint64_t e2 = f2pack(ex2(y.x), ex2(y.y));
         s2 = f2add(s2, e2);
         if constexpr (ENT) u2 = f2fma(e2, y2, u2);
       }
     } else {
-      now.unpack(f);
+      const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        const float ref = m == -INFINITY ? 0.0f : m;
-        const float y0 = floor_nan((f[i] - ref) * b2, -200.0f), y1 = floor_nan((f[i + 1] - ref) * b2, -200.0f);
+      for (int i = 0; i < St::kPer; i += 2) {
+        const float2 f = f2unpack(now.pair(i));
+        const float y0 = floor_nan((f.x - ref) * b2, -200.0f), y1 = floor_nan((f.y - ref) * b2, -200.0f);
         const uint64_t e2 = f2pack(ex2(y0), ex2(y1));
         s2 = f2add(s2, e2);
         if constexpr (ENT) u2 = f2fma(e2, f2pack(y0, y1), u2);
       }
     }
-    S += f2unpack(s2).x + f2unpack(s2).y;
-    if constexpr (ENT) U += f2unpack(u2).x + f2unpack(u2).y;
     if constexpr (TOP) {
       *note = (uint16_t)(order_of(top) >> 16);
       note += kThreads;
     }
   };
-  // two steps in flight behind the one that is worked on; candidates are taken every kNotes steps
-  const int whole = to / kStep;
+  // candidates are taken every kNotes steps
+  const int whole = to / St::kStep;
   const uint4* ahead = reinterpret_cast<const uint4*>(base) + tid;
   auto fetch = [&](St& v, int step, int end) {
     if (step >= end) return;
-    if (step < whole) v.load(ahead + (int64_t)step * (St::kVecs * kThreads));
+    if (step < whole) v.load(ahead + (int64_t)step * (kVecs * kThreads));
     else v.load_last(base, step, to);
   };
   uint64_t above = 0;
@@ -489,8 +485,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int p
 
   // the block's sums
   {
+    float S = f2unpack(s2).x + f2unpack(s2).y, U = f2unpack(u2).x + f2unpack(u2).y;
     const float wm = warp_max(m);
-    const float d = m == -INFINITY ? 0.0f : (m - wm) * b2 - lo2, c = ex2(d);
+    const float d = m == -INFINITY ? 0.0f : (m - wm) * b2 - off, c = ex2(d);
     // a thread that saw nothing but -inf and NaN has m = -inf, and S = 0 or NaN
     if constexpr (ENT) U = c == 0.0f || m == -INFINITY ? 0.0f : c * fmaf(S, d, U);
     S = warp_sum(S * c);
@@ -589,7 +586,7 @@ template <typename ZT, bool TOP, bool ENT>
 cudaError_t launch(const Logprobs& q, int64_t N, cudaStream_t st) {
   // as many blocks for a row as fill the GPU twice, while each has a whole step and their candidates fit one block's list
   int parts = 1;
-  while (parts < 8 && 2 * parts * N <= 2 * (int64_t)num_sms() && q.V / (2 * parts) >= kStep / 2 &&
+  while (parts < 8 && 2 * parts * N <= 2 * (int64_t)num_sms() && q.V / (2 * parts) >= Step<ZT>::kStep / 4 &&
          (!TOP || 2 * parts * q.K <= q.cap))
     parts *= 2;
   cudaLaunchConfig_t cfg = {};
