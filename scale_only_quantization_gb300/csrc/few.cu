@@ -5,13 +5,14 @@
 //   fc2:  Y = AQ(H) . W2_hat^T, out[t] = bf16(sum_j p[t, j] * Y_j)
 //
 // With so few rows the weights are all there is to move (2 bytes an element and its part of a scale), and each element
-// costs about seven instructions of fake-quantization whatever the number of tokens.  So the weights go straight from
-// global memory to registers in the tensor cores' fragment layout: a lane loads 16 consecutive weights of a row (one
-// 32-byte load, one quantization block), quantizes them, and four m16n8k16 products take them as they lie.  The order of
-// k inside a product does not matter as long as both operands agree, so the tokens' rows (shared memory, up to 8
-// columns) are read in the same order.  tcgen05 would want the quantized weights in shared memory first: a write and a
-// read of every element for products that are idle most of the time here.
+// costs about eight instructions of fake-quantization whatever the number of tokens.  So a lane copies 16 consecutive
+// weights of a row (one quantization block) ahead into its own corner of shared memory, quantizes them in registers in
+// the tensor cores' fragment layout, and four m16n8k16 products take them as they lie.  The order of k inside a product
+// does not matter as long as both operands agree, so the tokens' rows (shared memory, up to 8 columns) are read in the
+// same order.  No lane reads what another one copied: the ring needs no barrier.  tcgen05 would want the quantized weights
+// in shared memory: a write and a read of every element for products that are idle most of the time here.
 #include "common.cuh"
+#include "dependents.cuh"
 #include "internal.h"
 
 namespace qad {
@@ -19,8 +20,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCols = 8;    // tokens of one expert that a pass over its weights serves
-constexpr int kDepth = 4;   // chunks of a warp in flight
+constexpr int kDepth = 3;   // chunks of a warp in shared memory or on their way
 constexpr int kChunk = 64;  // elements along K of one step: 16 for each lane of a quad
+constexpr int kSlot = 4 * 512 + 2 * 128;  // bytes of a warp's chunk: 16 rows of weights, a scale for each lane and row
 
 struct FewParams {
   const __nv_bfloat16* act;  // fc1: x [T, K]; fc2: H [T * k, K]
@@ -33,8 +35,7 @@ struct FewParams {
   int32_t* err;
   uint32_t* arrivals;  // [d / 16]: experts' passes that have written a tile of Y
   int T, k, E, K, N, scales;  // scales: per row
-  int aq, team, d_tiles;      // team: warps that share a tile
-  bool wide;                  // weights on a 32-byte boundary
+  int team, cols, d_tiles;    // team: warps that share a tile; cols: token rows staged at once
 };
 
 __host__ __device__ constexpr int few_stride(int K) { return (K + kChunk - 1) / kChunk * kChunk * 2 + 16; }
@@ -44,6 +45,11 @@ struct Route {
   uint32_t* live;    // [T]: the slots of a token that count
   uint16_t* first;   // [E + 1]: the expert's first pass (8 tokens each)
 };
+
+// Dynamic shared memory: the warps' rings, the staged token rows, the masks and first passes of E experts.
+__host__ __device__ constexpr int few_rows_at() { return kWarps * kDepth * kSlot; }
+__host__ __device__ constexpr int few_mask_at(int K, int cols) { return few_rows_at() + cols * few_stride(K); }
+__host__ __device__ constexpr int few_smem(int K, int cols, int E) { return few_mask_at(K, cols) + 8 * E + 2 * (E + 1) + 6; }
 
 // The pairs by expert, in every block for itself: at most 2048 of them.  Returns the passes in all.
 __device__ __forceinline__ int route(const FewParams& q, const Route& r, int* err) {
@@ -99,24 +105,85 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void load16(const __nv_bfloat16* at, bool wide, uint32_t (&w)[8]) {
-  uint4 lo, hi;
-  if (wide) {
-    ld_nc_256(at, lo, hi);
-  } else {
-    lo = __ldg(reinterpret_cast<const uint4*>(at));
-    hi = __ldg(reinterpret_cast<const uint4*>(at) + 1);
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+struct Block16 {
+  uint32_t v[8];
+};
+// fakequant16_packed's way out, kept out of the loop's instructions
+template <int WK>
+__device__ __noinline__ Block16 quantize_any(Block16 w, float s) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = bf16lo(w.v[i]);
+    v[2 * i + 1] = bf16hi(w.v[i]);
   }
-  w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
-  w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
+  fakequant_inplace<WK, 16>(v, s);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w.v[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  return w;
+}
+
+// W_hat of 16 weights that share scale s: the arithmetic of fakequant16_packed (see there), the same bits.
+template <int WK>
+__device__ __forceinline__ Block16 quantize16(const Block16& w, float s) {
+  if constexpr (WK == kQNone) {
+    return w;
+  } else {
+  Block16 out;
+  const float r = __frcp_rn(s);
+  const uint64_t r2 = f2pack(r, r), ns2 = f2pack(-s, -s), zero2 = f2pack(0.0f, 0.0f);
+  const float sc = (WK == kQE2M1 || WK == kQE4M3) ? s * 0x1p112f : s;
+  const uint64_t sc2 = f2pack(sc, sc);
+  uint64_t probe = zero2;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t w2 = f2pack(bf16lo(w.v[i]), bf16hi(w.v[i]));
+    const uint64_t q2 = f2mul(w2, r2);
+    const uint64_t x2 = f2fma(f2fma(q2, ns2, w2), r2, q2);
+    probe = f2fma(x2, zero2, probe);
+    const float2 x = f2unpack(x2);
+    uint64_t m2;
+    if constexpr (WK == kQE2M1 || WK == kQE4M3) {
+      uint32_t h2;
+      if constexpr (WK == kQE2M1) {
+        asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+            : "=r"(h2) : "f"(x.x), "f"(x.y));
+      } else {
+        uint16_t c;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(x.x), "f"(x.y));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
+      }
+      const uint32_t la = (h2 << 13) & 0x0FFFE000u, lb = (h2 >> 3) & 0x0FFFE000u;
+      m2 = f2mul(f2pack(__uint_as_float(la), __uint_as_float(lb)), sc2);
+    } else {
+      const uint64_t big2 = f2pack(12582912.0f, 12582912.0f);  // 1.5 * 2^23
+      const float ta = fminf(fmaxf(x.x, Clip<WK>::lo), Clip<WK>::hi);
+      const float tb = fminf(fmaxf(x.y, Clip<WK>::lo), Clip<WK>::hi);
+      m2 = f2mul(f2sub(f2add(f2pack(ta, tb), big2), big2), sc2);
+    }
+    const float2 m = f2unpack(m2);
+    out.v[i] = pack_bf16(m.x, m.y) | (w.v[i] & 0x80008000u);
+  }
+  const float2 p = f2unpack(probe);
+  if (!(s >= 0x1p-60f && s < 0x1p16f) || !(p.x == 0.0f && p.y == 0.0f)) out = quantize_any<WK>(w, s);
+  return out;
+  }
 }
 
 // One activation row through its quantizer into shared memory, by one warp; zeros behind K.
-__device__ __forceinline__ void stage_row(const __nv_bfloat16* row, uint4* dst, int K, int aq, int lane) {
+template <int AK>
+__device__ __forceinline__ void stage_row(const __nv_bfloat16* row, uint4* dst, int K, int lane) {
   const uint4* src = reinterpret_cast<const uint4*>(row);
   const int nblk = K / 16, padded = (K + kChunk - 1) / kChunk * (kChunk / 16);
   float s_row = 0.0f;
-  if (act_needs_row(aq)) {
+  if constexpr (act_needs_row(AK)) {
     float amax = 0.0f;
     for (int b = lane; b < nblk; b += 32) {
       float f[16];
@@ -126,8 +193,8 @@ __device__ __forceinline__ void stage_row(const __nv_bfloat16* row, uint4* dst, 
       for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
     }
     amax = warp_max(amax);
-    s_row = aq == kQE4M3   ? __fdiv_rn(amax, 448.0f)
-            : aq == kQInt8 ? __fdiv_rn(amax, 127.0f)
+    s_row = AK == kQE4M3   ? __fdiv_rn(amax, 448.0f)
+            : AK == kQInt8 ? __fdiv_rn(amax, 127.0f)
                            : deploy_tensor_scale(__fdiv_rn(amax, 6.0f));
   }
   for (int b = lane; b < padded; b += 32) {
@@ -135,20 +202,18 @@ __device__ __forceinline__ void stage_row(const __nv_bfloat16* row, uint4* dst, 
     if (b < nblk) {
       u0 = src[2 * b];
       u1 = src[2 * b + 1];
-      if (aq != kQNone) {
+      if constexpr (AK != kQNone) {
         float f[16];
         unpack8(u0, f);
         unpack8(u1, f + 8);
-        if (aq == kQE4M3) {
-          fakequant_act_inplace<kQE4M3, 16>(f, s_row);
-        } else if (aq == kQInt8) {
-          fakequant_act_inplace<kQInt8, 16>(f, s_row);
+        if constexpr (row_scaled(AK)) {
+          fakequant_act_inplace<AK, 16>(f, s_row);
         } else {
           float amax = 0.0f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
           float sc = __fdiv_rn(amax, 6.0f);
-          if (aq == kQE2M1G) sc = deployed_scale(sc, s_row);
+          if constexpr (AK == kQE2M1G) sc = deployed_scale(sc, s_row);
           fakequant_act_inplace<kQE2M1, 16>(f, sc);
         }
         u0 = pack8(f);
@@ -161,27 +226,29 @@ __device__ __forceinline__ void stage_row(const __nv_bfloat16* row, uint4* dst, 
 }
 
 // Tiles of 16 weight rows: fc1 8 gate rows and the 8 up rows that go with them, fc2 16 output rows.  A block takes a
-// consecutive share of all (pass, tile) pairs, passes outermost, so that it stages few passes' tokens.
-template <int WK, bool FC1>
-__global__ void __launch_bounds__(kThreads, 2) few_kernel(FewParams q) {
+// consecutive share of all (pass, tile) pairs, passes outermost, so that it stages few passes' tokens; its teams of warps
+// take the tiles of a pass in turn, and the warps of a team the chunks of a tile along K.
+template <int WK, int AK, bool FC1>
+__global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t s_mask[1024];
   __shared__ uint32_t s_live[64];
-  __shared__ uint16_t s_first[1025];
   __shared__ float s_part[2][kWarps][16][kCols];
   __shared__ int s_row[kCols], s_src[kCols];
-  const Route r = {s_mask, s_live, s_first};
+  uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + few_mask_at(q.K, q.cols));
+  uint16_t* s_first = reinterpret_cast<uint16_t*>(s_mask + q.E);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, t4 = lane & 3;
   const int stride = few_stride(q.K), chunks = (q.K + kChunk - 1) / kChunk;
   const int team = q.team, my_team = warp / team, in_team = warp % team, teams = kWarps / team;
   const int tiles = FC1 ? q.N / 8 : q.N / 16;
+  if (FC1) let_next_kernel_start();
   int err;
-  const int passes = route(q, r, &err);
+  const int passes = route(q, {s_mask, s_live, s_first}, &err);
   if (FC1 && blockIdx.x == 0) {
     if (tid == 0) *q.err = err;
     for (int i = tid; i < q.d_tiles; i += kThreads) q.arrivals[i] = 0;
   }
   if (!FC1 && passes == 0) {  // every pair was dropped
+    wait_for_kernel_before();
     for (int i = blockIdx.x * kThreads + tid; i < q.T * q.N / 8; i += gridDim.x * kThreads)
       reinterpret_cast<uint4*>(q.out)[i] = make_uint4(0, 0, 0, 0);
     return;
@@ -189,46 +256,67 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(FewParams q) {
   const int64_t total = (int64_t)passes * tiles;
   const int lo = (int)(total * blockIdx.x / gridDim.x), hi = (int)(total * (blockIdx.x + 1) / gridDim.x);
   const int per_warp = (chunks + team - 1) / team;
-  for (int u = lo; u < hi;) {
-    const int pass = u / tiles, tile0 = u % tiles, ntiles = min(hi - u, tiles - tile0);
-    u += ntiles;
-    int e = 0;  // the last expert whose first pass is not behind this one
+  auto expert_of = [&](int pass) {  // the last expert whose first pass is not behind this one
+    int e = 0;
     for (int b = 512; b; b >>= 1)
       if (e + b < q.E && s_first[e + b] <= pass) e += b;
-    const int mine = my_team < ntiles ? (ntiles - my_team + teams - 1) / teams : 0;
-    const int steps = mine * per_warp;
-    const __nv_bfloat16* we = q.w + (int64_t)e * (FC1 ? 2 * q.N : q.N) * q.K;
-    const float* se = q.s + (int64_t)e * (FC1 ? 2 * q.N : q.N) * q.scales;
+    return e;
+  };
 
-    uint32_t wa[kDepth][8], wb[kDepth][8];
-    float sa[kDepth], sb[kDepth];
-    int ld_tile = tile0 + my_team, ld_c = 0;  // the next step to load
-    auto load = [&](int slot) {
-      const int k0 = (ld_c * team + in_team) * kChunk + 16 * t4;
-      const int ra = FC1 ? ld_tile * 8 + g : ld_tile * 16 + g, rb = FC1 ? q.N + ra : ra + 8;
-      if (k0 < q.K) {
-        load16(we + (int64_t)ra * q.K + k0, q.wide, wa[slot]);
-        load16(we + (int64_t)rb * q.K + k0, q.wide, wb[slot]);
+  // the chunks of this warp's tiles, in order, on their way into its ring
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + warp * kDepth * kSlot);
+  int ld_u = lo + my_team, ld_end = lo, ld_c = 0, ld_slot = 0;
+  const __nv_bfloat16* ld_w = nullptr;
+  const float* ld_s = nullptr;
+  auto next_tile = [&]() {  // ld_u is the team's next tile of the pass that ends at ld_end, or past it: then of a later one
+    while (ld_u >= ld_end && ld_end < hi) {
+      const int pass = ld_end / tiles, e = expert_of(pass);
+      ld_u = ld_end + my_team;
+      ld_end = min(hi, (pass + 1) * tiles);
+      ld_w = q.w + (int64_t)e * (FC1 ? 2 * q.N : q.N) * q.K;
+      ld_s = q.s + (int64_t)e * (FC1 ? 2 * q.N : q.N) * q.scales;
+    }
+  };
+  next_tile();
+  auto load = [&]() {
+    if (ld_u < ld_end) {
+      const int chunk = ld_c * team + in_team;
+      if (chunk < chunks) {
+        const int tile = ld_u % tiles, k0 = chunk * kChunk + 16 * t4;
+        const int ra = FC1 ? tile * 8 + g : tile * 16 + g, rb = FC1 ? q.N + ra : ra + 8;
+        const int bytes = k0 < q.K ? 16 : 0, kk = k0 < q.K ? k0 : 0;  // zeros behind K
+        const __nv_bfloat16 *pa = ld_w + (int64_t)ra * q.K + kk, *pb = ld_w + (int64_t)rb * q.K + kk;
+        const uint32_t at = ring + ld_slot * kSlot + lane * 16;
+        copy16(at, pa, bytes);
+        copy16(at + 512, pa + 8, bytes);
+        copy16(at + 1024, pb, bytes);
+        copy16(at + 1536, pb + 8, bytes);
         if constexpr (WK != kQNone) {
-          const int at = WK == kQE2M1 ? k0 / 16 : WK == kQInt4 ? k0 / 128 : 0;
-          sa[slot] = __ldg(se + (int64_t)ra * q.scales + at);
-          sb[slot] = __ldg(se + (int64_t)rb * q.scales + at);
+          const int sk = WK == kQE2M1 ? kk / 16 : WK == kQInt4 ? kk / 128 : 0;
+          const uint32_t sat = ring + ld_slot * kSlot + 2048 + lane * 4;
+          copy4(sat, ld_s + (int64_t)ra * q.scales + sk);
+          copy4(sat + 128, ld_s + (int64_t)rb * q.scales + sk);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) wa[slot][i] = wb[slot][i] = 0;
-        sa[slot] = sb[slot] = 0.0f;
       }
       if (++ld_c == per_warp) {
         ld_c = 0;
-        ld_tile += teams;
+        ld_u += teams;
+        next_tile();
       }
-    };
+    }
+    ld_slot = ld_slot + 1 == kDepth ? 0 : ld_slot + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i)
-      if (i < steps) load(i);
+  for (int i = 0; i < kDepth - 1; ++i) load();
+  if (!FC1) wait_for_kernel_before();
 
-    __syncthreads();  // the tokens of the segment before are no longer read
+  int slot = 0, parity = 0;
+  const int col = min(g, q.cols - 1);  // columns that are not staged give results that nobody reads
+  for (int u = lo; u < hi;) {
+    const int pass = u / tiles, tile0 = u % tiles, ntiles = min(hi - u, tiles - tile0), e = expert_of(pass);
+    u += ntiles;
+    __syncthreads();  // the tokens of the pass before are no longer read
     if (tid < kCols) {
       uint64_t m = s_mask[e];
       for (int i = (pass - s_first[e]) * kCols + tid; i > 0 && m; --i) m &= m - 1;
@@ -244,71 +332,59 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(FewParams q) {
     }
     __syncthreads();
     if (s_src[warp] >= 0)
-      stage_row(q.act + (int64_t)s_src[warp] * q.K, reinterpret_cast<uint4*>(smem + warp * stride), q.K, q.aq, lane);
+      stage_row<AK>(q.act + (int64_t)s_src[warp] * q.K,
+                    reinterpret_cast<uint4*>(smem + few_rows_at() + warp * stride), q.K, lane);
     __syncthreads();
 
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int c = 0, tile = tile0 + my_team, parity = 0;
-    for (int base = 0; base < steps; base += kDepth) {
-#pragma unroll
-      for (int slot = 0; slot < kDepth; ++slot) {
-        if (base + slot >= steps) break;
+    for (int tile = tile0 + my_team; tile < tile0 + ntiles; tile += teams) {
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (int c = 0; c < per_warp; ++c) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
         const int chunk = c * team + in_team;
         if (chunk < chunks) {
-          const uint4* xs = reinterpret_cast<const uint4*>(smem + g * stride + (chunk * kChunk + 16 * t4) * 2);
-          const uint4 x0 = xs[0], x1 = xs[1];
-          uint32_t a[8], b[8];
-          if constexpr (WK == kQNone) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              a[i] = wa[slot][i];
-              b[i] = wb[slot][i];
-            }
-          } else {
-            fakequant16_packed<WK>(wa[slot], sa[slot], a);
-            fakequant16_packed<WK>(wb[slot], sb[slot], b);
-          }
-          mma_bf16(acc, a[0], b[0], a[1], b[1], x0.x, x0.y);
-          mma_bf16(acc, a[2], b[2], a[3], b[3], x0.z, x0.w);
-          mma_bf16(acc, a[4], b[4], a[5], b[5], x1.x, x1.y);
-          mma_bf16(acc, a[6], b[6], a[7], b[7], x1.z, x1.w);
+          const uint8_t* mine = smem + (warp * kDepth + slot) * kSlot;
+          const uint4* wv = reinterpret_cast<const uint4*>(mine) + lane;
+          const float* sv = reinterpret_cast<const float*>(mine + 2048) + lane;
+          const bool in = chunk * kChunk + 16 * t4 < q.K;
+          const uint4* xs = reinterpret_cast<const uint4*>(smem + few_rows_at() + col * stride) + chunk * (kChunk / 8) + 2 * t4;
+          const uint4 a0 = wv[0], a1 = wv[32], b0 = wv[64], b1 = wv[96], x0 = xs[0], x1 = xs[1];
+          const Block16 a = quantize16<WK>({a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w}, in ? sv[0] : 1.0f);
+          const Block16 b = quantize16<WK>({b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w}, in ? sv[32] : 1.0f);
+          mma_bf16(acc, a.v[0], b.v[0], a.v[1], b.v[1], x0.x, x0.y);
+          mma_bf16(acc, a.v[2], b.v[2], a.v[3], b.v[3], x0.z, x0.w);
+          mma_bf16(acc, a.v[4], b.v[4], a.v[5], b.v[5], x1.x, x1.y);
+          mma_bf16(acc, a.v[6], b.v[6], a.v[7], b.v[7], x1.z, x1.w);
         }
-        if (base + slot + kDepth < steps) load(slot);
-        if (++c < per_warp) continue;
-        // the tile's end: the team's partial sums are joined in warp order
-        c = 0;
-        float(*part)[kCols] = s_part[parity][warp];
-        part[g][2 * t4] = acc[0];
-        part[g][2 * t4 + 1] = acc[1];
-        part[g + 8][2 * t4] = acc[2];
-        part[g + 8][2 * t4 + 1] = acc[3];
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + my_team), "r"(32 * team) : "memory");
-        const float(*sum)[16][kCols] = &s_part[parity][my_team * team];
-        for (int i = in_team * 32 + lane; i < (FC1 ? 64 : 128); i += 32 * team) {
-          if constexpr (FC1) {
-            const int col = i / 8, n = i % 8;
-            if (s_row[col] >= 0) {
-              float zg = 0.0f, zu = 0.0f;
-              for (int w = 0; w < team; ++w) {
-                zg += sum[w][n][col];
-                zu += sum[w][n + 8][col];
-              }
-              q.rows[(int64_t)s_row[col] * q.N + tile * 8 + n] =
-                  __float2bfloat16_rn(__fmul_rn(silu_f(round_bf16(zg)), round_bf16(zu)));
-            }
-          } else {
-            const int col = i / 16, n = i % 16;
-            if (s_row[col] >= 0) {
-              float y = 0.0f;
-              for (int w = 0; w < team; ++w) y += sum[w][n][col];
-              q.rows[(int64_t)s_row[col] * q.N + tile * 16 + n] = __float2bfloat16_rn(y);
-            }
-          }
-        }
-        parity ^= 1;
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-        tile += teams;
+        slot = slot + 1 == kDepth ? 0 : slot + 1;
+        load();
       }
+      // the team's partial sums are joined in warp order
+      float(*part)[kCols] = s_part[parity][warp];
+      part[g][2 * t4] = acc[0];
+      part[g][2 * t4 + 1] = acc[1];
+      part[g + 8][2 * t4] = acc[2];
+      part[g + 8][2 * t4 + 1] = acc[3];
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + my_team), "r"(32 * team) : "memory");
+      const float(*sum)[16][kCols] = &s_part[parity][my_team * team];
+      for (int i = in_team * 32 + lane; i < (FC1 ? 64 : 128); i += 32 * team) {
+        const int cc = FC1 ? i / 8 : i / 16, n = FC1 ? i % 8 : i % 16;
+        if (s_row[cc] < 0) continue;
+        if constexpr (FC1) {
+          float zg = 0.0f, zu = 0.0f;
+          for (int w = 0; w < team; ++w) {
+            zg += sum[w][n][cc];
+            zu += sum[w][n + 8][cc];
+          }
+          q.rows[(int64_t)s_row[cc] * q.N + tile * 8 + n] =
+              __float2bfloat16_rn(__fmul_rn(silu_f(round_bf16(zg)), round_bf16(zu)));
+        } else {
+          float y = 0.0f;
+          for (int w = 0; w < team; ++w) y += sum[w][n][cc];
+          q.rows[(int64_t)s_row[cc] * q.N + tile * 16 + n] = __float2bfloat16_rn(y);
+        }
+      }
+      parity ^= 1;
     }
     if constexpr (!FC1) {
       // the pass that completes a tile of Y combines it, in slot order whoever comes last
@@ -348,25 +424,30 @@ int team_of(int64_t K) {
   return 1;
 }
 
-template <int WK, bool FC1>
+template <int WK, int AK, bool FC1>
 cudaError_t launch(const FewParams& q, int64_t units, cudaStream_t st) {
-  const int bytes = kCols * few_stride(q.K);
-  if (cudaError_t e = cudaFuncSetAttribute(few_kernel<WK, FC1>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))
-    return e;
-  const int64_t slots = 2 * (int64_t)num_sms();
-  few_kernel<WK, FC1><<<(unsigned)(units < slots ? units : slots), kThreads, bytes, st>>>(q);
+  const int bytes = few_smem(q.K, q.cols, q.E);
+  const auto kernel = few_kernel<WK, AK, FC1>;
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+  // as many blocks as are resident at once: 227 KB of shared memory, of which each takes 10 KB more than it asks for
+  const int fit = 227 * 1024 / (bytes + 10 * 1024), per_sm = fit < 1 ? 1 : fit > 3 ? 3 : fit;
+  const int64_t slots = (int64_t)per_sm * num_sms();
+  const unsigned blocks = (unsigned)(units < slots ? units : slots);
+  if (!FC1) return launch_dependent(kernel, blocks, kThreads, bytes, st, q);
+  kernel<<<blocks, kThreads, bytes, st>>>(q);
   return cudaGetLastError();
 }
 
 template <bool FC1>
-cudaError_t launch_kind(int kind, const FewParams& q, int64_t units, cudaStream_t st) {
-  switch (kind) {
-    case kQE2M1: return launch<kQE2M1, FC1>(q, units, st);
-    case kQInt4: return launch<kQInt4, FC1>(q, units, st);
-    case kQE4M3: return launch<kQE4M3, FC1>(q, units, st);
-    case kQInt8: return launch<kQInt8, FC1>(q, units, st);
-    default: return launch<kQNone, FC1>(q, units, st);
-  }
+cudaError_t launch_kind(int wk, int ak, const FewParams& q, int64_t units, cudaStream_t st) {
+  if (wk == kQE2M1 && ak == kQE2M1) return launch<kQE2M1, kQE2M1, FC1>(q, units, st);
+  if (wk == kQE2M1 && ak == kQE2M1G) return launch<kQE2M1, kQE2M1G, FC1>(q, units, st);
+  if (wk == kQE2M1) return launch<kQE2M1, kQNone, FC1>(q, units, st);
+  if (wk == kQInt4 && ak == kQE4M3) return launch<kQInt4, kQE4M3, FC1>(q, units, st);
+  if (wk == kQInt4) return launch<kQInt4, kQNone, FC1>(q, units, st);
+  if (wk == kQE4M3) return launch<kQE4M3, kQE4M3, FC1>(q, units, st);
+  if (wk == kQInt8) return launch<kQInt8, kQInt8, FC1>(q, units, st);
+  return launch<kQNone, kQNone, FC1>(q, units, st);
 }
 
 }  // namespace
@@ -401,10 +482,10 @@ cudaError_t launch_moe_few(const qad_moe_shape& s, const FewLayout& L, const voi
   q.T = (int)s.T;
   q.k = s.topk;
   q.E = (int)s.E;
-  q.aq = quant ? act_kind(s.fmt) : kQNone;
+  const int ak = quant ? act_kind(s.fmt) : kQNone;
+  q.cols = (int)(s.T < kCols ? s.T : kCols);
   q.d_tiles = (int)(s.d / 16);
   const int64_t pairs = s.T * s.topk;  // no more passes than pairs
-  auto wide = [](const void* w) { return (reinterpret_cast<uintptr_t>(w) & 31u) == 0; };
 
   q.act = static_cast<const __nv_bfloat16*>(x);
   q.w = static_cast<const __nv_bfloat16*>(w13);
@@ -414,9 +495,8 @@ cudaError_t launch_moe_few(const qad_moe_shape& s, const FewLayout& L, const voi
   q.N = (int)s.F;
   q.scales = block ? q.K / block : 1;
   q.team = team_of(q.K);
-  q.wide = wide(w13);
   prof_begin(QAD_K_MOE_FEW, st);
-  cudaError_t e = launch_kind<true>(kind, q, pairs * (q.N / 8), st);
+  cudaError_t e = launch_kind<true>(kind, ak, q, pairs * (q.N / 8), st);
   if (e == cudaSuccess) {
     q.act = reinterpret_cast<const __nv_bfloat16*>(ws + L.h);
     q.w = static_cast<const __nv_bfloat16*>(w2);
@@ -426,9 +506,8 @@ cudaError_t launch_moe_few(const qad_moe_shape& s, const FewLayout& L, const voi
     q.N = (int)s.d;
     q.scales = block ? q.K / block : 1;
     q.team = team_of(q.K);
-    q.wide = wide(w2);
     note_launches(1);
-    e = launch_kind<false>(kind, q, pairs * (q.N / 16), st);
+    e = launch_kind<false>(kind, ak, q, pairs * (q.N / 16), st);
   }
   prof_end(QAD_K_MOE_FEW, st);
   return e;
