@@ -106,7 +106,8 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  // through L1: a lane's 32 bytes are one sector, whose second half the next copy finds there
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -130,78 +131,120 @@ __device__ __noinline__ Block16 quantize_any(Block16 w, float s) {
   return w;
 }
 
-// W_hat of 16 weights that share scale s: the arithmetic of fakequant16_packed (see there), the same bits.
+// W_hat of 16 weights that share scale s, the bits of fakequant16_packed (see there for the quotient).  What follows the
+// quotient x = fp32(w / s) takes fewer instructions here:
+//  - E2M1: bf16(fp32(q s)) takes eight magnitudes, which the 3-bit codes of four weights look up by two byte permutations.
+//    Four of them are halves or doubles of bf16(s) and bf16(1.5 s), that is their bits with the exponent moved;
+//  - INT4, INT8: bf16(fp32(q s)) does not fall as q rises, so that clamping q is clamping it, two at a time.
 template <int WK>
 __device__ __forceinline__ Block16 quantize16(const Block16& w, float s) {
   if constexpr (WK == kQNone) {
     return w;
   } else {
-  Block16 out;
-  const float r = __frcp_rn(s);
-  const uint64_t r2 = f2pack(r, r), ns2 = f2pack(-s, -s), zero2 = f2pack(0.0f, 0.0f);
-  const float sc = (WK == kQE2M1 || WK == kQE4M3) ? s * 0x1p112f : s;
-  const uint64_t sc2 = f2pack(sc, sc);
-  uint64_t probe = zero2;
+    Block16 out;
+    const float r = __frcp_rn(s);
+    const uint64_t r2 = f2pack(r, r), ns2 = f2pack(-s, -s), zero2 = f2pack(0.0f, 0.0f);
+    uint64_t probe = zero2;
+    auto quotient2 = [&](uint32_t v) {
+      const uint64_t w2 = f2pack(bf16lo(v), bf16hi(v));
+      const uint64_t q2 = f2mul(w2, r2), x2 = f2fma(f2fma(q2, ns2, w2), r2, q2);
+      probe = f2fma(x2, zero2, probe);  // stays 0 unless a quotient is inf or NaN
+      return x2;
+    };
+    if constexpr (WK == kQE2M1) {
+      const uint32_t m23 = pack_bf16(s, __fmul_rn(1.5f, s));
+      const uint32_t m01 = (m23 << 16) - 0x00800000u, m45 = m23 + 0x00800080u, m67 = m23 + 0x01000100u;
+      const uint32_t lo03 = __byte_perm(m01, m23, 0x6420), lo47 = __byte_perm(m45, m67, 0x6420);
+      const uint32_t hi03 = __byte_perm(m01, m23, 0x7531), hi47 = __byte_perm(m45, m67, 0x7531);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint64_t w2 = f2pack(bf16lo(w.v[i]), bf16hi(w.v[i]));
-    const uint64_t q2 = f2mul(w2, r2);
-    const uint64_t x2 = f2fma(f2fma(q2, ns2, w2), r2, q2);
-    probe = f2fma(x2, zero2, probe);
-    const float2 x = f2unpack(x2);
-    uint64_t m2;
-    if constexpr (WK == kQE2M1 || WK == kQE4M3) {
-      uint32_t h2;
-      if constexpr (WK == kQE2M1) {
-        asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
-            : "=r"(h2) : "f"(x.x), "f"(x.y));
-      } else {
+      for (int i = 0; i < 8; i += 4) {
+        const float2 a = f2unpack(quotient2(w.v[i])), b = f2unpack(quotient2(w.v[i + 1]));
+        const float2 c = f2unpack(quotient2(w.v[i + 2])), d = f2unpack(quotient2(w.v[i + 3]));
+        uint32_t codes;
+        asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n\t"
+            "mov.b32 %0, {c0, c1, c2, c3};\n\t}"
+            : "=r"(codes)
+            : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+        codes &= 0x77777777u;
+        const uint32_t up = codes >> 16;
+        const uint32_t l0 = __byte_perm(lo03, lo47, codes), h0 = __byte_perm(hi03, hi47, codes);
+        const uint32_t l1 = __byte_perm(lo03, lo47, up), h1 = __byte_perm(hi03, hi47, up);
+        out.v[i] = __byte_perm(l0, h0, 0x5140) | (w.v[i] & 0x80008000u);
+        out.v[i + 1] = __byte_perm(l0, h0, 0x7362) | (w.v[i + 1] & 0x80008000u);
+        out.v[i + 2] = __byte_perm(l1, h1, 0x5140) | (w.v[i + 2] & 0x80008000u);
+        out.v[i + 3] = __byte_perm(l1, h1, 0x7362) | (w.v[i + 3] & 0x80008000u);
+      }
+    } else if constexpr (WK == kQE4M3) {
+      const float sc = s * 0x1p112f;
+      const uint64_t sc2 = f2pack(sc, sc);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 x = f2unpack(quotient2(w.v[i]));
         uint16_t c;
+        uint32_t h2;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(x.x), "f"(x.y));
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
+        const uint32_t la = (h2 << 13) & 0x0FFFE000u, lb = (h2 >> 3) & 0x0FFFE000u;
+        const float2 m = f2unpack(f2mul(f2pack(__uint_as_float(la), __uint_as_float(lb)), sc2));
+        out.v[i] = pack_bf16(m.x, m.y) | (w.v[i] & 0x80008000u);
       }
-      const uint32_t la = (h2 << 13) & 0x0FFFE000u, lb = (h2 >> 3) & 0x0FFFE000u;
-      m2 = f2mul(f2pack(__uint_as_float(la), __uint_as_float(lb)), sc2);
     } else {
-      const uint64_t big2 = f2pack(12582912.0f, 12582912.0f);  // 1.5 * 2^23
-      const float ta = fminf(fmaxf(x.x, Clip<WK>::lo), Clip<WK>::hi);
-      const float tb = fminf(fmaxf(x.y, Clip<WK>::lo), Clip<WK>::hi);
-      m2 = f2mul(f2sub(f2add(f2pack(ta, tb), big2), big2), sc2);
+      const uint64_t big2 = f2pack(12582912.0f, 12582912.0f), s2 = f2pack(s, s);  // 1.5 * 2^23
+      const float lo = __fmul_rn(Clip<WK>::lo, s), hi = __fmul_rn(Clip<WK>::hi, s);
+      const uint32_t lo2 = pack_bf16(lo, lo), hi2 = pack_bf16(hi, hi);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 m = f2unpack(f2mul(f2sub(f2add(quotient2(w.v[i]), big2), big2), s2));
+        uint32_t v = pack_bf16(m.x, m.y);
+        asm("max.bf16x2 %0, %0, %1;\n\tmin.bf16x2 %0, %0, %2;" : "+r"(v) : "r"(lo2), "r"(hi2));
+        out.v[i] = v | (w.v[i] & 0x80008000u);
+      }
     }
-    const float2 m = f2unpack(m2);
-    out.v[i] = pack_bf16(m.x, m.y) | (w.v[i] & 0x80008000u);
-  }
-  const float2 p = f2unpack(probe);
-  if (!(s >= 0x1p-60f && s < 0x1p16f) || !(p.x == 0.0f && p.y == 0.0f)) out = quantize_any<WK>(w, s);
-  return out;
+    const float2 p = f2unpack(probe);
+    if (!(s >= 0x1p-60f && s < 0x1p16f) || !(p.x == 0.0f && p.y == 0.0f)) out = quantize_any<WK>(w, s);
+    return out;
   }
 }
 
-// One activation row through its quantizer into shared memory, by one warp; zeros behind K.
+// Token rows through their quantizer into shared memory, zeros behind K; `share` warps work on a row.  The scale of a
+// whole row needs a barrier in between (top: zeros before).
 template <int AK>
-__device__ __forceinline__ void stage_row(const __nv_bfloat16* row, uint4* dst, int K, int lane) {
-  const uint4* src = reinterpret_cast<const uint4*>(row);
+__device__ __forceinline__ void stage_rows(const __nv_bfloat16* act, const int* src, uint32_t* top, uint8_t* rows, int K,
+                                           int share) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, col = warp / share;
+  const int first = warp % share * 32 + lane, step = share * 32;
   const int nblk = K / 16, padded = (K + kChunk - 1) / kChunk * (kChunk / 16);
+  const bool has = src[col] >= 0;
+  const uint4* in = reinterpret_cast<const uint4*>(act + (int64_t)(has ? src[col] : 0) * K);
+  uint4* out = reinterpret_cast<uint4*>(rows + col * few_stride(K));
   float s_row = 0.0f;
   if constexpr (act_needs_row(AK)) {
     float amax = 0.0f;
-    for (int b = lane; b < nblk; b += 32) {
-      float f[16];
-      unpack8(src[2 * b], f);
-      unpack8(src[2 * b + 1], f + 8);
+    if (has)
+      for (int b = first; b < nblk; b += step) {
+        float f[16];
+        unpack8(in[2 * b], f);
+        unpack8(in[2 * b + 1], f + 8);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-    }
+        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
+      }
     amax = warp_max(amax);
+    if (lane == 0) atomicMax(top + col, __float_as_uint(amax));
+    __syncthreads();
+    amax = __uint_as_float(top[col]);
     s_row = AK == kQE4M3   ? __fdiv_rn(amax, 448.0f)
             : AK == kQInt8 ? __fdiv_rn(amax, 127.0f)
                            : deploy_tensor_scale(__fdiv_rn(amax, 6.0f));
   }
-  for (int b = lane; b < padded; b += 32) {
+  if (!has) return;
+#pragma unroll 1
+  for (int b = first; b < padded; b += step) {
     uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
     if (b < nblk) {
-      u0 = src[2 * b];
-      u1 = src[2 * b + 1];
+      u0 = in[2 * b];
+      u1 = in[2 * b + 1];
       if constexpr (AK != kQNone) {
         float f[16];
         unpack8(u0, f);
@@ -220,8 +263,8 @@ __device__ __forceinline__ void stage_row(const __nv_bfloat16* row, uint4* dst, 
         u1 = pack8(f + 8);
       }
     }
-    dst[2 * b] = u0;
-    dst[2 * b + 1] = u1;
+    out[2 * b] = u0;
+    out[2 * b + 1] = u1;
   }
 }
 
@@ -234,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
   __shared__ uint32_t s_live[64];
   __shared__ float s_part[2][kWarps][16][kCols];
   __shared__ int s_row[kCols], s_src[kCols];
+  __shared__ uint32_t s_top[kCols];
   uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + few_mask_at(q.K, q.cols));
   uint16_t* s_first = reinterpret_cast<uint16_t*>(s_mask + q.E);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, t4 = lane & 3;
@@ -264,44 +308,47 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
   };
 
   // the chunks of this warp's tiles, in order, on their way into its ring
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + warp * kDepth * kSlot);
-  int ld_u = lo + my_team, ld_end = lo, ld_c = 0, ld_slot = 0;
-  const __nv_bfloat16* ld_w = nullptr;
-  const float* ld_s = nullptr;
-  auto next_tile = [&]() {  // ld_u is the team's next tile of the pass that ends at ld_end, or past it: then of a later one
-    while (ld_u >= ld_end && ld_end < hi) {
-      const int pass = ld_end / tiles, e = expert_of(pass);
-      ld_u = ld_end + my_team;
-      ld_end = min(hi, (pass + 1) * tiles);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + warp * kDepth * kSlot) + lane * 16;
+  int ld_tile = 0, ld_last = 0, ld_next = lo, ld_chunk = 0, ld_slot = 0;  // ld_next: where the next pass's tiles begin
+  const __nv_bfloat16 *ld_w = nullptr, *pa = nullptr, *pb = nullptr;
+  const float *ld_s = nullptr, *sa = nullptr, *sb = nullptr;
+  auto open_tile = [&]() {
+    while (ld_tile >= ld_last && ld_next < hi) {
+      const int pass = ld_next / tiles, tile0 = ld_next - pass * tiles, e = expert_of(pass);
+      ld_last = min(tiles, tile0 + hi - ld_next);
+      ld_next += ld_last - tile0;
+      ld_tile = tile0 + my_team;
       ld_w = q.w + (int64_t)e * (FC1 ? 2 * q.N : q.N) * q.K;
       ld_s = q.s + (int64_t)e * (FC1 ? 2 * q.N : q.N) * q.scales;
     }
+    const int ra = FC1 ? ld_tile * 8 + g : ld_tile * 16 + g, rb = FC1 ? q.N + ra : ra + 8;
+    pa = ld_w + (int64_t)ra * q.K + 16 * t4;
+    pb = ld_w + (int64_t)rb * q.K + 16 * t4;
+    sa = ld_s + (int64_t)ra * q.scales;
+    sb = ld_s + (int64_t)rb * q.scales;
+    ld_chunk = in_team;
   };
-  next_tile();
+  open_tile();
   auto load = [&]() {
-    if (ld_u < ld_end) {
-      const int chunk = ld_c * team + in_team;
-      if (chunk < chunks) {
-        const int tile = ld_u % tiles, k0 = chunk * kChunk + 16 * t4;
-        const int ra = FC1 ? tile * 8 + g : tile * 16 + g, rb = FC1 ? q.N + ra : ra + 8;
-        const int bytes = k0 < q.K ? 16 : 0, kk = k0 < q.K ? k0 : 0;  // zeros behind K
-        const __nv_bfloat16 *pa = ld_w + (int64_t)ra * q.K + kk, *pb = ld_w + (int64_t)rb * q.K + kk;
-        const uint32_t at = ring + ld_slot * kSlot + lane * 16;
-        copy16(at, pa, bytes);
-        copy16(at + 512, pa + 8, bytes);
-        copy16(at + 1024, pb, bytes);
-        copy16(at + 1536, pb + 8, bytes);
+    if (ld_tile < ld_last) {
+      if (ld_chunk < chunks) {
+        const int k0 = ld_chunk * kChunk, bytes = k0 + 16 * t4 < q.K ? 16 : 0, kk = bytes ? k0 : 0;  // zeros behind K
+        const uint32_t at = ring + ld_slot * kSlot;
+        copy16(at, pa + kk, bytes);
+        copy16(at + 512, pa + kk + 8, bytes);
+        copy16(at + 1024, pb + kk, bytes);
+        copy16(at + 1536, pb + kk + 8, bytes);
         if constexpr (WK != kQNone) {
-          const int sk = WK == kQE2M1 ? kk / 16 : WK == kQInt4 ? kk / 128 : 0;
-          const uint32_t sat = ring + ld_slot * kSlot + 2048 + lane * 4;
-          copy4(sat, ld_s + (int64_t)ra * q.scales + sk);
-          copy4(sat + 128, ld_s + (int64_t)rb * q.scales + sk);
+          const int sk = WK == kQE2M1 ? (bytes ? k0 / 16 + t4 : 0) : WK == kQInt4 ? kk / 128 : 0;
+          const uint32_t sat = at - lane * 12 + 2048;
+          copy4(sat, sa + sk);
+          copy4(sat + 128, sb + sk);
         }
       }
-      if (++ld_c == per_warp) {
-        ld_c = 0;
-        ld_u += teams;
-        next_tile();
+      ld_chunk += team;
+      if (ld_chunk >= per_warp * team) {
+        ld_tile += teams;
+        open_tile();
       }
     }
     ld_slot = ld_slot + 1 == kDepth ? 0 : ld_slot + 1;
@@ -329,11 +376,11 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
       }
       s_row[tid] = row;
       s_src[tid] = src;
+      s_top[tid] = 0;
     }
     __syncthreads();
-    if (s_src[warp] >= 0)
-      stage_row<AK>(q.act + (int64_t)s_src[warp] * q.K,
-                    reinterpret_cast<uint4*>(smem + few_rows_at() + warp * stride), q.K, lane);
+    const int staged = min(kCols, __popcll(s_mask[e]) - (pass - s_first[e]) * kCols);
+    stage_rows<AK>(q.act, s_src, s_top, smem + few_rows_at(), q.K, staged > 4 ? 1 : staged > 2 ? 2 : staged > 1 ? 4 : 8);
     __syncthreads();
 
     for (int tile = tile0 + my_team; tile < tile0 + ntiles; tile += teams) {
