@@ -5,11 +5,11 @@
 //   fc2:  Y = AQ(H) . W2_hat^T, out[t] = bf16(sum_j p[t, j] * Y_j)
 //
 // With so few rows the weights are all there is to move (2 bytes an element and its part of a scale), and each element
-// costs about eight instructions of fake-quantization whatever the number of tokens.  So a lane copies 16 consecutive
-// weights of a row (one quantization block) ahead into its own corner of shared memory, quantizes them in registers in
+// costs about eight instructions of fake-quantization whatever the number of tokens.  So a warp copies 64 weights of 16
+// rows ahead into its ring in shared memory; a lane quantizes 16 of a row (one quantization block) in registers in
 // the tensor cores' fragment layout, and four m16n8k16 products take them as they lie.  The order of k inside a product
 // does not matter as long as both operands agree, so the tokens' rows (shared memory, up to 8 columns) are read in the
-// same order.  No lane reads what another one copied: the ring needs no barrier.  tcgen05 would want the quantized weights
+// same order.  A warp reads only what it copied itself: the ring needs no block barrier.  tcgen05 would want the quantized weights
 // in shared memory: a write and a read of every element for products that are idle most of the time here.
 #include "common.cuh"
 #include "dependents.cuh"
@@ -22,7 +22,8 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCols = 8;    // tokens of one expert that a pass over its weights serves
 constexpr int kDepth = 3;   // chunks of a warp in shared memory or on their way
 constexpr int kChunk = 64;  // elements along K of one step: 16 for each lane of a quad
-constexpr int kSlot = 4 * 512 + 2 * 128;  // bytes of a warp's chunk: 16 rows of weights, a scale for each lane and row
+constexpr int kPitch = 2 * kChunk + 16;   // bytes between the rows of a chunk: 16-byte reads of 8 lanes meet no bank twice
+constexpr int kSlot = 16 * kPitch + 256;  // bytes of a warp's chunk: 16 rows of weights, up to 4 scales a row
 
 struct FewParams {
   const __nv_bfloat16* act;  // fc1: x [T, K]; fc2: H [T * k, K]
@@ -106,8 +107,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  // through L1: a lane's 32 bytes are one sector, whose second half the next copy finds there
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -116,28 +116,20 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
 struct Block16 {
   uint32_t v[8];
 };
-// fakequant16_packed's way out, kept out of the loop's instructions
-template <int WK>
-__device__ __noinline__ Block16 quantize_any(Block16 w, float s) {
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[2 * i] = bf16lo(w.v[i]);
-    v[2 * i + 1] = bf16hi(w.v[i]);
-  }
-  fakequant_inplace<WK, 16>(v, s);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w.v[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-  return w;
-}
 
 // W_hat of 16 weights that share scale s, the bits of fakequant16_packed (see there for the quotient).  What follows the
 // quotient x = fp32(w / s) takes fewer instructions here:
 //  - E2M1: bf16(fp32(q s)) takes eight magnitudes, which the 3-bit codes of four weights look up by two byte permutations.
 //    Four of them are halves or doubles of bf16(s) and bf16(1.5 s), that is their bits with the exponent moved;
 //  - INT4, INT8: bf16(fp32(q s)) does not fall as q rises, so that clamping q is clamping it, two at a time.
+// Scales and quotients out of range: pair by pair, in the weights' place in shared memory (16-byte aligned).
 template <int WK>
-__device__ __forceinline__ Block16 quantize16(const Block16& w, float s) {
+__device__ __forceinline__ Block16 quantize16(uint32_t* place, float s) {
+  auto read = [&]() {
+    const uint4 lo = reinterpret_cast<const uint4*>(place)[0], hi = reinterpret_cast<const uint4*>(place)[1];
+    return Block16{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+  };
+  const Block16 w = read();
   if constexpr (WK == kQNone) {
     return w;
   } else {
@@ -203,7 +195,14 @@ __device__ __forceinline__ Block16 quantize16(const Block16& w, float s) {
       }
     }
     const float2 p = f2unpack(probe);
-    if (!(s >= 0x1p-60f && s < 0x1p16f) || !(p.x == 0.0f && p.y == 0.0f)) out = quantize_any<WK>(w, s);
+    if (__builtin_expect(!(s >= 0x1p-60f && s < 0x1p16f) || !(p.x == 0.0f && p.y == 0.0f), 0)) {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const float2 c = q_pair<WK>(quotient(bf16lo(place[i]), s), quotient(bf16hi(place[i]), s));
+        place[i] = pack_bf16(__fmul_rn(c.x, s), __fmul_rn(c.y, s));
+      }
+      return read();
+    }
     return out;
   }
 }
@@ -308,10 +307,13 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
   };
 
   // the chunks of this warp's tiles, in order, on their way into its ring
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + warp * kDepth * kSlot) + lane * 16;
+  // a copy of the warp takes 4 rows of 128 bytes: lane / 8 the row, lane % 8 its 16 bytes
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + warp * kDepth * kSlot);
+  const int piece = lane & 7;
+  const int64_t up = FC1 ? (int64_t)q.N * q.K : 8 * (int64_t)q.K, sup = FC1 ? (int64_t)q.N * q.scales : 8 * (int64_t)q.scales;
   int ld_tile = 0, ld_last = 0, ld_next = lo, ld_chunk = 0, ld_slot = 0;  // ld_next: where the next pass's tiles begin
-  const __nv_bfloat16 *ld_w = nullptr, *pa = nullptr, *pb = nullptr;
-  const float *ld_s = nullptr, *sa = nullptr, *sb = nullptr;
+  const __nv_bfloat16 *ld_w = nullptr, *pw = nullptr;
+  const float *ld_s = nullptr, *ps = nullptr;
   auto open_tile = [&]() {
     while (ld_tile >= ld_last && ld_next < hi) {
       const int pass = ld_next / tiles, tile0 = ld_next - pass * tiles, e = expert_of(pass);
@@ -321,28 +323,30 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
       ld_w = q.w + (int64_t)e * (FC1 ? 2 * q.N : q.N) * q.K;
       ld_s = q.s + (int64_t)e * (FC1 ? 2 * q.N : q.N) * q.scales;
     }
-    const int ra = FC1 ? ld_tile * 8 + g : ld_tile * 16 + g, rb = FC1 ? q.N + ra : ra + 8;
-    pa = ld_w + (int64_t)ra * q.K + 16 * t4;
-    pb = ld_w + (int64_t)rb * q.K + 16 * t4;
-    sa = ld_s + (int64_t)ra * q.scales;
-    sb = ld_s + (int64_t)rb * q.scales;
+    const int row = ld_tile * (FC1 ? 8 : 16);
+    pw = ld_w + (int64_t)(row + lane / 8) * q.K;
+    // E2M1: lane / 4 the row, lane % 4 its block of the chunk; else lane the row (16 of them)
+    ps = ld_s + (int64_t)(row + (WK == kQE2M1 ? lane / 4 : lane & 7)) * q.scales;
+    if (WK != kQE2M1 && (lane & 8)) ps += sup;
     ld_chunk = in_team;
   };
   open_tile();
   auto load = [&]() {
     if (ld_tile < ld_last) {
       if (ld_chunk < chunks) {
-        const int k0 = ld_chunk * kChunk, bytes = k0 + 16 * t4 < q.K ? 16 : 0, kk = bytes ? k0 : 0;  // zeros behind K
-        const uint32_t at = ring + ld_slot * kSlot;
-        copy16(at, pa + kk, bytes);
-        copy16(at + 512, pa + kk + 8, bytes);
-        copy16(at + 1024, pb + kk, bytes);
-        copy16(at + 1536, pb + kk + 8, bytes);
-        if constexpr (WK != kQNone) {
-          const int sk = WK == kQE2M1 ? (bytes ? k0 / 16 + t4 : 0) : WK == kQInt4 ? kk / 128 : 0;
-          const uint32_t sat = at - lane * 12 + 2048;
-          copy4(sat, sa + sk);
-          copy4(sat + 128, sb + sk);
+        const int k0 = ld_chunk * kChunk, bytes = k0 + 8 * piece < q.K ? 16 : 0;  // zeros behind K
+        const __nv_bfloat16* from = pw + (bytes ? k0 + 8 * piece : 0);
+        const uint32_t at = ring + ld_slot * kSlot, to = at + lane / 8 * kPitch + piece * 16;
+        copy16(to, from, bytes);
+        copy16(to + 4 * kPitch, from + 4 * (int64_t)q.K, bytes);
+        copy16(to + 8 * kPitch, from + up, bytes);
+        copy16(to + 12 * kPitch, from + up + 4 * (int64_t)q.K, bytes);
+        if constexpr (WK == kQE2M1) {
+          const int b = k0 / 16 + (lane & 3), in = b < q.scales ? b : 0;
+          copy4(at + 16 * kPitch + lane * 4, ps + in);
+          copy4(at + 16 * kPitch + 128 + lane * 4, ps + in + sup);
+        } else if constexpr (WK != kQNone) {
+          if (lane < 16) copy4(at + 16 * kPitch + lane * 4, ps + (WK == kQInt4 ? k0 / 128 : 0));
         }
       }
       ld_chunk += team;
@@ -388,16 +392,17 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
 #pragma unroll 1
       for (int c = 0; c < per_warp; ++c) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+        __syncwarp();  // the other lanes' copies too, and nobody reads the slot that the next load fills
         const int chunk = c * team + in_team;
         if (chunk < chunks) {
-          const uint8_t* mine = smem + (warp * kDepth + slot) * kSlot;
-          const uint4* wv = reinterpret_cast<const uint4*>(mine) + lane;
-          const float* sv = reinterpret_cast<const float*>(mine + 2048) + lane;
+          uint8_t* mine = smem + (warp * kDepth + slot) * kSlot;
+          const float* sv = reinterpret_cast<const float*>(mine + 16 * kPitch) + (WK == kQE2M1 ? lane : g);
+          uint32_t* wv = reinterpret_cast<uint32_t*>(mine + g * kPitch + t4 * 32);
           const bool in = chunk * kChunk + 16 * t4 < q.K;
+          const Block16 a = quantize16<WK>(wv, in ? sv[0] : 1.0f);
+          const Block16 b = quantize16<WK>(wv + 8 * kPitch / 4, in ? sv[WK == kQE2M1 ? 32 : 8] : 1.0f);
           const uint4* xs = reinterpret_cast<const uint4*>(smem + few_rows_at() + col * stride) + chunk * (kChunk / 8) + 2 * t4;
-          const uint4 a0 = wv[0], a1 = wv[32], b0 = wv[64], b1 = wv[96], x0 = xs[0], x1 = xs[1];
-          const Block16 a = quantize16<WK>({a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w}, in ? sv[0] : 1.0f);
-          const Block16 b = quantize16<WK>({b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w}, in ? sv[32] : 1.0f);
+          const uint4 x0 = xs[0], x1 = xs[1];
           mma_bf16(acc, a.v[0], b.v[0], a.v[1], b.v[1], x0.x, x0.y);
           mma_bf16(acc, a.v[2], b.v[2], a.v[3], b.v[3], x0.z, x0.w);
           mma_bf16(acc, a.v[4], b.v[4], a.v[5], b.v[5], x1.x, x1.y);
