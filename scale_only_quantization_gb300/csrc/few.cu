@@ -18,9 +18,9 @@
 namespace qad {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCols = 8;    // tokens of one expert that a pass over its weights serves
-constexpr int kDepth = 3;   // chunks of a warp in shared memory or on their way
+constexpr int kThreads = 768, kWarps = kThreads / 32;  // one block per SM
+constexpr int kCols = 8;    // tokens of one expert that a pass over its weights serves, at most
+constexpr int kMaxTeam = 8; // warps that share a tile
 constexpr int kChunk = 64;  // elements along K of one step: 16 for each lane of a quad
 constexpr int kPitch = 2 * kChunk + 16;   // bytes between the rows of a chunk: 16-byte reads of 8 lanes meet no bank twice
 constexpr int kSlot = 16 * kPitch + 256;  // bytes of a warp's chunk: 16 rows of weights, up to 4 scales a row
@@ -37,6 +37,7 @@ struct FewParams {
   uint32_t* arrivals;  // [d / 16]: experts' passes that have written a tile of Y
   int T, k, E, K, N, scales;  // scales: per row
   int team, cols, d_tiles;    // team: warps that share a tile; cols: token rows staged at once
+  int depth;                  // chunks of a warp in its ring: the one that is worked on and 1 or 2 on their way
 };
 
 __host__ __device__ constexpr int few_stride(int K) { return (K + kChunk - 1) / kChunk * kChunk * 2 + 16; }
@@ -44,13 +45,15 @@ __host__ __device__ constexpr int few_stride(int K) { return (K + kChunk - 1) / 
 struct Route {
   uint64_t* mask;    // [E]: the tokens that name the expert
   uint32_t* live;    // [T]: the slots of a token that count
-  uint16_t* first;   // [E + 1]: the expert's first pass (8 tokens each)
+  uint16_t* first;   // [E + 1]: the expert's first pass (`cols` tokens each)
 };
 
 // Dynamic shared memory: the warps' rings, the staged token rows, the masks and first passes of E experts.
-__host__ __device__ constexpr int few_rows_at() { return kWarps * kDepth * kSlot; }
-__host__ __device__ constexpr int few_mask_at(int K, int cols) { return few_rows_at() + cols * few_stride(K); }
-__host__ __device__ constexpr int few_smem(int K, int cols, int E) { return few_mask_at(K, cols) + 8 * E + 2 * (E + 1) + 6; }
+__host__ __device__ constexpr int few_rows_at(int depth) { return kWarps * depth * kSlot; }
+__host__ __device__ constexpr int few_mask_at(int K, int cols, int depth) { return few_rows_at(depth) + cols * few_stride(K); }
+__host__ __device__ constexpr int few_smem(int K, int cols, int E, int depth) {
+  return few_mask_at(K, cols, depth) + 8 * E + 2 * (E + 1) + 6;
+}
 
 // The pairs by expert, in every block for itself: at most 2048 of them.  Returns the passes in all.
 __device__ __forceinline__ int route(const FewParams& q, const Route& r, int* err) {
@@ -80,7 +83,7 @@ __device__ __forceinline__ int route(const FewParams& q, const Route& r, int* er
   if (tid < 32) {
     const int per = (q.E + 31) / 32, lo = min(q.E, tid * per), hi = min(q.E, lo + per);
     int n = 0;
-    for (int e = lo; e < hi; ++e) n += (__popcll(r.mask[e]) + kCols - 1) / kCols;
+    for (int e = lo; e < hi; ++e) n += (__popcll(r.mask[e]) + q.cols - 1) / q.cols;
     int at = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -90,7 +93,7 @@ __device__ __forceinline__ int route(const FewParams& q, const Route& r, int* er
     at -= n;
     for (int e = lo; e < hi; ++e) {
       r.first[e] = (uint16_t)at;
-      at += (__popcll(r.mask[e]) + kCols - 1) / kCols;
+      at += (__popcll(r.mask[e]) + q.cols - 1) / q.cols;
     }
     if (tid == 31) r.first[q.E] = (uint16_t)at;
   }
@@ -212,10 +215,10 @@ __device__ __forceinline__ Block16 quantize16(uint32_t* place, float s) {
 template <int AK>
 __device__ __forceinline__ void stage_rows(const __nv_bfloat16* act, const int* src, uint32_t* top, uint8_t* rows, int K,
                                            int share) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, col = warp / share;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, col = min(warp / share, kCols);  // the last warps may have none
   const int first = warp % share * 32 + lane, step = share * 32;
   const int nblk = K / 16, padded = (K + kChunk - 1) / kChunk * (kChunk / 16);
-  const bool has = src[col] >= 0;
+  const bool has = col < kCols && src[col] >= 0;
   const uint4* in = reinterpret_cast<const uint4*>(act + (int64_t)(has ? src[col] : 0) * K);
   uint4* out = reinterpret_cast<uint4*>(rows + col * few_stride(K));
   float s_row = 0.0f;
@@ -230,9 +233,9 @@ __device__ __forceinline__ void stage_rows(const __nv_bfloat16* act, const int* 
         for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
       }
     amax = warp_max(amax);
-    if (lane == 0) atomicMax(top + col, __float_as_uint(amax));
+    if (has && lane == 0) atomicMax(top + col, __float_as_uint(amax));
     __syncthreads();
-    amax = __uint_as_float(top[col]);
+    amax = has ? __uint_as_float(top[col]) : 0.0f;
     s_row = AK == kQE4M3   ? __fdiv_rn(amax, 448.0f)
             : AK == kQInt8 ? __fdiv_rn(amax, 127.0f)
                            : deploy_tensor_scale(__fdiv_rn(amax, 6.0f));
@@ -271,13 +274,13 @@ __device__ __forceinline__ void stage_rows(const __nv_bfloat16* act, const int* 
 // consecutive share of all (pass, tile) pairs, passes outermost, so that it stages few passes' tokens; its teams of warps
 // take the tiles of a pass in turn, and the warps of a team the chunks of a tile along K.
 template <int WK, int AK, bool FC1>
-__global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(FewParams q) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_live[64];
   __shared__ float s_part[2][kWarps][16][kCols];
   __shared__ int s_row[kCols], s_src[kCols];
   __shared__ uint32_t s_top[kCols];
-  uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + few_mask_at(q.K, q.cols));
+  uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + few_mask_at(q.K, q.cols, q.depth));
   uint16_t* s_first = reinterpret_cast<uint16_t*>(s_mask + q.E);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, t4 = lane & 3;
   const int stride = few_stride(q.K), chunks = (q.K + kChunk - 1) / kChunk;
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
 
   // the chunks of this warp's tiles, in order, on their way into its ring
   // a copy of the warp takes 4 rows of 128 bytes: lane / 8 the row, lane % 8 its 16 bytes
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + warp * kDepth * kSlot);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + warp * q.depth * kSlot);
   const int piece = lane & 7;
   const int64_t up = FC1 ? (int64_t)q.N * q.K : 8 * (int64_t)q.K, sup = FC1 ? (int64_t)q.N * q.scales : 8 * (int64_t)q.scales;
   int ld_tile = 0, ld_last = 0, ld_next = lo, ld_chunk = 0, ld_slot = 0;  // ld_next: where the next pass's tiles begin
@@ -355,11 +358,11 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
         open_tile();
       }
     }
-    ld_slot = ld_slot + 1 == kDepth ? 0 : ld_slot + 1;
+    ld_slot = ld_slot + 1 == q.depth ? 0 : ld_slot + 1;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
-  for (int i = 0; i < kDepth - 1; ++i) load();
+  load();
+  if (q.depth > 2) load();
   if (!FC1) wait_for_kernel_before();
 
   int slot = 0, parity = 0;
@@ -370,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
     __syncthreads();  // the tokens of the pass before are no longer read
     if (tid < kCols) {
       uint64_t m = s_mask[e];
-      for (int i = (pass - s_first[e]) * kCols + tid; i > 0 && m; --i) m &= m - 1;
+      for (int i = (pass - s_first[e]) * q.cols + tid; i > 0 && m; --i) m &= m - 1;
       int row = -1, src = -1;
-      if (m) {
+      if (m && tid < q.cols) {
         const int t = __ffsll((long long)m) - 1;
         for (int j = 0; j < q.k; ++j)
           if ((s_live[t] >> j & 1) && __ldg(q.idx + t * q.k + j) == e) row = t * q.k + j;
@@ -383,33 +386,34 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
       s_top[tid] = 0;
     }
     __syncthreads();
-    const int staged = min(kCols, __popcll(s_mask[e]) - (pass - s_first[e]) * kCols);
-    stage_rows<AK>(q.act, s_src, s_top, smem + few_rows_at(), q.K, staged > 4 ? 1 : staged > 2 ? 2 : staged > 1 ? 4 : 8);
+    const int staged = min(q.cols, __popcll(s_mask[e]) - (pass - s_first[e]) * q.cols);
+    stage_rows<AK>(q.act, s_src, s_top, smem + few_rows_at(q.depth), q.K, kWarps / staged);
     __syncthreads();
 
     for (int tile = tile0 + my_team; tile < tile0 + ntiles; tile += teams) {
       float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
       for (int c = 0; c < per_warp; ++c) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+        if (q.depth > 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncwarp();  // the other lanes' copies too, and nobody reads the slot that the next load fills
+        load();
         const int chunk = c * team + in_team;
         if (chunk < chunks) {
-          uint8_t* mine = smem + (warp * kDepth + slot) * kSlot;
+          uint8_t* mine = smem + (warp * q.depth + slot) * kSlot;
           const float* sv = reinterpret_cast<const float*>(mine + 16 * kPitch) + (WK == kQE2M1 ? lane : g);
           uint32_t* wv = reinterpret_cast<uint32_t*>(mine + g * kPitch + t4 * 32);
           const bool in = chunk * kChunk + 16 * t4 < q.K;
           const Block16 a = quantize16<WK>(wv, in ? sv[0] : 1.0f);
           const Block16 b = quantize16<WK>(wv + 8 * kPitch / 4, in ? sv[WK == kQE2M1 ? 32 : 8] : 1.0f);
-          const uint4* xs = reinterpret_cast<const uint4*>(smem + few_rows_at() + col * stride) + chunk * (kChunk / 8) + 2 * t4;
+          const uint4* xs = reinterpret_cast<const uint4*>(smem + few_rows_at(q.depth) + col * stride) + chunk * (kChunk / 8) + 2 * t4;
           const uint4 x0 = xs[0], x1 = xs[1];
           mma_bf16(acc, a.v[0], b.v[0], a.v[1], b.v[1], x0.x, x0.y);
           mma_bf16(acc, a.v[2], b.v[2], a.v[3], b.v[3], x0.z, x0.w);
           mma_bf16(acc, a.v[4], b.v[4], a.v[5], b.v[5], x1.x, x1.y);
           mma_bf16(acc, a.v[6], b.v[6], a.v[7], b.v[7], x1.z, x1.w);
         }
-        slot = slot + 1 == kDepth ? 0 : slot + 1;
-        load();
+        slot = slot + 1 == q.depth ? 0 : slot + 1;
       }
       // the team's partial sums are joined in warp order
       float(*part)[kCols] = s_part[parity][warp];
@@ -417,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
       part[g][2 * t4 + 1] = acc[1];
       part[g + 8][2 * t4] = acc[2];
       part[g + 8][2 * t4 + 1] = acc[3];
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + my_team), "r"(32 * team) : "memory");
+      if (team > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + my_team), "r"(32 * team) : "memory");
+      else __syncwarp();
       const float(*sum)[16][kCols] = &s_part[parity][my_team * team];
       for (int i = in_team * 32 + lane; i < (FC1 ? 64 : 128); i += 32 * team) {
         const int cc = FC1 ? i / 8 : i / 16, n = FC1 ? i % 8 : i % 16;
@@ -471,20 +476,21 @@ __global__ void __launch_bounds__(kThreads, 3) few_kernel(FewParams q) {
 // Warps that share a tile along K: as many as leave less than an eighth of them idle at the last chunk.
 int team_of(int64_t K) {
   const int chunks = (int)((K + kChunk - 1) / kChunk);
-  for (int w = kWarps; w > 1; w /= 2)
+  for (int w = kMaxTeam; w > 1; w /= 2)
     if ((chunks + w - 1) / w * w * 8 <= chunks * 9) return w;
   return 1;
 }
 
 template <int WK, int AK, bool FC1>
-cudaError_t launch(const FewParams& q, int64_t units, cudaStream_t st) {
-  const int bytes = few_smem(q.K, q.cols, q.E);
+cudaError_t launch(FewParams q, int64_t units, cudaStream_t st) {
+  constexpr int kMost = 227 * 1024 - 26 * 1024;  // less what the kernel declares itself
+  q.cols = q.T < kCols ? q.T : kCols;
+  while (q.cols > 1 && few_smem(q.K, q.cols, q.E, 2) > kMost) q.cols /= 2;  // 4 for rows of 8192
+  q.depth = few_smem(q.K, q.cols, q.E, 3) <= kMost ? 3 : 2;
+  const int bytes = few_smem(q.K, q.cols, q.E, q.depth);
   const auto kernel = few_kernel<WK, AK, FC1>;
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-  // as many blocks as are resident at once: 227 KB of shared memory, of which each takes 10 KB more than it asks for
-  const int fit = 227 * 1024 / (bytes + 10 * 1024), per_sm = fit < 1 ? 1 : fit > 3 ? 3 : fit;
-  const int64_t slots = (int64_t)per_sm * num_sms();
-  const unsigned blocks = (unsigned)(units < slots ? units : slots);
+  const unsigned blocks = (unsigned)(units < num_sms() ? units : num_sms());
   if (!FC1) return launch_dependent(kernel, blocks, kThreads, bytes, st, q);
   kernel<<<blocks, kThreads, bytes, st>>>(q);
   return cudaGetLastError();
@@ -535,7 +541,6 @@ cudaError_t launch_moe_few(const qad_moe_shape& s, const FewLayout& L, const voi
   q.k = s.topk;
   q.E = (int)s.E;
   const int ak = quant ? act_kind(s.fmt) : kQNone;
-  q.cols = (int)(s.T < kCols ? s.T : kCols);
   q.d_tiles = (int)(s.d / 16);
   const int64_t pairs = s.T * s.topk;  // no more passes than pairs
 
