@@ -1,52 +1,58 @@
-// The whole expert layer for a few tokens (generation): two launches, each of which reads the weights of the experts
-// that some token names once, fake-quantizes them in registers and multiplies them there.
+// The whole expert layer for a few tokens (generation), in one cooperative launch that reads the weights of the experts
+// that some token names once, fake-quantizes them on their way and multiplies them there.
 //
 //   fc1:  Z1 = A1 . W13_hat^T, H = bf16(silu(gate) * up)             A1 = AQ(x)
 //   fc2:  Y = AQ(H) . W2_hat^T, out[t] = bf16(sum_j p[t, j] * Y_j)
 //
 // With so few rows the weights are all there is to move (2 bytes an element and its part of a scale), and each element
-// costs about eight instructions of fake-quantization whatever the number of tokens.  So a warp copies 64 weights of 16
-// rows ahead into its ring in shared memory; a lane quantizes 16 of a row (one quantization block) in registers in
-// the tensor cores' fragment layout, and four m16n8k16 products take them as they lie.  The order of k inside a product
-// does not matter as long as both operands agree, so the tokens' rows (shared memory, up to 8 columns) are read in the
-// same order.  A warp reads only what it copied itself: the ring needs no block barrier.  tcgen05 would want the quantized weights
-// in shared memory: a write and a read of every element for products that are idle most of the time here.
+// costs about nine instructions of fake-quantization whatever the number of tokens: for many experts instructions bound
+// the kernel as much as memory does, for a single token latency does.  A warp copies 64 weights of 16 rows ahead into its
+// ring in shared memory; a lane quantizes 16 of a row (one quantization block) in registers in the tensor cores' fragment
+// layout, and four m16n8k16 products take them as they lie.  The order of k inside a product does not matter as long as
+// both operands agree, so the tokens' rows (shared memory, up to 8 columns) are read in the same order.  A warp reads only
+// what it copied itself: the ring needs no block barrier.  tcgen05 would want the quantized weights in shared memory: a
+// write and a read of every element for products that are idle most of the time here.  One block of 24 warps per SM: with
+// 16 in two blocks the quantizers' latencies were not hidden (32 tokens 358 against 302 us).
+//
+// Between fc1 and fc2 the blocks wait for one another; their first weights of fc2 are on their way by then.
 #include "common.cuh"
-#include "dependents.cuh"
 #include "internal.h"
 
 namespace qad {
 namespace {
 
-constexpr int kThreads = 768, kWarps = kThreads / 32;  // one block per SM
-constexpr int kCols = 8;    // tokens of one expert that a pass over its weights serves, at most
-constexpr int kMaxTeam = 8; // warps that share a tile
-constexpr int kChunk = 64;  // elements along K of one step: 16 for each lane of a quad
+constexpr int kThreads = 768, kWarps = kThreads / 32;
+constexpr int kCols = 8;     // tokens of one expert that a pass over its weights serves, at most
+constexpr int kMaxTeam = 8;  // warps that share a tile
+constexpr int kChunk = 64;   // elements along K of one step: 16 for each lane of a quad
 constexpr int kPitch = 2 * kChunk + 16;   // bytes between the rows of a chunk: 16-byte reads of 8 lanes meet no bank twice
 constexpr int kSlot = 16 * kPitch + 256;  // bytes of a warp's chunk: 16 rows of weights, up to 4 scales a row
+constexpr long long kWaitCycles = 4000000000ll;  // after which a block gives up on the others (two seconds)
+
+struct Half {                  // fc1 or fc2
+  const __nv_bfloat16* act;    // x [T, K], or H [T * k, K]
+  const __nv_bfloat16* w;      // [E, rows, K], rows = 2N (fc1) or N (fc2)
+  const float* s;
+  __nv_bfloat16* rows;         // [T * k, N]: H, or Y
+  int K, N, scales;            // scales: per weight row
+  int chunks, team, per_warp;  // of a tile along K; warps that share a tile; chunks for each of them
+  int tiles;                   // of an expert: fc1 8 gate rows and the 8 up rows that go with them, fc2 16 rows
+  int64_t up, sup;             // from a tile's first 8 rows to the others: weights, scales
+};
 
 struct FewParams {
-  const __nv_bfloat16* act;  // fc1: x [T, K]; fc2: H [T * k, K]
-  const __nv_bfloat16* w;    // [E, rows, K], rows = 2N (fc1) or N (fc2)
-  const float* s;
+  Half fc1, fc2;
   const int32_t* idx;
   const float* p;
-  __nv_bfloat16* rows;  // fc1: H [T * k, N]; fc2: Y [T * k, N]
-  __nv_bfloat16* out;   // fc2: [T, N]
+  __nv_bfloat16* out;
   int32_t* err;
-  uint32_t* arrivals;  // [d / 16]: experts' passes that have written a tile of Y
-  int T, k, E, K, N, scales;  // scales: per row
-  int team, cols, d_tiles;    // team: warps that share a tile; cols: token rows staged at once
-  int depth;                  // chunks of a warp in its ring: the one that is worked on and 1 or 2 on their way
+  uint32_t* arrived;   // blocks that are through with fc1 (0 before)
+  uint32_t* arrivals;  // [d / 16]: passes that have written a tile of Y (0 before)
+  int T, k, E;
+  int cols, depth;     // token rows of a pass; chunks of a warp in its ring: the one worked on and 1 or 2 on their way
 };
 
 __host__ __device__ constexpr int few_stride(int K) { return (K + kChunk - 1) / kChunk * kChunk * 2 + 16; }
-
-struct Route {
-  uint64_t* mask;    // [E]: the tokens that name the expert
-  uint32_t* live;    // [T]: the slots of a token that count
-  uint16_t* first;   // [E + 1]: the expert's first pass (`cols` tokens each)
-};
 
 // Dynamic shared memory: the warps' rings, the staged token rows, the masks and first passes of E experts.
 __host__ __device__ constexpr int few_rows_at(int depth) { return kWarps * depth * kSlot; }
@@ -55,16 +61,88 @@ __host__ __device__ constexpr int few_smem(int K, int cols, int E, int depth) {
   return few_mask_at(K, cols, depth) + 8 * E + 2 * (E + 1) + 6;
 }
 
-// The pairs by expert, in every block for itself: at most 2048 of them.  Returns the passes in all.
-__device__ __forceinline__ int route(const FewParams& q, const Route& r, int* err) {
-  const int tid = threadIdx.x;
-  for (int e = tid; e < q.E; e += kThreads) r.mask[e] = 0;
-  for (int t = tid; t < q.T; t += kThreads) r.live[t] = 0;
+// The pairs by expert, found by every block for itself.  A pass serves up to `cols` tokens of one expert.
+// Up to 32 pairs and a pass for each expert: a pair to a lane, in every warp alike and without a barrier; the passes stand
+// in the order of their experts' first pairs.  Else by masks in shared memory, the passes in the order of the experts.
+struct Route {
+  bool small;
+  int passes;
+  // small: this lane's pair
+  int expert;
+  uint32_t group, leaders, valid;  // the pairs of its expert; the first pair of each expert; the pairs that count
+  // else
+  uint64_t* mask;   // [E]: the tokens that name the expert
+  uint32_t* live;   // [T]: the slots of a token that count
+  uint16_t* first;  // [E + 1]: the expert's first pass
+  int E, k, cols;
+
+  __device__ __forceinline__ uint32_t below() const { return (1u << (threadIdx.x & 31)) - 1; }
+  __device__ __forceinline__ int leader_of(int pass) const {  // its lane
+    const bool mine = (group & below()) == 0 && group && __popc(leaders & below()) == pass;
+    return __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  }
+  // all lanes of a warp together
+  __device__ __forceinline__ int expert_of(int pass) const {
+    if (small) return __shfl_sync(0xffffffffu, expert, leader_of(pass));
+    int e = 0;  // the last expert whose first pass is not behind this one
+    for (int b = 512; b; b >>= 1)
+      if (e + b < E && first[e + b] <= pass) e += b;
+    return e;
+  }
+  // the pair (t * k + j) of lane's column of the pass, or -1: all lanes of a warp together
+  __device__ __forceinline__ int pair_of(int pass, int e, const int32_t* idx) const {
+    const int lane = threadIdx.x & 31;
+    if (small) {
+      uint32_t m = __shfl_sync(0xffffffffu, group, leader_of(pass));
+      for (int i = lane; i > 0 && m; --i) m &= m - 1;
+      return m ? __ffs(m) - 1 : -1;
+    }
+    uint64_t m = mask[e];
+    for (int i = (pass - first[e]) * cols + lane; i > 0 && m; --i) m &= m - 1;
+    int pair = -1;
+    if (m && lane < cols) {
+      const int t = __ffsll((long long)m) - 1;
+      for (int j = 0; j < k; ++j)
+        if ((live[t] >> j & 1) && __ldg(idx + t * k + j) == e) pair = t * k + j;
+    }
+    return pair;
+  }
+  __device__ __forceinline__ uint32_t slots_of(int t) const {
+    return small ? valid >> (t * k) & (k == 32 ? 0xffffffffu : (1u << k) - 1) : live[t];
+  }
+};
+
+__device__ __forceinline__ Route route(const FewParams& q, uint64_t* mask, uint16_t* first, uint32_t* live, int* err) {
+  const int tid = threadIdx.x, lane = tid & 31, pairs = q.T * q.k;
+  Route r;
+  r.mask = mask;
+  r.live = live;
+  r.first = first;
+  r.E = q.E;
+  r.k = q.k;
+  r.cols = q.cols;
+  r.small = pairs <= 32 && q.T <= q.cols;
+  if (r.small) {
+    const int e = lane < pairs ? __ldg(q.idx + lane) : -1;
+    const bool in = e >= 0 && e < q.E;
+    const uint32_t same = __match_any_sync(0xffffffffu, in ? e : -1 - lane);
+    const uint32_t earlier = r.below() & ~((1u << (lane < pairs ? lane / q.k * q.k : 0)) - 1);  // slots of this token
+    const bool again = in && (same & earlier);
+    r.valid = __ballot_sync(0xffffffffu, in && !again);
+    r.expert = e;
+    r.group = in && !again ? same & r.valid : 0;
+    r.leaders = __ballot_sync(0xffffffffu, r.group && !(r.group & r.below()));
+    r.passes = __popc(r.leaders);
+    *err = (__any_sync(0xffffffffu, lane < pairs && !in) ? QAD_DEV_BAD_INDEX : 0) |
+           (__any_sync(0xffffffffu, again) ? QAD_DEV_DUP_INDEX : 0);
+    return r;
+  }
+  for (int e = tid; e < q.E; e += kThreads) mask[e] = 0;
+  for (int t = tid; t < q.T; t += kThreads) live[t] = 0;
   __syncthreads();
   int bad = 0;
-  for (int i = tid; i < q.T * q.k; i += kThreads) {
-    const int t = i / q.k, j = i % q.k;
-    const int e = __ldg(q.idx + i);
+  for (int i = tid; i < pairs; i += kThreads) {
+    const int t = i / q.k, j = i % q.k, e = __ldg(q.idx + i);
     if (e < 0 || e >= q.E) {
       bad |= QAD_DEV_BAD_INDEX;
       continue;
@@ -75,15 +153,15 @@ __device__ __forceinline__ int route(const FewParams& q, const Route& r, int* er
       bad |= QAD_DEV_DUP_INDEX;
       continue;
     }
-    atomicOr(reinterpret_cast<unsigned long long*>(r.mask + e), 1ull << t);
-    atomicOr(r.live + t, 1u << j);
+    atomicOr(reinterpret_cast<unsigned long long*>(mask + e), 1ull << t);
+    atomicOr(live + t, 1u << j);
   }
   *err = (__syncthreads_or(bad & QAD_DEV_BAD_INDEX) ? QAD_DEV_BAD_INDEX : 0) |
          (__syncthreads_or(bad & QAD_DEV_DUP_INDEX) ? QAD_DEV_DUP_INDEX : 0);
   if (tid < 32) {
     const int per = (q.E + 31) / 32, lo = min(q.E, tid * per), hi = min(q.E, lo + per);
     int n = 0;
-    for (int e = lo; e < hi; ++e) n += (__popcll(r.mask[e]) + q.cols - 1) / q.cols;
+    for (int e = lo; e < hi; ++e) n += (__popcll(mask[e]) + q.cols - 1) / q.cols;
     int at = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -92,13 +170,14 @@ __device__ __forceinline__ int route(const FewParams& q, const Route& r, int* er
     }
     at -= n;
     for (int e = lo; e < hi; ++e) {
-      r.first[e] = (uint16_t)at;
-      at += (__popcll(r.mask[e]) + q.cols - 1) / q.cols;
+      first[e] = (uint16_t)at;
+      at += (__popcll(mask[e]) + q.cols - 1) / q.cols;
     }
-    if (tid == 31) r.first[q.E] = (uint16_t)at;
+    if (tid == 31) first[q.E] = (uint16_t)at;
   }
   __syncthreads();
-  return r.first[q.E];
+  r.passes = first[q.E];
+  return r;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -211,7 +290,7 @@ __device__ __forceinline__ Block16 quantize16(uint32_t* place, float s) {
 }
 
 // Token rows through their quantizer into shared memory, zeros behind K; `share` warps work on a row.  The scale of a
-// whole row needs a barrier in between (top: zeros before).
+// whole row needs a barrier in between (top: zeros before).  Read from L2: other blocks have written the rows of fc2.
 template <int AK>
 __device__ __forceinline__ void stage_rows(const __nv_bfloat16* act, const int* src, uint32_t* top, uint8_t* rows, int K,
                                            int share) {
@@ -227,8 +306,8 @@ __device__ __forceinline__ void stage_rows(const __nv_bfloat16* act, const int* 
     if (has)
       for (int b = first; b < nblk; b += step) {
         float f[16];
-        unpack8(in[2 * b], f);
-        unpack8(in[2 * b + 1], f + 8);
+        unpack8(__ldcg(in + 2 * b), f);
+        unpack8(__ldcg(in + 2 * b + 1), f + 8);
 #pragma unroll
         for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
       }
@@ -245,8 +324,8 @@ __device__ __forceinline__ void stage_rows(const __nv_bfloat16* act, const int* 
   for (int b = first; b < padded; b += step) {
     uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
     if (b < nblk) {
-      u0 = in[2 * b];
-      u1 = in[2 * b + 1];
+      u0 = __ldcg(in + 2 * b);
+      u1 = __ldcg(in + 2 * b + 1);
       if constexpr (AK != kQNone) {
         float f[16];
         unpack8(u0, f);
@@ -270,175 +349,167 @@ __device__ __forceinline__ void stage_rows(const __nv_bfloat16* act, const int* 
   }
 }
 
-// Tiles of 16 weight rows: fc1 8 gate rows and the 8 up rows that go with them, fc2 16 output rows.  A block takes a
-// consecutive share of all (pass, tile) pairs, passes outermost, so that it stages few passes' tokens; its teams of warps
-// take the tiles of a pass in turn, and the warps of a team the chunks of a tile along K.
-template <int WK, int AK, bool FC1>
-__global__ void __launch_bounds__(kThreads, 1) few_kernel(FewParams q) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t s_live[64];
-  __shared__ float s_part[2][kWarps][16][kCols];
-  __shared__ int s_row[kCols], s_src[kCols];
-  __shared__ uint32_t s_top[kCols];
-  uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + few_mask_at(q.K, q.cols, q.depth));
-  uint16_t* s_first = reinterpret_cast<uint16_t*>(s_mask + q.E);
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, t4 = lane & 3;
-  const int stride = few_stride(q.K), chunks = (q.K + kChunk - 1) / kChunk;
-  const int team = q.team, my_team = warp / team, in_team = warp % team, teams = kWarps / team;
-  const int tiles = FC1 ? q.N / 8 : q.N / 16;
-  if (FC1) let_next_kernel_start();
-  int err;
-  const int passes = route(q, {s_mask, s_live, s_first}, &err);
-  if (FC1 && blockIdx.x == 0) {
-    if (tid == 0) *q.err = err;
-    for (int i = tid; i < q.d_tiles; i += kThreads) q.arrivals[i] = 0;
+// A block takes a consecutive share [lo, hi) of all (pass, tile) pairs, passes outermost, so that it stages few passes'
+// tokens; its teams of warps take the tiles of a pass in turn, and the warps of a team the chunks of a tile along K.
+struct Share {
+  int lo, hi;
+  __device__ __forceinline__ Share(int passes, int tiles) {
+    const int64_t total = (int64_t)passes * tiles;
+    lo = (int)(total * blockIdx.x / gridDim.x);
+    hi = (int)(total * (blockIdx.x + 1) / gridDim.x);
   }
-  if (!FC1 && passes == 0) {  // every pair was dropped
-    wait_for_kernel_before();
-    for (int i = blockIdx.x * kThreads + tid; i < q.T * q.N / 8; i += gridDim.x * kThreads)
-      reinterpret_cast<uint4*>(q.out)[i] = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const int64_t total = (int64_t)passes * tiles;
-  const int lo = (int)(total * blockIdx.x / gridDim.x), hi = (int)(total * (blockIdx.x + 1) / gridDim.x);
-  const int per_warp = (chunks + team - 1) / team;
-  auto expert_of = [&](int pass) {  // the last expert whose first pass is not behind this one
-    int e = 0;
-    for (int b = 512; b; b >>= 1)
-      if (e + b < q.E && s_first[e + b] <= pass) e += b;
-    return e;
-  };
+};
 
-  // the chunks of this warp's tiles, in order, on their way into its ring
-  // a copy of the warp takes 4 rows of 128 bytes: lane / 8 the row, lane % 8 its 16 bytes
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + warp * q.depth * kSlot);
-  const int piece = lane & 7;
-  const int64_t up = FC1 ? (int64_t)q.N * q.K : 8 * (int64_t)q.K, sup = FC1 ? (int64_t)q.N * q.scales : 8 * (int64_t)q.scales;
-  int ld_tile = 0, ld_last = 0, ld_next = lo, ld_chunk = 0, ld_slot = 0;  // ld_next: where the next pass's tiles begin
-  const __nv_bfloat16 *ld_w = nullptr, *pw = nullptr;
-  const float *ld_s = nullptr, *ps = nullptr;
-  auto open_tile = [&]() {
-    while (ld_tile >= ld_last && ld_next < hi) {
-      const int pass = ld_next / tiles, tile0 = ld_next - pass * tiles, e = expert_of(pass);
-      ld_last = min(tiles, tile0 + hi - ld_next);
-      ld_next += ld_last - tile0;
-      ld_tile = tile0 + my_team;
-      ld_w = q.w + (int64_t)e * (FC1 ? 2 * q.N : q.N) * q.K;
-      ld_s = q.s + (int64_t)e * (FC1 ? 2 * q.N : q.N) * q.scales;
+// The chunks of this warp's tiles, in order, on their way into its ring.
+template <int WK, bool FC1>
+struct Loader {
+  const Half& h;
+  const Route& r;
+  const int hi, depth, my_team, in_team, teams;
+  const uint32_t ring;
+  int tile = 0, last = 0, next, chunk = 0, slot = 0;  // next: where the next pass's tiles begin
+  const __nv_bfloat16 *we = nullptr, *pw = nullptr;
+  const float *se = nullptr, *ps = nullptr;
+
+  __device__ __forceinline__ Loader(const Half& h, const Route& r, Share s, int depth, uint8_t* smem)
+      : h(h), r(r), hi(s.hi), depth(depth), my_team((int)threadIdx.x / 32 / h.team), in_team((int)threadIdx.x / 32 % h.team),
+        teams(kWarps / h.team), ring((uint32_t)__cvta_generic_to_shared(smem + threadIdx.x / 32 * depth * kSlot)),
+        next(s.lo) {
+    open_tile();
+    load();
+    if (depth > 2) load();
+  }
+  __device__ __forceinline__ void open_tile() {
+    const int lane = threadIdx.x & 31;
+    while (tile >= last && next < hi) {
+      const int pass = next / h.tiles, tile0 = next - pass * h.tiles, e = r.expert_of(pass);
+      last = min(h.tiles, tile0 + hi - next);
+      next += last - tile0;
+      tile = tile0 + my_team;
+      we = h.w + (int64_t)e * (FC1 ? 2 * h.N : h.N) * h.K;
+      se = h.s + (int64_t)e * (FC1 ? 2 * h.N : h.N) * h.scales;
     }
-    const int row = ld_tile * (FC1 ? 8 : 16);
-    pw = ld_w + (int64_t)(row + lane / 8) * q.K;
+    const int row = tile * (FC1 ? 8 : 16);
+    // a copy of the warp takes 4 rows of 128 bytes: lane / 8 the row, lane % 8 its 16 bytes
+    pw = we + (int64_t)(row + lane / 8) * h.K;
     // E2M1: lane / 4 the row, lane % 4 its block of the chunk; else lane the row (16 of them)
-    ps = ld_s + (int64_t)(row + (WK == kQE2M1 ? lane / 4 : lane & 7)) * q.scales;
-    if (WK != kQE2M1 && (lane & 8)) ps += sup;
-    ld_chunk = in_team;
-  };
-  open_tile();
-  auto load = [&]() {
-    if (ld_tile < ld_last) {
-      if (ld_chunk < chunks) {
-        const int k0 = ld_chunk * kChunk, bytes = k0 + 8 * piece < q.K ? 16 : 0;  // zeros behind K
+    ps = se + (int64_t)(row + (WK == kQE2M1 ? lane / 4 : lane & 7)) * h.scales;
+    if (WK != kQE2M1 && (lane & 8)) ps += h.sup;
+    chunk = in_team;
+  }
+  __device__ __forceinline__ void load() {
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+    if (tile < last) {
+      if (chunk < h.chunks) {
+        const int k0 = chunk * kChunk, bytes = k0 + 8 * piece < h.K ? 16 : 0;  // zeros behind K
         const __nv_bfloat16* from = pw + (bytes ? k0 + 8 * piece : 0);
-        const uint32_t at = ring + ld_slot * kSlot, to = at + lane / 8 * kPitch + piece * 16;
+        const uint32_t at = ring + slot * kSlot, to = at + lane / 8 * kPitch + piece * 16;
         copy16(to, from, bytes);
-        copy16(to + 4 * kPitch, from + 4 * (int64_t)q.K, bytes);
-        copy16(to + 8 * kPitch, from + up, bytes);
-        copy16(to + 12 * kPitch, from + up + 4 * (int64_t)q.K, bytes);
+        copy16(to + 4 * kPitch, from + 4 * (int64_t)h.K, bytes);
+        copy16(to + 8 * kPitch, from + h.up, bytes);
+        copy16(to + 12 * kPitch, from + h.up + 4 * (int64_t)h.K, bytes);
         if constexpr (WK == kQE2M1) {
-          const int b = k0 / 16 + (lane & 3), in = b < q.scales ? b : 0;
+          const int b = k0 / 16 + (lane & 3), in = b < h.scales ? b : 0;
           copy4(at + 16 * kPitch + lane * 4, ps + in);
-          copy4(at + 16 * kPitch + 128 + lane * 4, ps + in + sup);
+          copy4(at + 16 * kPitch + 128 + lane * 4, ps + in + h.sup);
         } else if constexpr (WK != kQNone) {
           if (lane < 16) copy4(at + 16 * kPitch + lane * 4, ps + (WK == kQInt4 ? k0 / 128 : 0));
         }
       }
-      ld_chunk += team;
-      if (ld_chunk >= per_warp * team) {
-        ld_tile += teams;
+      chunk += h.team;
+      if (chunk >= h.per_warp * h.team) {
+        tile += teams;
         open_tile();
       }
     }
-    ld_slot = ld_slot + 1 == q.depth ? 0 : ld_slot + 1;
+    slot = slot + 1 == depth ? 0 : slot + 1;
     asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  load();
-  if (q.depth > 2) load();
-  if (!FC1) wait_for_kernel_before();
+  }
+};
 
-  int slot = 0, parity = 0;
+struct FewSmem {
+  float part[2][kWarps][16][kCols];
+  uint32_t live[64], top[kCols];
+  int row[kCols], src[kCols];
+};
+
+template <int WK, int AK, bool FC1>
+__device__ __forceinline__ void run_half(const FewParams& q, const Half& h, const Route& r, Share share,
+                                         Loader<WK, FC1>& loader, uint8_t* smem, FewSmem& s) {
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, t4 = lane & 3;
+  const int team = h.team, my_team = loader.my_team, in_team = loader.in_team, teams = loader.teams;
+  const int stride = few_stride(h.K), depth = q.depth;
+  uint8_t* rows = smem + few_rows_at(depth);
   const int col = min(g, q.cols - 1);  // columns that are not staged give results that nobody reads
-  for (int u = lo; u < hi;) {
-    const int pass = u / tiles, tile0 = u % tiles, ntiles = min(hi - u, tiles - tile0), e = expert_of(pass);
+  int slot = 0, parity = 0;
+  for (int u = share.lo; u < share.hi;) {
+    const int pass = u / h.tiles, tile0 = u % h.tiles, ntiles = min(share.hi - u, h.tiles - tile0), e = r.expert_of(pass);
     u += ntiles;
     __syncthreads();  // the tokens of the pass before are no longer read
-    if (tid < kCols) {
-      uint64_t m = s_mask[e];
-      for (int i = (pass - s_first[e]) * q.cols + tid; i > 0 && m; --i) m &= m - 1;
-      int row = -1, src = -1;
-      if (m && tid < q.cols) {
-        const int t = __ffsll((long long)m) - 1;
-        for (int j = 0; j < q.k; ++j)
-          if ((s_live[t] >> j & 1) && __ldg(q.idx + t * q.k + j) == e) row = t * q.k + j;
-        src = FC1 ? t : row;
+    if (warp == 0) {
+      const int pair = r.pair_of(pass, e, q.idx);
+      if (lane < kCols) {
+        s.row[lane] = pair;
+        s.src[lane] = FC1 && pair >= 0 ? pair / q.k : pair;
+        s.top[lane] = 0;
       }
-      s_row[tid] = row;
-      s_src[tid] = src;
-      s_top[tid] = 0;
     }
     __syncthreads();
-    const int staged = min(q.cols, __popcll(s_mask[e]) - (pass - s_first[e]) * q.cols);
-    stage_rows<AK>(q.act, s_src, s_top, smem + few_rows_at(q.depth), q.K, kWarps / staged);
+    int staged = 0;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) staged += s.row[i] >= 0;
+    stage_rows<AK>(h.act, s.src, s.top, rows, h.K, kWarps / staged);
     __syncthreads();
 
     for (int tile = tile0 + my_team; tile < tile0 + ntiles; tile += teams) {
       float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-      for (int c = 0; c < per_warp; ++c) {
-        if (q.depth > 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      for (int c = 0; c < h.per_warp; ++c) {
+        if (depth > 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
         else asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncwarp();  // the other lanes' copies too, and nobody reads the slot that the next load fills
-        load();
+        loader.load();
         const int chunk = c * team + in_team;
-        if (chunk < chunks) {
-          uint8_t* mine = smem + (warp * q.depth + slot) * kSlot;
+        if (chunk < h.chunks) {
+          uint8_t* mine = smem + (warp * depth + slot) * kSlot;
           const float* sv = reinterpret_cast<const float*>(mine + 16 * kPitch) + (WK == kQE2M1 ? lane : g);
           uint32_t* wv = reinterpret_cast<uint32_t*>(mine + g * kPitch + t4 * 32);
-          const bool in = chunk * kChunk + 16 * t4 < q.K;
+          const bool in = chunk * kChunk + 16 * t4 < h.K;
           const Block16 a = quantize16<WK>(wv, in ? sv[0] : 1.0f);
           const Block16 b = quantize16<WK>(wv + 8 * kPitch / 4, in ? sv[WK == kQE2M1 ? 32 : 8] : 1.0f);
-          const uint4* xs = reinterpret_cast<const uint4*>(smem + few_rows_at(q.depth) + col * stride) + chunk * (kChunk / 8) + 2 * t4;
+          const uint4* xs = reinterpret_cast<const uint4*>(rows + col * stride) + chunk * (kChunk / 8) + 2 * t4;
           const uint4 x0 = xs[0], x1 = xs[1];
           mma_bf16(acc, a.v[0], b.v[0], a.v[1], b.v[1], x0.x, x0.y);
           mma_bf16(acc, a.v[2], b.v[2], a.v[3], b.v[3], x0.z, x0.w);
           mma_bf16(acc, a.v[4], b.v[4], a.v[5], b.v[5], x1.x, x1.y);
           mma_bf16(acc, a.v[6], b.v[6], a.v[7], b.v[7], x1.z, x1.w);
         }
-        slot = slot + 1 == q.depth ? 0 : slot + 1;
+        slot = slot + 1 == depth ? 0 : slot + 1;
       }
       // the team's partial sums are joined in warp order
-      float(*part)[kCols] = s_part[parity][warp];
+      float(*part)[kCols] = s.part[parity][warp];
       part[g][2 * t4] = acc[0];
       part[g][2 * t4 + 1] = acc[1];
       part[g + 8][2 * t4] = acc[2];
       part[g + 8][2 * t4 + 1] = acc[3];
       if (team > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + my_team), "r"(32 * team) : "memory");
       else __syncwarp();
-      const float(*sum)[16][kCols] = &s_part[parity][my_team * team];
+      const float(*sum)[16][kCols] = &s.part[parity][my_team * team];
       for (int i = in_team * 32 + lane; i < (FC1 ? 64 : 128); i += 32 * team) {
         const int cc = FC1 ? i / 8 : i / 16, n = FC1 ? i % 8 : i % 16;
-        if (s_row[cc] < 0) continue;
+        if (s.row[cc] < 0) continue;
         if constexpr (FC1) {
           float zg = 0.0f, zu = 0.0f;
           for (int w = 0; w < team; ++w) {
             zg += sum[w][n][cc];
             zu += sum[w][n + 8][cc];
           }
-          q.rows[(int64_t)s_row[cc] * q.N + tile * 8 + n] =
+          h.rows[(int64_t)s.row[cc] * h.N + tile * 8 + n] =
               __float2bfloat16_rn(__fmul_rn(silu_f(round_bf16(zg)), round_bf16(zu)));
         } else {
           float y = 0.0f;
           for (int w = 0; w < team; ++w) y += sum[w][n][cc];
-          q.rows[(int64_t)s_row[cc] * q.N + tile * 16 + n] = __float2bfloat16_rn(y);
+          h.rows[(int64_t)s.row[cc] * h.N + tile * 16 + n] = __float2bfloat16_rn(y);
         }
       }
       parity ^= 1;
@@ -452,60 +523,120 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(FewParams q) {
         uint32_t seen = 0;
         if (lane == 0) seen = atomicAdd(q.arrivals + tile0 + i, 1u);
         seen = __shfl_sync(0xffffffffu, seen, 0);
-        if (seen + 1 != (uint32_t)passes) continue;
+        if (seen + 1 != (uint32_t)r.passes) continue;
         __threadfence();
         for (int o = lane; o < q.T * 8; o += 32) {
           const int t = o / 8, n = n0 + 2 * (o % 8);
-          const uint32_t live = s_live[t];
+          const uint32_t live = r.slots_of(t);
           float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll 8
           for (int j = 0; j < q.k; ++j) {
             if (!(live >> j & 1)) continue;
-            const uint32_t y = __ldcg(reinterpret_cast<const uint32_t*>(q.rows + (int64_t)(t * q.k + j) * q.N + n));
+            const uint32_t y = __ldcg(reinterpret_cast<const uint32_t*>(h.rows + (int64_t)(t * q.k + j) * h.N + n));
             const float pj = __ldg(q.p + t * q.k + j);
             v0 = fmaf(pj, bf16lo(y), v0);
             v1 = fmaf(pj, bf16hi(y), v1);
           }
-          *reinterpret_cast<uint32_t*>(q.out + (int64_t)t * q.N + n) = pack_bf16(v0, v1);
+          *reinterpret_cast<uint32_t*>(q.out + (int64_t)t * h.N + n) = pack_bf16(v0, v1);
         }
       }
     }
   }
 }
 
+// Every block is through with fc1 (they are all resident: a cooperative launch).  False: some did not come.
+__device__ __forceinline__ bool all_arrived(uint32_t* arrived) {
+  __threadfence();
+  __syncthreads();
+  bool there = true;
+  if (threadIdx.x == 0) {
+    atomicAdd(arrived, 1u);
+    const long long t0 = clock64();
+    uint32_t seen;
+    do {
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(arrived) : "memory");
+      there = seen >= gridDim.x;
+    } while (!there && clock64() - t0 < kWaitCycles);
+  }
+  return __syncthreads_and(there);
+}
+
+template <int WK, int AK>
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewParams q) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ FewSmem s;
+  uint64_t* mask = reinterpret_cast<uint64_t*>(smem + few_mask_at(max(q.fc1.K, q.fc2.K), q.cols, q.depth));
+  int err;
+  const Route r = route(q, mask, reinterpret_cast<uint16_t*>(mask + q.E), s.live, &err);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && err) atomicOr(q.err, err);
+  if (r.passes == 0) {  // every pair was dropped
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < q.T * q.fc2.N / 8; i += gridDim.x * kThreads)
+      reinterpret_cast<uint4*>(q.out)[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  {
+    const Share share(r.passes, q.fc1.tiles);
+    Loader<WK, true> loader(q.fc1, r, share, q.depth, smem);
+    run_half<WK, AK, true>(q, q.fc1, r, share, loader, smem, s);
+  }
+  const Share share(r.passes, q.fc2.tiles);
+  Loader<WK, false> loader(q.fc2, r, share, q.depth, smem);
+  if (!all_arrived(q.arrived) && threadIdx.x == 0) atomicOr(q.err, QAD_DEV_TIMEOUT);
+  run_half<WK, AK, false>(q, q.fc2, r, share, loader, smem, s);
+}
+
 // Warps that share a tile along K: as many as leave less than an eighth of them idle at the last chunk.
-int team_of(int64_t K) {
-  const int chunks = (int)((K + kChunk - 1) / kChunk);
+int team_of(int chunks) {
   for (int w = kMaxTeam; w > 1; w /= 2)
     if ((chunks + w - 1) / w * w * 8 <= chunks * 9) return w;
   return 1;
 }
 
-template <int WK, int AK, bool FC1>
-cudaError_t launch(FewParams q, int64_t units, cudaStream_t st) {
-  constexpr int kMost = 227 * 1024 - 26 * 1024;  // less what the kernel declares itself
-  q.cols = q.T < kCols ? q.T : kCols;
-  while (q.cols > 1 && few_smem(q.K, q.cols, q.E, 2) > kMost) q.cols /= 2;  // 4 for rows of 8192
-  q.depth = few_smem(q.K, q.cols, q.E, 3) <= kMost ? 3 : 2;
-  const int bytes = few_smem(q.K, q.cols, q.E, q.depth);
-  const auto kernel = few_kernel<WK, AK, FC1>;
-  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-  const unsigned blocks = (unsigned)(units < num_sms() ? units : num_sms());
-  if (!FC1) return launch_dependent(kernel, blocks, kThreads, bytes, st, q);
-  kernel<<<blocks, kThreads, bytes, st>>>(q);
-  return cudaGetLastError();
+void shape_half(Half* h, int64_t K, int64_t N, int block, bool fc1) {
+  h->K = (int)K;
+  h->N = (int)N;
+  h->scales = block ? h->K / block : 1;
+  h->chunks = (h->K + kChunk - 1) / kChunk;
+  h->team = team_of(h->chunks);
+  h->per_warp = (h->chunks + h->team - 1) / h->team;
+  h->tiles = h->N / (fc1 ? 8 : 16);
+  h->up = (fc1 ? N : 8) * K;
+  h->sup = (fc1 ? N : 8) * h->scales;
 }
 
-template <bool FC1>
-cudaError_t launch_kind(int wk, int ak, const FewParams& q, int64_t units, cudaStream_t st) {
-  if (wk == kQE2M1 && ak == kQE2M1) return launch<kQE2M1, kQE2M1, FC1>(q, units, st);
-  if (wk == kQE2M1 && ak == kQE2M1G) return launch<kQE2M1, kQE2M1G, FC1>(q, units, st);
-  if (wk == kQE2M1) return launch<kQE2M1, kQNone, FC1>(q, units, st);
-  if (wk == kQInt4 && ak == kQE4M3) return launch<kQInt4, kQE4M3, FC1>(q, units, st);
-  if (wk == kQInt4) return launch<kQInt4, kQNone, FC1>(q, units, st);
-  if (wk == kQE4M3) return launch<kQE4M3, kQE4M3, FC1>(q, units, st);
-  if (wk == kQInt8) return launch<kQInt8, kQInt8, FC1>(q, units, st);
-  return launch<kQNone, kQNone, FC1>(q, units, st);
+template <int WK, int AK>
+cudaError_t launch(FewParams q, cudaStream_t st) {
+  constexpr int kMost = 227 * 1024 - (int)sizeof(FewSmem) - 1024;
+  const int K = q.fc1.K > q.fc2.K ? q.fc1.K : q.fc2.K;
+  q.cols = q.T < kCols ? q.T : kCols;
+  while (q.cols > 1 && few_smem(K, q.cols, q.E, 2) > kMost) q.cols /= 2;  // 4 for rows of 8192
+  q.depth = few_smem(K, q.cols, q.E, 3) <= kMost ? 3 : 2;
+  const int bytes = few_smem(K, q.cols, q.E, q.depth);
+  const auto kernel = few_kernel<WK, AK>;
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+  const int64_t units = (int64_t)q.T * q.k * (q.fc1.tiles > q.fc2.tiles ? q.fc1.tiles : q.fc2.tiles);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units < num_sms() ? units : num_sms()), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeCooperative;
+  a[0].val.cooperative = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, q);
+}
+
+cudaError_t launch_kind(int wk, int ak, const FewParams& q, cudaStream_t st) {
+  if (wk == kQE2M1 && ak == kQE2M1) return launch<kQE2M1, kQE2M1>(q, st);
+  if (wk == kQE2M1 && ak == kQE2M1G) return launch<kQE2M1, kQE2M1G>(q, st);
+  if (wk == kQE2M1) return launch<kQE2M1, kQNone>(q, st);
+  if (wk == kQInt4 && ak == kQE4M3) return launch<kQInt4, kQE4M3>(q, st);
+  if (wk == kQInt4) return launch<kQInt4, kQNone>(q, st);
+  if (wk == kQE4M3) return launch<kQE4M3, kQE4M3>(q, st);
+  if (wk == kQInt8) return launch<kQInt8, kQInt8>(q, st);
+  return launch<kQNone, kQNone>(q, st);
 }
 
 }  // namespace
@@ -518,8 +649,8 @@ int few_layout_of(const qad_moe_shape& s, FewLayout* L) {
   if (s.T > QAD_MOE_FEW_MAX_T || s.d > QAD_MOE_FEW_MAX_D || s.F > QAD_MOE_FEW_MAX_D) return QAD_ERR_UNSUPPORTED;
   auto up = [](int64_t v) { return (size_t)((v + 1023) / 1024 * 1024); };
   const int64_t R = s.T * s.topk;
-  L->arrivals = 256;
-  L->h = up(256 + 4 * (s.d / 16));
+  L->counters = 8 + 4 * (size_t)(s.d / 16);
+  L->h = up(L->counters);
   L->y = L->h + up(2 * R * s.F);
   L->total = L->y + up(2 * R * s.d);
   return QAD_OK;
@@ -529,43 +660,31 @@ cudaError_t launch_moe_few(const qad_moe_shape& s, const FewLayout& L, const voi
                            const void* w13, const float* s13, const void* w2, const float* s2, void* out, uint8_t* ws,
                            cudaStream_t st) {
   const bool quant = !(s.flags & QAD_FLAG_NO_QUANT);
-  const int kind = quant ? weight_kind(s.fmt) : kQNone;
-  const int block = kind == kQE2M1 ? 16 : kind == kQInt4 ? 128 : 0;
+  const int wk = quant ? weight_kind(s.fmt) : kQNone, ak = quant ? act_kind(s.fmt) : kQNone;
+  const int block = wk == kQE2M1 ? 16 : wk == kQInt4 ? 128 : 0;
   FewParams q = {};
+  shape_half(&q.fc1, s.d, s.F, block, true);
+  q.fc1.act = static_cast<const __nv_bfloat16*>(x);
+  q.fc1.w = static_cast<const __nv_bfloat16*>(w13);
+  q.fc1.s = s13;
+  q.fc1.rows = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
+  shape_half(&q.fc2, s.F, s.d, block, false);
+  q.fc2.act = q.fc1.rows;
+  q.fc2.w = static_cast<const __nv_bfloat16*>(w2);
+  q.fc2.s = s2;
+  q.fc2.rows = reinterpret_cast<__nv_bfloat16*>(ws + L.y);
   q.idx = idx;
   q.p = p;
   q.out = static_cast<__nv_bfloat16*>(out);
   q.err = reinterpret_cast<int32_t*>(ws);
-  q.arrivals = reinterpret_cast<uint32_t*>(ws + L.arrivals);
+  q.arrived = reinterpret_cast<uint32_t*>(ws) + 1;
+  q.arrivals = reinterpret_cast<uint32_t*>(ws) + 2;
   q.T = (int)s.T;
   q.k = s.topk;
   q.E = (int)s.E;
-  const int ak = quant ? act_kind(s.fmt) : kQNone;
-  q.d_tiles = (int)(s.d / 16);
-  const int64_t pairs = s.T * s.topk;  // no more passes than pairs
-
-  q.act = static_cast<const __nv_bfloat16*>(x);
-  q.w = static_cast<const __nv_bfloat16*>(w13);
-  q.s = s13;
-  q.rows = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
-  q.K = (int)s.d;
-  q.N = (int)s.F;
-  q.scales = block ? q.K / block : 1;
-  q.team = team_of(q.K);
+  if (cudaError_t e = cudaMemsetAsync(ws, 0, L.counters, st)) return e;
   prof_begin(QAD_K_MOE_FEW, st);
-  cudaError_t e = launch_kind<true>(kind, ak, q, pairs * (q.N / 8), st);
-  if (e == cudaSuccess) {
-    q.act = reinterpret_cast<const __nv_bfloat16*>(ws + L.h);
-    q.w = static_cast<const __nv_bfloat16*>(w2);
-    q.s = s2;
-    q.rows = reinterpret_cast<__nv_bfloat16*>(ws + L.y);
-    q.K = (int)s.F;
-    q.N = (int)s.d;
-    q.scales = block ? q.K / block : 1;
-    q.team = team_of(q.K);
-    note_launches(1);
-    e = launch_kind<false>(kind, ak, q, pairs * (q.N / 16), st);
-  }
+  const cudaError_t e = launch_kind(wk, ak, q, st);
   prof_end(QAD_K_MOE_FEW, st);
   return e;
 }

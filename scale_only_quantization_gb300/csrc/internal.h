@@ -160,8 +160,8 @@ cudaError_t launch_distill_topk(const void* h, int64_t ldh, const void* w, int64
                                 cudaStream_t st);
 
 // ---- the layer for a few tokens (few.cu) ----
-struct FewLayout {  // byte offsets of its workspace; the error word comes first
-  size_t arrivals, h, y, total;
+struct FewLayout {  // its workspace: the error word and the counters that a call clears (bytes), then H and Y (offsets)
+  size_t counters, h, y, total;
 };
 int few_layout_of(const qad_moe_shape& s, FewLayout* L);
 cudaError_t launch_moe_few(const qad_moe_shape& s, const FewLayout& L, const void* x, const int32_t* idx, const float* p,
