@@ -38,6 +38,7 @@ struct Half {                  // fc1 or fc2
   int chunks, team, per_warp;  // of a tile along K; warps that share a tile; chunks for each of them
   int tiles;                   // of an expert: fc1 8 gate rows and the 8 up rows that go with them, fc2 16 rows
   int64_t up, sup;             // from a tile's first 8 rows to the others: weights, scales
+  bool ragged;                 // K ends inside a chunk
 };
 
 struct FewParams {
@@ -198,20 +199,19 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
 struct Block16 {
   uint32_t v[8];
 };
+__device__ __forceinline__ Block16 read16(const uint32_t* place) {
+  const uint4 lo = reinterpret_cast<const uint4*>(place)[0], hi = reinterpret_cast<const uint4*>(place)[1];
+  return {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+}
 
 // W_hat of 16 weights that share scale s, the bits of fakequant16_packed (see there for the quotient).  What follows the
 // quotient x = fp32(w / s) takes fewer instructions here:
 //  - E2M1: bf16(fp32(q s)) takes eight magnitudes, which the 3-bit codes of four weights look up by two byte permutations.
 //    Four of them are halves or doubles of bf16(s) and bf16(1.5 s), that is their bits with the exponent moved;
 //  - INT4, INT8: bf16(fp32(q s)) does not fall as q rises, so that clamping q is clamping it, two at a time.
-// Scales and quotients out of range: pair by pair, in the weights' place in shared memory (16-byte aligned).
+// `odd` stays 0 while the scale is in [2^-60, 2^16) and no quotient is inf or NaN; else quantize_pairs has to do it.
 template <int WK>
-__device__ __forceinline__ Block16 quantize16(uint32_t* place, float s) {
-  auto read = [&]() {
-    const uint4 lo = reinterpret_cast<const uint4*>(place)[0], hi = reinterpret_cast<const uint4*>(place)[1];
-    return Block16{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
-  };
-  const Block16 w = read();
+__device__ __forceinline__ Block16 quantize16(const Block16& w, float s, uint32_t* odd) {
   if constexpr (WK == kQNone) {
     return w;
   } else {
@@ -277,16 +277,20 @@ __device__ __forceinline__ Block16 quantize16(uint32_t* place, float s) {
       }
     }
     const float2 p = f2unpack(probe);
-    if (__builtin_expect(!(s >= 0x1p-60f && s < 0x1p16f) || !(p.x == 0.0f && p.y == 0.0f), 0)) {
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const float2 c = q_pair<WK>(quotient(bf16lo(place[i]), s), quotient(bf16hi(place[i]), s));
-        place[i] = pack_bf16(__fmul_rn(c.x, s), __fmul_rn(c.y, s));
-      }
-      return read();
-    }
+    *odd |= (__float_as_uint(p.x + p.y) << 1) | (__float_as_uint(s) - 0x21800000u >= 0x47800000u - 0x21800000u);
     return out;
   }
+}
+
+// The same for any scale and weight, pair by pair in the block's place in shared memory.
+template <int WK>
+__device__ __forceinline__ Block16 quantize_pairs(uint32_t* place, float s) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const float2 c = q_pair<WK>(quotient(bf16lo(place[i]), s), quotient(bf16hi(place[i]), s));
+    place[i] = pack_bf16(__fmul_rn(c.x, s), __fmul_rn(c.y, s));
+  }
+  return read16(place);
 }
 
 // Token rows through their quantizer into shared memory, zeros behind K; `share` warps work on a row.  The scale of a
@@ -474,9 +478,16 @@ __device__ __forceinline__ void run_half(const FewParams& q, const Half& h, cons
           uint8_t* mine = smem + (warp * depth + slot) * kSlot;
           const float* sv = reinterpret_cast<const float*>(mine + 16 * kPitch) + (WK == kQE2M1 ? lane : g);
           uint32_t* wv = reinterpret_cast<uint32_t*>(mine + g * kPitch + t4 * 32);
-          const bool in = chunk * kChunk + 16 * t4 < h.K;
-          const Block16 a = quantize16<WK>(wv, in ? sv[0] : 1.0f);
-          const Block16 b = quantize16<WK>(wv + 8 * kPitch / 4, in ? sv[WK == kQE2M1 ? 32 : 8] : 1.0f);
+          float sa = sv[0], sb = sv[WK == kQE2M1 ? 32 : 8];
+          if (h.ragged && chunk * kChunk + 16 * t4 >= h.K) sa = sb = 1.0f;
+          uint32_t odd = 0;
+          Block16 a = quantize16<WK>(read16(wv), sa, &odd), b = quantize16<WK>(read16(wv + 8 * kPitch / 4), sb, &odd);
+          if constexpr (WK != kQNone) {
+            if (__builtin_expect(odd != 0, 0)) {
+              a = quantize_pairs<WK>(wv, sa);
+              b = quantize_pairs<WK>(wv + 8 * kPitch / 4, sb);
+            }
+          }
           const uint4* xs = reinterpret_cast<const uint4*>(rows + col * stride) + chunk * (kChunk / 8) + 2 * t4;
           const uint4 x0 = xs[0], x1 = xs[1];
           mma_bf16(acc, a.v[0], b.v[0], a.v[1], b.v[1], x0.x, x0.y);
@@ -602,6 +613,7 @@ void shape_half(Half* h, int64_t K, int64_t N, int block, bool fc1) {
   h->tiles = h->N / (fc1 ? 8 : 16);
   h->up = (fc1 ? N : 8) * K;
   h->sup = (fc1 ? N : 8) * h->scales;
+  h->ragged = h->K % kChunk != 0;
 }
 
 template <int WK, int AK>
