@@ -387,11 +387,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int p
   const int to = from + len;
   const int steps = (to + St::kStep - 1) / St::kStep;
   const float b2 = q.b * kLog2e;
-  // S = sum of 2^y and U = sum of 2^y y with y = b2 z - R, R = fp32(b2 m): one instruction for two logits.  R is off b2 m
+  // S = sum of 2^y and U = sum of 2^y y with y = b2 z - R, R = fp32(b2 m): one instruction for two logits.  m follows the
+  // largest logit only when that is above `enough` (2^y past 2^8): most steps rescale nothing.  R is off b2 m
   // by `off` (exact), which is taken out when sums join.  A logit below `least` (y <= -200, 2^y = 0) counts as `least`, so
   // that -inf gives 0 * y and not NaN.  `wild`: products of logits of 10^36 and more would leave fp32's range; there
   // y = b2 (z - m), clamped.
-  float m = -INFINITY, off = 0.0f;
+  float m = -INFINITY, enough = -INFINITY, off = 0.0f;
   const float span = 200.0f / b2;
   uint64_t s2 = f2pack(0.0f, 0.0f), u2 = s2, nr = s2;  // S and U of the even and odd logits; -R twice
   const uint64_t bb = f2pack(b2, b2);
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int p
   uint16_t* note = &ts.note[0][tid];
   auto see = [&](St& now) {
     const float top = now.largest();
-    if (top > m) {
+    if (top > enough) {
       const float R = top * b2, low = floor_of<ZT>(__fsub_rd(top, span));
       wild = !(fabsf(fmaf(low, b2, -R)) < 3e38f);
       const float off2 = wild ? 0.0f : fmaf(top, b2, -R);
@@ -415,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int p
         s2 = f2mul(s2, cc);
       }
       m = top;
+      enough = m + 8.0f / b2;
       off = off2;
       nr = f2pack(-R, -R);
       least = St::packed(low);
