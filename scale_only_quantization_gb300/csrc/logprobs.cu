@@ -26,9 +26,12 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 4;                  // 16-byte vectors of a thread per step
-constexpr int kNotes = 40;                // steps whose largest logits are noted before candidates are taken
+constexpr int kNotes = 20;                // steps whose largest logits are noted before candidates are taken
 // candidates of a block: about twice K logits reach the bound
 constexpr int kCapSmall = 1024, kCapLarge = 4096, kSmallK = 256;
+// sort_keys() works on powers of two from 2 * kThreads up to the capacity
+static_assert((kThreads & (kThreads - 1)) == 0 && 2 * kThreads <= kCapSmall && (kCapSmall & (kCapSmall - 1)) == 0 &&
+              (kCapLarge & (kCapLarge - 1)) == 0, "");
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float ex2(float v) {
@@ -125,25 +128,30 @@ struct Step {
       raw[0] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  // the largest; a NaN does not count
-  __device__ __forceinline__ float largest() const {
+  // the largest, and the upper 16 bits of the largest of each half; a NaN does not count (except among NaNs)
+  __device__ __forceinline__ float largest(uint16_t* note0, uint16_t* note1) const {
     if constexpr (sizeof(ZT) == 4) {
-      float top = __uint_as_float(raw[0].x);
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        top = fmaxf(top, fmaxf(__uint_as_float(raw[i].x), __uint_as_float(raw[i].y)));
-        top = fmaxf(top, fmaxf(__uint_as_float(raw[i].z), __uint_as_float(raw[i].w)));
-      }
-      return top;
+      auto most = [](const uint4& a, const uint4& b) {
+        const float x = fmaxf(fmaxf(__uint_as_float(a.x), __uint_as_float(a.y)), fmaxf(__uint_as_float(a.z), __uint_as_float(a.w)));
+        const float y = fmaxf(fmaxf(__uint_as_float(b.x), __uint_as_float(b.y)), fmaxf(__uint_as_float(b.z), __uint_as_float(b.w)));
+        return fmaxf(x, y);
+      };
+      const float t0 = most(raw[0], raw[1]), t1 = most(raw[2], raw[3]);
+      *note0 = (uint16_t)(__float_as_uint(t0) >> 16);
+      *note1 = (uint16_t)(__float_as_uint(t1) >> 16);
+      return fmaxf(t0, t1);
     } else {
-      auto pair = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); };
-      __nv_bfloat162 top = pair(raw[0].x);
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        top = __hmax2(top, __hmax2(pair(raw[i].x), pair(raw[i].y)));
-        top = __hmax2(top, __hmax2(pair(raw[i].z), pair(raw[i].w)));
-      }
-      return fmaxf(__low2float(top), __high2float(top));
+      auto most = [](const uint4& a, const uint4& b) {
+        auto pair = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); };
+        const __nv_bfloat162 x = __hmax2(__hmax2(pair(a.x), pair(a.y)), __hmax2(pair(a.z), pair(a.w)));
+        const __nv_bfloat162 y = __hmax2(__hmax2(pair(b.x), pair(b.y)), __hmax2(pair(b.z), pair(b.w)));
+        const __nv_bfloat162 m = __hmax2(x, y), r = __hmax2(m, __lowhigh2highlow(m));
+        return *reinterpret_cast<const uint32_t*>(&r);
+      };
+      const uint32_t t0 = most(raw[0], raw[1]), t1 = most(raw[2], raw[3]);
+      *note0 = (uint16_t)t0;
+      *note1 = (uint16_t)t1;
+      return fmaxf(bf16lo(t0), bf16lo(t1));
     }
   }
   // a lower bound of the logits as raise() takes it
@@ -221,19 +229,20 @@ __device__ __forceinline__ void sort_keys(uint64_t* s_key, int n2) {
 }
 
 // Orders the n candidates and keeps the K best; returns how many are left.  Up to kThreads of them each thread counts the
-// keys above its own (all differ); more are sorted.
+// keys above one (all differ), two threads a key if there are half as many; more are sorted.
 __device__ __forceinline__ int keep_best(uint64_t* s_key, int n, int K) {
   __syncthreads();
   if (n <= kThreads) {
-    const int i = threadIdx.x;
+    const int share = n <= kThreads / 2 ? 2 : 1, i = threadIdx.x / share;
     const uint64_t mine = i < n ? s_key[i] : 0;
     int rank = 0;
-    if ((i & ~31) < n) {
+    if ((threadIdx.x & ~31) < n * share) {
 #pragma unroll 8
-      for (int j = 0; j < n; ++j) rank += s_key[j] > mine;
+      for (int j = threadIdx.x % share; j < n; j += share) rank += s_key[j] > mine;
+      if (share > 1) rank += __shfl_xor_sync(0xffffffffu, rank, 1);
     }
     __syncthreads();
-    if (i < n) s_key[rank] = mine;
+    if (i < n && threadIdx.x % share == 0) s_key[rank] = mine;
     __syncthreads();
   } else {
     int n2 = 2 * kThreads;
@@ -257,7 +266,12 @@ __device__ __forceinline__ uint32_t warp_qth(uint32_t v, int q, int lane) {
   return __shfl_sync(0xffffffffu, v, q - 1);
 }
 
-// The r-th largest of a thread's n notes (0 if there are fewer).
+// The upper 16 bits of order_of() from those of the number, or one less for -0, which no bound of take() tells apart.
+__device__ __forceinline__ uint32_t note_order(uint32_t b) {
+  return (b & 0x7fffu) > 0x7f80u ? 0u : (b & 0x8000u) ? b ^ 0xffffu : b | 0x8000u;
+}
+
+// The r-th largest of a thread's n notes, by their orders (0 if there are fewer).
 template <int R>
 __device__ __forceinline__ uint32_t rth_note(const uint16_t* notes, int n, int r) {
   uint32_t best[R];
@@ -265,7 +279,7 @@ __device__ __forceinline__ uint32_t rth_note(const uint16_t* notes, int n, int r
   for (int i = 0; i < R; ++i) best[i] = 0;
 #pragma unroll 8
   for (int s = 0; s < n; ++s) {
-    uint32_t v = notes[s * kThreads];
+    uint32_t v = note_order(notes[s * kThreads]);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const uint32_t hi = max(best[i], v);
@@ -280,7 +294,7 @@ __device__ __forceinline__ uint32_t rth_note(const uint16_t* notes, int n, int r
 }
 
 struct TopSmem {  // in front of `cap` keys (8 bytes) and groups (2 bytes) in dynamic shared memory
-  uint16_t note[kNotes][kThreads];
+  uint16_t note[2 * kNotes][kThreads];  // of each half of a thread's logits of a step: the largest, its upper 16 bits
   uint32_t bound[kWarps];
   int n, groups, pad[2];
 };
@@ -291,7 +305,7 @@ struct Top {
   using St = Step<ZT>;
   TopSmem& s;
   uint64_t* key;    // the candidates
-  uint16_t* group;  // groups of 16 to read again: step * kThreads + thread
+  uint16_t* group;  // groups (halves) to read again: number * kThreads + thread
   const ZT* base;
   int lo, from, to, K, cap;
   uint64_t above;  // a candidate's key is larger: K better ones are listed
@@ -307,35 +321,38 @@ struct Top {
     if (threadIdx.x == 0) s.n = n;
     __syncthreads();
   }
-  // the candidates of the steps [first, first + steps) behind the `held` listed ones
-  __device__ __forceinline__ void take(int first, int steps, int held) {
+  // the candidates of the steps [first, first + steps) behind the `held` listed ones; peak: this thread's largest logit
+  __device__ __forceinline__ void take(int first, int steps, int held, float peak) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     // warps all of whose lanes have logits; q lanes of each of them, r notes of a lane
     const int full = min(kWarps, max(1, to / (32 * St::kVec)));
     const int quota = (K + full - 1) / full, r = (quota + 15) / 16, q = (quota + r - 1) / r;
     const uint16_t* mine = &s.note[0][tid];
     uint32_t w = 0;
-    if (r == 1) w = warp_qth(rth_note<1>(mine, steps, 1), q, lane);
-    else if (r <= 8) w = warp_qth(rth_note<8>(mine, steps, r), q, lane);
+    if (r == 1) w = warp_qth(order_of(peak) >> 16, q, lane);
+    else if (r <= 8) w = warp_qth(rth_note<8>(mine, 2 * steps, r), q, lane);
     if (lane == 0) s.bound[warp] = w;
     if (tid == 0) s.groups = 0;
     __syncthreads();
     w = __reduce_min_sync(0xffffffffu, s.bound[min(lane, full - 1)]);
     const uint32_t bound = max(w << 16, (uint32_t)(above >> 32));
+    const uint32_t least = bound >> 16 == 0x8000u ? 0x7fffu : bound >> 16;
+    if (order_of(peak) >> 16 >= least) {
 #pragma unroll 8
-    for (int i = 0; i < steps; ++i) {
-      if (mine[i * kThreads] >= bound >> 16) {
-        const int slot = atomicAdd(&s.groups, 1);
-        if (slot < cap) group[slot] = (uint16_t)(i * kThreads + tid);
+      for (int i = 0; i < 2 * steps; ++i) {
+        if (note_order(mine[i * kThreads]) >= least) {
+          const int slot = atomicAdd(&s.groups, 1);
+          if (slot < cap) group[slot] = (uint16_t)(i * kThreads + tid);
+        }
       }
     }
     __syncthreads();
     const int groups = s.groups;
     if (groups <= cap) {
       const float bound_f = bound <= 0x007fffffu ? -INFINITY : value_of(bound);
-      for (int i = tid; i < groups * kVecs; i += kThreads) {
-        const int g = group[i / kVecs];
-        const int at = St::place(first + g / kThreads, i % kVecs, g % kThreads);
+      for (int i = tid; i < 2 * groups; i += kThreads) {  // a vector to a thread, a group has two
+        const int g = group[i / 2], half = g / kThreads;
+        const int at = St::place(first + half / 2, half % 2 * 2 + i % 2, g % kThreads);
         float f[St::kVec];
         St::vector(base, at, to, f);
 #pragma unroll
@@ -370,56 +387,54 @@ struct Top {
   }
 };
 
-template <typename ZT, bool TOP, bool ENT>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int parts) {
-  using St = Step<ZT>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float s_m[kWarps], s_s[kWarps], s_u[kWarps];
-  __shared__ float s_sum[3];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-  const int64_t row = blockIdx.x / parts;
-  const int part = (int)(blockIdx.x % parts);
-  const ZT* zrow = static_cast<const ZT*>(q.z) + row * q.ldz;
-  const int share = ((q.V + parts - 1) / parts + 63) / 64 * 64;
-  const int lo = min(q.V, part * share), len = min(q.V - lo, share);
-  const int from = (int)((reinterpret_cast<uintptr_t>(zrow + lo) & 15u) / sizeof(ZT));
-  const ZT* base = zrow + lo - from;
-  const int to = from + len;
-  const int steps = (to + St::kStep - 1) / St::kStep;
-  const float b2 = q.b * kLog2e;
-  // S = sum of 2^y and U = sum of 2^y y with y = b2 z - R, R = fp32(b2 m): one instruction for two logits.  m follows the
-  // largest logit only when that is above `enough` (2^y past 2^8): most steps rescale nothing.  R is off b2 m
-  // by `off` (exact), which is taken out when sums join.  A logit below `least` (y <= -200, 2^y = 0) counts as `least`, so
-  // that -inf gives 0 * y and not NaN.  `wild`: products of logits of 10^36 and more would leave fp32's range; there
-  // y = b2 (z - m), clamped.
-  float m = -INFINITY, enough = -INFINITY, off = 0.0f;
-  const float span = 200.0f / b2;
-  uint64_t s2 = f2pack(0.0f, 0.0f), u2 = s2, nr = s2;  // S and U of the even and odd logits; -R twice
-  const uint64_t bb = f2pack(b2, b2);
-  uint32_t least = St::packed(floor_of<ZT>(-span));
-  bool wild = !(span < 3e38f);
-  TopSmem& ts = *reinterpret_cast<TopSmem*>(smem);
-  uint64_t* keys = reinterpret_cast<uint64_t*>(smem + sizeof(TopSmem));
-  if (TOP && tid == 0) ts.n = 0;
+// What a thread keeps of the logits it has seen.
+struct Seen {
+  float m, off, peak;  // the reference; see stream(); the largest logit (TOP)
+  uint64_t s2, u2;     // S and U of the even and odd logits
+};
 
-  uint16_t* note = &ts.note[0][tid];
+// The steps [first, end) of a block's part of a row.  Not inlined: the loop keeps its registers to itself.
+//
+// S = sum of 2^y and U = sum of 2^y y with y = b2 z - R, R = fp32(b2 m): one instruction for two logits.  m follows the
+// largest logit only when that is above `enough` (2^y past 2^8): most steps rescale nothing.  R is off b2 m by `off`
+// (exact), which is taken out when sums join.  A logit below `least` (y <= -200, 2^y = 0) counts as `least`, so that -inf
+// gives 0 * y and not NaN.  `wild`: products of logits of 10^36 and more would leave fp32's range; there y = b2 (z - m),
+// clamped.
+template <typename ZT, bool TOP, bool ENT>
+__device__ __noinline__ Seen stream(const ZT* base, int first, int end, int from, int to, uint16_t* note, float b2,
+                                    Seen seen) {
+  using St = Step<ZT>;
+  float m = seen.m, off = seen.off, peak = seen.peak;
+  uint64_t s2 = seen.s2, u2 = seen.u2;
+  const float span = 200.0f / b2;
+  const uint64_t bb = f2pack(b2, b2);
+  float enough;
+  uint64_t nr;
+  uint32_t least;
+  bool wild;
+  auto refer = [&]() {  // by m: R and what goes with it; returns `off`
+    const float ref = m == -INFINITY ? 0.0f : m, R = ref * b2, low = floor_of<ZT>(__fsub_rd(ref, span));
+    wild = !(fabsf(fmaf(low, b2, -R)) < 3e38f);
+    enough = m + 8.0f / b2;
+    nr = f2pack(-R, -R);
+    least = St::packed(low);
+    return wild ? 0.0f : fmaf(ref, b2, -R);
+  };
+  refer();
   auto see = [&](St& now) {
-    const float top = now.largest();
+    uint16_t note0, note1;
+    const float top = now.largest(&note0, &note1);
     if (top > enough) {
-      const float R = top * b2, low = floor_of<ZT>(__fsub_rd(top, span));
-      wild = !(fabsf(fmaf(low, b2, -R)) < 3e38f);
-      const float off2 = wild ? 0.0f : fmaf(top, b2, -R);
-      if (m > -INFINITY) {
-        const float d = (m - top) * b2 - off + off2, c = ex2(d);
+      const float old = m;
+      m = top;
+      const float off2 = refer();
+      if (old > -INFINITY) {
+        const float d = (old - top) * b2 - off + off2, c = ex2(d);
         const uint64_t cc = f2pack(c, c);
         if constexpr (ENT) u2 = c == 0.0f ? 0 : f2mul(cc, f2fma(s2, f2pack(d, d), u2));
         s2 = f2mul(s2, cc);
       }
-      m = top;
-      enough = m + 8.0f / b2;
       off = off2;
-      nr = f2pack(-R, -R);
-      least = St::packed(low);
     }
     if (!wild) {
       now.raise(least);
@@ -443,54 +458,79 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int p
       }
     }
     if constexpr (TOP) {
-      *note = (uint16_t)(order_of(top) >> 16);
-      note += kThreads;
+      peak = fmaxf(peak, top);
+      note[0] = note0;
+      note[kThreads] = note1;
+      note += 2 * kThreads;
     }
   };
-  // candidates are taken every kNotes steps
   const int whole = to / St::kStep;
-  const uint4* ahead = reinterpret_cast<const uint4*>(base) + tid;
-  auto fetch = [&](St& v, int step, int end) {
+  const uint4* ahead = reinterpret_cast<const uint4*>(base) + threadIdx.x;
+  auto fetch = [&](St& v, int step) {
     if (step >= end) return;
     if (step < whole) v.load(ahead + (int64_t)step * (kVecs * kThreads));
     else v.load_last(base, step, to);
   };
+  St even, odd;
+  fetch(even, first);
+  fetch(odd, first + 1);
+  if (first == 0) even.cut_front(from);
+  for (int step = first; step < end; step += 2) {
+    see(even);
+    fetch(even, step + 2);
+    if (step + 1 < end) {
+      see(odd);
+      fetch(odd, step + 3);
+    }
+  }
+  return {m, off, peak, s2, u2};
+}
+
+template <typename ZT, bool TOP, bool ENT>
+__global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprobs_kernel(Logprobs q, int parts) {
+  using St = Step<ZT>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float s_m[kWarps], s_s[kWarps], s_u[kWarps];
+  __shared__ float s_sum[3], s_zt;
+  __shared__ int s_token;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  const int64_t row = blockIdx.x / parts;
+  const int part = (int)(blockIdx.x % parts);
+  const ZT* zrow = static_cast<const ZT*>(q.z) + row * q.ldz;
+  const int share = ((q.V + parts - 1) / parts + 63) / 64 * 64;
+  const int lo = min(q.V, part * share), len = min(q.V - lo, share);
+  const int from = (int)((reinterpret_cast<uintptr_t>(zrow + lo) & 15u) / sizeof(ZT));
+  const ZT* base = zrow + lo - from;
+  const int to = from + len;
+  const int steps = (to + St::kStep - 1) / St::kStep;
+  const float b2 = q.b * kLog2e;
+  if (tid == 0 && part == 0 && q.token) {  // the row's token and its logit, read early
+    s_token = __ldg(q.token + row);
+    if (q.logp && s_token >= 0 && s_token < q.V) s_zt = St::one(zrow, s_token);
+  }
+  TopSmem& ts = *reinterpret_cast<TopSmem*>(smem);
+  uint64_t* keys = reinterpret_cast<uint64_t*>(smem + sizeof(TopSmem));
+  if (TOP && tid == 0) ts.n = 0;
+  // candidates are taken every kNotes steps
+  Seen seen = {-INFINITY, 0.0f, -INFINITY, f2pack(0.0f, 0.0f), f2pack(0.0f, 0.0f)};
   uint64_t above = 0;
   for (int first = 0; first < steps; first += kNotes) {
     const int end = min(steps, first + kNotes);
-    St even, odd;
-    fetch(even, first, end);
-    fetch(odd, first + 1, end);
-    if (first == 0) even.cut_front(from);
-    note = &ts.note[0][tid];
-    for (int step = first; step < end; step += 2) {
-      see(even);
-      fetch(even, step + 2, end);
-      if (step + 1 < end) {
-        see(odd);
-        fetch(odd, step + 3, end);
-      }
-    }
+    seen = stream<ZT, TOP, ENT>(base, first, end, from, to, &ts.note[0][tid], b2, seen);
     if constexpr (TOP) {
       Top<ZT> alt = {ts, keys, reinterpret_cast<uint16_t*>(keys + q.cap), base, lo, from, to, q.K, q.cap, above};
       __syncthreads();
       if (first > 0) alt.cut(ts.n);
-      alt.take(first, end - first, ts.n);
+      alt.take(first, end - first, ts.n, seen.peak);
       above = alt.above;
     }
   }
-  int n = 0;
-  if constexpr (TOP) {
-    __syncthreads();
-    n = keep_best(keys, ts.n, q.K);
-  }
-
-  // the block's sums
+  // the warps' sums; a thread that saw nothing but -inf and NaN has m = -inf, and S = 0 or NaN
   {
-    float S = f2unpack(s2).x + f2unpack(s2).y, U = f2unpack(u2).x + f2unpack(u2).y;
+    const float m = seen.m, off = seen.off;
+    float S = f2unpack(seen.s2).x + f2unpack(seen.s2).y, U = f2unpack(seen.u2).x + f2unpack(seen.u2).y;
     const float wm = warp_max(m);
     const float d = m == -INFINITY ? 0.0f : (m - wm) * b2 - off, c = ex2(d);
-    // a thread that saw nothing but -inf and NaN has m = -inf, and S = 0 or NaN
     if constexpr (ENT) U = c == 0.0f || m == -INFINITY ? 0.0f : c * fmaf(S, d, U);
     S = warp_sum(S * c);
     if constexpr (ENT) U = warp_sum(U);
@@ -501,38 +541,28 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int p
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    float M = s_m[0];
-    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-    float s = 0.0f, u = 0.0f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float d = s_m[w] == -INFINITY ? 0.0f : (s_m[w] - M) * b2, c = ex2(d);
-      s = fmaf(s_s[w], c, s);
-      if (ENT && c > 0.0f) u = fmaf(c, fmaf(s_s[w], d, s_u[w]), u);
-    }
-    s_sum[0] = M;
-    s_sum[1] = s;
-    s_sum[2] = u;
-    if constexpr (TOP) ts.n = n;
-  }
+  int n = 0;
+  if constexpr (TOP) n = keep_best(keys, ts.n, q.K);
+  // sums of the warps or blocks, one to a lane: (M, S, U)
+  auto join = [&](float M, float S, float U) {
+    const float top = warp_max(M), d = M == -INFINITY ? 0.0f : (M - top) * b2, c = ex2(d);
+    s_sum[1] = warp_sum(S * c);
+    if constexpr (ENT) s_sum[2] = warp_sum(c > 0.0f ? c * fmaf(S, d, U) : c * 0.0f);
+    s_sum[0] = top;
+  };
+  static_assert(kWarps <= 32, "");
+  // the last warp joins the sums while the others write the alternatives
+  if (warp == kWarps - 1) join(lane < kWarps ? s_m[lane] : -INFINITY, lane < kWarps ? s_s[lane] : 0.0f, lane < kWarps ? s_u[lane] : 0.0f);
   if (parts > 1) {
+    if constexpr (TOP) {
+      if (tid == 0) ts.n = n;
+    }
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     if (part == 0) {
-      if (tid == 0) {
-        float M = s_sum[0];
-        for (int r = 1; r < parts; ++r) M = fmaxf(M, cluster.map_shared_rank(s_sum, r)[0]);
-        float s = 0.0f, u = 0.0f;
-        for (int r = 0; r < parts; ++r) {
-          const float* o = cluster.map_shared_rank(s_sum, r);
-          const float d = o[0] == -INFINITY ? 0.0f : (o[0] - M) * b2, c = ex2(d);
-          s = fmaf(o[1], c, s);
-          if (ENT && c > 0.0f) u = fmaf(c, fmaf(o[1], d, o[2]), u);
-        }
-        s_m[0] = M;
-        s_s[0] = s;
-        s_u[0] = u;
-      }
+      float v[3] = {-INFINITY, 0.0f, 0.0f};
+      if (warp == kWarps - 1 && lane < parts)
+        for (int i = 0; i < 3; ++i) v[i] = cluster.map_shared_rank(s_sum, lane)[i];
       if constexpr (TOP) {
         for (int r = 1; r < parts; ++r) {
           const int more = *cluster.map_shared_rank(&ts.n, r);
@@ -542,37 +572,23 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Logprobs q, int p
         }
         n = keep_best(keys, n, q.K);
       }
+      __syncwarp();
+      if (warp == kWarps - 1) join(v[0], v[1], v[2]);
     }
     cluster.sync();  // the others' shared memory has been read
     if (part) return;
-    __syncthreads();
-    if (tid == 0) {
-      s_sum[0] = s_m[0];
-      s_sum[1] = s_s[0];
-      s_sum[2] = s_u[0];
-    }
   }
-  if (tid == 0) {
+  if (tid == kThreads - 32) {
     const float M = s_sum[0], s = s_sum[1];
     const bool empty = M == -INFINITY && s == 0.0f;
     const float l2 = log2f(s), ls = kLn2 * l2;
     if (q.lse) q.lse[row] = empty ? -INFINITY : M == -INFINITY ? s + NAN : fmaf(M, q.b, ls);
     if (ENT) q.entropy[row] = empty ? 0.0f : M == -INFINITY ? NAN : fmaxf(kLn2 * (l2 - s_sum[2] / s), 0.0f) + 0.0f * s;
+    const int token = q.token ? s_token : -1;
+    if (token >= q.V && q.err) atomicOr(q.err, QAD_DEV_BAD_INDEX);
     if (q.logp) {
-      const int t = q.token[row];
-      float lp = 0.0f;
-      if (t >= q.V) {
-        if (q.err) atomicOr(q.err, QAD_DEV_BAD_INDEX);
-      } else if (t >= 0) {
-        const ZT* at = zrow + t;
-        float zt;
-        if constexpr (sizeof(ZT) == 4) zt = *reinterpret_cast<const float*>(at);
-        else zt = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
-        lp = empty ? -INFINITY : M == -INFINITY ? NAN : (zt - M) * q.b - ls;
-      }
-      q.logp[row] = lp;
-    } else if (q.token && q.err && q.token[row] >= q.V) {
-      atomicOr(q.err, QAD_DEV_BAD_INDEX);
+      const bool live = token >= 0 && token < q.V;
+      q.logp[row] = !live ? 0.0f : empty ? -INFINITY : M == -INFINITY ? NAN : (s_zt - M) * q.b - ls;
     }
   }
   if constexpr (TOP) {
