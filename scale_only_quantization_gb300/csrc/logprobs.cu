@@ -337,14 +337,25 @@ struct Top {
     w = __reduce_min_sync(0xffffffffu, s.bound[min(lane, full - 1)]);
     const uint32_t bound = max(w << 16, (uint32_t)(above >> 32));
     const uint32_t least = bound >> 16 == 0x8000u ? 0x7fffu : bound >> 16;
-    if (order_of(peak) >> 16 >= least) {
+    {
+      uint64_t which = 0;  // this thread's groups that may reach the bound
+      if (order_of(peak) >> 16 >= least) {
 #pragma unroll 8
-      for (int i = 0; i < 2 * steps; ++i) {
-        if (note_order(mine[i * kThreads]) >= least) {
-          const int slot = atomicAdd(&s.groups, 1);
-          if (slot < cap) group[slot] = (uint16_t)(i * kThreads + tid);
-        }
+        for (int i = 0; i < 2 * steps; ++i) which |= (uint64_t)(note_order(mine[i * kThreads]) >= least) << i;
       }
+      // places for them by one atomic for the warp: waiting for one each took twice as long as all the rest of this
+      int at = __popcll(which);
+      const int own = at;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+      }
+      int start = 0;
+      if (lane == 31 && at) start = atomicAdd(&s.groups, at);
+      at += __shfl_sync(0xffffffffu, start, 31) - own;
+      for (; which; which &= which - 1, ++at)
+        if (at < cap) group[at] = (uint16_t)((__ffsll((long long)which) - 1) * kThreads + tid);
     }
     __syncthreads();
     const int groups = s.groups;
@@ -564,11 +575,19 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprobs_kernel(Logprob
       if (warp == kWarps - 1 && lane < parts)
         for (int i = 0; i < 3; ++i) v[i] = cluster.map_shared_rank(s_sum, lane)[i];
       if constexpr (TOP) {
-        for (int r = 1; r < parts; ++r) {
-          const int more = *cluster.map_shared_rank(&ts.n, r);
+        // a warp to a block's list
+        static_assert(kWarps >= 7, "");
+        const int r = warp + 1, listed = lane < parts ? *cluster.map_shared_rank(&ts.n, lane) : 0;
+        int at = 0;
+        n = 0;
+        for (int i = 0; i < parts; ++i) {
+          if (i == r) at = n;
+          n += __shfl_sync(0xffffffffu, listed, i);
+        }
+        if (r < parts) {
           const uint64_t* theirs = cluster.map_shared_rank(keys, r);
-          for (int i = tid; i < more; i += kThreads) keys[n + i] = theirs[i];
-          n += more;
+          const int more = __shfl_sync(0xffffffffu, listed, r);
+          for (int i = lane; i < more; i += 32) keys[at + i] = theirs[i];
         }
         n = keep_best(keys, n, q.K);
       }
