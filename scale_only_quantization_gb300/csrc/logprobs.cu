@@ -337,25 +337,14 @@ struct Top {
     w = __reduce_min_sync(0xffffffffu, s.bound[min(lane, full - 1)]);
     const uint32_t bound = max(w << 16, (uint32_t)(above >> 32));
     const uint32_t least = bound >> 16 == 0x8000u ? 0x7fffu : bound >> 16;
-    {
-      uint64_t which = 0;  // this thread's groups that may reach the bound
-      if (order_of(peak) >> 16 >= least) {
+    if (order_of(peak) >> 16 >= least) {
 #pragma unroll 8
-        for (int i = 0; i < 2 * steps; ++i) which |= (uint64_t)(note_order(mine[i * kThreads]) >= least) << i;
+      for (int i = 0; i < 2 * steps; ++i) {
+        if (note_order(mine[i * kThreads]) >= least) {
+          const int slot = atomicAdd(&s.groups, 1);
+          if (slot < cap) group[slot] = (uint16_t)(i * kThreads + tid);
+        }
       }
-      // places for them by one atomic for the warp: waiting for one each took twice as long as all the rest of this
-      int at = __popcll(which);
-      const int own = at;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, at, o);
-        if (lane >= o) at += v;
-      }
-      int start = 0;
-      if (lane == 31 && at) start = atomicAdd(&s.groups, at);
-      at += __shfl_sync(0xffffffffu, start, 31) - own;
-      for (; which; which &= which - 1, ++at)
-        if (at < cap) group[at] = (uint16_t)((__ffsll((long long)which) - 1) * kThreads + tid);
     }
     __syncthreads();
     const int groups = s.groups;
