@@ -414,8 +414,8 @@ typedef struct {
 } qad_tensor;
 
 /*
- * norm[0] = sqrt(sum over all n tensors of g^2), n >= 0.  Squares are summed in fp32 over 16 values, and those sums in
- * 64 bits (values whose squares leave fp32's range as well), in a fixed order: the same bits from call to call.
+ * norm[0] = sqrt(sum over all n tensors of g^2), n >= 0.  Squares are summed in fp32 over up to 16 values, and those sums
+ * in 64 bits (values whose squares leave fp32's range as well), in a fixed order: the same bits from call to call.
  *   norm  fp32 [1] (written)      ws  256-byte aligned, ws_bytes >= qad_grad_norm_workspace_bytes()
  */
 size_t qad_grad_norm_workspace_bytes(void);

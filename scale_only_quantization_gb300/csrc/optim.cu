@@ -30,6 +30,9 @@ struct Table {
   int log_chunk;
 };
 constexpr int kSmall = 32, kLarge = 480;
+// The norm of up to 64 chunks of 1024 elements in 32 tensors by one block: a small model's step waits for launches.  (A
+// cluster of 8 blocks took 6.4 us for 50 thousand gradients, its launch and two barriers nearly all of it.)
+constexpr int kFewThreads = 1024, kFewChunks = 64, kLogFew = 10;
 
 struct Chunk {
   int tensor;
@@ -53,7 +56,8 @@ __device__ __forceinline__ Chunk chunk_of(const T& t, int c) {
   return k;
 }
 
-// The squares of N values: in fp32 where none of them leaves its range (the largest in [2^-50, 2^50]), else in 64 bits.
+// The squares of N <= 16 values: in fp32 where none of them leaves its range (the largest in [2^-50, 2^50]), else in 64
+// bits.
 template <int N>
 __device__ __forceinline__ double squares(const float* f) {
   uint32_t top = 0;
@@ -72,63 +76,98 @@ __device__ __forceinline__ double squares(const float* f) {
   return s;
 }
 
+// The block's sum, in its first thread.
+template <int THREADS = kThreads>
 __device__ __forceinline__ double block_sum(double v) {
-  __shared__ double s[kThreads / 32];
+  __shared__ double s[THREADS / 32];
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if ((threadIdx.x & 31) == 0) s[threadIdx.x / 32] = v;
   __syncthreads();
-  v = 0.0;
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < THREADS / 32 ? s[threadIdx.x] : 0.0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) v += s[i];
+    for (int o = THREADS / 64; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
   return v;
+}
+
+// fp32(sqrt(v)), in fp32 where v is in its range (64-bit square roots are slow here): off by one rounding more
+__device__ __forceinline__ float root(double v) {
+  return v > 1e-30 && v < 1e30 ? sqrtf((float)v) : (float)sqrt(v);
+}
+
+// A thread's part of a chunk's sum of squares: `lane` of `width` threads that share it, N values on
+// their way at once.
+template <int N, class T>
+__device__ __forceinline__ double chunk_squares(const T& t, const Chunk& k, int lane, int width) {
+  double sum = 0.0;
+  float f[N];
+  if (t.bf16[k.tensor]) {
+    const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(t.ptr[0][k.tensor]) + k.at;
+    const int whole = k.len / 8;
+    for (int i = lane; i < whole; i += N / 8 * width) {
+      uint4 v[N / 8];
+#pragma unroll
+      for (int j = 0; j < N / 8; ++j)
+        v[j] = i + j * width < whole ? __ldg(reinterpret_cast<const uint4*>(g) + i + j * width) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < N / 8; ++j) unpack8(v[j], f + 8 * j);
+#pragma unroll
+      for (int j = 0; j < N; j += 16) sum += squares<16>(f + j);
+    }
+    for (int i = whole * 8 + lane; i < k.len; i += width) {
+      const float one = __bfloat162float(g[i]);
+      sum += squares<1>(&one);
+    }
+  } else {
+    const float* g = static_cast<const float*>(t.ptr[0][k.tensor]) + k.at;
+    const int whole = k.len / 4;
+    for (int i = lane; i < whole; i += N / 4 * width) {
+      float4 v[N / 4];
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j)
+        v[j] = i + j * width < whole ? __ldg(reinterpret_cast<const float4*>(g) + i + j * width)
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j) {
+        f[4 * j] = v[j].x;
+        f[4 * j + 1] = v[j].y;
+        f[4 * j + 2] = v[j].z;
+        f[4 * j + 3] = v[j].w;
+      }
+#pragma unroll
+      for (int j = 0; j < N; j += 16) sum += squares<16>(f + j);
+    }
+    for (int i = whole * 4 + lane; i < k.len; i += width) sum += squares<1>(g + i);
+  }
+  return sum;
 }
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ Table<1, CAP> t, double* part,
                                                              bool add) {
   double sum = 0.0;
-  for (int c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
-    const Chunk k = chunk_of(t, c);
-    if (t.bf16[k.tensor]) {
-      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(t.ptr[0][k.tensor]) + k.at;
-      const int whole = k.len / 8;
-      for (int i = threadIdx.x; i < whole; i += 2 * kThreads) {
-        float f[16];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(g) + i), f);
-        const bool two = i + kThreads < whole;
-        unpack8(two ? __ldg(reinterpret_cast<const uint4*>(g) + i + kThreads) : make_uint4(0, 0, 0, 0), f + 8);
-        sum += squares<16>(f);
-      }
-      for (int i = whole * 8 + threadIdx.x; i < k.len; i += kThreads) {
-        const float f = __bfloat162float(g[i]);
-        sum += squares<1>(&f);
-      }
-    } else {
-      const float* g = static_cast<const float*>(t.ptr[0][k.tensor]) + k.at;
-      const int whole = k.len / 4;
-      for (int i = threadIdx.x; i < whole; i += 4 * kThreads) {
-        float4 v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[j] = i + j * kThreads < whole ? __ldg(reinterpret_cast<const float4*>(g) + i + j * kThreads)
-                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float f[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
-                             v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
-        sum += squares<16>(f);
-      }
-      for (int i = whole * 4 + threadIdx.x; i < k.len; i += kThreads) sum += squares<1>(g + i);
-    }
-  }
+  for (int c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) sum += chunk_squares<16>(t, chunk_of(t, c), threadIdx.x, kThreads);
   sum = block_sum(sum);
   if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + sum : sum;
+}
+
+// One block, a chunk to a warp.
+__global__ void __launch_bounds__(kFewThreads) grad_norm_few_kernel(const __grid_constant__ Table<1, kSmall> t,
+                                                                    float* norm) {
+  double sum = 0.0;
+  for (int c = threadIdx.x / 32; c < t.first[t.n]; c += kFewThreads / 32)
+    sum += chunk_squares<32>(t, chunk_of(t, c), threadIdx.x & 31, 32);
+  sum = block_sum<kFewThreads>(sum);
+  if (threadIdx.x == 0) norm[0] = root(sum);
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(const double* part, int n, float* norm) {
   double v = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) v += part[i];
   v = block_sum(v);
-  if (threadIdx.x == 0) norm[0] = (float)sqrt(v);
+  if (threadIdx.x == 0) norm[0] = root(v);
 }
 
 // min(1, max_norm / (norm + 1e-6)), and a NaN's NaN
@@ -184,19 +223,28 @@ struct Coef {
   int skip;                    // the norm is not finite
 };
 
+// b^n by squaring
+__device__ __forceinline__ double power(double b, int64_t n) {
+  double v = 1.0;
+  for (; n; n >>= 1, b *= b)
+    if (n & 1) v *= b;
+  return v;
+}
+
+// One warp: lane 1 takes beta2's power beside lane 0's.
 __global__ void adamw_coef_kernel(const float* norm, float max_norm, double beta1, double beta2, int64_t* steps,
                                   Coef* coef) {
   Coef c = {1.0f, 1.0f, 1.0f, 0};
+  const int64_t t = steps[0] + 1;
   if (norm) {
     c.skip = !isfinite(norm[0]);
     c.clip = clip_factor(norm[0], max_norm);
   }
-  if (!c.skip) {
-    const double t = (double)(steps[0] + 1);
-    steps[0] += 1;
-    c.inv_c1 = (float)(1.0 / (1.0 - pow(beta1, t)));
-    c.inv_c2 = (float)(1.0 / (1.0 - pow(beta2, t)));
-  }
+  const float inv = 1.0f / (float)(1.0 - power(threadIdx.x == 1 ? beta2 : beta1, t));
+  c.inv_c1 = __shfl_sync(0xffffffffu, inv, 0);
+  c.inv_c2 = __shfl_sync(0xffffffffu, inv, 1);
+  if (threadIdx.x) return;
+  if (!c.skip) steps[0] = t;
   *coef = c;
 }
 
@@ -332,6 +380,15 @@ cudaError_t launch_grad_norm(const qad_tensor* grads, int64_t n, float* norm, ui
   const qad_tensor* lists[1] = {grads};
   int parts = 0;
   prof_begin(QAD_K_GRAD_NORM, st);
+  int64_t chunks = 0;
+  for (int64_t i = 0; i < n && n <= kSmall; ++i) chunks += (grads[i].numel + (1 << kLogFew) - 1) >> kLogFew;
+  if (n <= kSmall && chunks <= kFewChunks) {
+    Table<1, kSmall> t;
+    fill(&t, lists, 0, 0, n, kLogFew);
+    grad_norm_few_kernel<<<1, kFewThreads, 0, st>>>(t, norm);
+    prof_end(QAD_K_GRAD_NORM, st);
+    return cudaGetLastError();
+  }
   // every launch but the first adds to the partial sums of the first ones' blocks
   cudaError_t e = for_tables<1>(lists, 0, n, [&](const auto& t, int blocks, bool) {
     if (blocks == 0) return cudaSuccess;
@@ -381,7 +438,7 @@ cudaError_t launch_adamw(const qad_tensor* params, const qad_tensor* grads, cons
   a.decay = decay;
   a.floor = floor;
   prof_begin(QAD_K_ADAMW, st);
-  adamw_coef_kernel<<<1, 1, 0, st>>>(norm, max_norm, beta1, beta2, steps, reinterpret_cast<Coef*>(ws + kCoef));
+  adamw_coef_kernel<<<1, 32, 0, st>>>(norm, max_norm, beta1, beta2, steps, reinterpret_cast<Coef*>(ws + kCoef));
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
     e = for_tables<4>(lists, 1, n, [&](const auto& t, int blocks, bool) {
