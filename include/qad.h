@@ -350,10 +350,11 @@ int qad_distill_topk_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t 
  *           scales that qad_nvfp4_deploy_scales makes (per_mat = 2F * d / 16 and d * F / 16): a generating program
  *           makes them once.
  *   ws      256-byte aligned, ws_bytes >= qad_moe_few_workspace_bytes(s); its first word is the device error word
- *           (QAD_DEV_BAD_INDEX, QAD_DEV_DUP_INDEX: that (token, slot) pair is dropped), written by each call.
+ *           (QAD_DEV_BAD_INDEX, QAD_DEV_DUP_INDEX: that (token, slot) pair is dropped; QAD_DEV_TIMEOUT: the blocks did
+ *           not all come within two seconds, out is invalid), written by each call.
  * Supported: T <= QAD_MOE_FEW_MAX_T, d and F at most QAD_MOE_FEW_MAX_D, and what qad_moe_fwd supports; flags 0 or
- * QAD_FLAG_NO_QUANT (others: QAD_ERR_INVALID_ARG).  32-byte aligned weights are read with one 256-bit load per 16, others
- * with two 16-byte loads; the results are the same bits.
+ * QAD_FLAG_NO_QUANT (others: QAD_ERR_INVALID_ARG).  One cooperative launch of a block per SM: it starts when all SMs have
+ * room for it.  Weights are read once for each 8 tokens that name an expert (4 with d or F above about 5100).
  */
 enum { QAD_MOE_FEW_MAX_T = 64, QAD_MOE_FEW_MAX_D = 8192 };
 size_t qad_moe_few_workspace_bytes(const qad_moe_shape* s); /* 0 if the shape is not supported; host-only */

@@ -98,13 +98,14 @@ class QADMoE(torch.nn.Module):
                 d, x.dtype, tuple(x.shape), topk_idx.dtype, tuple(topk_idx.shape), topk_w.dtype, tuple(topk_w.shape)))
         s = shape(T, d, two_f // 2, E, k, self.fmt, 0 if quant else QAD_FLAG_NO_QUANT)
         s13, s2 = self.s13, self.s2
-        if quant and self.fmt == QAD_FMT_NVFP4_E4M3:  # a program that generates much keeps these between updates
-            s13, s2 = torch.empty_like(self.s13), torch.empty_like(self.s2)
-            for a, b in ((self.s13, s13), (self.s2, s2)):
-                qad_nvfp4_deploy_scales(a, b, E, a.numel() // E)
-        ws = torch.empty(max(1, qad_moe_few_workspace_bytes(s)), dtype=torch.uint8, device=x.device)
-        out = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
-        qad_moe_few_fwd(s, _packed(x), _packed(topk_idx), _packed(topk_w), self.w13, s13, self.w2, s2, out, ws)
+        with torch.cuda.device(self.w13.device):
+            if quant and self.fmt == QAD_FMT_NVFP4_E4M3:  # a program that generates much keeps these between updates
+                s13, s2 = torch.empty_like(self.s13), torch.empty_like(self.s2)
+                for a, b in ((self.s13, s13), (self.s2, s2)):
+                    qad_nvfp4_deploy_scales(a, b, E, a.numel() // E)
+            ws = torch.empty(max(1, qad_moe_few_workspace_bytes(s)), dtype=torch.uint8, device=x.device)
+            out = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+            qad_moe_few_fwd(s, _packed(x), _packed(topk_idx), _packed(topk_w), self.w13, s13, self.w2, s2, out, ws)
         return out
 
 
@@ -339,7 +340,9 @@ class QADTokenLogprobsFunction(torch.autograd.Function):
         logp = None if token is None else torch.empty_like(lse)
         top_idx = torch.empty((N, top), dtype=torch.int32, device=z.device) if top else None
         top_logit = torch.empty((N, top), dtype=torch.float32, device=z.device) if top else None
-        qad_token_logprobs(z, kinds[z.dtype], ld, token, 1.0 / tau, logp, lse, entropy, top_idx, top_logit, N, V, top, err)
+        with torch.cuda.device(z.device):
+            qad_token_logprobs(z, kinds[z.dtype], ld, token, 1.0 / tau, logp, lse, entropy, top_idx, top_logit, N, V, top,
+                               err)
         ctx.save_for_backward(z, lse, entropy, *(() if token is None else (token,)))
         ctx.tau, ctx.ld, ctx.kind = tau, ld, kinds[z.dtype]
         ctx.set_materialize_grads(False)
@@ -355,8 +358,9 @@ class QADTokenLogprobsFunction(torch.autograd.Function):
         N, V = z.shape
         dz = torch.empty((N, V), dtype=z.dtype, device=z.device)
         g_logp, g_entropy = (None if g is None else g.to(torch.float32).contiguous() for g in (g_logp, g_entropy))
-        qad_token_logprobs_bwd(z, ctx.kind, ctx.ld, token[0] if token else None, 1.0 / ctx.tau, lse, entropy, g_logp,
-                               g_entropy, dz, V, N, V)
+        with torch.cuda.device(z.device):
+            qad_token_logprobs_bwd(z, ctx.kind, ctx.ld, token[0] if token else None, 1.0 / ctx.tau, lse, entropy, g_logp,
+                                   g_entropy, dz, V, N, V)
         return dz, None, None, None, None
 
 
@@ -383,8 +387,8 @@ class QADTokenLogprobs(torch.nn.Module):
 
 
 class QADAdamW(torch.optim.Optimizer):
-    """AdamW of the quantizer scales with clipping by the norm over all gradients, in three launches for any number of
-    tensors ("MCoreQAD Backend", YAML optim: lr, betas, weight decay, grad_clip).
+    """AdamW of the quantizer scales with clipping by the norm over all gradients, in four launches at most for up to 480
+    tensors of the same settings ("MCoreQAD Backend", YAML optim: lr, betas, weight decay, grad_clip).
 
     Parameters are fp32; groups may set lr, betas, eps, weight_decay and floor, the lower bound that keeps a scale
     positive (-inf: none).  max_norm None: no clipping.  Every parameter needs a gradient (fp32 or bf16) at each step; a
@@ -405,9 +409,9 @@ class QADAdamW(torch.optim.Optimizer):
             key = (*group["betas"], group["eps"], group["weight_decay"], group["floor"])
             sets.setdefault(key, []).extend((p, group) for p in group["params"])
         plan = []
+        dev = next((p.device for group in self.param_groups for p in group["params"]), None)
         for key, members in sets.items():
             ps = [p for p, _ in members]
-            dev = ps[0].device
             for p in ps:
                 if p.dtype != torch.float32 or not p.is_contiguous() or p.device != dev:
                     raise ValueError("parameters are contiguous fp32 tensors of one device")
@@ -450,6 +454,11 @@ class QADAdamW(torch.optim.Optimizer):
             if any(p.grad is None for p, _ in part["members"]):
                 raise ValueError("every parameter needs a gradient")
             grads.append([_packed(p.grad) for p, _ in part["members"]])
+        with torch.cuda.device(self._ws.device if grads else None):
+            self._launch(grads)
+        return loss
+
+    def _launch(self, grads):
         norm = None
         if self.max_norm is not None and grads:
             norm = self.last_norm
@@ -462,4 +471,3 @@ class QADAdamW(torch.optim.Optimizer):
             p, m, v = part["lists"]
             qad_adamw_step(p, gs, m, v, part["rates"], b1, b2, eps, decay, floor, norm,
                            0.0 if norm is None else self.max_norm, part["steps"], self._ws)
-        return loss
