@@ -15,10 +15,10 @@
 // Rows are split over the blocks of a cluster when there are too few to fill the GPU; the cluster's first block joins
 // the others' sums and candidates out of their shared memory.
 //
-// 4096 x 151936 bf16 (1.24 GB): without alternatives 188 us, 6.6 TB/s, bound by memory; with the top 64 283 us, 4.4 TB/s: a
-// row's last 17 of 55 thousand cycles go into its alternatives, most of them latencies, and the blocks that stream meanwhile
-// are bound by the loads they have in flight.  One row of 151936 fp32 logits with 20 alternatives 12.5 us.  The gradient of
-// 4096 x 151936 392 us, 6.3 TB/s.
+// 4096 x 151936 bf16 (1.24 GB): without alternatives 188 us, 6.6 TB/s, bound by memory; with the top 64 283 us, 4.4 TB/s:
+// 19 of a row's 57 thousand cycles (by clocks in an earlier form) go into its alternatives, most of them latencies, and the
+// blocks that stream meanwhile are bound by the loads they have in flight.  One row of 151936 fp32 logits with 20
+// alternatives 12.3 us.  The gradient of 4096 x 151936 392 us, 6.3 TB/s.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
