@@ -393,7 +393,8 @@ class QADAdamW(torch.optim.Optimizer):
     Parameters are fp32; groups may set lr, betas, eps, weight_decay and floor, the lower bound that keeps a scale
     positive (-inf: none).  max_norm None: no clipping.  Every parameter needs a gradient (fp32 or bf16) at each step; a
     step whose norm is not finite changes nothing, the count of steps neither.  last_norm [1] is the norm before
-    clipping.  State: exp_avg, exp_avg_sq and step (an int64 on the device that the parameters of a group share).
+    clipping.  State: exp_avg, exp_avg_sq and step (an int64 on the device that parameters of the same settings and the
+    same number of steps share).
     """
 
     def __init__(self, params, lr=2e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, floor=-math.inf, max_norm=1.0):
@@ -403,14 +404,19 @@ class QADAdamW(torch.optim.Optimizer):
         self._ws = self._plan = None
 
     def _make_plan(self):
-        """Groups of equal settings step together: (settings, parameters, their lists, rates, steps)."""
-        sets = {}
+        """Parameters of equal settings and as many steps behind them go together: (settings, parameters, their lists,
+        rates, steps).  Each part counts in a tensor of its own: two of them with one counter would count twice."""
+        sets, counts, counters = {}, {}, set()
         for group in self.param_groups:
             key = (*group["betas"], group["eps"], group["weight_decay"], group["floor"])
-            sets.setdefault(key, []).extend((p, group) for p in group["params"])
+            for p in group["params"]:
+                step = self.state[p].get("step")
+                if step is not None and id(step) not in counts:
+                    counts[id(step)] = int(step)
+                sets.setdefault((key, 0 if step is None else counts[id(step)]), []).append((p, group))
         plan = []
         dev = next((p.device for group in self.param_groups for p in group["params"]), None)
-        for key, members in sets.items():
+        for (key, _), members in sets.items():
             ps = [p for p, _ in members]
             for p in ps:
                 if p.dtype != torch.float32 or not p.is_contiguous() or p.device != dev:
@@ -420,6 +426,9 @@ class QADAdamW(torch.optim.Optimizer):
                     st["exp_avg"], st["exp_avg_sq"] = torch.zeros_like(p), torch.zeros_like(p)
             steps = next((self.state[p]["step"] for p in ps if "step" in self.state[p]), None)
             steps = torch.zeros(1, dtype=torch.int64, device=dev) if steps is None else steps.to(dev, torch.int64).view(1)
+            if steps.data_ptr() in counters:
+                steps = steps.clone()
+            counters.add(steps.data_ptr())
             for p in ps:
                 self.state[p]["step"] = steps
             lists = [tensor_list(x) for x in ([p.detach() for p in ps], [self.state[p]["exp_avg"] for p in ps],

@@ -270,6 +270,36 @@ def test_optimizer():
 
 
 @pytest.mark.gpu
+def test_optimizer_settings_that_part_and_groups_that_join():
+    """Two groups step together, then one's decay changes, then a third joins: each counts its own steps, as
+    torch.optim.AdamW does."""
+    from scale_only_quantization_gb300.autograd import QADAdamW
+    _build()
+    g = _gen(12)
+    init = [torch.rand(n, generator=g, device="cuda") + 0.5 for n in (100, 33, 257)]
+    ps = [torch.nn.Parameter(t.clone()) for t in init]
+    rs = [torch.nn.Parameter(t.double()) for t in init]
+    make = lambda x: [dict(params=[x[0]], lr=1e-2), dict(params=[x[1]], lr=1e-2)]  # noqa: E731
+    opt = QADAdamW(make(ps), max_norm=None)
+    ref = torch.optim.AdamW(make(rs), betas=(0.9, 0.95), weight_decay=0.0)
+    for k in range(9):
+        if k == 3:
+            for o in (opt, ref):
+                o.param_groups[1]["weight_decay"] = 0.1
+        if k == 6:
+            opt.add_param_group(dict(params=[ps[2]], lr=1e-2))
+            ref.add_param_group(dict(params=[rs[2]], lr=1e-2))
+        for p, r in zip(ps, rs):
+            r.grad = torch.randn(p.shape, generator=g, device="cuda", dtype=torch.float64) * 0.1
+            p.grad = r.grad.float()
+        opt.step()
+        ref.step()
+    assert [int(opt.state[p]["step"]) for p in ps] == [9, 9, 3]
+    for p, r in zip(ps, rs):  # 9 steps, each with errors of a few 2^-24 of the step (1e-2) and of p
+        assert torch.all((p.detach().double() - r.detach()).abs() <= 9 * (4 * U24 * 2 + 64 * U24 * 1e-2))
+
+
+@pytest.mark.gpu
 def test_rollout_teacher_and_step_together():
     """The operators as an on-policy step uses them: the quantized model writes, the unquantized one reads, the scales
     move; every scale gets a finite gradient and stays at or above the floor."""
