@@ -96,6 +96,8 @@ class QADMoE(torch.nn.Module):
                 x.shape != (T, d) or topk_w.shape != (T, k):
             raise ValueError("x bf16 [T, %d], topk_idx int32 [T, k] and topk_w fp32 [T, k], got %s %s, %s %s, %s %s" % (
                 d, x.dtype, tuple(x.shape), topk_idx.dtype, tuple(topk_idx.shape), topk_w.dtype, tuple(topk_w.shape)))
+        if {x.device, topk_idx.device, topk_w.device} != {self.w13.device}:
+            raise ValueError("x, topk_idx and topk_w lie on the weights' device, %s" % self.w13.device)
         s = shape(T, d, two_f // 2, E, k, self.fmt, 0 if quant else QAD_FLAG_NO_QUANT)
         s13, s2 = self.s13, self.s2
         with torch.cuda.device(self.w13.device):
@@ -335,6 +337,8 @@ class QADTokenLogprobsFunction(torch.autograd.Function):
             token = _packed(_tokens(token.reshape(-1), V))
             if token.numel() != N:
                 raise ValueError("one token per row of z")
+            if token.device != z.device:
+                raise ValueError("tokens on %s, logits on %s" % (token.device, z.device))
         ld = z.stride(0) if N > 1 else V
         lse, entropy = (torch.empty(N, dtype=torch.float32, device=z.device) for _ in range(2))
         logp = None if token is None else torch.empty_like(lse)

@@ -286,6 +286,8 @@ def test_module():
             moe.few(inp["x"].float(), inp["topk_idx"], inp["topk_w"])
         with pytest.raises(ValueError):
             moe.few(inp["x"], inp["topk_idx"].long(), inp["topk_w"])
+        with pytest.raises(ValueError):
+            moe.few(inp["x"], inp["topk_idx"].cpu(), inp["topk_w"])
         with pytest.raises(Q.QADError):
             many = inp["x"].repeat(13, 1)
             moe.few(many, inp["topk_idx"].repeat(13, 1), inp["topk_w"].repeat(13, 1))

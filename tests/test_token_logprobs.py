@@ -387,3 +387,11 @@ def test_refusals():
                 dict(a9=None), dict(a9=P + 8), dict(a10=99), dict(a9=P, a10=104), dict(a7=P + 2), dict(a4=-1.0)):
         assert call(put(back, **bad)) == inv, bad
     assert call(put(back, a11=0)) == Q.QAD_OK
+
+
+@pytest.mark.gpu
+def test_tensors_of_another_device_are_refused():
+    from scale_only_quantization_gb300.autograd import QADTokenLogprobs
+    _build()
+    with pytest.raises(ValueError):
+        QADTokenLogprobs()(torch.zeros(2, 64, device="cuda"), torch.zeros(2, dtype=torch.int32))
