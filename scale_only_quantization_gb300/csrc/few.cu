@@ -15,7 +15,7 @@
 // 16 in two blocks the quantizers' latencies were not hidden (32 tokens 358 against 302 us).
 //
 // One nvfp4 token naming 8 of 128 experts of 2048 x 768 (85 MB): 39 us, 5.5 of them clearing and launch; 32 w4a16 tokens naming
-// 111 of them 299 us, 3.6 TB/s; 5 fp8 tokens on 32 experts of 2880 x 2880 163 us.  8 tokens on 64 experts issue 13
+// 111 of them 293 to 299 us, 3.6 TB/s; 5 fp8 tokens on 32 experts of 2880 x 2880 163 to 169 us.  8 tokens on 64 experts issue 13
 // instructions a weight at 2.5 a cycle.
 //
 // Between fc1 and fc2 the blocks wait for one another; their first weights of fc2 are on their way by then.
