@@ -403,8 +403,9 @@ struct Seen {
 // S = sum of 2^y and U = sum of 2^y y with y = b2 z - R, R = fp32(b2 m): one instruction for two logits.  m follows the
 // largest logit only when that is above `enough` (2^y past 2^8): most steps rescale nothing.  R is off b2 m by `off`
 // (exact), which is taken out when sums join.  A logit below `least` (y <= -200, 2^y = 0) counts as `least`, so that -inf
-// gives 0 * y and not NaN.  `wild`: products of logits of 10^36 and more would leave fp32's range; there y = b2 (z - m),
-// clamped.
+// gives 0 * y and not NaN.  `wild`: there y = b2 (z - m), clamped, without R.  It is for |R| from 2^24 on, where `off` (half
+// a unit of R's last place) would pass 1 and then the exponents themselves (a thread that has seen only a mask's -1e10 would
+// add up 2^off), and for logits of 10^36 and more, whose products with b2 would leave fp32's range.
 template <typename ZT, bool TOP, bool ENT>
 __device__ __noinline__ Seen stream(const ZT* base, int first, int end, int from, int to, uint16_t* note, float b2,
                                     Seen seen) {
@@ -419,7 +420,7 @@ __device__ __noinline__ Seen stream(const ZT* base, int first, int end, int from
   bool wild;
   auto refer = [&]() {  // by m: R and what goes with it; returns `off`
     const float ref = m == -INFINITY ? 0.0f : m, R = ref * b2, low = floor_of<ZT>(__fsub_rd(ref, span));
-    wild = !(fabsf(fmaf(low, b2, -R)) < 3e38f);
+    wild = !(fabsf(fmaf(low, b2, -R)) < 3e38f && fabsf(R) < 0x1p24f);
     enough = m + 8.0f / b2;
     nr = f2pack(-R, -R);
     least = St::packed(low);

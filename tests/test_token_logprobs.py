@@ -395,3 +395,40 @@ def test_tensors_of_another_device_are_refused():
     _build()
     with pytest.raises(ValueError):
         QADTokenLogprobs()(torch.zeros(2, 64, device="cuda"), torch.zeros(2, dtype=torch.int32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fill", [-1e5, -1e9, -1e10, -3e10, -1e20, -1e30, -1e35])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tau", [1.0, 0.6, 2.0 ** 20])
+def test_low_finite_fills(tau, dtype, fill):
+    """Masks of finite numbers: most of a row, its front, single logits left, a whole row, two levels of them.  A fill's
+    probability is 0 beside logits of ordinary size (of a size that the temperature leaves ordinary), so that the bounds
+    are those of the live logits; in a row of nothing else log p = -ln V has no part of the fill's size."""
+    _build()
+    V, K = 20011, 4
+    z = (torch.randn((6, V), generator=_gen(21), device="cuda") * 2 * tau).to(dtype)
+    z[0, 40:] = fill
+    z[1, :V - 7] = fill
+    z[2, 1::2] = fill
+    z[3] = fill
+    z[4] = fill
+    z[4, 12345] = tau
+    z[5, :9000] = fill
+    z[5, 9000:18000] = 2 * fill
+    live = z.double() > 0.5 * fill
+    live[3] = True
+    token = torch.tensor([3, V - 2, 10, 77, 12345, 19000], dtype=torch.int32, device="cuda")
+    got, ref = _forward(z, token, K, tau), _reference(z, token, K, tau)
+    if fill < -1e3 * tau:
+        e = (V / 512 + 128) * U24
+        big = (z.double().abs() * live).amax(1) / tau + ref["lse"].abs()
+        assert torch.all((got["lse"] - ref["lse"]).abs() <= e + 4 * U24 * big)
+        assert torch.all((got["entropy"] - ref["entropy"]).abs() <= (2 * e + 4 * U24) * (40 + math.log(V)))
+        big[3] = math.log(V)
+        assert torch.all((got["logp"] - ref["logp"]).abs() <= e + 4 * U24 * big)
+        dz = _backward(z, token, got, torch.ones(6, device="cuda"), torch.ones(6, device="cuda"), tau)
+        rows = [0, 1, 2, 4, 5]  # the uniform row: lse holds nothing smaller than the fill's own rounding
+        assert torch.isfinite(dz[rows].float()).all() and torch.all(dz[rows][~live[rows]] == 0)
+    assert torch.equal(got["idx"], ref["idx"]) and torch.equal(got["top"].double() + 0.0, ref["top"])
+    assert all(torch.isfinite(got[name]).all() for name in ("lse", "entropy", "logp"))
