@@ -51,6 +51,9 @@ __device__ __forceinline__ float floor_nan(float v, float lo) {
   return r;
 }
 
+// b (v - ref), where v - ref may leave fp32's range: halves do not
+__device__ __forceinline__ float over(float v, float ref, float b) { return fmaf(0.5f, v, -0.5f * ref) * (2.0f * b); }
+
 // A number whose order as an unsigned integer is the float's order (-0 as +0); 0 for a NaN, which is below -inf's.
 __device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);
@@ -405,7 +408,8 @@ struct Seen {
 // (exact), which is taken out when sums join.  A logit below `least` (y <= -200, 2^y = 0) counts as `least`, so that -inf
 // gives 0 * y and not NaN.  `wild`: there y = b2 (z - m), clamped, without R.  It is for |R| from 2^24 on, where `off` (half
 // a unit of R's last place) would pass 1 and then the exponents themselves (a thread that has seen only a mask's -1e10 would
-// add up 2^off), and for logits of 10^36 and more, whose products with b2 would leave fp32's range.
+// add up 2^off), and where 200 / b2 or products of logits of 10^36 and more would leave fp32's range.  There m follows every
+// larger logit: 8 / b2 may not be a number either.
 template <typename ZT, bool TOP, bool ENT>
 __device__ __noinline__ Seen stream(const ZT* base, int first, int end, int from, int to, uint16_t* note, float b2,
                                     Seen seen) {
@@ -421,7 +425,7 @@ __device__ __noinline__ Seen stream(const ZT* base, int first, int end, int from
   auto refer = [&]() {  // by m: R and what goes with it; returns `off`
     const float ref = m == -INFINITY ? 0.0f : m, R = ref * b2, low = floor_of<ZT>(__fsub_rd(ref, span));
     wild = !(fabsf(fmaf(low, b2, -R)) < 3e38f && fabsf(R) < 0x1p24f);
-    enough = m + 8.0f / b2;
+    enough = wild ? m : m + 8.0f / b2;
     nr = f2pack(-R, -R);
     least = St::packed(low);
     return wild ? 0.0f : fmaf(ref, b2, -R);
@@ -435,7 +439,7 @@ __device__ __noinline__ Seen stream(const ZT* base, int first, int end, int from
       m = top;
       const float off2 = refer();
       if (old > -INFINITY) {
-        const float d = (old - top) * b2 - off + off2, c = ex2(d);
+        const float d = over(old, top, b2) - off + off2, c = ex2(d);
         const uint64_t cc = f2pack(c, c);
         if constexpr (ENT) u2 = c == 0.0f ? 0 : f2mul(cc, f2fma(s2, f2pack(d, d), u2));
         s2 = f2mul(s2, cc);
@@ -457,7 +461,7 @@ __device__ __noinline__ Seen stream(const ZT* base, int first, int end, int from
 #pragma unroll
       for (int i = 0; i < St::kPer; i += 2) {
         const float2 f = f2unpack(now.pair(i));
-        const float y0 = floor_nan((f.x - ref) * b2, -200.0f), y1 = floor_nan((f.y - ref) * b2, -200.0f);
+        const float y0 = floor_nan(over(f.x, ref, b2), -200.0f), y1 = floor_nan(over(f.y, ref, b2), -200.0f);
         const uint64_t e2 = f2pack(ex2(y0), ex2(y1));
         s2 = f2add(s2, e2);
         if constexpr (ENT) u2 = f2fma(e2, f2pack(y0, y1), u2);
@@ -536,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprobs_kernel(Logprob
     const float m = seen.m, off = seen.off;
     float S = f2unpack(seen.s2).x + f2unpack(seen.s2).y, U = f2unpack(seen.u2).x + f2unpack(seen.u2).y;
     const float wm = warp_max(m);
-    const float d = m == -INFINITY ? 0.0f : (m - wm) * b2 - off, c = ex2(d);
+    const float d = m == -INFINITY ? 0.0f : over(m, wm, b2) - off, c = ex2(d);
     if constexpr (ENT) U = c == 0.0f || m == -INFINITY ? 0.0f : c * fmaf(S, d, U);
     S = warp_sum(S * c);
     if constexpr (ENT) U = warp_sum(U);
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprobs_kernel(Logprob
   if constexpr (TOP) n = keep_best(keys, ts.n, q.K);
   // sums of the warps or blocks, one to a lane: (M, S, U)
   auto join = [&](float M, float S, float U) {
-    const float top = warp_max(M), d = M == -INFINITY ? 0.0f : (M - top) * b2, c = ex2(d);
+    const float top = warp_max(M), d = M == -INFINITY ? 0.0f : over(M, top, b2), c = ex2(d);
     s_sum[1] = warp_sum(S * c);
     if constexpr (ENT) s_sum[2] = warp_sum(c > 0.0f ? c * fmaf(S, d, U) : c * 0.0f);
     s_sum[0] = top;
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprobs_kernel(Logprob
     if (token >= q.V && q.err) atomicOr(q.err, QAD_DEV_BAD_INDEX);
     if (q.logp) {
       const bool live = token >= 0 && token < q.V;
-      q.logp[row] = !live ? 0.0f : empty ? -INFINITY : M == -INFINITY ? NAN : (s_zt - M) * q.b - ls;
+      q.logp[row] = !live ? 0.0f : empty ? -INFINITY : M == -INFINITY ? NAN : over(s_zt, M, q.b) - ls;
     }
   }
   if constexpr (TOP) {

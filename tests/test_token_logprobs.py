@@ -432,3 +432,32 @@ def test_low_finite_fills(tau, dtype, fill):
         assert torch.isfinite(dz[rows].float()).all() and torch.all(dz[rows][~live[rows]] == 0)
     assert torch.equal(got["idx"], ref["idx"]) and torch.equal(got["top"].double() + 0.0, ref["top"])
     assert all(torch.isfinite(got[name]).all() for name in ("lse", "entropy", "logp"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tau", [1e30, 1e37, 1e38, 2e38])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_smallest_inverse_temperatures(tau, dtype):
+    """1 / tau down to fp32's subnormal numbers, logits of up to the largest finite ones: the span of a row can pass what
+    fp32 holds.  b itself is given as fp32, and the reference takes that number; its product with log2(e) is rounded once
+    more, to 2^-149 where it is subnormal, which the exponents |z| <= 3.4e38 multiply."""
+    _build()
+    V = 5003
+    b = float(torch.tensor(1 / tau, dtype=torch.float32))
+    top = torch.finfo(dtype).max
+    z = (torch.rand((4, V), generator=_gen(22), device="cuda", dtype=torch.float64) * 2 - 1)
+    z = torch.stack([z[0] * 5, z[1] * min(tau, 1e38) * 3, z[2] * 3.3e38, z[3] * 3.3e38]).to(dtype)
+    z[3] = torch.sort(z[3].float()).values.to(dtype)  # rising: the reference moves at nearly every step
+    if tau < 1e37:
+        z = z[:2]
+    assert torch.all(z.abs() <= top)
+    N = z.shape[0]
+    token = torch.tensor([0, 17, 2, V - 1], dtype=torch.int32, device="cuda")[:N]
+    got = _forward(z, token, 3, tau)
+    ref = _reference(z, token, 3, 1 / b)
+    e = (V / 512 + 128) * U24
+    big = z.double().abs().amax(1)
+    off = e + 8 * U24 * big * b + 4 * 2.0 ** -149 * big
+    for name in ("lse", "entropy", "logp"):
+        assert torch.all((got[name] - ref[name]).abs() <= (2 * off) * (1 if name != "entropy" else 40 + math.log(V))), name
+    assert torch.equal(got["idx"], ref["idx"])
