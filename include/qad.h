@@ -439,7 +439,8 @@ int qad_grad_clip(const qad_tensor* grads, const qad_tensor* out, int64_t n, con
  *   lr      fp32 [n] on the device: a rate for each tensor (a schedule rewrites it, a captured step reads it again)
  *   floor   lower bound of the parameters (a quantizer's scale must stay positive); -inf: none
  *   norm    fp32 [1] or NULL (c = 1).  A norm that is not finite leaves everything as it was, steps too.
- *   steps   int64 [1] on the device: steps done so far
+ *   steps   int64 [1] on the device: steps done so far, from 0 on (a count below 0 or of 2^63 - 1 leaves everything as
+ *           it was)
  *   ws      256-byte aligned, ws_bytes >= qad_grad_norm_workspace_bytes() (it may be qad_grad_norm's)
  * Requires 0 <= beta < 1, eps >= 0, decay >= 0, floor not NaN, max_norm >= 0.
  */

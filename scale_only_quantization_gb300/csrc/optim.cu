@@ -223,13 +223,13 @@ __global__ void __launch_bounds__(kThreads) grad_clip_kernel(const __grid_consta
 
 struct Coef {
   float clip, inv_c1, inv_c2;  // the clip factor, 1 / (1 - b1^t), 1 / (1 - b2^t)
-  int skip;                    // the norm is not finite
+  int skip;                    // the norm is not finite, or the step count below 0 or at its end
 };
 
-// b^n by squaring
+// b^n by squaring (n <= 0: 1)
 __device__ __forceinline__ double power(double b, int64_t n) {
   double v = 1.0;
-  for (; n; n >>= 1, b *= b)
+  for (; n > 0; n >>= 1, b *= b)
     if (n & 1) v *= b;
   return v;
 }
@@ -238,9 +238,10 @@ __device__ __forceinline__ double power(double b, int64_t n) {
 __global__ void adamw_coef_kernel(const float* norm, float max_norm, double beta1, double beta2, int64_t* steps,
                                   Coef* coef) {
   Coef c = {1.0f, 1.0f, 1.0f, 0};
-  const int64_t t = steps[0] + 1;
+  const int64_t t = (int64_t)((uint64_t)steps[0] + 1);
+  c.skip = t < 1;
   if (norm) {
-    c.skip = !isfinite(norm[0]);
+    c.skip |= !isfinite(norm[0]);
     c.clip = clip_factor(norm[0], max_norm);
   }
   const float inv = 1.0f / (float)(1.0 - power(threadIdx.x == 1 ? beta2 : beta1, t));

@@ -368,3 +368,27 @@ def test_refusals():
     with pytest.raises(ValueError):
         Q.qad_adamw_step(three, three, two, three, None, 0.9, 0.9, 0.0, 0.0, 0.0, None, 0.0, None, None)
     assert ctypes.sizeof(Q.Tensor) == 24
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("steps", [-1, -2, -5, -(1 << 63), (1 << 63) - 1])
+def test_a_step_count_below_zero_or_past_the_last_leaves_everything(steps):
+    _build()
+    s = _state([1000, 7], 13)
+    s["steps"].fill_(steps)
+    before = _copy(s)
+    _step(s, _norm(s["g"]), 1.0)
+    assert int(s["steps"]) == steps
+    for k in ("p", "m", "v"):
+        assert all(torch.equal(a, b) for a, b in zip(s[k], before[k]))
+
+
+@pytest.mark.gpu
+def test_a_large_step_count():
+    """The powers of beta are 0 by then."""
+    _build()
+    s = _state([1000, 7], 14)
+    s["steps"].fill_(10 ** 12)
+    before = _copy(s)
+    _step(s)
+    _check_step(before, s, 1.0)
