@@ -419,12 +419,17 @@ class QADAdamW(torch.optim.Optimizer):
                     counts[id(step)] = int(step)
                 sets.setdefault((key, 0 if step is None else counts[id(step)]), []).append((p, group))
         plan = []
-        dev = next((p.device for group in self.param_groups for p in group["params"]), None)
+        every = [p for group in self.param_groups for p in group["params"]]
+        dev = every[0].device if every else None
+        for p in every:
+            if p.dtype != torch.float32 or not p.is_contiguous() or not p.is_cuda or p.device != dev:
+                raise ValueError("parameters are contiguous fp32 tensors of one CUDA device, got %s on %s" % (p.dtype, p.device))
+            st = self.state[p]
+            if "exp_avg" in st and {st["exp_avg"].device, st["exp_avg_sq"].device} != {dev}:
+                raise ValueError("parameters on %s, their moments on %s: load the state again" % (dev, st["exp_avg"].device))
         for (key, _), members in sets.items():
             ps = [p for p, _ in members]
             for p in ps:
-                if p.dtype != torch.float32 or not p.is_contiguous() or p.device != dev:
-                    raise ValueError("parameters are contiguous fp32 tensors of one device")
                 st = self.state[p]
                 if "exp_avg" not in st:
                     st["exp_avg"], st["exp_avg_sq"] = torch.zeros_like(p), torch.zeros_like(p)
@@ -438,9 +443,9 @@ class QADAdamW(torch.optim.Optimizer):
             lists = [tensor_list(x) for x in ([p.detach() for p in ps], [self.state[p]["exp_avg"] for p in ps],
                                               [self.state[p]["exp_avg_sq"] for p in ps])]
             plan.append(dict(key=key, members=members, lists=lists, steps=steps, lr=None, rates=None))
-        if self._ws is None and plan:
-            self._ws = torch.empty(qad_grad_norm_workspace_bytes(), dtype=torch.uint8, device=plan[0]["steps"].device)
-            self.last_norm = torch.zeros(1, device=self._ws.device)
+        if plan and (self._ws is None or self._ws.device != dev):
+            self._ws = torch.empty(qad_grad_norm_workspace_bytes(), dtype=torch.uint8, device=dev)
+            self.last_norm = torch.zeros(1, device=dev)
         return plan
 
     def load_state_dict(self, state_dict):
@@ -466,6 +471,8 @@ class QADAdamW(torch.optim.Optimizer):
         for part in self._plan:
             if any(p.grad is None for p, _ in part["members"]):
                 raise ValueError("every parameter needs a gradient")
+            if any(p.grad.device != self._ws.device for p, _ in part["members"]):
+                raise ValueError("gradients lie on the parameters' device, %s" % self._ws.device)
             grads.append([_packed(p.grad) for p, _ in part["members"]])
         with torch.cuda.device(self._ws.device if grads else None):
             self._launch(grads)

@@ -392,3 +392,66 @@ def test_a_large_step_count():
     before = _copy(s)
     _step(s)
     _check_step(before, s, 1.0)
+
+
+class _NoLaunches:
+    """The optimizer's launches replaced by records of what they would have been given."""
+
+    def __init__(self, monkeypatch):
+        from scale_only_quantization_gb300 import autograd
+        self.norms, self.steps = [], []
+        monkeypatch.setattr(autograd, "qad_grad_norm", lambda grads, norm, ws: self.norms.append((grads, norm, ws)))
+        monkeypatch.setattr(autograd, "qad_adamw_step", lambda *args: self.steps.append(args))
+
+
+def _filled(ps):
+    for p in ps:
+        p.grad = torch.ones_like(p)
+
+
+def test_optimizer_of_tensors_on_the_host_is_refused(monkeypatch):
+    import contextlib
+    from scale_only_quantization_gb300.autograd import QADAdamW
+    _build()
+    calls = _NoLaunches(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+    ps = [torch.nn.Parameter(torch.ones(3))]
+    opt = QADAdamW(ps)
+    _filled(ps)
+    with pytest.raises(ValueError):
+        opt.step()
+    assert not calls.norms and not calls.steps
+
+
+@pytest.mark.gpu
+def test_optimizer_of_tensors_that_moved_is_refused(monkeypatch):
+    """Parameters, moments or gradients that lie elsewhere since the last step: nothing is launched on them."""
+    from scale_only_quantization_gb300.autograd import QADAdamW
+    _build()
+    for moved in ("parameters", "one parameter", "moments", "gradient"):
+        ps = [torch.nn.Parameter(torch.ones(n, device="cuda")) for n in (5, 6)]
+        opt = QADAdamW(ps)
+        _filled(ps)
+        opt.step()
+        with monkeypatch.context() as m:
+            calls = _NoLaunches(m)
+            if moved == "parameters":
+                for p in ps:
+                    p.data = p.data.cpu()
+                    p.grad = torch.ones_like(p)
+            elif moved == "one parameter":
+                ps[1].data = ps[1].data.cpu()
+                ps[1].grad = torch.ones_like(ps[1])
+            elif moved == "moments":
+                state = opt.state_dict()
+                opt.load_state_dict(state)
+                opt.state[ps[0]]["exp_avg"] = opt.state[ps[0]]["exp_avg"].cpu()
+            else:
+                keep = ps[1].data
+                ps[1].grad = None
+                ps[1].data = keep.cpu()
+                ps[1].grad = torch.ones(6)
+                ps[1].data = keep
+            with pytest.raises(ValueError):
+                opt.step()
+            assert not calls.norms and not calls.steps
