@@ -629,7 +629,8 @@ cudaError_t launch(FewParams q, cudaStream_t st) {
   q.depth = few_smem(K, q.cols, q.E, 3) <= kMost ? 3 : 2;
   const int bytes = few_smem(K, q.cols, q.E, q.depth);
   const auto kernel = few_kernel<WK, AK>;
-  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+  // the same limit at every call: it belongs to the kernel, and another host thread's call may come before this launch
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost)) return e;
   const int64_t units = (int64_t)q.T * q.k * (q.fc1.tiles > q.fc2.tiles ? q.fc1.tiles : q.fc2.tiles);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units < num_sms() ? units : num_sms()), 1, 1);

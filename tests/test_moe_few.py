@@ -323,3 +323,43 @@ def test_refusals():
     assert call(good, Q.shape(1, 256, 128, 4, 2, 0, Q.QAD_FLAG_RECOMPUTE)) == Q.QAD_ERR_INVALID_ARG
     assert L.qad_moe_few_fwd(None, *good) == Q.QAD_ERR_INVALID_ARG
     assert Q.qad_moe_few_workspace_bytes(Q.shape(1, 256, 128, 4, 2, 0)) % 1024 == 0
+
+
+@pytest.mark.gpu
+def test_threads_and_captures_of_two_sizes_of_one_format():
+    """One format's kernel takes 190 KB of shared memory for one token of 2048 and 157 KB for eight: neither call's limit
+    reaches the other's launch, from two host threads or between a capture and its graph."""
+    import threading
+    _build()
+    one, eight = _inputs(1, 2048, 128, 8, 2, 0, seed=31), _inputs(8, 2048, 128, 8, 2, 0, seed=32)
+    want = [_few(one)[0].clone(), _few(eight)[0].clone()]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(inp, ref):
+        try:
+            st = torch.cuda.Stream()
+            out, ws = torch.empty_like(ref), None
+            with torch.cuda.stream(st):
+                for _ in range(3000):
+                    out, ws = _few(inp, out=out, ws=ws)
+            st.synchronize()
+            assert torch.equal(out, ref)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in 3 * list(zip((one, eight), want))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    outs = [torch.zeros_like(w) for w in want]
+    wss = [_few(inp)[1] for inp in (one, eight)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for inp, o, w in zip((one, eight), outs, wss):
+            _few(inp, out=o, ws=w)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
