@@ -398,7 +398,8 @@ class QADAdamW(torch.optim.Optimizer):
     positive (-inf: none).  max_norm None: no clipping.  Every parameter needs a gradient (fp32 or bf16) at each step; a
     step whose norm is not finite changes nothing, the count of steps neither.  last_norm [1] is the norm before
     clipping.  State: exp_avg, exp_avg_sq and step (an int64 on the device that parameters of the same settings and the
-    same number of steps share).
+    same number of steps share).  A step may be captured once one has been taken eagerly; its replays read the rates that
+    write_rates() has written, until other settings change or the parameters' memory does.
     """
 
     def __init__(self, params, lr=2e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, floor=-math.inf, max_norm=1.0):
@@ -410,6 +411,16 @@ class QADAdamW(torch.optim.Optimizer):
     def _make_plan(self):
         """Parameters of equal settings and as many steps behind them go together: (settings, parameters, their lists,
         rates, steps).  Each part counts in a tensor of its own: two of them with one counter would count twice."""
+        every = [p for group in self.param_groups for p in group["params"]]
+        dev = every[0].device if every else None
+        for p in every:
+            if p.dtype != torch.float32 or not p.is_contiguous() or not p.is_cuda or p.device != dev:
+                raise ValueError("parameters are contiguous fp32 tensors of one CUDA device, got %s on %s" % (p.dtype, p.device))
+            st = self.state[p]
+            if "exp_avg" in st and {st["exp_avg"].device, st["exp_avg_sq"].device} != {dev}:
+                raise ValueError("parameters on %s, their moments on %s: load the state again" % (dev, st["exp_avg"].device))
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a first step, or one of changed settings or parameters, is not captured: step once before")
         sets, counts, counters = {}, {}, set()
         for group in self.param_groups:
             key = (*group["betas"], group["eps"], group["weight_decay"], group["floor"])
@@ -419,14 +430,6 @@ class QADAdamW(torch.optim.Optimizer):
                     counts[id(step)] = int(step)
                 sets.setdefault((key, 0 if step is None else counts[id(step)]), []).append((p, group))
         plan = []
-        every = [p for group in self.param_groups for p in group["params"]]
-        dev = every[0].device if every else None
-        for p in every:
-            if p.dtype != torch.float32 or not p.is_contiguous() or not p.is_cuda or p.device != dev:
-                raise ValueError("parameters are contiguous fp32 tensors of one CUDA device, got %s on %s" % (p.dtype, p.device))
-            st = self.state[p]
-            if "exp_avg" in st and {st["exp_avg"].device, st["exp_avg_sq"].device} != {dev}:
-                raise ValueError("parameters on %s, their moments on %s: load the state again" % (dev, st["exp_avg"].device))
         for (key, _), members in sets.items():
             ps = [p for p, _ in members]
             for p in ps:
@@ -442,7 +445,8 @@ class QADAdamW(torch.optim.Optimizer):
                 self.state[p]["step"] = steps
             lists = [tensor_list(x) for x in ([p.detach() for p in ps], [self.state[p]["exp_avg"] for p in ps],
                                               [self.state[p]["exp_avg_sq"] for p in ps])]
-            plan.append(dict(key=key, members=members, lists=lists, steps=steps, lr=None, rates=None))
+            plan.append(dict(key=key, members=members, lists=lists, steps=steps, lr=None,
+                             rates=torch.empty(len(ps), dtype=torch.float32, device=dev)))
         if plan and (self._ws is None or self._ws.device != dev):
             self._ws = torch.empty(qad_grad_norm_workspace_bytes(), dtype=torch.uint8, device=dev)
             self.last_norm = torch.zeros(1, device=dev)
@@ -478,15 +482,24 @@ class QADAdamW(torch.optim.Optimizer):
             self._launch(grads)
         return loss
 
+    def write_rates(self):
+        """Writes the groups' rates to where the steps read them, on the current stream and without waiting for it.  step()
+        does it; a program that replays a captured step calls it whenever its schedule has moved them."""
+        for part in self._plan or ():
+            lr = [float(group["lr"]) for _, group in part["members"]]
+            if lr != part["lr"]:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("rates have changed: call write_rates() before the capture")
+                part["rates"].copy_(torch.tensor(lr, dtype=torch.float32, pin_memory=True), non_blocking=True)
+                part["lr"] = lr
+
     def _launch(self, grads):
+        self.write_rates()
         norm = None
         if self.max_norm is not None and grads:
             norm = self.last_norm
             qad_grad_norm([g for part in grads for g in part], norm, self._ws)
         for part, gs in zip(self._plan, grads):
-            lr = [float(group["lr"]) for _, group in part["members"]]
-            if lr != part["lr"]:
-                part["lr"], part["rates"] = lr, torch.tensor(lr, dtype=torch.float32).to(part["steps"].device)
             b1, b2, eps, decay, floor = part["key"]
             p, m, v = part["lists"]
             qad_adamw_step(p, gs, m, v, part["rates"], b1, b2, eps, decay, floor, norm,

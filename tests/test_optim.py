@@ -455,3 +455,86 @@ def test_optimizer_of_tensors_that_moved_is_refused(monkeypatch):
             with pytest.raises(ValueError):
                 opt.step()
             assert not calls.norms and not calls.steps
+
+
+@pytest.mark.gpu
+def test_rates_are_rewritten_in_place(monkeypatch):
+    """A schedule writes new rates where the last step read them, which a captured step reads again."""
+    from scale_only_quantization_gb300.autograd import QADAdamW
+    _build()
+    ps = [torch.nn.Parameter(torch.ones(n, device="cuda")) for n in (5, 6)]
+    opt = QADAdamW([dict(params=ps[:1], lr=0.5), dict(params=ps[1:], lr=0.25)])
+    _filled(ps)
+    calls = _NoLaunches(monkeypatch)
+    opt.step()
+    rates = calls.steps[0][4]
+    assert rates.tolist() == [0.5, 0.25]
+    opt.param_groups[1]["lr"] = 0.125
+    opt.step()
+    assert calls.steps[1][4].data_ptr() == rates.data_ptr() and rates.tolist() == [0.5, 0.125]
+
+
+@pytest.mark.gpu
+def test_a_schedule_does_not_wait_for_the_device():
+    from scale_only_quantization_gb300.autograd import QADAdamW
+    _build()
+    ps = [torch.nn.Parameter(torch.ones(n, device="cuda")) for n in (5, 6)]
+    opt = QADAdamW(ps, lr=0.5)
+    _filled(ps)
+    opt.step()
+    torch.cuda.synchronize()
+    mode = torch.cuda.get_sync_debug_mode()
+    torch.cuda.set_sync_debug_mode("error")
+    try:
+        for k in range(3):
+            opt.param_groups[0]["lr"] = 0.25 / (1 + k)
+            opt.step()
+    finally:
+        torch.cuda.set_sync_debug_mode(mode)
+    assert int(opt.state[ps[0]]["step"]) == 4
+
+
+@pytest.mark.gpu
+def test_captured_optimizer_step_under_a_schedule():
+    """A captured step() replayed under a schedule equals eager steps under it; a first step, or one whose rates have not
+    been written, is not captured."""
+    from scale_only_quantization_gb300.autograd import QADAdamW
+    _build()
+    g = _gen(41)
+    init = [torch.rand(n, generator=g, device="cuda") + 0.5 for n in (1000, 7)]
+    grads = [torch.randn(n, generator=g, device="cuda") for n in (1000, 7)]
+    ps = [[torch.nn.Parameter(t.clone()) for t in init] for _ in range(2)]
+    opts = [QADAdamW(p, lr=1e-2) for p in ps]
+    for p in ps:
+        for q, t in zip(p, grads):
+            q.grad = t.clone()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError):
+        with torch.cuda.graph(graph, stream=st):
+            opts[0].step()
+    with torch.cuda.stream(st):
+        opts[0].step()
+    opts[1].step()
+    torch.cuda.synchronize()
+    opts[0].param_groups[0]["lr"] = 5e-3
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError):
+        with torch.cuda.graph(graph, stream=st):
+            opts[0].step()
+    with torch.cuda.stream(st):
+        opts[0].write_rates()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        opts[0].step()
+    for k in range(4):
+        for o in opts:
+            o.param_groups[0]["lr"] = 5e-3 / (1 + k)
+        with torch.cuda.stream(st):
+            opts[0].write_rates()
+            graph.replay()
+        opts[1].step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(*ps))
+    assert int(opts[0].state[ps[0][0]]["step"]) == 5
