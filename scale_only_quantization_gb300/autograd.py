@@ -504,3 +504,5 @@ class QADAdamW(torch.optim.Optimizer):
             p, m, v = part["lists"]
             qad_adamw_step(p, gs, m, v, part["rates"], b1, b2, eps, decay, floor, norm,
                            0.0 if norm is None else self.max_norm, part["steps"], self._ws)
+            for x, _ in part["members"]:  # written behind autograd's back: a graph that saved it must not be used
+                torch.autograd.graph.increment_version(x)

@@ -538,3 +538,19 @@ def test_captured_optimizer_step_under_a_schedule():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(*ps))
     assert int(opts[0].state[ps[0][0]]["step"]) == 5
+
+
+@pytest.mark.gpu
+def test_a_backward_pass_over_parameters_that_moved_is_refused():
+    from scale_only_quantization_gb300.autograd import QADAdamW
+    _build()
+    p = torch.nn.Parameter(torch.full((5,), 2.0, device="cuda"))
+    opt = QADAdamW([p])
+    p.grad = torch.ones_like(p)
+    early = (p * p).sum()
+    opt.step()
+    with pytest.raises(RuntimeError):
+        early.backward()
+    p.grad = None
+    (p * p).sum().backward()
+    assert torch.equal(p.grad, 2 * p.detach())
