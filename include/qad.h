@@ -394,7 +394,8 @@ int qad_token_logprobs(const void* z, int dtype, int64_t ldz, const int32_t* tok
  *          g_entropy); a row with token < 0 or >= V has no g_logp part
  *   g_logp, g_entropy fp32 [N]: the gradients arriving; one may be NULL (none)
  *   dz     [N, V] of z's type, lddz >= V between rows (written; may be z when lddz == ldz)
- * log p = b z - lse is as exact as the stored lse: logits of magnitude X give p to about X * 2^-23 of itself.
+ * log p = b z - lse is as exact as the stored lse: logits of magnitude X give p to about X * 2^-23 of itself (and never
+ * above 1: rows of larger logits have finite gradients, but no known ones).
  * A masked logit (-inf) has gradient 0, and so has a whole row of them.  Rows whose z and dz lie alike relative to
  * 16 bytes are read and written 16 bytes at a time.  Sizes and alignment as in the forward.
  */

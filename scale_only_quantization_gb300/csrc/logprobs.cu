@@ -54,6 +54,13 @@ __device__ __forceinline__ float floor_nan(float v, float lo) {
 // b (v - ref), where v - ref may leave fp32's range: halves do not
 __device__ __forceinline__ float over(float v, float ref, float b) { return fmaf(0.5f, v, -0.5f * ref) * (2.0f * b); }
 
+// min(max(v, lo), hi) that keeps a NaN
+__device__ __forceinline__ float clamp_nan(float v, float lo, float hi) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(floor_nan(v, lo)), "f"(hi));
+  return r;
+}
+
 // A number whose order as an unsigned integer is the float's order (-0 as +0); 0 for a NaN, which is below -inf's.
 __device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);
@@ -693,7 +700,8 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(LogprobsBwd q
   const float nlse = -lse, scale = -q.b;
   const int from = (int)((reinterpret_cast<uintptr_t>(dz) & 15u) / sizeof(ZT));
   auto grad = [&](float zv, int v) {
-    const float lp = floor_nan(fmaf(zv, q.b, nlse), -1e4f);
+    // of a row of 10^7 and more lse's rounding may leave a positive log p of any size: p is a probability all the same
+    const float lp = clamp_nan(fmaf(zv, q.b, nlse), -1e4f, 0.0f);
     const float p = ex2(lp * kLog2e);
     float d = scale * p * fmaf(h, lp + H, g);
     if (v == token) d += q.b * g;

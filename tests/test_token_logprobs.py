@@ -461,3 +461,23 @@ def test_the_smallest_inverse_temperatures(tau, dtype):
     for name in ("lse", "entropy", "logp"):
         assert torch.all((got[name] - ref[name]).abs() <= (2 * off) * (1 if name != "entropy" else 40 + math.log(V))), name
     assert torch.equal(got["idx"], ref["idx"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tau", [0.6, 0.7, 3.0])
+def test_gradient_of_rows_of_large_logits_is_finite(tau, dtype):
+    """Rows of one low number (a padded row): b z - lse is what lse's rounding leaves, of any size and sign, so that p is
+    not known; it is a probability all the same, and a row whose gradients are 0 stays 0."""
+    _build()
+    V = 1003
+    fills = [-1e8, -1e10, -1e20, -1e30, float(torch.finfo(dtype).min) * 0.5, 3e10, 1e30]
+    z = torch.tensor(fills, device="cuda").to(dtype)[:, None].expand(-1, V).contiguous()
+    n = len(fills)
+    token = torch.arange(n, device="cuda", dtype=torch.int32)
+    got = _forward(z, token, 0, tau)
+    one, zero = torch.ones(n, device="cuda"), torch.zeros(n, device="cuda")
+    dz = _backward(z, token, got, one, one, tau).double()
+    # |dz| <= b (g + h p |log p + H|), |p log p| <= 1/e
+    assert torch.all(dz.abs() <= 1 / tau * (2 + math.log(V)) * 1.01)
+    assert torch.all(_backward(z, token, got, zero, zero, tau) == 0)
