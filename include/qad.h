@@ -396,7 +396,7 @@ int qad_token_logprobs(const void* z, int dtype, int64_t ldz, const int32_t* tok
  *   dz     [N, V] of z's type, lddz >= V between rows (written; may be z when lddz == ldz)
  * log p = b z - lse is as exact as the stored lse: logits of magnitude X give p to about X * 2^-23 of itself (and never
  * above 1: rows of larger logits have finite gradients, but no known ones).
- * A masked logit (-inf) has gradient 0, and so has a whole row of them.  Rows whose z and dz lie alike relative to
+ * A masked logit (-inf) has gradient 0, the token's own too, and so has a whole row of them.  Rows whose z and dz lie alike relative to
  * 16 bytes are read and written 16 bytes at a time.  Sizes and alignment as in the forward.
  */
 int qad_token_logprobs_bwd(const void* z, int dtype, int64_t ldz, const int32_t* token, float inv_temp,

@@ -699,14 +699,18 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(LogprobsBwd q
   const bool empty = lse == -INFINITY;
   const float nlse = -lse, scale = -q.b;
   const int from = (int)((reinterpret_cast<uintptr_t>(dz) & 15u) / sizeof(ZT));
-  auto grad = [&](float zv, int v) {
+  // all but the target's own term
+  auto grad = [&](float zv) {
     // of a row of 10^7 and more lse's rounding may leave a positive log p of any size: p is a probability all the same
     const float lp = clamp_nan(fmaf(zv, q.b, nlse), -1e4f, 0.0f);
-    const float p = ex2(lp * kLog2e);
-    float d = scale * p * fmaf(h, lp + H, g);
-    if (v == token) d += q.b * g;
+    const float d = scale * ex2(lp * kLog2e) * fmaf(h, lp + H, g);
     return empty ? 0.0f : d;
   };
+  // The target is written again, by the thread that has its vector, with the term of its own (asked for at every element:
+  // 4096 x 151936 bf16 414 us against 388).  A masked logit is a constant, the target's too.
+  const int at = token + from;
+  const bool own = live && at / (kVec * kBwdThreads * kBwdVecs) == (int)seg && at / kVec % kBwdThreads == (int)threadIdx.x;
+  const float zt = own ? read_one(z + token) : 0.0f;
 #pragma unroll
   for (int i = 0; i < kBwdVecs; ++i) {
     const int v0 = (int)((seg * kBwdVecs + i) * kBwdThreads + threadIdx.x) * kVec - from;
@@ -728,7 +732,7 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(LogprobsBwd q
         for (int j = 0; j < kVec; ++j) f[j] = read_one(z + v0 + j);
       }
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) f[j] = grad(f[j], v0 + j);
+      for (int j = 0; j < kVec; ++j) f[j] = grad(f[j]);
       uint4 o;
       if constexpr (sizeof(ZT) == 4)
         o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
@@ -737,9 +741,10 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(LogprobsBwd q
       *reinterpret_cast<uint4*>(dz + v0) = o;
     } else {
       for (int j = 0; j < kVec; ++j)
-        if (v0 + j >= 0 && v0 + j < q.V) write_one(dz + v0 + j, grad(read_one(z + v0 + j), v0 + j));
+        if (v0 + j >= 0 && v0 + j < q.V) write_one(dz + v0 + j, grad(read_one(z + v0 + j)));
     }
   }
+  if (own) write_one(dz + token, zt == -INFINITY ? grad(zt) : grad(zt) + q.b * g);
 }
 
 template <typename ZT>

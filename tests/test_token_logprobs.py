@@ -481,3 +481,26 @@ def test_gradient_of_rows_of_large_logits_is_finite(tau, dtype):
     # |dz| <= b (g + h p |log p + H|), |p log p| <= 1/e
     assert torch.all(dz.abs() <= 1 / tau * (2 + math.log(V)) * 1.01)
     assert torch.all(_backward(z, token, got, zero, zero, tau) == 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradient_of_a_masked_target_is_zero_there(dtype):
+    _build()
+    V = 5003
+    z = torch.randn((3, V), generator=_gen(23), device="cuda").to(dtype)
+    z[0, 5] = -float("inf")
+    z[1, 10:] = -float("inf")
+    z[2, 4000] = -float("inf")
+    token = torch.tensor([5, 4999, 4001], dtype=torch.int32, device="cuda")
+    got = _forward(z, token, 0)
+    assert float(got["logp"][0]) == float(got["logp"][1]) == -float("inf")
+    g, h = torch.full((3,), 2.0, device="cuda"), torch.full((3,), 0.5, device="cuda")
+    dz = _backward(z, token, got, g, h)
+    assert torch.all(dz[torch.isinf(z)] == 0) and torch.isfinite(dz.float()).all()
+    assert float(dz[2, 4001]) > 1.9
+    # the other logits: log p is off by 2^-23 (|z| + |lse|) <= 2^-18, p and log p + H follow it
+    p = torch.softmax(z[0].double(), 0)
+    lp = torch.log(p).clamp_min(-1e4)
+    ref = -2.0 * p - 0.5 * p * (lp + float(got["entropy"][0]))
+    assert torch.all((dz[0].double() - ref).abs() <= (2.0 ** -8 if dtype == torch.bfloat16 else 0) * ref.abs() + 2.0 ** -18 * p * 20)
