@@ -354,7 +354,8 @@ int qad_distill_topk_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t 
  *           not all come within two seconds, out is invalid), written by each call.
  * Supported: T <= QAD_MOE_FEW_MAX_T, d and F at most QAD_MOE_FEW_MAX_D, and what qad_moe_fwd supports; flags 0 or
  * QAD_FLAG_NO_QUANT (others: QAD_ERR_INVALID_ARG).  One cooperative launch of a block per SM: it starts when all SMs have
- * room for it.  Weights are read once for each 8 tokens that name an expert (4 with d or F above about 5100).
+ * room for it.  Weights are read once for each 8 tokens that name an expert (fewer where d or F is above about 5100: 6 at
+ * 6144, 5 at 8192, or 4 there beside 1024 experts).
  */
 enum { QAD_MOE_FEW_MAX_T = 64, QAD_MOE_FEW_MAX_D = 8192 };
 size_t qad_moe_few_workspace_bytes(const qad_moe_shape* s); /* 0 if the shape is not supported; host-only */

@@ -625,7 +625,7 @@ cudaError_t launch(FewParams q, cudaStream_t st) {
   constexpr int kMost = 227 * 1024 - (int)sizeof(FewSmem) - 1024;
   const int K = q.fc1.K > q.fc2.K ? q.fc1.K : q.fc2.K;
   q.cols = q.T < kCols ? q.T : kCols;
-  while (q.cols > 1 && few_smem(K, q.cols, q.E, 2) > kMost) q.cols /= 2;  // 4 for rows of 8192
+  while (q.cols > 1 && few_smem(K, q.cols, q.E, 2) > kMost) --q.cols;  // rows of 8192: 5, or 4 beside 1024 experts
   q.depth = few_smem(K, q.cols, q.E, 3) <= kMost ? 3 : 2;
   const int bytes = few_smem(K, q.cols, q.E, q.depth);
   const auto kernel = few_kernel<WK, AK>;
