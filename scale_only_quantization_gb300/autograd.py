@@ -81,15 +81,23 @@ class QADMoE(torch.nn.Module):
         self.s2 = torch.nn.Parameter(s2.contiguous())
         self.fmt = int(fmt)
         self.flags = int(flags)
+        self._err = {}  # device -> error word of few(), as QADHeadLoss keeps it
+
+    def device_error(self):
+        """The QAD_DEV_* bits of few()'s calls since it was last read (0: none), and clears them; waits for the device.
+        QAD_DEV_TIMEOUT: an output is invalid."""
+        return QADHeadLoss.device_error(self)
 
     def forward(self, x, topk_idx, topk_w):
         return QADMoEFunction.apply(x.contiguous(), topk_idx.contiguous(), topk_w.contiguous(), self.w13, self.s13,
                                     self.w2, self.s2, self.fmt, self.flags)
 
     @torch.no_grad()
-    def few(self, x, topk_idx, topk_w, quant=True):
+    def few(self, x, topk_idx, topk_w, quant=None):
         """The layer's output for at most QAD_MOE_FEW_MAX_T tokens, without a gradient: what a generation loop calls.
-        quant False: the unquantized teacher."""
+        quant False: the unquantized teacher; None: as the module's flags say.  device_error() has what went wrong."""
+        if quant is None:
+            quant = not self.flags & QAD_FLAG_NO_QUANT
         E, two_f, d = self.w13.shape
         T, k = topk_idx.shape
         if x.dtype != torch.bfloat16 or topk_idx.dtype != torch.int32 or topk_w.dtype != torch.float32 or \
@@ -105,9 +113,12 @@ class QADMoE(torch.nn.Module):
                 s13, s2 = torch.empty_like(self.s13), torch.empty_like(self.s2)
                 for a, b in ((self.s13, s13), (self.s2, s2)):
                     qad_nvfp4_deploy_scales(a, b, E, a.numel() // E)
-            ws = torch.empty(max(1, qad_moe_few_workspace_bytes(s)), dtype=torch.uint8, device=x.device)
+            ws = torch.empty((qad_moe_few_workspace_bytes(s) + 3) // 4, dtype=torch.int32, device=x.device)
             out = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
             qad_moe_few_fwd(s, _packed(x), _packed(topk_idx), _packed(topk_w), self.w13, s13, self.w2, s2, out, ws)
+            if x.device not in self._err:
+                self._err[x.device] = torch.zeros(1, dtype=torch.int32, device=x.device)
+            self._err[x.device].bitwise_or_(ws[:1])
         return out
 
 

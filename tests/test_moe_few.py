@@ -411,3 +411,28 @@ def test_short_rings_and_few_columns(shape, fmt):
     assert np.all(np.abs(vals(out) - ref) <= tol)
     for _ in range(3):  # the same bits again
         assert torch.equal(_few(inp)[0], out)
+
+
+@pytest.mark.gpu
+def test_module_flags_and_error_word():
+    """few() is the layer that the module is: quantized or not as its flags say, unless the call says; what the call's
+    error word held is there to be read."""
+    from scale_only_quantization_gb300.autograd import QADMoE
+    _build()
+    inp = _inputs(5, 256, 128, 4, 2, 0, seed=33)
+    args = (inp["x"], inp["topk_idx"], inp["topk_w"])
+    plain = QADMoE(inp["w13"], inp["s13"], inp["w2"], inp["s2"], 0, Q.QAD_FLAG_NO_QUANT)
+    quant = QADMoE(inp["w13"], inp["s13"], inp["w2"], inp["s2"], 0, Q.QAD_FLAG_RECOMPUTE)
+    off, on = _few(inp, Q.QAD_FLAG_NO_QUANT)[0], _few(inp)[0]
+    assert not torch.equal(off, on)
+    assert torch.equal(plain.few(*args), off) and torch.equal(quant.few(*args), on)
+    assert torch.equal(plain.few(*args, quant=True), on) and torch.equal(quant.few(*args, quant=False), off)
+    assert quant.device_error() == 0 and plain.device_error() == 0
+    idx = inp["topk_idx"].clone()
+    idx[1, 0] = 4
+    quant.few(inp["x"], idx, inp["topk_w"])
+    idx[1, 0] = idx[1, 1]
+    quant.few(inp["x"], idx, inp["topk_w"])
+    quant.few(*args)
+    assert quant.device_error() == Q.QAD_DEV_BAD_INDEX | Q.QAD_DEV_DUP_INDEX and quant.device_error() == 0
+    assert quant.few(inp["x"][:0], idx[:0], inp["topk_w"][:0]).shape == (0, 256) and quant.device_error() == 0
