@@ -463,9 +463,15 @@ class QADAdamW(torch.optim.Optimizer):
             self.last_norm = torch.zeros(1, device=dev)
         return plan
 
-    def load_state_dict(self, state_dict):
-        super().load_state_dict(state_dict)
+    def __getstate__(self):
+        return dict(super().__getstate__(), max_norm=self.max_norm)
+
+    def __setstate__(self, state):
+        """Of a copied or unpickled optimizer, and of load_state_dict(): the plan is made again."""
+        super().__setstate__(state)
         self._plan = None
+        for name in ("_ws", "last_norm"):
+            self.__dict__.setdefault(name, None)
 
     def add_param_group(self, group):
         super().add_param_group(group)

@@ -554,3 +554,26 @@ def test_a_backward_pass_over_parameters_that_moved_is_refused():
     p.grad = None
     (p * p).sum().backward()
     assert torch.equal(p.grad, 2 * p.detach())
+
+
+@pytest.mark.gpu
+def test_a_copied_optimizer_goes_on():
+    import copy
+    import io
+    from scale_only_quantization_gb300.autograd import QADAdamW
+    _build()
+    p = torch.nn.Parameter(torch.linspace(0.5, 1, 100, device="cuda"))
+    opt = QADAdamW([p], lr=1e-2, max_norm=0.5)
+    p.grad = torch.linspace(-1, 2, 100, device="cuda")
+    opt.step()
+    file = io.BytesIO()
+    torch.save(opt, file)
+    file.seek(0)
+    others = [copy.deepcopy(opt), torch.load(file, weights_only=False)]
+    opt.step()
+    for other in others:
+        q = other.param_groups[0]["params"][0]
+        assert q.data_ptr() != p.data_ptr() and other.max_norm == 0.5
+        q.grad = p.grad.clone()
+        other.step()
+        assert torch.equal(q, p) and int(other.state[q]["step"]) == 2 and torch.equal(other.last_norm, opt.last_norm)
