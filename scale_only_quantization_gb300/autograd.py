@@ -406,11 +406,11 @@ class QADAdamW(torch.optim.Optimizer):
     tensors of the same settings ("MCoreQAD Backend", YAML optim: lr, betas, weight decay, grad_clip).
 
     Parameters are fp32; groups may set lr, betas, eps, weight_decay and floor, the lower bound that keeps a scale
-    positive (-inf: none).  max_norm None: no clipping.  Every parameter needs a gradient (fp32 or bf16) at each step; a
-    step whose norm is not finite changes nothing, the count of steps neither.  last_norm [1] is the norm before
-    clipping.  State: exp_avg, exp_avg_sq and step (an int64 on the device that parameters of the same settings and the
-    same number of steps share).  A step may be captured once one has been taken eagerly; its replays read the rates that
-    write_rates() has written, until other settings change or the parameters' memory does.
+    positive (-inf: none).  max_norm None: no clipping (the norm is taken all the same).  Every parameter needs a gradient
+    (fp32 or bf16) at each step; a step whose norm is not finite changes nothing, the count of steps neither.  last_norm
+    [1] is the norm before clipping.  State: exp_avg, exp_avg_sq and step (an int64 on the device that parameters of the
+    same settings and the same number of steps share).  A step may be captured once one has been taken eagerly; its
+    replays read the rates that write_rates() has written, until other settings change or the parameters' memory does.
     """
 
     def __init__(self, params, lr=2e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, floor=-math.inf, max_norm=1.0):
@@ -512,14 +512,13 @@ class QADAdamW(torch.optim.Optimizer):
 
     def _launch(self, grads):
         self.write_rates()
-        norm = None
-        if self.max_norm is not None and grads:
-            norm = self.last_norm
-            qad_grad_norm([g for part in grads for g in part], norm, self._ws)
+        if grads:  # without clipping too: a step whose norm is not finite is left out
+            qad_grad_norm([g for part in grads for g in part], self.last_norm, self._ws)
+        max_norm = math.inf if self.max_norm is None else self.max_norm
         for part, gs in zip(self._plan, grads):
             b1, b2, eps, decay, floor = part["key"]
             p, m, v = part["lists"]
-            qad_adamw_step(p, gs, m, v, part["rates"], b1, b2, eps, decay, floor, norm,
-                           0.0 if norm is None else self.max_norm, part["steps"], self._ws)
+            qad_adamw_step(p, gs, m, v, part["rates"], b1, b2, eps, decay, floor, self.last_norm, max_norm, part["steps"],
+                           self._ws)
             for x, _ in part["members"]:  # written behind autograd's back: a graph that saved it must not be used
                 torch.autograd.graph.increment_version(x)

@@ -577,3 +577,20 @@ def test_a_copied_optimizer_goes_on():
         q.grad = p.grad.clone()
         other.step()
         assert torch.equal(q, p) and int(other.state[q]["step"]) == 2 and torch.equal(other.last_norm, opt.last_norm)
+
+
+@pytest.mark.gpu
+def test_without_clipping_the_norm_is_kept_and_checked():
+    from scale_only_quantization_gb300.autograd import QADAdamW
+    _build()
+    ps = [torch.nn.Parameter(torch.ones(n, device="cuda")) for n in (5, 4)]
+    opt = QADAdamW(ps, lr=0.1, max_norm=None)
+    _filled(ps)
+    opt.step()
+    assert float(opt.last_norm) == 3.0
+    after = [p.detach().clone() for p in ps]
+    assert torch.all((after[0] - 0.9).abs() <= 1e-6)  # lr m / sqrt(v) with m and v of one gradient of 1: not clipped
+    for bad in (float("nan"), float("inf")):
+        ps[1].grad[2] = bad
+        opt.step()
+        assert int(opt.state[ps[0]]["step"]) == 1 and all(torch.equal(p, a) for p, a in zip(ps, after))
