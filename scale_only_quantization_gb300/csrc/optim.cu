@@ -393,11 +393,12 @@ cudaError_t launch_grad_norm(const qad_tensor* grads, int64_t n, float* norm, ui
     prof_end(QAD_K_GRAD_NORM, st);
     return cudaGetLastError();
   }
-  // every launch but the first adds to the partial sums of the first ones' blocks
+  // every launch but the first adds to the partial sums of the first one's blocks: where others follow it has as many as
+  // any of them may want (those without a chunk write a 0)
   cudaError_t e = for_tables<1>(lists, 0, n, [&](const auto& t, int blocks, bool) {
     if (blocks == 0) return cudaSuccess;
     constexpr int CAP = sizeof(t.bf16);
-    if (parts && blocks > parts) blocks = parts;  // blocks beyond those of the first launch have no sum to add to
+    if (!parts && n > CAP) blocks = max_blocks();
     grad_norm_kernel<CAP><<<blocks, kThreads, 0, st>>>(t, part, parts > 0);
     if (parts) note_launches(1);
     else parts = blocks;

@@ -594,3 +594,26 @@ def test_without_clipping_the_norm_is_kept_and_checked():
         ps[1].grad[2] = bad
         opt.step()
         assert int(opt.state[ps[0]]["step"]) == 1 and all(torch.equal(p, a) for p, a in zip(ps, after))
+
+
+@pytest.mark.gpu
+def test_norm_of_a_large_tensor_behind_many_empty_ones():
+    """The tensors that come first do not decide how many blocks the others get: the same time in either order, within
+    what launches and noise may differ (one block for all took over a hundred times as long)."""
+    _build()
+    big, one, none = torch.ones(1 << 26, device="cuda"), torch.ones(1, device="cuda"), torch.empty(0, device="cuda")
+    ws, norm = _ws(), torch.zeros(1, device="cuda")
+
+    def spent(tensors):
+        grads, best = Q.tensor_list(tensors), math.inf
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            Q.qad_grad_norm(grads, norm, ws)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+            assert abs(float(norm) - 8192.0) <= 8192 * 10 * U24 + 1e-3
+        return best
+
+    assert spent([one] + [none] * 500 + [big]) <= 5 * spent([big] + [none] * 500 + [one])
