@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(const double* 
   if (threadIdx.x == 0) norm[0] = root(v);
 }
 
-// min(1, max_norm / (norm + 1e-6)), and a NaN's NaN
+// min(1, max_norm / (norm + 1e-6)), and a NaN's NaN; 0 for an infinite norm, whatever max_norm
 __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
-  const float f = max_norm / (norm + 1e-6f);
+  const float f = norm == INFINITY ? 0.0f : max_norm / (norm + 1e-6f);
   return f >= 1.0f ? 1.0f : f;
 }
 

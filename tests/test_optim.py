@@ -617,3 +617,15 @@ def test_norm_of_a_large_tensor_behind_many_empty_ones():
         return best
 
     assert spent([one] + [none] * 500 + [big]) <= 5 * spent([big] + [none] * 500 + [one])
+
+
+@pytest.mark.gpu
+def test_clip_without_a_bound_by_a_norm_that_is_infinite():
+    """max_norm is infinite too: the finite gradients become 0 all the same, the others NaN (inf times 0)."""
+    _build()
+    g = [torch.tensor([1.0, -2.0, float("inf"), 0.0], device="cuda"), torch.ones(9, device="cuda", dtype=torch.bfloat16)]
+    Q.qad_grad_clip(g, None, torch.full((1,), float("inf"), device="cuda"), float("inf"))
+    assert g[0][[0, 1, 3]].tolist() == [0, 0, 0] and math.isnan(float(g[0][2])) and torch.all(g[1] == 0)
+    h = [torch.tensor([1.0, -2.0], device="cuda")]
+    Q.qad_grad_clip(h, None, _norm(h), float("inf"))
+    assert h[0].tolist() == [1.0, -2.0]
