@@ -423,16 +423,16 @@ __device__ __noinline__ Seen stream(const ZT* base, int first, int end, int from
   using St = Step<ZT>;
   float m = seen.m, off = seen.off, peak = seen.peak;
   uint64_t s2 = seen.s2, u2 = seen.u2;
-  const float span = 200.0f / b2;
   const uint64_t bb = f2pack(b2, b2);
   float enough;
   uint64_t nr;
   uint32_t least;
   bool wild;
   auto refer = [&]() {  // by m: R and what goes with it; returns `off`
-    const float ref = m == -INFINITY ? 0.0f : m, R = ref * b2, low = floor_of<ZT>(__fsub_rd(ref, span));
+    const float unit = 8.0f / b2;  // taken again each time: a register less over the loop, which has none to spare
+    const float ref = m == -INFINITY ? 0.0f : m, R = ref * b2, low = floor_of<ZT>(__fsub_rd(ref, 25.0f * unit));
     wild = !(fabsf(fmaf(low, b2, -R)) < 3e38f && fabsf(R) < 0x1p24f);
-    enough = wild ? m : m + 8.0f / b2;
+    enough = wild ? m : m + unit;
     nr = f2pack(-R, -R);
     least = St::packed(low);
     return wild ? 0.0f : fmaf(ref, b2, -R);
