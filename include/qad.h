@@ -344,8 +344,8 @@ int qad_distill_topk_fwd_bwd(const void* h, int64_t ldh, const void* w, int64_t 
 /*
  * The layer for a few tokens: generation, where qad_moe_fwd would fake-quantize every expert to serve one token.
  * The same definition as qad_moe_fwd (A1, Z1, H, H_hat, Y and out are rounded where that call rounds them), on the
- * weights of the experts that some token names, each read once and fake-quantized on its way to the tensor cores; no
- * copy of the weights is made and nothing is kept for a backward pass.  Only the order of the sums differs.
+ * weights of the experts that some token names, fake-quantized on their way to the tensor cores; no copy of the weights
+ * is made and nothing is kept for a backward pass.  Only the order of the sums differs.
  *   x, topk_idx, topk_w, w13, s13, w2, s2, out as in qad_moe_fwd.  With QAD_FMT_NVFP4_E4M3, s13 and s2 are the deployed
  *           scales that qad_nvfp4_deploy_scales makes (per_mat = 2F * d / 16 and d * F / 16): a generating program
  *           makes them once.

@@ -385,7 +385,7 @@ class QADTokenLogprobs(torch.nn.Module):
     logp [N] is the log probability of each row's token at temperature tau (None without tokens, 0 where the token is
     negative); top_idx and top_logit [N, top] the row's largest logits, which are teacher_idx and teacher_logits of
     QADHeadLoss (None with top 0).  logp and entropy have a gradient.  A token past the vocabulary sets a bit that
-    device_error() returns.
+    device_error() returns.  Logits that do not start on a 16-byte boundary (z[1:] of an odd vocabulary) are copied first.
     """
 
     def __init__(self, tau=1.0, top=0):
@@ -520,5 +520,5 @@ class QADAdamW(torch.optim.Optimizer):
             p, m, v = part["lists"]
             qad_adamw_step(p, gs, m, v, part["rates"], b1, b2, eps, decay, floor, self.last_norm, max_norm, part["steps"],
                            self._ws)
-            for x, _ in part["members"]:  # written behind autograd's back: a graph that saved it must not be used
-                torch.autograd.graph.increment_version(x)
+            # written behind autograd's back: a graph that saved one of them must not be used
+            torch.autograd.graph.increment_version([x for x, _ in part["members"]])

@@ -1,5 +1,5 @@
 // The whole expert layer for a few tokens (generation), in one cooperative launch that reads the weights of the experts
-// that some token names once, fake-quantizes them on their way and multiplies them there.
+// that some token names (once for each 8 tokens of an expert), fake-quantizes them on their way and multiplies them there.
 //
 //   fc1:  Z1 = A1 . W13_hat^T, H = bf16(silu(gate) * up)             A1 = AQ(x)
 //   fc2:  Y = AQ(H) . W2_hat^T, out[t] = bf16(sum_j p[t, j] * Y_j)
@@ -15,8 +15,8 @@
 // 16 in two blocks the quantizers' latencies were not hidden (32 tokens 358 against 302 us).
 //
 // One nvfp4 token naming 8 of 128 experts of 2048 x 768 (85 MB): 39 us, 5.5 of them clearing and launch; 32 w4a16 tokens naming
-// 111 of them 293 to 299 us, 3.6 TB/s; 5 fp8 tokens on 32 experts of 2880 x 2880 163 to 169 us.  8 tokens on 64 experts issue 13
-// instructions a weight at 2.5 a cycle.
+// 111 of them 292 to 300 us, 3.6 TB/s; 5 fp8 tokens on 32 experts of 2880 x 2880 161 to 177 us, by how
+// many experts they name.  8 nvfp4 tokens on 64 experts issue 13 instructions a weight at 2.5 a cycle.
 //
 // Between fc1 and fc2 the blocks wait for one another; their first weights of fc2 are on their way by then.
 #include "common.cuh"

@@ -15,10 +15,10 @@
 // Rows are split over the blocks of a cluster when there are too few to fill the GPU; the cluster's first block joins
 // the others' sums and candidates out of their shared memory.
 //
-// 4096 x 151936 bf16 (1.24 GB): without alternatives 188 us, 6.6 TB/s, bound by memory; with the top 64 283 us, 4.4 TB/s:
+// 4096 x 151936 bf16 (1.24 GB): without alternatives 191 us, 6.5 TB/s, bound by memory; with the top 64 282 us, 4.4 TB/s:
 // 19 of a row's 57 thousand cycles (by clocks in an earlier form) go into its alternatives, most of them latencies, and the
 // blocks that stream meanwhile are bound by the loads they have in flight.  One row of 151936 fp32 logits with 20
-// alternatives 12.3 us.  The gradient of 4096 x 151936 392 us, 6.3 TB/s.
+// alternatives 12.3 us.  The gradient of 4096 x 151936 385 to 394 us, 6.3 to 6.5 TB/s.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -31,7 +31,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 4;                  // 16-byte vectors of a thread per step
-constexpr int kNotes = 20;                // steps whose largest logits are noted before candidates are taken
+// Steps whose largest logits are noted before candidates are taken, a capacity: 20 KB of shared memory hold the notes of
+// 163840 bf16 logits (81920 fp32 ones) of a block; a longer part of a row takes candidates more than once.
+constexpr int kNotes = 20;
 // candidates of a block: about twice K logits reach the bound
 constexpr int kCapSmall = 1024, kCapLarge = 4096, kSmallK = 256;
 // sort_keys() works on powers of two from 2 * kThreads up to the capacity

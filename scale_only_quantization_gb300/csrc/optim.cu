@@ -10,7 +10,7 @@
 // chunks backwards: what the norm read last is still in L2.
 //
 // Norm and clipping of 302 M gradients 556 to 562 us (6.4 to 6.5 TB/s, both readings counted); norm and AdamW of 151 M scales 757 to
-// 768 us (6.3 to 6.4 TB/s).  Of 50 thousand elements 12.3 and 16.4 us, bound by the launches.
+// 773 us (6.2 to 6.4 TB/s).  Of 50 thousand elements 12.3 and 16.4 us, bound by the launches.
 #include "common.cuh"
 #include "internal.h"
 
