@@ -95,7 +95,8 @@ class QADMoE(torch.nn.Module):
     @torch.no_grad()
     def few(self, x, topk_idx, topk_w, quant=None):
         """The layer's output for at most QAD_MOE_FEW_MAX_T tokens, without a gradient: what a generation loop calls.
-        quant False: the unquantized teacher; None: as the module's flags say.  device_error() has what went wrong."""
+        quant False: the unquantized teacher; None: by the module's QAD_FLAG_NO_QUANT.  device_error() has what went
+        wrong."""
         if quant is None:
             quant = not self.flags & QAD_FLAG_NO_QUANT
         E, two_f, d = self.w13.shape
@@ -116,10 +117,17 @@ class QADMoE(torch.nn.Module):
             ws = torch.empty((qad_moe_few_workspace_bytes(s) + 3) // 4, dtype=torch.int32, device=x.device)
             out = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
             qad_moe_few_fwd(s, _packed(x), _packed(topk_idx), _packed(topk_w), self.w13, s13, self.w2, s2, out, ws)
-            if x.device not in self._err:
-                self._err[x.device] = torch.zeros(1, dtype=torch.int32, device=x.device)
-            self._err[x.device].bitwise_or_(ws[:1])
+            _error_word(self._err, x.device).bitwise_or_(ws[:1])
         return out
+
+
+def _error_word(words, device):
+    """The device's error word in `words` (device -> word), made at its first use: an ordinary tensor also where that is in
+    inference mode, since it is written and cleared outside as well."""
+    if device not in words:
+        with torch.inference_mode(False):
+            words[device] = torch.zeros(1, dtype=torch.int32, device=device)
+    return words[device]
 
 
 def _packed(t):
@@ -325,10 +333,8 @@ class QADHeadLoss(torch.nn.Module):
                 g_kd.mul_(self.distill_weight)
         if not torch.is_grad_enabled():
             h = h.detach()
-        if h.device not in self._err:
-            self._err[h.device] = torch.zeros(1, dtype=torch.int32, device=h.device)
         total, ce, kd = QADHeadLossFunction.apply(h, self.w, target, g_lm, teacher_idx, teacher_logits, g_kd, self.tau,
-                                                  mix, self._err[h.device])
+                                                  mix, _error_word(self._err, h.device))
         return total, None if ce is None else ce.sum() / lm_rows, None if kd is None else kd.sum() / kd_rows
 
 
@@ -396,9 +402,7 @@ class QADTokenLogprobs(torch.nn.Module):
     device_error = QADHeadLoss.device_error
 
     def forward(self, z, token=None):
-        if z.device not in self._err:
-            self._err[z.device] = torch.zeros(1, dtype=torch.int32, device=z.device)
-        return QADTokenLogprobsFunction.apply(z, token, self.tau, self.top, self._err[z.device])
+        return QADTokenLogprobsFunction.apply(z, token, self.tau, self.top, _error_word(self._err, z.device))
 
 
 class QADAdamW(torch.optim.Optimizer):

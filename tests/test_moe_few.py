@@ -436,3 +436,29 @@ def test_module_flags_and_error_word():
     quant.few(*args)
     assert quant.device_error() == Q.QAD_DEV_BAD_INDEX | Q.QAD_DEV_DUP_INDEX and quant.device_error() == 0
     assert quant.few(inp["x"][:0], idx[:0], inp["topk_w"][:0]).shape == (0, 256) and quant.device_error() == 0
+
+
+@pytest.mark.gpu
+def test_error_words_of_modules_first_used_in_inference_mode():
+    """A generation loop runs in inference mode; its errors are read, and its modules used, outside as well."""
+    from scale_only_quantization_gb300.autograd import QADHeadLoss, QADMoE, QADTokenLogprobs
+    _build()
+    inp = _inputs(5, 256, 128, 4, 2, 0, seed=35)
+    moe, read = QADMoE(inp["w13"], inp["s13"], inp["w2"], inp["s2"], 0), QADTokenLogprobs()
+    head = QADHeadLoss(torch.randn((64, 256), device="cuda"))
+    bad = inp["topk_idx"].clone()
+    bad[0, 0] = 4
+    z, token = torch.randn((3, 64), device="cuda"), torch.tensor([1, 64, 2], device="cuda")
+    h = torch.randn((3, 256), device="cuda").to(torch.bfloat16)
+    with torch.inference_mode():
+        moe.few(inp["x"], bad, inp["topk_w"])
+        read(z, token)
+        head(h, token)
+    for m in (moe, read, head):
+        assert m.device_error() == Q.QAD_DEV_BAD_INDEX and m.device_error() == 0
+    moe.few(inp["x"], inp["topk_idx"], inp["topk_w"])
+    read(z, token)
+    head(h, token)
+    assert moe.device_error() == 0 and read.device_error() == head.device_error() == Q.QAD_DEV_BAD_INDEX
+    with torch.inference_mode():
+        assert moe.device_error() == 0
